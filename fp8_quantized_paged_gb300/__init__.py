@@ -358,3 +358,20 @@ def new_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, device="cuda"):
     if n == 0:
         raise KvqError(KVQ_ERR_ARG, "kvq_decode_workspace_size")
     return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+# --------------------------------------------------------------------------
+# the microscaled 4-bit cache
+# --------------------------------------------------------------------------
+
+_FP4 = ("kvq_fp4_write", "kvq_fp4_read", "kvq_fp4_workspace_size", "kvq_fp4_decode_attn",
+        "kvq_fp4_prefill_attn", "new_fp4_cache", "new_fp4_workspace")
+
+
+def __getattr__(name):
+    """The names of ``fp4``, which needs torch at import where this module does not."""
+    if name in _FP4:
+        from . import fp4
+        globals().update({n: getattr(fp4, n) for n in _FP4})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

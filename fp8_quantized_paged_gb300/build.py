@@ -18,9 +18,10 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libkvq.so")
 SOURCES = ["kvq_host.cu", "kvq_write.cu", "kvq_decode.cu", "kvq_decode_tc.cu", "kvq_decode_blk.cu",
-           "kvq_static.cu", "kvq_calib.cu", "kvq_prefill.cu", "kvq_decode_variant.cu"]
+           "kvq_static.cu", "kvq_calib.cu", "kvq_prefill.cu", "kvq_decode_variant.cu",
+           "kvq_fp4_write.cu", "kvq_fp4_attn.cu"]
 HEADERS = ["kvq_common.cuh", "kvq_host.h", "kvq_decode.cuh", "kvq_tc.cuh", "kvq_decode_tc.cuh",
-           "kvq_decode_blk.cuh", "kvq_prefill_tc.cuh"]
+           "kvq_decode_blk.cuh", "kvq_prefill_tc.cuh", "kvq_fp4.cuh"]
 # (object, source, defines): one object per translation unit, the decode
 # variants once per (format, head size); kvq_fmt 0 = BF16, 1 = E4M3, 2 = E5M2
 UNITS = [(os.path.splitext(s)[0], s, []) for s in SOURCES if s != "kvq_decode_variant.cu"] + [
@@ -40,8 +41,9 @@ def _nvcc() -> str:
 
 
 def _inputs():
-    inc = os.path.join(os.path.dirname(HERE), "include", "kvq.h")
-    return [os.path.join(CSRC, s) for s in SOURCES + HEADERS] + [inc, os.path.abspath(__file__)]
+    inc = os.path.join(os.path.dirname(HERE), "include")
+    return ([os.path.join(CSRC, s) for s in SOURCES + HEADERS] +
+            [os.path.join(inc, h) for h in ("kvq.h", "kvq_fp4.h")] + [os.path.abspath(__file__)])
 
 
 # The tests' timeout build: the same sources with the test hooks compiled in

@@ -1,0 +1,377 @@
+// kvq_fp4_write.cu -- quantize-and-scatter into the microscaled 4-bit cache,
+// and the gather back to bf16.
+//
+// Both are HBM streams.  A thread owns one block of 16 consecutive dims of
+// one (token, KV head) row, the unit that shares a scale: the write loads two
+// 16-byte words per tensor and stores 8 bytes of codes and one of scale, the
+// read the reverse, so a row's lanes move whole contiguous runs.
+#include "kvq_fp4.cuh"
+#include "kvq_host.h"
+
+namespace kvq {
+namespace fp4 {
+
+struct WriteParams {
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t token_stride;
+  const int64_t* slots;
+  int64_t num_tokens;
+  int hkv;
+  uint8_t* kc;
+  uint8_t* vc;
+  int64_t capacity;  // num_blocks * 16
+  const float* ks;
+  const float* vs;
+  int per_head;
+  uint32_t* status;
+};
+
+// x / d for bf16 x as the IEEE binary32 quotient: for d in [2^-80, 2^80] from
+// r = RN(1/d) and one fused residual correction (Markstein's iteration, exact
+// for every bf16 significand over every binary32 one), else by division.  The
+// numerator is first clamped to +-2^20 d rounded toward zero, far past what
+// the codes and scales hold, so that no intermediate overflows.
+struct Divider {
+  float d, r;
+  uint32_t L2;  // bf16x2 (L, L), L the clamp
+  bool fast;
+};
+
+KVQ_DEVI Divider divider(float d) {
+  Divider v;
+  v.d = d;
+  v.fast = d >= 0x1p-80f && d <= 0x1p80f;
+  v.r = __frcp_rn(d);
+  uint16_t L;
+  asm("cvt.rz.bf16.f32 %0, %1;" : "=h"(L) : "f"(v.fast ? d * 1048576.f : 0.f));
+  v.L2 = static_cast<uint32_t>(L) * 0x10001u;
+  return v;
+}
+
+// The two bf16 of a word over v.d.
+KVQ_DEVI float2 quotient2(uint32_t w, const Divider& v) {
+  if (!v.fast)
+    return make_float2(__fdiv_rn(bf16lo_to_f32(w), v.d), __fdiv_rn(bf16hi_to_f32(w), v.d));
+  uint32_t c;  // sign(x) min(|x|, L)
+  asm("min.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(w), "r"(v.L2));
+  const float2 x = make_float2(bf16lo_to_f32(c), bf16hi_to_f32(c));
+  const float2 r2 = make_float2(v.r, v.r), nd2 = make_float2(-v.d, -v.d);
+  const float2 q0 = __fmul2_rn(x, r2);
+  const float2 e = __ffma2_rn(q0, nd2, x);
+  return __ffma2_rn(e, r2, q0);
+}
+
+// One block: 16 bf16 (a, b) -> 8 bytes of codes and the scale byte.
+// s: the head's scale; six: the divider of 6 s.
+KVQ_DEVI uint2 quantize_block(const uint4& a, const uint4& b, float s, const Divider& six,
+                              uint32_t& scale) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  // magnitudes order like their bits: finite < infinity (0x7F80) < NaN
+  uint32_t m2 = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m2 = __vmaxu2(m2, w[i] & 0x7FFF7FFFu);
+  const uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+  if (m > 0x7F80u) {  // a NaN: the scale code NaN, codes of 0
+    scale = 0x7Fu;
+    return make_uint2(0u, 0u);
+  }
+  const uint32_t amax = min(m, 0x7F7Fu);
+  scale = f32x2_to_fp8x2<KVQ_FMT_E4M3>(quotient2(amax, six).x, 0.f) & 0xFFu;
+  const float r = __fmul_rn(e4m3_to_f32(scale), s);
+  if (!(r > 0.f)) return make_uint2(0u, 0u);
+  const Divider div = divider(r);
+  uint2 o;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = quotient2(w[4 * h + i], div);
+      q[2 * i] = v.x;
+      q[2 * i + 1] = v.y;
+    }
+    uint32_t c = f32x8_to_e2m1x8(q);
+    // the residual form loses the sign of a zero quotient: take all signs
+    // (bits 15 and 31 of word i) from the inputs, to bits 8i + 3 and 8i + 7
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = w[4 * h + i];
+      c |= (((x >> 12) & 8u) | ((x >> 24) & 0x80u)) << (8 * i);
+    }
+    (h ? o.y : o.x) = c;
+  }
+  return o;
+}
+
+// The grid's thread count is a multiple of the Hkv * DH / 16 blocks of a token
+// (token_row_shape), so a thread keeps its block and its head's scales and
+// strides over the tokens; the next token's loads are issued before the
+// current one is converted.
+template <int DH>
+__global__ void __launch_bounds__(256, 3) write_kernel(const WriteParams p) {
+  using P = Page<DH>;
+  constexpr int CH = DH / 16;
+  pdl_allow_next();
+  pdl_wait();  // the inputs may come from the kernel before this one
+  const int row_units = p.hkv * CH;
+  const int64_t gtid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int rem = static_cast<int>(gtid % row_units);
+  const int h = rem / CH, c = rem % CH;
+  const int64_t tstride = static_cast<int64_t>(gridDim.x) * blockDim.x / row_units;
+  int64_t t = gtid / row_units;
+  if (t >= p.num_tokens) return;
+  const float sk = __ldg(p.ks + (p.per_head ? h : 0)), sv = __ldg(p.vs + (p.per_head ? h : 0));
+  const Divider dk = divider(__fmul_rn(6.f, sk)), dv = divider(__fmul_rn(6.f, sv));
+  uint4 k[2], v[2];
+  int64_t slot;
+  auto load = [&](int64_t tt, uint4 (&kk)[2], uint4 (&vv)[2], int64_t& s) {
+    const int64_t src = tt * p.token_stride + rem * 16;
+    const uint4* kp = reinterpret_cast<const uint4*>(p.k + src);
+    const uint4* vp = reinterpret_cast<const uint4*>(p.v + src);
+    kk[0] = __ldcs(kp);
+    kk[1] = __ldcs(kp + 1);
+    vv[0] = __ldcs(vp);
+    vv[1] = __ldcs(vp + 1);
+    s = __ldg(p.slots + tt);
+  };
+  load(t, k, v, slot);
+  while (true) {
+    const int64_t tn = t + tstride;
+    uint4 kn[2], vn[2];
+    int64_t sn = -1;
+    if (tn < p.num_tokens) load(tn, kn, vn, sn);
+    if (slot >= p.capacity) {
+      if (rem == 0) flag_status(p.status, KVQ_DEV_BAD_SLOT);
+    } else if (slot >= 0) {  // a negative slot is a padding token
+      const int64_t page = ((slot >> 4) * p.hkv + h) * P::kBytes;
+      const int row = static_cast<int>(slot & 15);
+      const int64_t code = page + row * P::kRow + c * 8, sc = page + P::kScaleOff + row * P::kScales + c;
+      uint32_t bk, bv;
+      *reinterpret_cast<uint2*>(p.kc + code) = quantize_block(k[0], k[1], sk, dk, bk);
+      *reinterpret_cast<uint2*>(p.vc + code) = quantize_block(v[0], v[1], sv, dv, bv);
+      p.kc[sc] = static_cast<uint8_t>(bk);
+      p.vc[sc] = static_cast<uint8_t>(bv);
+    }
+    if (tn >= p.num_tokens) break;
+    t = tn;
+    k[0] = kn[0];
+    k[1] = kn[1];
+    v[0] = vn[0];
+    v[1] = vn[1];
+    slot = sn;
+  }
+}
+
+struct ReadParams {
+  const uint8_t* kc;
+  const uint8_t* vc;
+  int64_t num_blocks;
+  int hkv;
+  const int32_t* block_tables;
+  int max_blocks;
+  const int32_t* starts;
+  const int32_t* cu;
+  int num_seqs;
+  int64_t num_rows;
+  const float* ks;
+  const float* vs;
+  int per_head;
+  uint16_t* ko;
+  uint16_t* vo;
+  int64_t out_stride;
+  uint32_t* status;
+};
+
+// 16 values of one block: (code * block scale) exact in f16 and binary32, one
+// binary32 product with s, then bf16.
+KVQ_DEVI void read_block(const uint8_t* cache, int64_t code, int64_t sc, float s, uint16_t* dst) {
+  const uint2 w = __ldg(reinterpret_cast<const uint2*>(cache + code));
+  const float sb = e4m3_to_f32(__ldg(cache + sc));
+  uint32_t o[8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t f[4];
+    e2m1x8_to_f16x2x4(h ? w.y : w.x, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[4 * h + i] = f32x2_to_bf16x2(__fmul_rn(__fmul_rn(f16lo_to_f32(f[i]), sb), s),
+                                     __fmul_rn(__fmul_rn(f16hi_to_f32(f[i]), sb), s));
+  }
+  uint4* d = reinterpret_cast<uint4*>(dst);
+  __stcs(d, make_uint4(o[0], o[1], o[2], o[3]));
+  __stcs(d + 1, make_uint4(o[4], o[5], o[6], o[7]));
+}
+
+template <int DH>
+__global__ void __launch_bounds__(256) read_kernel(const ReadParams p) {
+  using P = Page<DH>;
+  constexpr int CH = DH / 16;
+  pdl_allow_next();
+  pdl_wait();
+  const int row_units = p.hkv * CH;
+  const int64_t gtid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int rem = static_cast<int>(gtid % row_units);
+  const int h = rem / CH, c = rem % CH;
+  const int64_t tstride = static_cast<int64_t>(gridDim.x) * blockDim.x / row_units;
+  const int64_t rows = min(p.num_rows, static_cast<int64_t>(__ldg(p.cu + p.num_seqs)));
+  const float sk = __ldg(p.ks + (p.per_head ? h : 0)), sv = __ldg(p.vs + (p.per_head ? h : 0));
+  for (int64_t r = gtid / row_units; r < rows; r += tstride) {
+    int lo = 0, hi = p.num_seqs - 1;  // last b with cu[b] <= r
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (__ldg(p.cu + mid) <= r)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    const int64_t pos = r - __ldg(p.cu + lo) + (p.starts ? __ldg(p.starts + lo) : 0);
+    int64_t blk = -1;
+    if (pos < 0 || pos >= static_cast<int64_t>(p.max_blocks) * kTok) {
+      if (rem == 0) flag_status(p.status, KVQ_DEV_BAD_SEQLEN);
+    } else {
+      blk = __ldg(p.block_tables + static_cast<int64_t>(lo) * p.max_blocks + pos / kTok);
+      if (blk < 0 || blk >= p.num_blocks) {
+        if (rem == 0) flag_status(p.status, KVQ_DEV_BAD_BLOCK);
+        blk = -1;
+      }
+    }
+    const int64_t dst = r * p.out_stride + rem * 16;
+    if (blk < 0) {
+      const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+      uint4* kd = reinterpret_cast<uint4*>(p.ko + dst);
+      uint4* vd = reinterpret_cast<uint4*>(p.vo + dst);
+      kd[0] = kd[1] = z;
+      vd[0] = vd[1] = z;
+      continue;
+    }
+    const int row = static_cast<int>(pos % kTok);
+    const int64_t page = (blk * p.hkv + h) * P::kBytes;
+    const int64_t code = page + row * P::kRow + c * 8, sc = page + P::kScaleOff + row * P::kScales + c;
+    read_block(p.kc, code, sc, sk, p.ko + dst);
+    read_block(p.vc, code, sc, sv, p.vo + dst);
+  }
+}
+
+static int check_scales(const float* k_scale, int k_len, const float* v_scale, int v_len, int gran,
+                        int num_kv_heads) {
+  if (gran != KVQ_SCALE_PER_TENSOR && gran != KVQ_SCALE_PER_HEAD) return KVQ_ERR_ARG;
+  if (!k_scale || !v_scale) return KVQ_ERR_NULL;
+  const int want = gran == KVQ_SCALE_PER_HEAD ? num_kv_heads : 1;
+  if (k_len != want || v_len != want) return KVQ_ERR_SHAPE;
+  if ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & 3u)
+    return KVQ_ERR_ALIGN;
+  return KVQ_OK;
+}
+
+}  // namespace fp4
+}  // namespace kvq
+
+using namespace kvq;
+
+extern "C" int kvq_fp4_write(const void* k, const void* v, int64_t token_stride,
+                             const int64_t* slot_mapping, int64_t num_tokens, int num_kv_heads,
+                             int head_dim, void* k_cache, void* v_cache, int64_t num_blocks,
+                             int block_size, const float* k_scale, int k_scale_len,
+                             const float* v_scale, int v_scale_len, int scale_granularity,
+                             uint32_t* dev_status, kvq_stream_t stream) {
+  if (num_tokens < 0 || num_kv_heads <= 0 || num_blocks <= 0) return KVQ_ERR_ARG;
+  const int sc = fp4::check_scales(k_scale, k_scale_len, v_scale, v_scale_len, scale_granularity,
+                                   num_kv_heads);
+  if (sc != KVQ_OK) return sc;
+  if (!k_cache || !v_cache) return KVQ_ERR_NULL;
+  if (num_tokens > 0 && (!k || !v || !slot_mapping)) return KVQ_ERR_NULL;
+  if (head_dim != 64 && head_dim != 128) return KVQ_ERR_UNSUPPORTED;
+  if (block_size != fp4::kTok) return KVQ_ERR_UNSUPPORTED;
+  if (num_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;
+  if (token_stride < static_cast<int64_t>(num_kv_heads) * head_dim) return KVQ_ERR_SHAPE;
+  if (token_stride % 8 != 0) return KVQ_ERR_ALIGN;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+    return KVQ_ERR_ALIGN;
+  if (num_blocks > (INT64_MAX / 16) / (static_cast<int64_t>(num_kv_heads) * head_dim) ||
+      (num_tokens > 0 && token_stride > (INT64_MAX / 16) / num_tokens))
+    return KVQ_ERR_SHAPE;
+  if (num_tokens == 0) return KVQ_OK;
+  if (device_sm_count() <= 0) return KVQ_ERR_CUDA;
+  fp4::WriteParams p;
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.token_stride = token_stride;
+  p.slots = slot_mapping;
+  p.num_tokens = num_tokens;
+  p.hkv = num_kv_heads;
+  p.kc = static_cast<uint8_t*>(k_cache);
+  p.vc = static_cast<uint8_t*>(v_cache);
+  p.capacity = num_blocks * block_size;
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.per_head = scale_granularity == KVQ_SCALE_PER_HEAD;
+  p.status = dev_status;
+  int grid = 0, block = 0;
+  token_row_shape(num_tokens, num_kv_heads * (head_dim / 16), 3, grid, block);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = head_dim == 128
+                            ? launch_pdl(fp4::write_kernel<128>, dim3(grid), dim3(block), 0, s, p)
+                            : launch_pdl(fp4::write_kernel<64>, dim3(grid), dim3(block), 0, s, p);
+  if (e != cudaSuccess) return KVQ_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+extern "C" int kvq_fp4_read(const void* k_cache, const void* v_cache, int64_t num_blocks,
+                            int block_size, int num_kv_heads, int head_dim,
+                            const int32_t* block_tables, int max_blocks_per_seq,
+                            const int32_t* starts, const int32_t* cu_lens, int num_seqs,
+                            int64_t num_rows, const float* k_scale, int k_scale_len,
+                            const float* v_scale, int v_scale_len, int scale_granularity,
+                            void* k_out, void* v_out, int64_t out_stride, uint32_t* dev_status,
+                            kvq_stream_t stream) {
+  if (num_rows < 0 || num_kv_heads <= 0 || num_blocks <= 0 || num_seqs <= 0 ||
+      max_blocks_per_seq <= 0)
+    return KVQ_ERR_ARG;
+  const int sc = fp4::check_scales(k_scale, k_scale_len, v_scale, v_scale_len, scale_granularity,
+                                   num_kv_heads);
+  if (sc != KVQ_OK) return sc;
+  if (!k_cache || !v_cache || !block_tables || !cu_lens) return KVQ_ERR_NULL;
+  if (num_rows > 0 && (!k_out || !v_out)) return KVQ_ERR_NULL;
+  if (head_dim != 64 && head_dim != 128) return KVQ_ERR_UNSUPPORTED;
+  if (block_size != fp4::kTok) return KVQ_ERR_UNSUPPORTED;
+  if (num_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;
+  if (out_stride < static_cast<int64_t>(num_kv_heads) * head_dim) return KVQ_ERR_SHAPE;
+  if (out_stride % 8 != 0) return KVQ_ERR_ALIGN;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out) ||
+      ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(starts) |
+        reinterpret_cast<uintptr_t>(cu_lens)) & 3u))
+    return KVQ_ERR_ALIGN;
+  if (num_blocks > (INT64_MAX / 16) / (static_cast<int64_t>(num_kv_heads) * head_dim) ||
+      (num_rows > 0 && out_stride > (INT64_MAX / 16) / num_rows))
+    return KVQ_ERR_SHAPE;
+  if (num_rows == 0) return KVQ_OK;
+  if (device_sm_count() <= 0) return KVQ_ERR_CUDA;
+  fp4::ReadParams p;
+  p.kc = static_cast<const uint8_t*>(k_cache);
+  p.vc = static_cast<const uint8_t*>(v_cache);
+  p.num_blocks = num_blocks;
+  p.hkv = num_kv_heads;
+  p.block_tables = block_tables;
+  p.max_blocks = max_blocks_per_seq;
+  p.starts = starts;
+  p.cu = cu_lens;
+  p.num_seqs = num_seqs;
+  p.num_rows = num_rows;
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.per_head = scale_granularity == KVQ_SCALE_PER_HEAD;
+  p.ko = static_cast<uint16_t*>(k_out);
+  p.vo = static_cast<uint16_t*>(v_out);
+  p.out_stride = out_stride;
+  p.status = dev_status;
+  int grid = 0, block = 0;
+  token_row_shape(num_rows, num_kv_heads * (head_dim / 16), 8, grid, block);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = head_dim == 128
+                            ? launch_pdl(fp4::read_kernel<128>, dim3(grid), dim3(block), 0, s, p)
+                            : launch_pdl(fp4::read_kernel<64>, dim3(grid), dim3(block), 0, s, p);
+  if (e != cudaSuccess) return KVQ_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
