@@ -1,0 +1,118 @@
+// kvq_fp4_decode.cu -- entry point and launch of the 4-bit cache's decode.
+#include "kvq_fp4_decode.cuh"
+#include "kvq_fp4_host.h"
+
+namespace kvq {
+namespace fp4 {
+
+// Segments of at most this many pages, each with an SM to itself, go whole to
+// one CTA.
+#ifndef KVQ_FP4_SEG
+#define KVQ_FP4_SEG 128
+#endif
+constexpr int kSegPages = KVQ_FP4_SEG;
+constexpr int kMaxSmem = 227 * 1024 - 1024;  // the static part and the system's
+
+template <int DH>
+static int launch_decode(DecParams p, bool seg, int grid, cudaStream_t s) {
+  static DeviceOnce once;
+  if (!once.run(current_device(), [] {
+        auto configure = [](auto kernel) {
+          return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      kMaxSmem / kDecCtas) == cudaSuccess &&
+                 cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                      cudaSharedmemCarveoutMaxShared) == cudaSuccess;
+        };
+        return configure(decode_kernel<DH, true>) && configure(decode_kernel<DH, false>);
+      }))
+    return KVQ_ERR_CUDA;
+  p.S = kMaxStages;
+  while (p.S > 1 && dec_smem<DH>(p.S, p.G, p.B, seg).total > kMaxSmem / kDecCtas) --p.S;
+  const size_t smem = dec_smem<DH>(p.S, p.G, p.B, seg).total;
+  const cudaError_t e =
+      seg ? launch_pdl(decode_kernel<DH, true>, dim3(grid), dim3(kDecThreads), smem, s, p)
+          : launch_pdl(decode_kernel<DH, false>, dim3(grid), dim3(kDecThreads), smem, s, p);
+  if (e != cudaSuccess) return KVQ_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+}  // namespace fp4
+}  // namespace kvq
+
+using namespace kvq;
+
+extern "C" size_t kvq_fp4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
+                                         int head_dim, int num_sms) {
+  if (num_seqs <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads)
+    return 0;
+  if (head_dim != 64 && head_dim != 128) return 0;
+  if (num_sms <= 0) num_sms = device_sm_count();
+  if (num_sms <= 0) return 0;
+  return fp4::dec_ws(num_seqs, num_q_heads / num_kv_heads, num_kv_heads, head_dim,
+                     fp4::kDecCtas * num_sms).total;
+}
+
+extern "C" int kvq_fp4_decode_attn(const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_tables, int max_blocks_per_seq,
+                                   const int32_t* seq_lens, int num_seqs, int num_q_heads,
+                                   int num_kv_heads, int head_dim, int64_t num_blocks,
+                                   int block_size, const float* k_scale, int k_scale_len,
+                                   const float* v_scale, int v_scale_len, int scale_granularity,
+                                   int sliding_window, int num_sinks, void* workspace,
+                                   size_t workspace_bytes, void* out, uint32_t* dev_status,
+                                   kvq_stream_t stream) {
+  const int st = fp4::check_attn(q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens,
+                                 num_seqs, num_q_heads, num_kv_heads, head_dim, num_blocks,
+                                 block_size, k_scale, k_scale_len, v_scale, v_scale_len,
+                                 scale_granularity, sliding_window, num_sinks, workspace, out);
+  if (st != KVQ_OK) return st;
+  if (num_seqs > kMaxSeqs || num_seqs * num_kv_heads > kMaxSegments) return KVQ_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_seqs) * (static_cast<int64_t>(max_blocks_per_seq) + fp4::kPc) *
+          num_kv_heads >= (int64_t(1) << 31))
+    return KVQ_ERR_UNSUPPORTED;
+  const int G = num_q_heads / num_kv_heads, sms = device_sm_count();
+  if (sms <= 0) return KVQ_ERR_CUDA;
+  const int P = fp4::kDecCtas * sms;
+  const fp4::DecWs wl = fp4::dec_ws(num_seqs, G, num_kv_heads, head_dim, P);
+  if (workspace_bytes < wl.total) return KVQ_ERR_WORKSPACE;
+
+  // the most pages that one segment can have, from what the host knows
+  int64_t pages = max_blocks_per_seq;
+  if (sliding_window > 0)
+    pages = std::min<int64_t>(pages, (static_cast<int64_t>(sliding_window) + fp4::kTok - 1) / fp4::kTok + 1 +
+                                         (static_cast<int64_t>(num_sinks) + fp4::kTok - 1) / fp4::kTok);
+  const int segs = num_seqs * num_kv_heads;
+  const bool seg = segs <= P && pages <= fp4::kSegPages;
+  const int64_t ctas = seg ? segs : (segs * pages + fp4::kDecWarps - 1) / fp4::kDecWarps;
+
+  fp4::DecParams p;
+  p.q = static_cast<const uint16_t*>(q);
+  p.kc = static_cast<const uint8_t*>(k_cache);
+  p.vc = static_cast<const uint8_t*>(v_cache);
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.max_blocks = max_blocks_per_seq;
+  p.B = num_seqs;
+  p.Hq = num_q_heads;
+  p.Hkv = num_kv_heads;
+  p.G = G;
+  p.num_blocks = num_blocks;
+  p.window = sliding_window;
+  p.sinks = num_sinks;
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.per_head = scale_granularity == KVQ_SCALE_PER_HEAD;
+  p.logit_scale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(head_dim)));
+  p.P = P;
+  p.S = 0;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.ws_cnt = reinterpret_cast<uint32_t*>(ws);
+  p.ws_ml = reinterpret_cast<float2*>(ws + wl.ml);
+  p.ws_o = reinterpret_cast<float*>(ws + wl.o);
+  p.out = static_cast<uint16_t*>(out);
+  p.status = dev_status;
+  const int grid = static_cast<int>(std::min<int64_t>(ctas, seg ? ctas : P));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return head_dim == 128 ? fp4::launch_decode<128>(p, seg, grid, s)
+                         : fp4::launch_decode<64>(p, seg, grid, s);
+}

@@ -1,5 +1,5 @@
-// kvq_fp4_attn.cu -- attention over the microscaled 4-bit cache: the decode
-// and prefill entry points and a plain kernel that serves both.
+// kvq_fp4_prefill.cu -- prefill attention over the microscaled 4-bit cache: a
+// plain kernel.
 //
 // One CTA per (query token, KV head).  Its four warps take the visible pages
 // in turn; a page's 16 tokens go two lanes a token for the logits, and the
@@ -9,13 +9,13 @@
 #include <cmath>
 
 #include "kvq_fp4.cuh"
-#include "kvq_host.h"
+#include "kvq_fp4_host.h"
 
 namespace kvq {
 namespace fp4 {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
-constexpr int kMaxG = 8;
+constexpr int kMaxG = 8;  // query heads per KV head
 constexpr int kWarps = 4;
 
 struct AttnParams {
@@ -151,34 +151,6 @@ __global__ void __launch_bounds__(kWarps * 32) attn_kernel(const AttnParams p) {
   }
 }
 
-// What the two entry points check alike.
-static int check_attn(const void* q, const void* k_cache, const void* v_cache,
-                      const int32_t* block_tables, int max_blocks, const int32_t* seq_lens,
-                      int num_seqs, int hq, int hkv, int dh, int64_t num_blocks, int block_size,
-                      const float* k_scale, int k_len, const float* v_scale, int v_len, int gran,
-                      int window, int sinks, const void* workspace, const void* out) {
-  if (gran != KVQ_SCALE_PER_TENSOR && gran != KVQ_SCALE_PER_HEAD) return KVQ_ERR_ARG;
-  if (num_seqs <= 0 || hq <= 0 || hkv <= 0 || num_blocks <= 0 || max_blocks <= 0 || window < 0 ||
-      sinks < 0)
-    return KVQ_ERR_ARG;
-  if (!q || !k_cache || !v_cache || !block_tables || !seq_lens || !workspace || !out || !k_scale ||
-      !v_scale)
-    return KVQ_ERR_NULL;
-  if (dh != 64 && dh != 128) return KVQ_ERR_UNSUPPORTED;
-  if (block_size != kTok) return KVQ_ERR_UNSUPPORTED;
-  if (hq % hkv) return KVQ_ERR_SHAPE;
-  if (hq / hkv > kMaxG || hkv > 256) return KVQ_ERR_UNSUPPORTED;
-  const int want = gran == KVQ_SCALE_PER_HEAD ? hkv : 1;
-  if (k_len != want || v_len != want) return KVQ_ERR_SHAPE;
-  if (num_blocks > (INT64_MAX / 16) / (static_cast<int64_t>(hkv) * dh)) return KVQ_ERR_SHAPE;
-  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
-      (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
-      ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(seq_lens) |
-        reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & 3u))
-    return KVQ_ERR_ALIGN;
-  return KVQ_OK;
-}
-
 static int launch_attn(const AttnParams& p, int dh, cudaStream_t s) {
   const dim3 grid(p.max_q, p.Hkv, p.B), block(kWarps * 32);
   const cudaError_t e = dh == 128 ? launch_pdl(attn_kernel<128>, grid, block, 0, s, p)
@@ -191,45 +163,6 @@ static int launch_attn(const AttnParams& p, int dh, cudaStream_t s) {
 }  // namespace kvq
 
 using namespace kvq;
-
-extern "C" size_t kvq_fp4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
-                                         int head_dim, int num_sms) {
-  if (num_seqs <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads)
-    return 0;
-  if (head_dim != 64 && head_dim != 128) return 0;
-  return KVQ_WS_COUNTER_BYTES;
-}
-
-extern "C" int kvq_fp4_decode_attn(const void* q, const void* k_cache, const void* v_cache,
-                                   const int32_t* block_tables, int max_blocks_per_seq,
-                                   const int32_t* seq_lens, int num_seqs, int num_q_heads,
-                                   int num_kv_heads, int head_dim, int64_t num_blocks,
-                                   int block_size, const float* k_scale, int k_scale_len,
-                                   const float* v_scale, int v_scale_len, int scale_granularity,
-                                   int sliding_window, int num_sinks, void* workspace,
-                                   size_t workspace_bytes, void* out, uint32_t* dev_status,
-                                   kvq_stream_t stream) {
-  const int st = fp4::check_attn(q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens,
-                                 num_seqs, num_q_heads, num_kv_heads, head_dim, num_blocks,
-                                 block_size, k_scale, k_scale_len, v_scale, v_scale_len,
-                                 scale_granularity, sliding_window, num_sinks, workspace, out);
-  if (st != KVQ_OK) return st;
-  if (num_seqs > 4096 || num_seqs * num_kv_heads > 65536) return KVQ_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(num_seqs) * (static_cast<int64_t>(max_blocks_per_seq) + 16) *
-          num_kv_heads >= (int64_t(1) << 31))
-    return KVQ_ERR_UNSUPPORTED;
-  const size_t need = kvq_fp4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, 0);
-  if (need == 0) return KVQ_ERR_CUDA;
-  if (workspace_bytes < need) return KVQ_ERR_WORKSPACE;
-  const fp4::AttnParams p = {
-      static_cast<const uint16_t*>(q), static_cast<const uint8_t*>(k_cache),
-      static_cast<const uint8_t*>(v_cache), block_tables, seq_lens, nullptr, max_blocks_per_seq,
-      num_seqs, num_q_heads, num_kv_heads, num_q_heads / num_kv_heads, num_blocks, num_seqs, 1,
-      sliding_window, num_sinks, k_scale, v_scale, scale_granularity == KVQ_SCALE_PER_HEAD,
-      static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(head_dim))),
-      static_cast<uint16_t*>(out), dev_status};
-  return fp4::launch_attn(p, head_dim, reinterpret_cast<cudaStream_t>(stream));
-}
 
 extern "C" int kvq_fp4_prefill_attn(const void* q, const int32_t* cu_q_lens, int64_t num_q_tokens,
                                     int max_q_len, const void* k_cache, const void* v_cache,

@@ -6,7 +6,7 @@
 // 16-byte words per tensor and stores 8 bytes of codes and one of scale, the
 // read the reverse, so a row's lanes move whole contiguous runs.
 #include "kvq_fp4.cuh"
-#include "kvq_host.h"
+#include "kvq_fp4_host.h"
 
 namespace kvq {
 namespace fp4 {
@@ -253,17 +253,6 @@ __global__ void __launch_bounds__(256) read_kernel(const ReadParams p) {
   }
 }
 
-static int check_scales(const float* k_scale, int k_len, const float* v_scale, int v_len, int gran,
-                        int num_kv_heads) {
-  if (gran != KVQ_SCALE_PER_TENSOR && gran != KVQ_SCALE_PER_HEAD) return KVQ_ERR_ARG;
-  if (!k_scale || !v_scale) return KVQ_ERR_NULL;
-  const int want = gran == KVQ_SCALE_PER_HEAD ? num_kv_heads : 1;
-  if (k_len != want || v_len != want) return KVQ_ERR_SHAPE;
-  if ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & 3u)
-    return KVQ_ERR_ALIGN;
-  return KVQ_OK;
-}
-
 }  // namespace fp4
 }  // namespace kvq
 
@@ -281,16 +270,14 @@ extern "C" int kvq_fp4_write(const void* k, const void* v, int64_t token_stride,
   if (sc != KVQ_OK) return sc;
   if (!k_cache || !v_cache) return KVQ_ERR_NULL;
   if (num_tokens > 0 && (!k || !v || !slot_mapping)) return KVQ_ERR_NULL;
-  if (head_dim != 64 && head_dim != 128) return KVQ_ERR_UNSUPPORTED;
-  if (block_size != fp4::kTok) return KVQ_ERR_UNSUPPORTED;
-  if (num_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;
+  const int cc = fp4::check_caches(num_blocks, block_size, num_kv_heads, head_dim);
+  if (cc != KVQ_OK) return cc;
   if (token_stride < static_cast<int64_t>(num_kv_heads) * head_dim) return KVQ_ERR_SHAPE;
   if (token_stride % 8 != 0) return KVQ_ERR_ALIGN;
   if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
       (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
     return KVQ_ERR_ALIGN;
-  if (num_blocks > (INT64_MAX / 16) / (static_cast<int64_t>(num_kv_heads) * head_dim) ||
-      (num_tokens > 0 && token_stride > (INT64_MAX / 16) / num_tokens))
+  if (num_tokens > 0 && token_stride > (INT64_MAX / 16) / num_tokens)
     return KVQ_ERR_SHAPE;
   if (num_tokens == 0) return KVQ_OK;
   if (device_sm_count() <= 0) return KVQ_ERR_CUDA;
@@ -334,17 +321,15 @@ extern "C" int kvq_fp4_read(const void* k_cache, const void* v_cache, int64_t nu
   if (sc != KVQ_OK) return sc;
   if (!k_cache || !v_cache || !block_tables || !cu_lens) return KVQ_ERR_NULL;
   if (num_rows > 0 && (!k_out || !v_out)) return KVQ_ERR_NULL;
-  if (head_dim != 64 && head_dim != 128) return KVQ_ERR_UNSUPPORTED;
-  if (block_size != fp4::kTok) return KVQ_ERR_UNSUPPORTED;
-  if (num_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;
+  const int cc = fp4::check_caches(num_blocks, block_size, num_kv_heads, head_dim);
+  if (cc != KVQ_OK) return cc;
   if (out_stride < static_cast<int64_t>(num_kv_heads) * head_dim) return KVQ_ERR_SHAPE;
   if (out_stride % 8 != 0) return KVQ_ERR_ALIGN;
   if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out) ||
       ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(starts) |
         reinterpret_cast<uintptr_t>(cu_lens)) & 3u))
     return KVQ_ERR_ALIGN;
-  if (num_blocks > (INT64_MAX / 16) / (static_cast<int64_t>(num_kv_heads) * head_dim) ||
-      (num_rows > 0 && out_stride > (INT64_MAX / 16) / num_rows))
+  if (num_rows > 0 && out_stride > (INT64_MAX / 16) / num_rows)
     return KVQ_ERR_SHAPE;
   if (num_rows == 0) return KVQ_OK;
   if (device_sm_count() <= 0) return KVQ_ERR_CUDA;

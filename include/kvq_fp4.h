@@ -142,7 +142,7 @@ KVQ_API size_t kvq_fp4_workspace_size(int num_seqs, int num_q_heads, int num_kv_
  *                  block_size: a zero row), KVQ_DEV_WAIT_TIMEOUT
  * Statistics and sums are binary32.  The logits use q exactly (scaled by a
  * power of two, as in kvq_decode_attn); each probability reaches the product
- * with V^ as one f16, within 2^-11 of its value.
+ * with V^ as one f16, within 2^-11 of its value or 2^-32 of the row's largest.
  * Limits: num_seqs <= 4096; num_seqs * num_kv_heads <= 65536; num_seqs *
  * (max_blocks_per_seq + 16) * num_kv_heads < 2^31; num_kv_heads <= 256.
  */

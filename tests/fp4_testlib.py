@@ -100,6 +100,10 @@ def attention(q, K, V, ks, vs, table, lens, cu_q, window, sinks):
 
       2^-8 |out|                   the rounding to bf16
       2^-11 A                      one f16 per probability, A = sum p |V|
+      2^-32 B                      B = sum |V|: a weight 2^(x - m) reaches f16
+        times 2^7, where the least step is 2^-24, so it is off by at most half of
+        2^-31 when it lies below f16's normal values; m is at most the row's
+        largest logit, so the weights' sum is at least 1
       (2^-17 S + 2^-16) A          S = sum |q_i K_i| / sqrt(dh) at its largest: a
         logit's binary32 sum over at most 8 matrix steps is off by at most
         2^-18 S, and enters the numerator and the denominator; the base-2
@@ -143,7 +147,8 @@ def attention(q, K, V, ks, vs, table, lens, cu_q, window, sinks):
                 A = p @ np.abs(v)
                 r = slice(g * G, (g + 1) * G)
                 out[cu_q[b] + j, r] = o
-                tol[cu_q[b] + j, r] = 2.0 ** -8 * np.abs(o) + A * (2.0 ** -11 + 2.0 ** -17 * S[:, None] + 2.0 ** -16)
+                tol[cu_q[b] + j, r] = 2.0 ** -8 * np.abs(o) + A * (2.0 ** -11 + 2.0 ** -17 * S[:, None] + 2.0 ** -16) \
+                    + 2.0 ** -32 * np.abs(v).sum(0)
     return out, tol
 
 
