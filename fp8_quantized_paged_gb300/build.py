@@ -21,7 +21,8 @@ SOURCES = ["kvq_host.cu", "kvq_write.cu", "kvq_decode.cu", "kvq_decode_tc.cu", "
            "kvq_static.cu", "kvq_calib.cu", "kvq_prefill.cu", "kvq_decode_variant.cu",
            "kvq_fp4_write.cu", "kvq_fp4_decode.cu", "kvq_fp4_prefill.cu"]
 HEADERS = ["kvq_common.cuh", "kvq_host.h", "kvq_decode.cuh", "kvq_tc.cuh", "kvq_decode_tc.cuh",
-           "kvq_decode_blk.cuh", "kvq_prefill_tc.cuh", "kvq_fp4.cuh", "kvq_fp4_host.h", "kvq_fp4_decode.cuh"]
+           "kvq_decode_blk.cuh", "kvq_prefill_tc.cuh", "kvq_fp4.cuh", "kvq_fp4_host.h", "kvq_fp4_decode.cuh",
+           "kvq_fp4_prefill.cuh"]
 # (object, source, defines): one object per translation unit, the decode
 # variants once per (format, head size); kvq_fmt 0 = BF16, 1 = E4M3, 2 = E5M2
 UNITS = [(os.path.splitext(s)[0], s, []) for s in SOURCES if s != "kvq_decode_variant.cu"] + [

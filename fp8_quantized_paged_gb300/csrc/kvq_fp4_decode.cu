@@ -1,6 +1,7 @@
 // kvq_fp4_decode.cu -- entry point and launch of the 4-bit cache's decode.
 #include "kvq_fp4_decode.cuh"
 #include "kvq_fp4_host.h"
+#include "kvq_fp4_prefill.cuh"
 
 namespace kvq {
 namespace fp4 {
@@ -48,8 +49,9 @@ extern "C" size_t kvq_fp4_workspace_size(int num_seqs, int num_q_heads, int num_
   if (head_dim != 64 && head_dim != 128) return 0;
   if (num_sms <= 0) num_sms = device_sm_count();
   if (num_sms <= 0) return 0;
-  return fp4::dec_ws(num_seqs, num_q_heads / num_kv_heads, num_kv_heads, head_dim,
-                     fp4::kDecCtas * num_sms).total;
+  return std::max(fp4::dec_ws(num_seqs, num_q_heads / num_kv_heads, num_kv_heads, head_dim,
+                              fp4::kDecCtas * num_sms).total,
+                  fp4::pre_ws(head_dim, num_sms).total);
 }
 
 extern "C" int kvq_fp4_decode_attn(const void* q, const void* k_cache, const void* v_cache,

@@ -1,0 +1,635 @@
+// kvq_fp4_prefill.cuh -- prefill attention over the microscaled 4-bit cache on
+// the 5th-generation tensor cores (tcgen05, accumulators in tensor memory).
+//
+//   O = softmax(q K^^T / sqrt(dh)) V^,  K^ = code * block scale * sK
+//
+// One CTA per (sequence, KV head, one or two tiles of query rows, share of the
+// keys).  A row is a (query token, query head of the group) pair, a tile 128
+// of them (128 / G tokens).  The visible pages of the CTA's rows (the first
+// tokens' pages, then the window's) form a list, taken in blocks of 8 pages =
+// 128 keys:
+//   warp 12 (producer)    copies a block's 8 K pages, then its 8 V pages (one
+//     bulk copy a page: codes and scales), into a ring of 3 stages
+//   warps 8-11 (converters)  code * block scale as f16 (exact), K and V both
+//     token-major in the 128-byte-swizzled layout, two buffers each
+//   warps 13, 14 (one per tile)  one lane each issues, block by block,
+//     S = Q K^T (M 128, N 128) and, as the softmax delivers them, the two
+//     halves of O += P V (A = P from tensor memory, K 64 each)
+//   warps 0-3, 4-7 (softmax of tiles 0, 1; thread = row = TMEM lane)  64 keys
+//     at a time: S from TMEM, mask, running maximum with a lazy rescale of O,
+//     P = 2^(x - m + 7) as f16 over the S columns that it came from
+// 128 keys a block because a matrix step of M 128 takes about 76 cycles for any
+// N up to 128: with 64 the two tiles' steps alone took 1824 cycles per 64 keys.
+// S and P share columns (2 tiles x (128 S + 128 O) fill the 512), so a tile's
+// next S waits for its last P to be read; the other tile's softmax and matrix
+// steps fill that time.
+//
+// Where the tiles are fewer than the SMs, the host splits each tile's blocks
+// over several CTAs; each leaves (m, l, O) of its rows in the workspace and the
+// one that completes the tile merges them.
+//
+// Every wait is bounded; a timeout sets KVQ_DEV_WAIT_TIMEOUT, the roles stop,
+// and the CTA waits (bounded) for copies and matrix steps in flight.
+#pragma once
+
+#include "kvq_decode.cuh"
+#include "kvq_fp4.cuh"
+#include "kvq_tc.cuh"
+
+namespace kvq {
+namespace fp4 {
+
+constexpr int kRows = 128;   // query rows of a tile (MMA M)
+constexpr int kTiles = 2;    // tiles of a CTA
+constexpr int kKeys = 128;   // keys of a block
+constexpr int kBlkPages = kKeys / kTok;
+constexpr int kPreThreads = 480;
+constexpr int kConvWarp = 8, kProdWarp = 12, kMmaWarp = 13;
+constexpr uint32_t kTmemCols = 512, kTileCols = 256;  // per tile: S and P at +0, O at +128
+constexpr int kPreStages = 3, kBufs = 2;
+constexpr float kPreBias = 7.f;  // log2 of the factor that the weights carry
+
+struct PreParams {
+  const uint16_t* q;
+  const int32_t* cu_q;
+  const uint8_t* kc;
+  const uint8_t* vc;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  int max_blocks, B, Hq, Hkv, G;
+  int64_t num_blocks, total_q;
+  int window, sinks;
+  int tiles;   // tiles of the longest chunk
+  int tpc;     // tiles of a CTA
+  int groups;  // CTAs that cover the tiles
+  int ns;      // shares of the keys
+  const float* ks;
+  const float* vs;
+  int per_head;
+  float logit_scale;  // log2(e) / sqrt(dh)
+  uint32_t* ws_cnt;   // [B * Hkv * groups] arrivals (ns > 1)
+  float2* ws_ml;      // [CTA][kTiles * kRows]
+  float* ws_o;        // [CTA][kTiles * kRows][DH]
+  uint16_t* out;
+  uint32_t* status;
+};
+
+// Workspace: the arrival counters (kvq_decode_attn's table), then per CTA of a
+// call that shares out its keys (at most one per SM) the states of its rows.
+struct PreWs {
+  size_t ml, o, total;
+};
+inline PreWs pre_ws(int DH, int sms) {
+  const size_t rows = static_cast<size_t>(sms) * kTiles * kRows;
+  PreWs w;
+  w.ml = KVQ_WS_COUNTER_BYTES;
+  w.o = w.ml + round256(rows * sizeof(float2));
+  w.total = w.o + round256(rows * DH * sizeof(float));
+  return w;
+}
+
+template <int DH>
+struct PreSmem {
+  static constexpr int kStage = kBlkPages * Page<DH>::kBytes;
+  static constexpr int kTile = kKeys * DH * 2;  // K or V buffer, f16
+  static constexpr int q = 0;                   // kTiles x [128][DH] f16
+  static constexpr int k = q + kTiles * kRows * DH * 2;
+  static constexpr int v = k + kBufs * kTile;
+  static constexpr int stage = v + kBufs * kTile;
+  static constexpr int bars = stage + kPreStages * kStage;
+  static constexpr int kBars = 2 * kPreStages + 4 * kBufs + 5 * kTiles + 2;
+  static constexpr int misc = bars + kBars * 8;
+  // tmem address, abort flag, V NaN flag, merge flag, page flags [stages][8], issued [stages], masks [4]
+  static constexpr int total = misc + (4 + kPreStages * 9 + 4) * 4 + 1024;
+  static_assert(total <= 227 * 1024, "shared memory");
+};
+
+// Byte offset of f16 element (row, col) in a 128-row tile of 128-byte-swizzled
+// rows of 64 columns (wider tiles: further 64-column blocks).
+KVQ_DEVI uint32_t tile_off(int row, int col) {
+  const int blk = col >> 6, c16 = (col & 63) >> 3;
+  return static_cast<uint32_t>(blk * (128 * 128) + (row >> 3) * 1024 + (row & 7) * 128 +
+                               ((c16 ^ (row & 7)) << 4) + ((col & 7) << 1));
+}
+
+// The pages that a CTA's rows see, as a list: the first tokens' pages [0, sink),
+// then [first, last].
+struct PageList {
+  int sink, first, count;
+  KVQ_DEVI int col(int i) const { return i < sink ? i : first + i - sink; }
+};
+
+template <int DH>
+__global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_constant__ PreParams p) {
+  using SM = PreSmem<DH>;
+  using PG = Page<DH>;
+  constexpr int S = kPreStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::bars);  // [S] a stage landed
+  uint64_t* empty = full + S;            // [S] a stage converted (128 arrivals)
+  uint64_t* conv_k = empty + S;          // [kBufs] K buffer filled (128)
+  uint64_t* conv_v = conv_k + kBufs;     // [kBufs]
+  uint64_t* done_k = conv_v + kBufs;     // [kBufs] K buffer read by both tiles (a commit each)
+  uint64_t* done_v = done_k + kBufs;     // [kBufs]
+  uint64_t* sfull = done_v + kBufs;      // [kTiles] S written (commit, and the issuer's arrival)
+  uint64_t* pfull = sfull + kTiles;      // [kTiles][2] a half of P written, of S read (128)
+  uint64_t* phalf = pfull + 2 * kTiles;  // [kTiles] the first half's PV done (commit)
+  uint64_t* pdone = phalf + kTiles;      // [kTiles] a block's PVs done (commit, and the issuer's arrival)
+  uint64_t* fin = pdone + kTiles;        // every matrix step done (a commit of each issuer)
+  uint64_t* qready = fin + 1;            // both Q tiles written (256)
+  volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + SM::misc);
+  volatile uint32_t* tmem_slot = misc;
+  volatile uint32_t* abort_flag = misc + 1;
+  volatile uint32_t* vnan = misc + 2;    // a V block of the list has a NaN scale
+  volatile uint32_t* merge_s = misc + 3;
+  volatile uint32_t* pg_bad = misc + 4;  // [S][8]
+  volatile int32_t* issued = reinterpret_cast<volatile int32_t*>(misc + 4 + S * 8);  // [S] last item
+  // masked pages of block j at [j % 4]: rewritten for block j + 4, whose K waits
+  // for the QKs of block j + 2, which come after the softmax of block j + 1
+  volatile uint32_t* bmask = misc + 4 + S * 9;
+
+  // A parity wait for phase k of a barrier is sound while the barrier has
+  // completed k or k + 1 phases.  Each waiter takes its barriers' phases in
+  // order, but for phalf (waited only where O is rescaled between the halves):
+  // S of block i comes after the PVs of block i - 1, so phase i - 1 is complete,
+  // and phase i + 1 needs this softmax's own later progress.
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.z, gkv = blockIdx.y;
+  const int share = static_cast<int>(blockIdx.x) % p.ns;
+  const int group = p.groups - 1 - static_cast<int>(blockIdx.x) / p.ns;  // longest first
+  const int TQ = kRows / p.G;  // query tokens of a tile
+
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 128);
+      issued[i] = -1;
+    }
+    for (int i = 0; i < kBufs; ++i) {
+      mbar_init(&conv_k[i], 128);
+      mbar_init(&conv_v[i], 128);
+      mbar_init(&done_k[i], kTiles);
+      mbar_init(&done_v[i], kTiles);
+    }
+    for (int t = 0; t < kTiles; ++t) {
+      mbar_init(&sfull[t], 2);
+      mbar_init(&pfull[2 * t], 128);
+      mbar_init(&pfull[2 * t + 1], 128);
+      mbar_init(&phalf[t], 1);
+      mbar_init(&pdone[t], 2);
+    }
+    mbar_init(fin, kTiles);
+    mbar_init(qready, kTiles * 128);
+    *abort_flag = 0u;
+    *vnan = 0u;
+    fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_allow_next();
+
+  const int q0 = __ldg(p.cu_q + b);
+  const int n = __ldg(p.cu_q + b + 1) - q0;
+  const int j0 = group * p.tpc * TQ;  // first query token of tile 0
+  if (blockIdx.x == 0 && gkv == 0 && tid == 0 && n > p.tiles * TQ)
+    flag_status(p.status, KVQ_DEV_BAD_QLEN);
+  if (n <= 0 || j0 >= min(n, p.tiles * TQ) || q0 < 0 || static_cast<int64_t>(q0) + n > p.total_q) return;
+  const int nc = min(n, p.tiles * TQ);  // query tokens that the grid covers
+  const int j1 = min(nc, j0 + p.tpc * TQ);
+  const int L = __ldg(p.seq_lens + b);
+  if (L < n || L > p.max_blocks * kTok) {
+    if (group == 0 && share == 0 && gkv == 0 && tid == 0) flag_status(p.status, KVQ_DEV_BAD_SEQLEN);
+    if (share == 0)
+      for (int i = tid; i < (j1 - j0) * p.G * DH; i += kPreThreads) {
+        const int r = i / DH, d = i - r * DH;
+        p.out[((static_cast<int64_t>(q0) + j0 + r / p.G) * p.Hq + gkv * p.G + r % p.G) * DH + d] = 0;
+      }
+    return;
+  }
+  const int base = L - n;  // position of query token 0
+  // the list from what the first row sees to the last row's own token
+  const Visible v0 = visible(p.window, p.sinks, base + j0 + 1);
+  const PageList list = {v0.sink, v0.first, v0.sink + (base + j1 - 1) / kTok - v0.first + 1};
+  const int nall = (list.count + kBlkPages - 1) / kBlkPages;
+  // this CTA's blocks [c0, c1) and tile t's [jb, je) of them
+  const int c0 = static_cast<int>(static_cast<int64_t>(nall) * share / p.ns);
+  const int c1 = static_cast<int>(static_cast<int64_t>(nall) * (share + 1) / p.ns);
+  int jb[kTiles], je[kTiles];
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) {
+    const int a = j0 + t * TQ, e = min(nc, a + TQ);
+    if (t >= p.tpc || a >= nc) {
+      jb[t] = je[t] = c0;
+    } else {
+      const int lo = visible(p.window, p.sinks, base + a + 1).first;
+      jb[t] = max(c0, list.sink > 0 ? 0 : (lo - list.first) / kBlkPages);
+      je[t] = min(c1, (list.sink + (base + e - 1) / kTok - list.first) / kBlkPages + 1);
+      if (je[t] < jb[t]) je[t] = jb[t];
+    }
+  }
+
+  if (warp == kMmaWarp) tc::tmem_alloc(const_cast<uint32_t*>(tmem_slot), kTmemCols);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  auto fail = [&] {
+    if (!*abort_flag) {
+      *abort_flag = 1u;
+      flag_status(p.status, KVQ_DEV_WAIT_TIMEOUT);
+    }
+  };
+  auto wait_w = [&](uint64_t* bar, int phase) {  // warp-uniform
+    return __all_sync(kFull, wait_or_abort(bar, static_cast<uint32_t>(phase & 1), abort_flag));
+  };
+
+  if (warp == kProdWarp) {
+    // ------------------------------------------------------------ producer
+    // Item 2i is K of the CTA's block i, item 2i + 1 its V.  The 32 lanes look
+    // up the block ids of 4 blocks at once; lanes 0-7 copy a page each.
+    int64_t my_at = -1;  // byte offset of list page 8 (c0 + i - i % 4) + lane, -1: masked out
+    for (int it = 0; it < 2 * (c1 - c0); ++it) {
+      const int i = it >> 1, s = it % S;
+      if ((it & 7) == 0) {
+        const int lp = kBlkPages * (c0 + i) + lane;
+        my_at = -1;
+        if (lp < list.count) {
+          const int col = list.col(lp);
+          const int blk = col >= 0 && col < p.max_blocks
+                              ? __ldg(p.block_tables + static_cast<int64_t>(b) * p.max_blocks + col)
+                              : -1;
+          if (blk >= 0 && blk < p.num_blocks)
+            my_at = (static_cast<int64_t>(blk) * p.Hkv + gkv) * PG::kBytes;
+          else
+            flag_status(p.status, KVQ_DEV_BAD_BLOCK);
+        }
+      }
+      const int64_t at = __shfl_sync(kFull, my_at, 8 * (i & 3) + (lane & 7));
+      const bool ok = it < S || wait_w(&empty[s], it / S - 1);
+      if (__any_sync(kFull, !ok || *abort_flag)) {
+        if (lane == 0) fail();
+        break;
+      }
+      const uint32_t good = __ballot_sync(kFull, lane < kBlkPages && at >= 0);
+      if (lane < kBlkPages) pg_bad[s * 8 + lane] = at < 0;
+      __syncwarp();
+      if (lane == 0) {
+        issued[s] = it;
+        if (good == 0)
+          mbar_arrive(&full[s]);  // nothing to copy
+        else
+          mbar_arrive_expect_tx(&full[s], __popc(good) * PG::kBytes);
+      }
+      __syncwarp();
+      if (lane < kBlkPages && at >= 0)
+        bulk_load(smem + SM::stage + s * SM::kStage + lane * PG::kBytes, ((it & 1) ? p.vc : p.kc) + at,
+                  PG::kBytes, &full[s]);
+    }
+  } else if (warp >= kMmaWarp) {
+    // ------------------------------------------------------------ matrix steps of one tile
+    const int t = warp - kMmaWarp;
+    if (lane == 0) {
+      const uint32_t id_qk = tc::idesc_f16(kRows, kKeys), id_pv = tc::idesc_f16(kRows, DH) | (1u << 16);
+      const uint32_t tm = tmem + t * kTileCols;
+      auto wait = [&](uint64_t* bar, int phase) {
+        return wait_or_abort(bar, static_cast<uint32_t>(phase & 1), abort_flag);
+      };
+      bool ok = wait(qready, 0);
+      for (int j = c0; j < c1 && ok; ++j) {
+        const int i = j - jb[t], x = (j - c0) % kBufs, ph = (j - c0) / kBufs;
+        const bool active = j >= jb[t] && j < je[t];
+        if (!(ok = wait(&conv_k[x], ph))) break;
+        if (active) {
+          tc::tc_fence_after();
+          const uint32_t a = sbase + SM::q + t * kRows * DH * 2, bk = sbase + SM::k + x * SM::kTile;
+#pragma unroll
+          for (int k = 0; k < DH / 16; ++k) {
+            const uint32_t o = (k >> 2) * (128 * 128) + (k & 3) * 32;
+            tc::mma_f16_ss(tm, tc::sw128_desc(a + o), tc::sw128_desc(bk + o), id_qk, k > 0 ? 1u : 0u);
+          }
+          mbar_arrive(&sfull[t]);  // hands on what conv_k's arrival showed (bmask)
+          tc::mma_commit(&sfull[t]);
+        }
+        tc::mma_commit(&done_k[x]);
+        if (!(ok = wait(&conv_v[x], ph))) break;
+        for (int h = 0; h < 2 && active && ok; ++h) {
+          if (!(ok = wait(&pfull[2 * t + h], i))) break;
+          tc::tc_fence_after();
+          // V token-major: MN-major B, 64 dims a 128-byte row, 16 tokens = two 8-row groups
+          const uint32_t bv = sbase + SM::v + x * SM::kTile + h * 8192;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc::mma_f16_ts(tm + 128, tm + h * 64 + k * 8, tc::sw128_desc(bv + k * 2048, 128 * 128, 1024),
+                           id_pv, (i > 0 || h > 0 || k > 0) ? 1u : 0u);
+          if (h) mbar_arrive(&pdone[t]);  // hands on what conv_v's arrival showed (vnan)
+          tc::mma_commit(h ? &pdone[t] : &phalf[t]);
+        }
+        if (!ok) break;
+        tc::mma_commit(&done_v[x]);
+        if (active) ok = wait(&pdone[t], i);  // P read: the next S may overwrite it
+      }
+      if (!ok) fail();
+      tc::mma_commit(fin);
+      if (!mbar_wait(fin, 0u)) fail();
+    }
+  } else if (warp >= kConvWarp) {
+    // ------------------------------------------------------------ converters
+    const int ct = tid - kConvWarp * 32;  // 0 .. 127
+    for (int it = 0; it < 2 * (c1 - c0); ++it) {
+      const int i = it >> 1, s = it % S, x = i % kBufs;
+      const bool is_v = it & 1;
+      bool ok = wait_w(&full[s], it / S);
+      if (ok && i >= kBufs) ok = wait_w(is_v ? &done_v[x] : &done_k[x], i / kBufs - 1);
+      if (!ok) {
+        fail();
+        break;
+      }
+      uint32_t bm = 0;
+#pragma unroll
+      for (int e = 0; e < kBlkPages; ++e) bm |= (pg_bad[s * 8 + e] ? 1u : 0u) << e;
+      if (ct == 0 && !is_v) bmask[(c0 + i) & 3] = bm;
+      const uint32_t stg = sbase + SM::stage + s * SM::kStage;
+      const uint32_t dst = sbase + (is_v ? SM::v : SM::k) + x * SM::kTile;
+      // Block of 16 dims e of the tile: 4 of a 64-column block of row r, rows in
+      // turn, so that eight lanes' 16-byte stores (two rows, four swizzled
+      // columns each) cover all banks.
+      constexpr int kIter = kKeys * (DH / 16) / 128;
+      bool nan = false;
+#pragma unroll 4
+      for (int y = 0; y < kIter; ++y) {
+        const int e = ct + 128 * y;
+        const int c = (e & 3) + 4 * (e >> 9), r = (e >> 2) & 127;
+        const uint32_t page = stg + (r >> 4) * PG::kBytes, tr = r & 15;
+        uint32_t sb = 0;
+        uint2 w = make_uint2(0u, 0u);
+        if (!(bm >> (r >> 4) & 1u)) {
+          asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(page + tr * PG::kRow + c * 8));
+          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sb) : "r"(page + PG::kScaleOff + tr * PG::kScales + c));
+        }
+        if (is_v) {
+          // weights of 0 do not clear a NaN: tokens past the sequence count as 0,
+          // and so do NaN blocks, which the epilogue puts back where they are seen
+          if (list.col(kBlkPages * (c0 + i) + (r >> 4)) * kTok + static_cast<int>(tr) >= L) sb = 0;
+          if ((sb & 0x7Fu) == 0x7Fu) {
+            sb = 0;
+            nan = true;
+          }
+        }
+        const uint32_t f = fp8x2_to_f16x2<KVQ_FMT_E4M3>(static_cast<uint16_t>(sb * 0x101u));
+        uint32_t a[4], d[4];
+        e2m1x8_to_f16x2x4(w.x, a);
+        e2m1x8_to_f16x2x4(w.y, d);
+        tc::sts128(dst + tile_off(r, 16 * c), hmul2(a[0], f), hmul2(a[1], f), hmul2(a[2], f), hmul2(a[3], f));
+        tc::sts128(dst + tile_off(r, 16 * c + 8), hmul2(d[0], f), hmul2(d[1], f), hmul2(d[2], f), hmul2(d[3], f));
+      }
+      if (nan) *vnan = 1u;
+      fence_proxy_async_smem();  // generic writes -> the tensor core's reads
+      mbar_arrive(is_v ? &conv_v[x] : &conv_k[x]);
+      mbar_arrive(&empty[s]);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int t = warp >> 2, r = tid & 127;
+    const int jr = j0 + t * TQ + r / p.G;  // query token of this row
+    const bool live = t < p.tpc && r < TQ * p.G && jr < nc;
+    const int pos = live ? base + jr : -1;
+    const int lo = live && p.window > 0 && pos >= p.window ? pos + 1 - p.window : 0;
+    const int64_t qrow = live ? (static_cast<int64_t>(q0) + jr) * p.Hq + gkv * p.G + r % p.G : 0;
+    const uint32_t tm_s = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * kTileCols;
+    const uint32_t tm_o = tm_s + 128;
+    // the query row times a power of two 2^a, its largest value in [2^14, 2^15): f16, exact
+    // but for values 2^38 times smaller than that
+    // (kept above 0 where it would underflow, so that it times -inf stays -inf)
+    float lscale = __ldg(p.ks + (p.per_head ? gkv : 0)) * p.logit_scale;
+    {
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + qrow * DH);
+      float amax = 0.f;
+#pragma unroll
+      for (int c = 0; c < DH / 8; ++c) {
+        const uint4 w = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          amax = fmaxf(amax, fmaxf(fabsf(bf16lo_to_f32(u[e])), fabsf(bf16hi_to_f32(u[e]))));
+      }
+      int a = 0;
+      if (amax > 0.f) {
+        a = 14 - (static_cast<int>((__float_as_uint(amax) >> 23) & 0xFFu) - 127);
+        a = a > 126 ? 126 : (a < -126 ? -126 : a);
+      }
+      const float up = __int_as_float((a + 127) << 23);
+      lscale = fmaxf(lscale * __int_as_float((127 - a) << 23), 0x1p-120f);
+#pragma unroll
+      for (int c = 0; c < DH / 8; ++c) {
+        const uint4 w = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = f32x2_to_f16x2(bf16lo_to_f32(u[e]) * up, bf16hi_to_f32(u[e]) * up);
+        tc::sts128(sbase + SM::q + t * kRows * DH * 2 + tile_off(r, 8 * c), h[0], h[1], h[2], h[3]);
+      }
+    }
+    fence_proxy_async_smem();
+    mbar_arrive(qready);
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    const int nI = je[t] - jb[t];
+    for (int i = 0; i < nI && ok; ++i) {
+      const int j = jb[t] + i;
+      if (!(ok = wait_w(&sfull[t], i))) break;
+      const uint32_t bm8 = bmask[j & 3];
+      tc::tc_fence_after();
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        float x[64];
+        {
+          float a[32], d[32];
+          tc::tmem_ld32(tm_s + h * 64, a);
+          tc::tmem_ld32(tm_s + h * 64 + 32, d);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            x[e] = a[e];
+            x[32 + e] = d[e];
+          }
+        }
+        const int lp = j * kBlkPages + h * 4;  // list page of the half's first key
+        const uint32_t bm = (bm8 >> (4 * h)) & 15u;
+        const int k0 = list.col(lp) * kTok;
+        float mx8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mx8[e] = -INFINITY;
+        // the row sees all 64 keys: four consecutive pages inside its window, or of its first tokens
+        const bool whole = live && bm == 0u && k0 + 63 <= pos &&
+                           (lp >= list.sink ? k0 >= lo : lp + 3 < list.sink && k0 + 63 < p.sinks);
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e) mx8[e & 7] = fmaxf(mx8[e & 7], x[e]);
+        } else {
+#pragma unroll
+          for (int e4 = 0; e4 < 4; ++e4) {
+            const int kp0 = list.col(lp + e4) * kTok;
+            const bool page = live && !(bm >> e4 & 1u);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int kp = kp0 + e;
+              const bool seen = page && kp <= pos && (kp >= lo || kp < p.sinks);
+              x[16 * e4 + e] = seen ? x[16 * e4 + e] : -INFINITY;
+              mx8[e & 7] = fmaxf(mx8[e & 7], x[16 * e4 + e]);
+            }
+          }
+        }
+        const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                               fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))) * lscale;
+        const bool grow = mx > m + kRescaleThreshold;
+        if (__any_sync(kFull, grow)) {
+          // O's last writer: the first half's PV of this block, or (done before S came) block i - 1
+          if (h == 1 && !(ok = wait_w(&phalf[t], i))) break;
+          tc::tc_fence_after();
+          const float nm = grow ? mx : m;
+          const float a = m == -INFINITY ? 0.f : fast_exp2(m - nm);
+          if (i > 0 || h > 0) {
+#pragma unroll 1
+            for (int c = 0; c < DH; c += 16) {
+              uint32_t o[16];
+              tc::tmem_ld16(tm_o + c, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (grow ? a : 1.f));
+              tc::tmem_st16(tm_o + c, o);
+            }
+          }
+          if (grow) l *= a;
+          m = nm;
+        }
+        // while every key so far is masked m is -inf: any finite value keeps 2^-inf = 0 (and a NaN)
+        const float mb = m == -INFINITY ? 0.f : m - kPreBias;
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t ph[4];
+#pragma unroll
+          for (int e2 = 0; e2 < 4; ++e2) {
+            const int e = 8 * c + 2 * e2;
+            const float p0 = fast_exp2(fmaf(x[e], lscale, -mb));
+            const float p1 = fast_exp2(fmaf(x[e + 1], lscale, -mb));
+            l4[e2] += p0 + p1;
+            ph[e2] = f32x2_to_f16x2(p0, p1);
+          }
+          tc::tmem_st4(tm_s + h * 64 + 4 * c, ph[0], ph[1], ph[2], ph[3]);
+        }
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        mbar_arrive(&pfull[2 * t + h]);
+      }
+    }
+    if (ok && nI > 0) ok = wait_w(&pdone[t], nI - 1);
+    if (!ok) fail();
+    // ---- epilogue: the row of O, normalised, or (keys shared out) as it is
+    const float sv = __ldg(p.vs + (p.per_head ? gkv : 0));
+    const float f = p.ns > 1 ? 1.f : (l > 0.f ? sv / l : 0.f);
+    const int64_t cta = (static_cast<int64_t>(b) * p.Hkv + gkv) * gridDim.x + blockIdx.x;
+    const int64_t part = cta * (kTiles * kRows) + t * kRows + r;
+    tc::tc_fence_after();
+    if (ok) {
+      if (p.ns > 1 && live) p.ws_ml[part] = make_float2(m, l);
+#pragma unroll 1
+      for (int c = 0; c < DH; c += 32) {
+        float o[32];
+        if (nI > 0) {
+          tc::tmem_ld32(tm_o + c, o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        }
+        if (*vnan && live) {  // put back the NaN of the blocks that this row sees
+          for (int lp = c0 * kBlkPages; lp < min(list.count, c1 * kBlkPages); ++lp) {
+            const int col = list.col(lp);
+            const int blk = __ldg(p.block_tables + static_cast<int64_t>(b) * p.max_blocks + col);
+            if (blk < 0 || blk >= p.num_blocks) continue;
+            const uint8_t* sc = p.vc + (static_cast<int64_t>(blk) * p.Hkv + gkv) * PG::kBytes + PG::kScaleOff + c / 16;
+            for (int e = 0; e < kTok; ++e) {
+              const int kp = col * kTok + e;
+              if (!(kp <= pos && (kp >= lo || kp < p.sinks))) continue;
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                if ((sc[e * PG::kScales + y] & 0x7Fu) == 0x7Fu)
+#pragma unroll
+                  for (int z = 0; z < 16; ++z) o[16 * y + z] = NAN;
+            }
+          }
+        }
+        if (live && p.ns == 1) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + qrow * DH + c);
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            dst[y] = make_uint4(f32x2_to_bf16x2(o[8 * y] * f, o[8 * y + 1] * f),
+                                f32x2_to_bf16x2(o[8 * y + 2] * f, o[8 * y + 3] * f),
+                                f32x2_to_bf16x2(o[8 * y + 4] * f, o[8 * y + 5] * f),
+                                f32x2_to_bf16x2(o[8 * y + 6] * f, o[8 * y + 7] * f));
+        } else if (live) {
+          float4* dst = reinterpret_cast<float4*>(p.ws_o + part * DH + c);
+#pragma unroll
+          for (int y = 0; y < 8; ++y) dst[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+        }
+      }
+    }
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  // After an abort: wait (bounded) for the copies in flight; the issuers waited for their steps.
+  if (*abort_flag && tid == 0)
+    for (int s = 0; s < S; ++s)
+      if (issued[s] >= 0) mbar_wait(&full[s], static_cast<uint32_t>((issued[s] / S) & 1));
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+  if (p.ns == 1) return;
+
+  // ---- the CTA that completes a tile group merges its shares: the barriers above
+  // order every thread's stores before thread 0's acquire-release arrival
+  const int64_t first = (static_cast<int64_t>(b) * p.Hkv + gkv) * gridDim.x + (blockIdx.x - share);
+  uint32_t* cnt = p.ws_cnt + (static_cast<int64_t>(b) * p.Hkv + gkv) * p.groups + group;
+  if (tid == 0) *merge_s = atom_add_acq_rel_gpu(cnt, 1u) + 1 == static_cast<uint32_t>(p.ns);
+  __syncthreads();
+  if (!*merge_s) return;
+  if (tid == 0) *cnt = 0u;
+  const float sv = __ldg(p.vs + (p.per_head ? gkv : 0));
+  const int rows = kTiles * kRows;
+  for (int i = tid; i < rows * (DH / 4); i += kPreThreads) {
+    const int row = i / (DH / 4), e = i - row * (DH / 4);
+    const int t = row / kRows, r = row - t * kRows;
+    const int jr = j0 + t * TQ + r / p.G;
+    if (t >= p.tpc || r >= TQ * p.G || jr >= nc) continue;
+    float M = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int y = 0; y < p.ns; ++y) {
+      const int64_t at = (first + y) * rows + row;
+      const float2 ml = __ldcg(p.ws_ml + at);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(p.ws_o + at * DH) + e);
+      const float nm = fmaxf(M, ml.x);
+      const float a = M == -INFINITY ? 1.f : fast_exp2(M - nm), w = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - nm);
+      l = l * a + ml.y * w;
+      acc.x = acc.x * a + v.x * w;
+      acc.y = acc.y * a + v.y * w;
+      acc.z = acc.z * a + v.z * w;
+      acc.w = acc.w * a + v.w * w;
+      M = nm;
+    }
+    const float f = l > 0.f ? sv / l : 0.f;
+    uint2 o;
+    o.x = f32x2_to_bf16x2(acc.x * f, acc.y * f);
+    o.y = f32x2_to_bf16x2(acc.z * f, acc.w * f);
+    const int64_t qrow = (static_cast<int64_t>(q0) + jr) * p.Hq + gkv * p.G + r % p.G;
+    *reinterpret_cast<uint2*>(p.out + qrow * DH + 4 * e) = o;
+  }
+}
+
+}  // namespace fp4
+}  // namespace kvq

@@ -350,6 +350,18 @@ def test_prefill_bad_blocks_lengths_and_rows_behind(kvq):
     assert bool((big[out.shape[0]:] == 7).all())
 
 
+def test_prefill_nan_only_where_seen(kvq):
+    """NaN keys and values in tokens that a row does not see (later ones, ones before
+    its window, ones between the first tokens and the window) leave it alone."""
+    b = f4.Batch(18, [300, 150], 8, 2, 128)
+    b.k[200, 0, 3] = b.k[310, 1, 90] = 0x7FC0
+    b.v[250, 1, 40] = b.v[3, 0, 127] = b.v[420, 0, 0] = 0x7FC0
+    for window, sinks in ((0, 0), (40, 0), (40, 5), (40, 2)):
+        g = OnGpu(kvq, b, [140, 150])
+        g.prefill(window, sinks)
+        g.check(window, sinks, f"{window} {sinks}")
+
+
 def test_prefill_chunk_longer_than_its_bound(kvq):
     b = f4.Batch(16, [600], 4, 1, 128)
     g = OnGpu(kvq, b, [600])
