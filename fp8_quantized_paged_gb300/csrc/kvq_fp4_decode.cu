@@ -28,7 +28,7 @@ static int launch_decode(DecParams p, bool seg, int grid, cudaStream_t s) {
       }))
     return KVQ_ERR_CUDA;
   p.S = kMaxStages;
-  while (p.S > 1 && dec_smem<DH>(p.S, p.G, p.B, seg).total > kMaxSmem / kDecCtas) --p.S;
+  while (p.S > 2 && dec_smem<DH>(p.S, p.G, p.B, seg).total > kMaxSmem / kDecCtas) --p.S;
   const size_t smem = dec_smem<DH>(p.S, p.G, p.B, seg).total;
   const cudaError_t e =
       seg ? launch_pdl(decode_kernel<DH, true>, dim3(grid), dim3(kDecThreads), smem, s, p)

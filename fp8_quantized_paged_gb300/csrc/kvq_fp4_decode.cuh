@@ -14,10 +14,14 @@
 // has an SM to itself, a CTA takes one whole segment, with no plan to build
 // and nothing to merge (SEG).
 //
-// A CTA's 16 warps take its pages in turn, each on its own: a warp's lane 0
-// copies the warp's next pages (codes and scales of K, then of V: one bulk
-// copy each) into the warp's own ring of shared memory, and all of it works
-// through them, with no barrier between warps before the segment's end.
+// A CTA's run is cut once more into one contiguous run per warp, and each warp
+// goes through its own: its lanes copy the warp's next pages (codes and scales
+// of K, then of V: one bulk copy each) into the warp's own ring of shared
+// memory, and it works through them two at a time, with no barrier between
+// warps before the end.  A segment that lies whole in a warp's run is written
+// by that warp; the others' states (a warp has at most two: of the segment
+// that its run begins in and of the one that it ends in) are merged after one
+// barrier.
 // Per page, 16 tokens against the group's G <= 8 query heads:
 //   S = K^ Q^T  m16n8k16 f16 matrix steps: lane (g, t) converts the codes of
 //               token rows g and g + 8, dims t dh/4 .. (t + 1) dh/4, and
@@ -42,6 +46,9 @@ namespace fp4 {
 #endif
 #ifndef KVQ_FP4_CTAS
 #define KVQ_FP4_CTAS 1
+#endif
+#ifndef KVQ_FP4_NP
+#define KVQ_FP4_NP 2
 #endif
 #ifndef KVQ_FP4_PC
 #define KVQ_FP4_PC 16
@@ -92,17 +99,16 @@ inline DecWs dec_ws(int B, int G, int Hkv, int DH, int P) {
 
 // Dynamic shared memory (byte offsets).
 struct DecSmem {
-  int ring, bars, bad, comb, plan, total;
+  int bars, bad, ml, o, plan, total;
 };
 template <int DH>
 __host__ __device__ inline DecSmem dec_smem(int S, int G, int B, bool seg) {
   DecSmem s;
-  s.ring = 0;
-  s.bars = kDecWarps * S * 2 * Page<DH>::kBytes;
+  s.bars = kDecWarps * S * 2 * Page<DH>::kBytes;  // the rings are at 0
   s.bad = s.bars + kDecWarps * S * 8;
-  s.comb = (s.bad + kDecWarps * S * 4 + 15) & ~15;
-  // [warps][G] (m, l), [warps][G][DH] o
-  s.plan = s.comb + kDecWarps * G * (DH + 2) * 4;
+  s.ml = (s.bad + kDecWarps * S * 4 + 15) & ~15;  // [warps][2][G] (m, l) of a warp's first and last piece
+  s.o = s.ml + kDecWarps * 2 * G * 8;             // [warps][G][DH] o of the first; the last's is in the ring
+  s.plan = s.o + kDecWarps * G * DH * 4;
   s.total = s.plan + (seg ? 0 : (3 * B + 2) * 4);
   return s;
 }
@@ -152,112 +158,126 @@ KVQ_DEVI void dec_plan(const DecParams& p, int32_t* off, int32_t* len, int32_t* 
   __syncthreads();
 }
 
-KVQ_DEVI uint32_t lds32(uint32_t addr) {
-  uint32_t r;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(addr));
-  return r;
-}
-KVQ_DEVI uint32_t lds16(uint32_t addr) {
-  uint16_t r;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(addr));
-  return r;
-}
-KVQ_DEVI uint32_t lds8(uint32_t addr) {
-  uint32_t r;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr));
-  return r;
-}
-
 // Bits of a where m is set, of b elsewhere.
 KVQ_DEVI uint32_t select_bits(uint32_t a, uint32_t b, uint32_t m) { return (a & m) | (b & ~m); }
 
-// One staged page of one warp: logits, online softmax, weighted sum.
-//   kp, vp: shared addresses; tok0: first token; [lo, L) and [0, sinks) visible
-template <int DH>
-KVQ_DEVI void dec_page(uint32_t kp, uint32_t vp, int tok0, int lo, int sinks, int L, bool bad, int g,
-                       int t, const uint32_t (&qb)[DH / 16][2], float (&o)[DH / 16][4],
-                       SoftmaxState& st, float ls0, float ls1) {
+// What a warp needs to know of the piece that it works on.
+struct PieceView {
+  int lo, sinks, L;  // tokens [lo, L) and [0, sinks) are visible
+  float ls[2];       // logit scale (log2 units) of heads 2t, 2t + 1
+};
+
+// Running maximum (of the raw dot products), the exponent's offset
+// 7 - max * ls, and the lane's share of the denominator, of heads 2t, 2t + 1.
+struct Running {
+  float m[2], c[2], l[2];
+};
+
+// NP staged pages of one warp: dot products, online softmax, weighted sum.
+//   page[i]: K page, V page behind it; tok0[i]: first token; skip[i]: masked out
+template <int DH, int NP>
+KVQ_DEVI void dec_pages(const uint8_t* const (&page)[NP], const int (&tok0)[NP], const bool (&skip)[NP],
+                        const PieceView& pv, int g, int t, const uint32_t (&qb)[DH / 16][2],
+                        float (&o)[DH / 16][4], Running& st) {
   using P = Page<DH>;
   constexpr int KW = DH / 32;  // code words of a K row that a lane converts
   constexpr int VW = DH / 64;  // of a V row
-  // ---- S = K^ Q^T
-  uint32_t k0[KW], k1[KW];
-  uint32_t sc0[2], sc1[2];  // block scales of rows g, g + 8, in both halves
-  if (DH == 128) {
-    const uint4 a = lds128(kp + g * P::kRow + t * 16), b = lds128(kp + (g + 8) * P::kRow + t * 16);
-    k0[0] = a.x; k0[1] = a.y; k0[KW - 2] = a.z; k0[KW - 1] = a.w;
-    k1[0] = b.x; k1[1] = b.y; k1[KW - 2] = b.z; k1[KW - 1] = b.w;
-    const uint32_t s0 = fp8x2_to_f16x2<KVQ_FMT_E4M3>(lds16(kp + P::kScaleOff + g * 8 + 2 * t));
-    const uint32_t s1 = fp8x2_to_f16x2<KVQ_FMT_E4M3>(lds16(kp + P::kScaleOff + (g + 8) * 8 + 2 * t));
-    sc0[0] = prmt(s0, s0, 0x1010u);
-    sc0[1] = prmt(s0, s0, 0x3232u);
-    sc1[0] = prmt(s1, s1, 0x1010u);
-    sc1[1] = prmt(s1, s1, 0x3232u);
-  } else {
-    const uint2 a = lds64(kp + g * P::kRow + t * 8), b = lds64(kp + (g + 8) * P::kRow + t * 8);
-    k0[0] = a.x; k0[1] = a.y;
-    k1[0] = b.x; k1[1] = b.y;
-    const uint32_t r0 = lds8(kp + P::kScaleOff + g * 4 + t), r1 = lds8(kp + P::kScaleOff + (g + 8) * 4 + t);
-    const uint32_t s0 = fp8x2_to_f16x2<KVQ_FMT_E4M3>(static_cast<uint16_t>(r0 | (r1 << 8)));
-    sc0[0] = sc0[1] = prmt(s0, s0, 0x1010u);
-    sc1[0] = sc1[1] = prmt(s0, s0, 0x3232u);
-  }
-  float s[2][4];
+  // ---- S = K^ Q^T: x of (token g, head 2t), (g, 2t + 1), (g + 8, 2t), (g + 8, 2t + 1)
+  float x[NP][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) s[0][i] = s[1][i] = 0.f;
-#pragma unroll
-  for (int w = 0; w < KW; ++w) {
-    uint32_t a[4], b[4];
-    e2m1x8_to_f16x2x4(k0[w], a);
-    e2m1x8_to_f16x2x4(k1[w], b);
-    const uint32_t f0 = sc0[w * 2 / KW], f1 = sc1[w * 2 / KW];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint32_t f[4] = {hmul2(a[2 * e], f0), hmul2(b[2 * e], f1), hmul2(a[2 * e + 1], f0),
-                             hmul2(b[2 * e + 1], f1)};
-      mma_f16(s[e], f, qb[2 * w + e][0], qb[2 * w + e][1]);
-    }
-  }
-  // ---- V's codes and scales, in flight while the softmax runs
-  const int row[4] = {t, t + 8, t + 4, t + 12};
-  uint32_t v[4][VW], vs[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < NP; ++i) {
+    const uint8_t* kp = page[i];
+    uint32_t k0[KW], k1[KW], sc0[2], sc1[2];  // codes, block scales (in both halves) of rows g, g + 8
     if (DH == 128) {
-      const uint2 w = lds64(vp + row[i] * P::kRow + g * 8);
-      v[i][0] = w.x;
-      v[i][VW - 1] = w.y;
-      vs[i] = lds8(vp + P::kScaleOff + row[i] * 8 + g);
+      const uint4 a = *reinterpret_cast<const uint4*>(kp + g * P::kRow + t * 16);
+      const uint4 b = *reinterpret_cast<const uint4*>(kp + (g + 8) * P::kRow + t * 16);
+      k0[0] = a.x; k0[1] = a.y; k0[KW - 2] = a.z; k0[KW - 1] = a.w;
+      k1[0] = b.x; k1[1] = b.y; k1[KW - 2] = b.z; k1[KW - 1] = b.w;
+      const uint32_t s0 = fp8x2_to_f16x2<KVQ_FMT_E4M3>(
+          *reinterpret_cast<const uint16_t*>(kp + P::kScaleOff + g * 8 + 2 * t));
+      const uint32_t s1 = fp8x2_to_f16x2<KVQ_FMT_E4M3>(
+          *reinterpret_cast<const uint16_t*>(kp + P::kScaleOff + (g + 8) * 8 + 2 * t));
+      sc0[0] = prmt(s0, s0, 0x1010u);
+      sc0[1] = prmt(s0, s0, 0x3232u);
+      sc1[0] = prmt(s1, s1, 0x1010u);
+      sc1[1] = prmt(s1, s1, 0x3232u);
     } else {
-      v[i][0] = lds32(vp + row[i] * P::kRow + g * 4);
-      vs[i] = lds8(vp + P::kScaleOff + row[i] * 4 + (g >> 1));
+      const uint2 a = *reinterpret_cast<const uint2*>(kp + g * P::kRow + t * 8);
+      const uint2 b = *reinterpret_cast<const uint2*>(kp + (g + 8) * P::kRow + t * 8);
+      k0[0] = a.x; k0[1] = a.y;
+      k1[0] = b.x; k1[1] = b.y;
+      const uint32_t r0 = kp[P::kScaleOff + g * 4 + t], r1 = kp[P::kScaleOff + (g + 8) * 4 + t];
+      const uint32_t s0 = fp8x2_to_f16x2<KVQ_FMT_E4M3>(static_cast<uint16_t>(r0 | (r1 << 8)));
+      sc0[0] = sc0[1] = prmt(s0, s0, 0x1010u);
+      sc1[0] = sc1[1] = prmt(s0, s0, 0x3232u);
+    }
+    x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {
+      uint32_t a[4], b[4];
+      e2m1x8_to_f16x2x4(k0[w], a);
+      e2m1x8_to_f16x2x4(k1[w], b);
+      const uint32_t f0 = sc0[w * 2 / KW], f1 = sc1[w * 2 / KW];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t f[4] = {hmul2(a[2 * e], f0), hmul2(b[2 * e], f1), hmul2(a[2 * e + 1], f0),
+                               hmul2(b[2 * e + 1], f1)};
+        mma_f16(x[i], f, qb[2 * w + e][0], qb[2 * w + e][1]);
+      }
     }
   }
-  // ---- softmax: x of (token g, head 2t), (g, 2t + 1), (g + 8, 2t), (g + 8, 2t + 1)
-  float x[4], pr[4];
+  // ---- V's codes and scales of tokens t, t + 8, t + 4, t + 12
+  uint32_t v[NP][4][VW], vs[NP][2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = (s[0][i] + s[1][i]) * ((i & 1) ? ls1 : ls0);
-  const bool edge = bad || tok0 + kTok > L || (tok0 < lo && tok0 + kTok > sinks);
-  auto seen = [&](int r) { return !bad && tok0 + r < L && (tok0 + r >= lo || tok0 + r < sinks); };
-  if (edge) {
-    if (!seen(g)) x[0] = x[1] = -INFINITY;
-    if (!seen(g + 8)) x[2] = x[3] = -INFINITY;
-    // a masked token may hold anything; its weight is 0, so its scale has to be finite
+  for (int i = 0; i < NP; ++i) {
+    const uint8_t* vp = page[i] + P::kBytes;
+    uint32_t s4[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) vs[i] = seen(row[i]) ? vs[i] : 0u;
+    for (int y = 0; y < 4; ++y) {
+      const int row = t + 8 * (y & 1) + 4 * (y >> 1);
+      if (DH == 128) {
+        const uint2 w = *reinterpret_cast<const uint2*>(vp + row * P::kRow + g * 8);
+        v[i][y][0] = w.x;
+        v[i][y][VW - 1] = w.y;
+        s4[y] = vp[P::kScaleOff + row * 8 + g];
+      } else {
+        v[i][y][0] = *reinterpret_cast<const uint32_t*>(vp + row * P::kRow + g * 4);
+        s4[y] = vp[P::kScaleOff + row * 4 + (g >> 1)];
+      }
+    }
+    vs[i][0] = s4[0] | (s4[1] << 8);
+    vs[i][1] = s4[2] | (s4[3] << 8);
+    // the edges of what is visible: masked keys get -inf, and masked values, which may hold
+    // anything, a scale of 0 (their weight of 0 would not clear a NaN)
+    if (skip[i] || tok0[i] + kTok > pv.L || (tok0[i] < pv.lo && tok0[i] + kTok > pv.sinks)) {
+      auto seen = [&](int r) {
+        const int tok = tok0[i] + r;
+        return !skip[i] && tok < pv.L && (tok >= pv.lo || tok < pv.sinks);
+      };
+      if (!seen(g)) x[i][0] = x[i][1] = -INFINITY;
+      if (!seen(g + 8)) x[i][2] = x[i][3] = -INFINITY;
+      vs[i][0] &= (seen(t) ? 0xFFu : 0u) | (seen(t + 8) ? 0xFF00u : 0u);
+      vs[i][1] &= (seen(t + 4) ? 0xFFu : 0u) | (seen(t + 12) ? 0xFF00u : 0u);
+    }
   }
-  const float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
-  if (__any_sync(kFull, mx0 > st.m[0] + kRescaleThreshold || mx1 > st.m[1] + kRescaleThreshold)) {
-    float n0 = mx0, n1 = mx1;
+  // ---- online softmax; the maximum is raised only when it grows by over 8 (in log2 units)
+  float mx0 = fmaxf(x[0][0], x[0][2]), mx1 = fmaxf(x[0][1], x[0][3]);
+#pragma unroll
+  for (int i = 1; i < NP; ++i) {
+    mx0 = fmaxf(mx0, fmaxf(x[i][0], x[i][2]));
+    mx1 = fmaxf(mx1, fmaxf(x[i][1], x[i][3]));
+  }
+  if (__any_sync(kFull, (mx0 - st.m[0]) * pv.ls[0] > kRescaleThreshold ||
+                            (mx1 - st.m[1]) * pv.ls[1] > kRescaleThreshold)) {
 #pragma unroll
     for (int d = 4; d < 32; d <<= 1) {
-      n0 = fmaxf(n0, __shfl_xor_sync(kFull, n0, d));
-      n1 = fmaxf(n1, __shfl_xor_sync(kFull, n1, d));
+      mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, d));
+      mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, d));
     }
-    n0 = fmaxf(st.m[0], n0);
-    n1 = fmaxf(st.m[1], n1);
-    const float a0 = n0 == -INFINITY ? 1.f : fast_exp2(st.m[0] - n0);
-    const float a1 = n1 == -INFINITY ? 1.f : fast_exp2(st.m[1] - n1);
+    const float n0 = fmaxf(st.m[0], mx0), n1 = fmaxf(st.m[1], mx1);
+    // (-inf to -inf: nothing seen yet, nothing to scale)
+    const float a0 = n0 == -INFINITY ? 1.f : fast_exp2((st.m[0] - n0) * pv.ls[0]);
+    const float a1 = n1 == -INFINITY ? 1.f : fast_exp2((st.m[1] - n1) * pv.ls[1]);
     st.l[0] *= a0;
     st.l[1] *= a1;
 #pragma unroll
@@ -269,60 +289,82 @@ KVQ_DEVI void dec_page(uint32_t kp, uint32_t vp, int tok0, int lo, int sinks, in
     }
     st.m[0] = n0;
     st.m[1] = n1;
+    // with nothing seen any finite offset keeps 2^-inf = 0 (and a NaN a NaN)
+    st.c[0] = n0 == -INFINITY ? 0.f : fmaf(-n0, pv.ls[0], kPBias);
+    st.c[1] = n1 == -INFINITY ? 0.f : fmaf(-n1, pv.ls[1], kPBias);
   }
-  const float c0 = st.m[0] - kPBias, c1 = st.m[1] - kPBias;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) pr[i] = x[i] == -INFINITY ? 0.f : fast_exp2(x[i] - ((i & 1) ? c1 : c0));
-  st.l[0] += pr[0] + pr[2];
-  st.l[1] += pr[1] + pr[3];
   // ---- P^T as the B operand: head g of tokens (t, t + 8) and (t + 4, t + 12)
-  const uint32_t h0 = f32x2_to_f16x2(pr[0], pr[2]), h1 = f32x2_to_f16x2(pr[1], pr[3]);
-  const int src = 4 * t + (g >> 1);
-  const uint32_t pa0 = __shfl_sync(kFull, h0, src), pa1 = __shfl_sync(kFull, h1, src);
-  const uint32_t pb0 = __shfl_sync(kFull, h0, src + 16), pb1 = __shfl_sync(kFull, h1, src + 16);
-  const uint32_t b0 = (g & 1) ? pa1 : pa0, b1 = (g & 1) ? pb1 : pb0;
+  uint32_t pb[NP][2];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const float p0 = fast_exp2(fmaf(x[i][0], pv.ls[0], st.c[0])), p1 = fast_exp2(fmaf(x[i][1], pv.ls[1], st.c[1]));
+    const float p2 = fast_exp2(fmaf(x[i][2], pv.ls[0], st.c[0])), p3 = fast_exp2(fmaf(x[i][3], pv.ls[1], st.c[1]));
+    st.l[0] += p0 + p2;
+    st.l[1] += p1 + p3;
+    const uint32_t h0 = f32x2_to_f16x2(p0, p2), h1 = f32x2_to_f16x2(p1, p3);
+    const int src = 4 * t + (g >> 1);
+    const uint32_t pa0 = __shfl_sync(kFull, h0, src), pa1 = __shfl_sync(kFull, h1, src);
+    const uint32_t pc0 = __shfl_sync(kFull, h0, src + 16), pc1 = __shfl_sync(kFull, h1, src + 16);
+    pb[i][0] = (g & 1) ? pa1 : pa0;
+    pb[i][1] = (g & 1) ? pc1 : pc0;
+  }
   // ---- O^T += V^T P^T
-  const uint32_t sp0 = fp8x2_to_f16x2<KVQ_FMT_E4M3>(static_cast<uint16_t>(vs[0] | (vs[1] << 8)));
-  const uint32_t sp1 = fp8x2_to_f16x2<KVQ_FMT_E4M3>(static_cast<uint16_t>(vs[2] | (vs[3] << 8)));
   constexpr uint32_t kLow = 0x0F0F0F0Fu;
 #pragma unroll
-  for (int w = 0; w < VW; ++w) {
-    // even dims and odd dims of the eight, the two tokens side by side
-    uint32_t e0[4], d0[4], e1[4], d1[4];
-    e2m1x8_to_f16x2x4(select_bits(v[0][w], v[1][w] << 4, kLow), e0);
-    e2m1x8_to_f16x2x4(select_bits(v[0][w] >> 4, v[1][w], kLow), d0);
-    e2m1x8_to_f16x2x4(select_bits(v[2][w], v[3][w] << 4, kLow), e1);
-    e2m1x8_to_f16x2x4(select_bits(v[2][w] >> 4, v[3][w], kLow), d1);
+  for (int i = 0; i < NP; ++i) {
+    const uint32_t sp0 = fp8x2_to_f16x2<KVQ_FMT_E4M3>(static_cast<uint16_t>(vs[i][0]));
+    const uint32_t sp1 = fp8x2_to_f16x2<KVQ_FMT_E4M3>(static_cast<uint16_t>(vs[i][1]));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t f[4] = {hmul2(e0[i], sp0), hmul2(d0[i], sp0), hmul2(e1[i], sp1), hmul2(d1[i], sp1)};
-      mma_f16(o[4 * w + i], f, b0, b1);
+    for (int w = 0; w < VW; ++w) {
+      // even dims and odd dims of the eight, the two tokens side by side
+      uint32_t e0[4], d0[4], e1[4], d1[4];
+      e2m1x8_to_f16x2x4(select_bits(v[i][0][w], v[i][1][w] << 4, kLow), e0);
+      e2m1x8_to_f16x2x4(select_bits(v[i][0][w] >> 4, v[i][1][w], kLow), d0);
+      e2m1x8_to_f16x2x4(select_bits(v[i][2][w], v[i][3][w] << 4, kLow), e1);
+      e2m1x8_to_f16x2x4(select_bits(v[i][2][w] >> 4, v[i][3][w], kLow), d1);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const uint32_t f[4] = {hmul2(e0[y], sp0), hmul2(d0[y], sp0), hmul2(e1[y], sp1), hmul2(d1[y], sp1)};
+        mma_f16(o[4 * w + y], f, pb[i][0], pb[i][1]);
+      }
     }
   }
 }
+
+// A segment that warps share, or CTAs: units [a, z) of it in this CTA.
+struct Shared {
+  int b, gkv, first, pages;  // first unit of the whole segment, its pages
+  int wa, wz;                // first and last warp that hold some of it
+  int np, c_lo;              // pieces over CTAs (1: all of it is here), the first one's CTA
+};
 
 template <int DH, bool SEG>
 __global__ void __launch_bounds__(kDecThreads, kDecCtas) decode_kernel(const __grid_constant__ DecParams p) {
   using PG = Page<DH>;
   constexpr int MT = DH / 16;
   constexpr int kSlot = 2 * PG::kBytes;
+  constexpr int kNP = KVQ_FP4_NP;  // pages of a step
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t warp_tot[kDecWarps];
   __shared__ int32_t bounds[2];
-  __shared__ uint32_t merge_s;
+  __shared__ Shared list[kDecWarps + 1];
+  __shared__ int list_n;
+  __shared__ int32_t wstart[kDecWarps + 1];  // first unit of each warp's run
+  __shared__ uint32_t merge_s[kDecWarps + 1];
   const DecSmem sm = dec_smem<DH>(p.S, p.G, p.B, SEG);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
-  uint8_t* ring = smem + sm.ring + warp * p.S * kSlot;
+  uint8_t* ring = smem + warp * p.S * kSlot;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + sm.bars) + warp * p.S;
   uint32_t* bad_s = reinterpret_cast<uint32_t*>(smem + sm.bad) + warp * p.S;
-  float2* cml = reinterpret_cast<float2*>(smem + sm.comb);        // [warps][G]
-  float* co = reinterpret_cast<float*>(cml + kDecWarps * p.G);    // [warps][G][DH]
-  int32_t* off = reinterpret_cast<int32_t*>(smem + sm.plan);      // [B + 1]
-  int32_t* len = off + p.B + 1;                                   // [B]
-  int32_t* voff = len + p.B;                                      // [B + 1]
+  float2* cml = reinterpret_cast<float2*>(smem + sm.ml);
+  float* co = reinterpret_cast<float*>(smem + sm.o);
+  int32_t* off = reinterpret_cast<int32_t*>(smem + sm.plan);  // [B + 1]
+  int32_t* len = off + p.B + 1;                               // [B]
+  int32_t* voff = len + p.B;                                  // [B + 1]
 
   if (lane < p.S) mbar_init(&full[lane], 1);
+  if (tid == 0) list_n = 0;
   fence_mbar_init();
   __syncwarp();
   pdl_wait();
@@ -330,7 +372,6 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) decode_kernel(const __g
 
   const int c = blockIdx.x;
   int u0 = 0, u1 = 0, seg_b = 0, seg_g = 0, seg_len = 0;
-  Visible seg_vis = {};
   int V = 0, Pe = 1;
   if (SEG) {
     seg_b = c / p.Hkv;
@@ -340,8 +381,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) decode_kernel(const __g
       if (seg_g == 0 && tid == 0) flag_status(p.status, KVQ_DEV_BAD_SEQLEN);
       seg_len = 0;
     }
-    seg_vis = visible(p.window, p.sinks, seg_len);
-    u1 = seg_vis.count;
+    u1 = visible(p.window, p.sinks, seg_len).count;
     if (u1 == 0) {  // nothing to attend to
       uint16_t* o = p.out + (static_cast<int64_t>(seg_b) * p.Hq + seg_g * p.G) * DH;
       for (int i = tid; i < p.G * DH; i += kDecThreads) o[i] = 0;
@@ -356,7 +396,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) decode_kernel(const __g
     }
     const int W = off[p.B];
     V = voff[p.B];
-    // a CTA has a page for every warp at least
+    // a CTA has a step for every warp at least
     Pe = min(p.P, (W + kDecWarps - 1) / kDecWarps);
     const CostSplit split(V, Pe);
     if ((tid == 0 || tid == 32) && c < Pe)
@@ -367,75 +407,23 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) decode_kernel(const __g
       u1 = bounds[1];
     }
   }
-  const CostSplit split(V, Pe);
 
-  // ---- this warp's pages: units u0 + warp, u0 + warp + 16, ...
+  // ---- this warp's run of pages [w0, w1)
   const int total = u1 - u0;
-  const int mine = total > warp ? (total - warp + kDecWarps - 1) / kDecWarps : 0;
-  // lane j holds the block id (and KV head) of the warp's page 32 i + j, fetched 32 pages ahead
-  int blk_now = -1, head_now = 0, blk_next = -1, head_next = 0;
-  auto fetch = [&](int k, int& blk, int& head) {
-    blk = -1;
-    head = 0;
-    if (k >= mine) return;
-    const int u = u0 + warp + k * kDecWarps;
-    int b, pg;
-    Visible vis;
-    if (SEG) {
-      b = seg_b;
-      head = seg_g;
-      pg = u;
-      vis = seg_vis;
-    } else {
-      b = find_seq(off, p.B, u);
-      const int pages = (off[b + 1] - off[b]) / p.Hkv;
-      head = (u - off[b]) / pages;
-      pg = u - off[b] - head * pages;
-      vis = visible(p.window, p.sinks, len[b]);
-    }
-    const int col = pg < vis.sink ? pg : vis.first + pg - vis.sink;
-    if (col >= 0 && col < p.max_blocks) blk = __ldg(p.block_tables + static_cast<int64_t>(b) * p.max_blocks + col);
+  auto run_start = [&](int w) { return u0 + static_cast<int>(static_cast<int64_t>(total) * w / kDecWarps); };
+  auto warp_of = [&](int u) {  // the warp whose run holds unit u
+    return static_cast<int>((static_cast<int64_t>(u - u0 + 1) * kDecWarps - 1) / total);
   };
-  int issued = 0;
-  auto issue = [&](int s) {  // the warp's next page into stage s = issued % S (all lanes)
-    if ((issued & 31) == 0) {
-      if (issued == 0) fetch(lane, blk_now, head_now);
-      else {
-        blk_now = blk_next;
-        head_now = head_next;
-      }
-      fetch(issued + 32 + lane, blk_next, head_next);
-    }
-    const int blk = __shfl_sync(kFull, blk_now, issued & 31), head = __shfl_sync(kFull, head_now, issued & 31);
-    if (lane == 0) {
-      const bool bad = blk < 0 || blk >= p.num_blocks;
-      bad_s[s] = bad;
-      if (bad) {
-        flag_status(p.status, KVQ_DEV_BAD_BLOCK);
-        mbar_arrive(&full[s]);
-      } else {
-        const int64_t at = (static_cast<int64_t>(blk) * p.Hkv + head) * PG::kBytes;
-        mbar_arrive_expect_tx(&full[s], kSlot);
-        bulk_load(ring + s * kSlot, p.kc + at, PG::kBytes, &full[s]);
-        bulk_load(ring + s * kSlot + PG::kBytes, p.vc + at, PG::kBytes, &full[s]);
-      }
-    }
-    ++issued;
-  };
-  while (issued < p.S && issued < mine) issue(issued);
-
-  int done = 0, stage = 0;
-  uint32_t parity = 0;
-  bool dead = false;
-  int pos = 0;  // units of the CTA's earlier pieces
-  for (int u = u0; u < u1;) {
-    // ---- a piece: the part of one (sequence, KV head) segment inside [u0, u1)
-    int b, gkv, pages, p0, L;
+  const int w0 = run_start(warp), w1 = run_start(warp + 1);
+  const int mine = w1 - w0;
+  if (lane < 2) wstart[warp + lane] = lane ? w1 : w0;  // (neighbours write the same)
+  // the (sequence, KV head) segment of unit u
+  auto segment = [&](int u, int& b, int& gkv, int& pages, int& p0, int& L) {
     if (SEG) {
       b = seg_b;
       gkv = seg_g;
       pages = total;
-      p0 = 0;
+      p0 = u;
       L = seg_len;
     } else {
       b = find_seq(off, p.B, u);
@@ -444,14 +432,84 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) decode_kernel(const __g
       p0 = u - off[b] - gkv * pages;
       L = len[b];
     }
+  };
+  // lane j holds the block id (and KV head) of the warp's page 32 i + j, fetched 32 pages ahead
+  int blk_now = -1, head_now = 0, blk_next = -1, head_next = 0;
+  auto fetch = [&](int k, int& blk, int& head) {
+    blk = -1;
+    head = 0;
+    if (k >= mine) return;
+    int b, pages, p0, L;
+    segment(w0 + k, b, head, pages, p0, L);
     const Visible vis = visible(p.window, p.sinks, L);
-    const int n = min(u1 - u, pages - p0);
-    const bool single = SEG || n == pages;
-    const float ls = __ldg(p.ks + (p.per_head ? gkv : 0)) * p.logit_scale;
-    const float sv = __ldg(p.vs + (p.per_head ? gkv : 0));
+    const int col = p0 < vis.sink ? p0 : vis.first + p0 - vis.sink;
+    if (col >= 0 && col < p.max_blocks)
+      blk = __ldg(p.block_tables + static_cast<int64_t>(b) * p.max_blocks + col);
+  };
+  // The warp's next `n` <= 2 pages into stages s and the one after: lanes 0 and
+  // 1 copy K and V of the first, lanes 2 and 3 of the second.
+  int issued = 0;
+  auto issue = [&](int s, int n) {
+    const int k = issued + ((lane >> 1) & 1);
+    if ((issued & 31) == 0) {
+      if (issued == 0) {
+        fetch(lane, blk_now, head_now);
+      } else {
+        blk_now = blk_next;
+        head_now = head_next;
+      }
+      fetch(issued + 32 + lane, blk_next, head_next);
+    }
+    int blk = __shfl_sync(kFull, blk_now, k & 31), head = __shfl_sync(kFull, head_now, k & 31);
+    if (n == 2 && (issued & 31) == 31) {  // the second page begins the next 32
+      const int b2 = __shfl_sync(kFull, blk_next, 0), h2 = __shfl_sync(kFull, head_next, 0);
+      if (lane & 2) {
+        blk = b2;
+        head = h2;
+      }
+      blk_now = blk_next;
+      head_now = head_next;
+      fetch(issued + 33 + lane, blk_next, head_next);
+    }
+    if (lane < 2 * n) {
+      int st = s + (lane >> 1);
+      if (st >= p.S) st -= p.S;
+      const bool bad = blk < 0 || blk >= p.num_blocks;
+      if (!(lane & 1)) {
+        bad_s[st] = bad;
+        if (bad) {
+          flag_status(p.status, KVQ_DEV_BAD_BLOCK);
+          mbar_arrive(&full[st]);
+        } else {
+          mbar_arrive_expect_tx(&full[st], kSlot);
+        }
+      }
+      __syncwarp((1u << (2 * n)) - 1u);
+      if (!bad)
+        bulk_load(ring + st * kSlot + (lane & 1) * PG::kBytes,
+                  ((lane & 1) ? p.vc : p.kc) + (static_cast<int64_t>(blk) * p.Hkv + head) * PG::kBytes,
+                  PG::kBytes, &full[st]);
+    }
+    issued += n;
+  };
+  for (int s = 0; s < p.S && issued < mine; s += 2) issue(s, min(2, min(p.S - s, mine - issued)));
+
+  int done = 0, stage = 0;
+  uint32_t parity = 0;
+  bool dead = false;
+  for (int u = w0; u < w1;) {
+    // ---- a piece: the part of one segment inside the warp's run
+    int b, gkv, pages, p0;
+    PieceView pv;
+    segment(u, b, gkv, pages, p0, pv.L);
+    const Visible vis = visible(p.window, p.sinks, pv.L);
+    pv.lo = vis.lo;
+    pv.sinks = p.sinks;
+    const int n = min(w1 - u, pages - p0);
     // the group's queries: head g, dims t dh/4 .. (t + 1) dh/4, scaled by a power of two to f16
-    uint32_t raw[DH / 8], qb[MT][2];
+    uint32_t qb[MT][2];
     {
+      uint32_t raw[DH / 8];
       const uint4* src = reinterpret_cast<const uint4*>(
           p.q + (static_cast<int64_t>(b) * p.Hq + gkv * p.G + (g < p.G ? g : 0)) * DH + t * (DH / 4));
 #pragma unroll
@@ -459,120 +517,203 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) decode_kernel(const __g
         const uint4 w = g < p.G ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
         raw[4 * i] = w.x; raw[4 * i + 1] = w.y; raw[4 * i + 2] = w.z; raw[4 * i + 3] = w.w;
       }
+      const float ls = __ldg(p.ks + (p.per_head ? gkv : 0)) * p.logit_scale;
+      const int qa = q_fragments<KVQ_FMT_E4M3, DH>(raw, qb);
+      // (kept above 0 where it would underflow, so that it times -inf stays -inf)
+      pv.ls[0] = fmaxf(ls * __int_as_float((127 - __shfl_sync(kFull, qa, 8 * t)) << 23), 0x1p-120f);
+      pv.ls[1] = fmaxf(ls * __int_as_float((127 - __shfl_sync(kFull, qa, 8 * t + 4)) << 23), 0x1p-120f);
     }
-    const int qa = q_fragments<KVQ_FMT_E4M3, DH>(raw, qb);
-    const float ls0 = ls * __int_as_float((127 - __shfl_sync(kFull, qa, 8 * t)) << 23);
-    const float ls1 = ls * __int_as_float((127 - __shfl_sync(kFull, qa, 8 * t + 4)) << 23);
-    SoftmaxState st;
+    Running st;
     st.m[0] = st.m[1] = -INFINITY;
-    st.l[0] = st.l[1] = 0.f;
+    st.l[0] = st.l[1] = st.c[0] = st.c[1] = 0.f;
     float o[MT][4];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
 
-    // this warp's next page is unit warp + 16 done of the CTA's run
-    while (warp + kDecWarps * done < pos + n) {
-      if (!dead && !__all_sync(kFull, mbar_wait(&full[stage], parity))) {
-        dead = true;  // the wait ran out: no more copies, the rest is skipped
-        if (lane == 0) flag_status(p.status, KVQ_DEV_WAIT_TIMEOUT);
+    for (int j = 0; j < n; j += kNP) {
+      const uint8_t* page[kNP];
+      int tok0[kNP];
+      bool skip[kNP];
+      const int first = stage, have = min(kNP, n - j);
+#pragma unroll
+      for (int i = 0; i < kNP; ++i) {
+        const int pg = p0 + j + i;
+        tok0[i] = (pg < vis.sink ? pg : vis.first + pg - vis.sink) * kTok;
+        page[i] = ring + stage * kSlot;
+        skip[i] = true;
+        if (i < have) {
+          if (!dead && !__all_sync(kFull, mbar_wait(&full[stage], parity))) {
+            dead = true;  // the wait ran out: no more copies, the rest is skipped
+            if (lane == 0) flag_status(p.status, KVQ_DEV_WAIT_TIMEOUT);
+          }
+          skip[i] = bad_s[stage] != 0;
+          if (++stage == p.S) {
+            stage = 0;
+            parity ^= 1u;
+          }
+        }
       }
       if (!dead) {
-        const int pg = p0 + warp + kDecWarps * done - pos;
-        const int tok0 = (pg < vis.sink ? pg : vis.first + pg - vis.sink) * kTok;
-        const uint32_t kp = smem_u32(ring + stage * kSlot);
-        dec_page<DH>(kp, kp + PG::kBytes, tok0, vis.lo, p.sinks, L, bad_s[stage] != 0, g, t, qb, o, st, ls0, ls1);
+        dec_pages<DH, kNP>(page, tok0, skip, pv, g, t, qb, o, st);
         __syncwarp();
-        if (issued < mine) issue(stage);
+        const int more = min(have, mine - issued);
+        if (more > 0) issue(first, more);
       }
-      ++done;
-      if (++stage == p.S) {
-        stage = 0;
-        parity ^= 1u;
-      }
+      if (!dead) done += have;
     }
-    pos += n;
 
-    // ---- merge the warps' states of the piece
 #pragma unroll
     for (int d = 4; d < 32; d <<= 1) {
       st.l[0] += __shfl_xor_sync(kFull, st.l[0], d);
       st.l[1] += __shfl_xor_sync(kFull, st.l[1], d);
     }
+    if (n == pages) {  // the whole segment: its output
+      const float sv = __ldg(p.vs + (p.per_head ? gkv : 0));
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int h = 2 * t + e;
-      if (h < p.G) {
-        if (g == 0) cml[warp * p.G + h] = make_float2(st.m[e], st.l[e]);
-        if (st.m[e] != -INFINITY || st.l[e] != 0.f) {
-          float* dst = co + (warp * p.G + h) * DH + g * (DH / 8);
+      for (int e = 0; e < 2; ++e) {
+        const int h = 2 * t + e;
+        if (h >= p.G) continue;
+        const float f = st.l[e] > 0.f ? sv / st.l[e] : 0.f;
+        uint4* dst = reinterpret_cast<uint4*>(
+            p.out + (static_cast<int64_t>(b) * p.Hq + gkv * p.G + h) * DH + g * (DH / 8));
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-            *reinterpret_cast<float2*>(dst + 2 * mt) = make_float2(o[mt][e], o[mt][2 + e]);
+        for (int mt = 0; mt < MT; mt += 4)
+          dst[mt / 4] = make_uint4(f32x2_to_bf16x2(o[mt][e] * f, o[mt][2 + e] * f),
+                                   f32x2_to_bf16x2(o[mt + 1][e] * f, o[mt + 1][2 + e] * f),
+                                   f32x2_to_bf16x2(o[mt + 2][e] * f, o[mt + 2][2 + e] * f),
+                                   f32x2_to_bf16x2(o[mt + 3][e] * f, o[mt + 3][2 + e] * f));
+      }
+    } else {
+      // its state: the warp's first piece, or its last (all of the ring's pages are used by then)
+      const int k = u == w0 ? 0 : 1;
+      float* dst0 = k == 0 ? co + warp * p.G * DH : reinterpret_cast<float*>(ring);
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int h = 2 * t + e;
+        if (h >= p.G) continue;
+        // m in log2 units
+        if (g == 0)
+          cml[(warp * 2 + k) * p.G + h] = make_float2(st.m[e] == -INFINITY ? -INFINITY : st.m[e] * pv.ls[e], st.l[e]);
+        float* dst = dst0 + h * DH + g * (DH / 8);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+          *reinterpret_cast<float2*>(dst + 2 * mt) = make_float2(o[mt][e], o[mt][2 + e]);
+      }
+      const int a = u - p0;  // the segment's first unit
+      if (lane == 0 && u == max(a, u0)) {  // the first of its pieces in the CTA announces it
+        Shared s;
+        s.b = b;
+        s.gkv = gkv;
+        s.first = a;
+        s.pages = pages;
+        s.wa = warp;
+        s.wz = warp_of(min(a + pages, u1) - 1);
+        s.np = 1;
+        s.c_lo = 0;
+        if (!SEG && (a < u0 || a + pages > u1)) {
+          const CostSplit split(V, Pe);
+          const int v_first = voff[b] + gkv * (pages + kPc) + kPc;
+          s.c_lo = split.cta_of(v_first);
+          s.np = split.cta_of(v_first + pages - 1) - s.c_lo + 1;
         }
+        list[atomicAdd(&list_n, 1)] = s;
       }
     }
-    __syncthreads();
-    const int64_t sigma = static_cast<int64_t>(b) * p.Hkv + gkv;
-    const int64_t slot = c + sigma;
-    uint16_t* orow = p.out + (static_cast<int64_t>(b) * p.Hq + gkv * p.G) * DH;
-    for (int i = tid; i < p.G * DH; i += kDecThreads) {
-      const int h = i / DH, d = i - h * DH;
-      float M = -INFINITY, l = 0.f, acc = 0.f;
+    u += n;
+  }
+  __syncthreads();
+
+  // ---- the shared segments: a float4 of one head's output a thread
+  const int n4 = p.G * DH / 4, shared = list_n;
+  bool split_any = false;
+  for (int i = tid; i < shared * n4; i += kDecThreads) {
+    const int k = i / n4, e = i - k * n4, h = 4 * e / DH;
+    const Shared s = list[k];
+    float M = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w0_ = s.wa; w0_ <= s.wz; w0_ += 4) {  // four warps at a time, their loads together
+      float2 ml[4];
+      float4 v[4];
 #pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, cml[w * p.G + h].x);
-#pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) {
-        const float2 ml = cml[w * p.G + h];
-        if (ml.x != -INFINITY || ml.y != 0.f) {  // (-inf, 0): no visible token; its o is not there
-          const float a = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - M);
-          l += ml.y * a;
-          acc += co[(w * p.G + h) * DH + d] * a;
+      for (int y = 0; y < 4; ++y) {
+        const int w = w0_ + y;
+        ml[y] = make_float2(-INFINITY, 0.f);
+        v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (w <= s.wz && wstart[w] < wstart[w + 1]) {
+          const bool head = wstart[w] >= s.first;
+          ml[y] = cml[(w * 2 + (head ? 0 : 1)) * p.G + h];
+          v[y] = *reinterpret_cast<const float4*>(
+              (head ? co + w * p.G * DH : reinterpret_cast<const float*>(smem + w * p.S * kSlot)) + 4 * e);
         }
       }
-      if (single) {
-        const float r = acc * (l > 0.f ? sv / l : 0.f);
-        orow[i] = static_cast<uint16_t>(f32x2_to_bf16x2(r, 0.f) & 0xFFFFu);
-      } else {
-        p.ws_o[slot * p.G * DH + i] = acc;
-        if (d == 0) p.ws_ml[slot * p.G + h] = make_float2(M, l);
+      const float nm = fmaxf(fmaxf(M, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
+      const float r = M == -INFINITY ? 1.f : fast_exp2(M - nm);
+      l *= r;
+      acc.x *= r;
+      acc.y *= r;
+      acc.z *= r;
+      acc.w *= r;
+      M = nm;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const float a = ml[y].x == -INFINITY ? 1.f : fast_exp2(ml[y].x - M);  // (-inf: l and o are 0, or NaN)
+        l += ml[y].y * a;
+        acc.x += v[y].x * a;
+        acc.y += v[y].y * a;
+        acc.z += v[y].z * a;
+        acc.w += v[y].w * a;
       }
     }
-    __syncthreads();
-    if (!single) {
-      // Publish the piece: the barrier above orders every thread's stores
-      // before thread 0's acquire-release arrival, and the arrival that
-      // completes the count makes all pieces visible to this CTA.
-      const int v_first = voff[b] + gkv * (pages + kPc) + kPc;
-      const int c_lo = split.cta_of(v_first);
-      const int np = split.cta_of(v_first + pages - 1) - c_lo + 1;
-      if (tid == 0)
-        merge_s = atom_add_acq_rel_gpu(p.ws_cnt + sigma, 1u) + 1 == static_cast<uint32_t>(np);
+    if (s.np == 1) {
+      const float f = l > 0.f ? __ldg(p.vs + (p.per_head ? s.gkv : 0)) / l : 0.f;
+      *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(s.b) * p.Hq + s.gkv * p.G) * DH + 4 * e) =
+          make_uint2(f32x2_to_bf16x2(acc.x * f, acc.y * f), f32x2_to_bf16x2(acc.z * f, acc.w * f));
+    } else {
+      const int64_t slot = c + static_cast<int64_t>(s.b) * p.Hkv + s.gkv;
+      *reinterpret_cast<float4*>(p.ws_o + slot * p.G * DH + 4 * e) = acc;
+      if (4 * e % DH == 0) p.ws_ml[slot * p.G + h] = make_float2(M, l);
+    }
+  }
+  if (!SEG) {
+    for (int k = 0; k < shared; ++k) split_any |= list[k].np > 1;
+    if (split_any) {  // the same for every thread
+      // Publish the pieces: the barrier orders every thread's stores before the
+      // acquire-release arrivals, and an arrival that completes a count makes all
+      // pieces of that segment visible to this CTA.
       __syncthreads();
-      if (merge_s) {
-        // thread (k, i): the pieces k, k + K, ... of output float4 i
-        const int n4 = p.G * DH / 4;
-        const int K = max(1, min(kDecThreads / n4, kDecWarps));  // [K][n4] fits co
-        const float2* ml = p.ws_ml + (c_lo + sigma) * p.G;
-        const float4* ob = reinterpret_cast<const float4*>(p.ws_o + (c_lo + sigma) * p.G * DH);
-        float4* part = reinterpret_cast<float4*>(co);  // [K][n4]
-        float2* pml = cml;                              // [K][G]
+      if (tid < shared) {
+        const Shared s = list[tid];
+        merge_s[tid] = s.np > 1 && atom_add_acq_rel_gpu(p.ws_cnt + static_cast<int64_t>(s.b) * p.Hkv + s.gkv, 1u) + 1 ==
+                                       static_cast<uint32_t>(s.np);
+      }
+      __syncthreads();
+      const int K = max(1, min(kDecThreads / n4, kDecWarps));  // [K][n4] fits co
+      float4* part = reinterpret_cast<float4*>(co);
+      for (int k = 0; k < shared; ++k) {
+        if (!merge_s[k]) continue;
+        const Shared s = list[k];
+        // thread (y, e): the pieces y, y + K, ... of output float4 e
+        const int64_t sigma = static_cast<int64_t>(s.b) * p.Hkv + s.gkv;
+        const float2* ml = p.ws_ml + (s.c_lo + sigma) * p.G;
+        const float4* ob = reinterpret_cast<const float4*>(p.ws_o + (s.c_lo + sigma) * p.G * DH);
         for (int i = tid; i < K * n4; i += kDecThreads) {
-          const int k = i / n4, e = i - k * n4, h = 4 * e / DH;
+          const int y0 = i / n4, e = i - y0 * n4, h = 4 * e / DH;
           float M = -INFINITY, l = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int j = k; j < np; j += 8 * K) {  // eight pieces at a time, their loads together
+          for (int j = y0; j < s.np; j += 8 * K) {  // eight pieces at a time, their loads together
             float2 m8[8];
             float4 v8[8];
 #pragma unroll
             for (int y = 0; y < 8; ++y) {
               const int x = j + y * K;
-              m8[y] = x < np ? __ldcg(ml + static_cast<int64_t>(x) * p.G + h) : make_float2(-INFINITY, 0.f);
-              v8[y] = x < np ? __ldcg(ob + static_cast<int64_t>(x) * n4 + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+              m8[y] = x < s.np ? __ldcg(ml + static_cast<int64_t>(x) * p.G + h) : make_float2(-INFINITY, 0.f);
+              v8[y] = x < s.np ? __ldcg(ob + static_cast<int64_t>(x) * n4 + e) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
             float nm = M;
 #pragma unroll
             for (int y = 0; y < 8; ++y) nm = fmaxf(nm, m8[y].x);
-            const float a = (M == -INFINITY) ? 1.f : fast_exp2(M - nm);
+            const float a = M == -INFINITY ? 1.f : fast_exp2(M - nm);
             l *= a;
             acc.x *= a;
             acc.y *= a;
@@ -590,17 +731,17 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) decode_kernel(const __g
             }
           }
           part[i] = acc;
-          if (4 * e % DH == 0) pml[k * p.G + h] = make_float2(M, l);
+          if (4 * e % DH == 0) cml[y0 * p.G + h] = make_float2(M, l);
         }
         __syncthreads();
         for (int e = tid; e < n4; e += kDecThreads) {
           const int h = 4 * e / DH;
           float M = -INFINITY, l = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int k = 0; k < K; ++k) M = fmaxf(M, pml[k * p.G + h].x);
-          for (int k = 0; k < K; ++k) {
-            const float2 x = pml[k * p.G + h];
-            const float4 v = part[k * n4 + e];
+          for (int y = 0; y < K; ++y) M = fmaxf(M, cml[y * p.G + h].x);
+          for (int y = 0; y < K; ++y) {
+            const float2 x = cml[y * p.G + h];
+            const float4 v = part[y * n4 + e];
             const float w = x.x == -INFINITY ? 1.f : fast_exp2(x.x - M);
             l += x.y * w;
             acc.x += v.x * w;
@@ -608,22 +749,18 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) decode_kernel(const __g
             acc.z += v.z * w;
             acc.w += v.w * w;
           }
-          const float f = l > 0.f ? sv / l : 0.f;
-          uint2 r;
-          r.x = f32x2_to_bf16x2(acc.x * f, acc.y * f);
-          r.y = f32x2_to_bf16x2(acc.z * f, acc.w * f);
-          *reinterpret_cast<uint2*>(orow + 4 * e) = r;
+          const float f = l > 0.f ? __ldg(p.vs + (p.per_head ? s.gkv : 0)) / l : 0.f;
+          *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(s.b) * p.Hq + s.gkv * p.G) * DH + 4 * e) =
+              make_uint2(f32x2_to_bf16x2(acc.x * f, acc.y * f), f32x2_to_bf16x2(acc.z * f, acc.w * f));
         }
         if (tid == 0) p.ws_cnt[sigma] = 0u;
         __syncthreads();
       }
     }
-    u += n;
   }
   // after a timeout: the copies still in flight land (or the wait runs out) before the CTA leaves
-  for (; dead && done < issued; ++done) {
+  for (; dead && done < issued; ++done)
     mbar_wait(&full[done % p.S], static_cast<uint32_t>((done / p.S) & 1));
-  }
 }
 
 }  // namespace fp4
