@@ -446,30 +446,26 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) decode_kernel(const __g
     if (col >= 0 && col < p.max_blocks)
       blk = __ldg(p.block_tables + static_cast<int64_t>(b) * p.max_blocks + col);
   };
-  // The warp's next `n` <= 2 pages into stages s and the one after: lanes 0 and
-  // 1 copy K and V of the first, lanes 2 and 3 of the second.
+  // The warp's next n pages into stages s, s + 1, ...: lanes 2i and 2i + 1 copy
+  // K and V of page i.
+  fetch(lane, blk_now, head_now);
+  fetch(32 + lane, blk_next, head_next);
   int issued = 0;
   auto issue = [&](int s, int n) {
-    const int k = issued + ((lane >> 1) & 1);
-    if ((issued & 31) == 0) {
-      if (issued == 0) {
-        fetch(lane, blk_now, head_now);
-      } else {
-        blk_now = blk_next;
-        head_now = head_next;
+    const int k = issued + (lane >> 1);
+    const int ba = __shfl_sync(kFull, blk_now, k & 31), ha = __shfl_sync(kFull, head_now, k & 31);
+    int blk = ba, head = ha;
+    if (((issued + n - 1) ^ issued) & 32) {  // the last of them are of the next 32
+      const int bb = __shfl_sync(kFull, blk_next, k & 31), hb = __shfl_sync(kFull, head_next, k & 31);
+      if ((k ^ issued) & 32) {
+        blk = bb;
+        head = hb;
       }
-      fetch(issued + 32 + lane, blk_next, head_next);
     }
-    int blk = __shfl_sync(kFull, blk_now, k & 31), head = __shfl_sync(kFull, head_now, k & 31);
-    if (n == 2 && (issued & 31) == 31) {  // the second page begins the next 32
-      const int b2 = __shfl_sync(kFull, blk_next, 0), h2 = __shfl_sync(kFull, head_next, 0);
-      if (lane & 2) {
-        blk = b2;
-        head = h2;
-      }
+    if (((issued + n) ^ issued) & 32) {
       blk_now = blk_next;
       head_now = head_next;
-      fetch(issued + 33 + lane, blk_next, head_next);
+      fetch(((issued + n) | 31) + 1 + lane, blk_next, head_next);
     }
     if (lane < 2 * n) {
       int st = s + (lane >> 1);
@@ -484,7 +480,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) decode_kernel(const __g
           mbar_arrive_expect_tx(&full[st], kSlot);
         }
       }
-      __syncwarp((1u << (2 * n)) - 1u);
+      __syncwarp((1u << (2 * n)) - 1u);  // (n <= 8)
       if (!bad)
         bulk_load(ring + st * kSlot + (lane & 1) * PG::kBytes,
                   ((lane & 1) ? p.vc : p.kc) + (static_cast<int64_t>(blk) * p.Hkv + head) * PG::kBytes,
@@ -492,7 +488,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) decode_kernel(const __g
     }
     issued += n;
   };
-  for (int s = 0; s < p.S && issued < mine; s += 2) issue(s, min(2, min(p.S - s, mine - issued)));
+  if (mine > 0) issue(0, min(p.S, mine));
 
   int done = 0, stage = 0;
   uint32_t parity = 0;
