@@ -29,6 +29,9 @@ UNITS = [(os.path.splitext(s)[0], s, []) for s in SOURCES if s != "kvq_decode_va
     (f"kvq_decode_f{fmt}_d{dh}", "kvq_decode_variant.cu",
      [f"-DKVQ_VARIANT_FMT={fmt}", f"-DKVQ_VARIANT_DH={dh}"])
     for fmt in (1, 2, 0) for dh in (128, 64)]
+# the 4-bit cache's Python binding: host code against torch's headers
+BINDING = "fp4_binding.cpp"
+BINDING_LIB = os.path.join(BUILD, "_kvq_fp4.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]
@@ -43,7 +46,7 @@ def _nvcc() -> str:
 
 def _inputs():
     inc = os.path.join(os.path.dirname(HERE), "include")
-    return ([os.path.join(CSRC, s) for s in SOURCES + HEADERS] +
+    return ([os.path.join(CSRC, s) for s in SOURCES + HEADERS + [BINDING]] +
             [os.path.join(inc, h) for h in ("kvq.h", "kvq_fp4.h")] + [os.path.abspath(__file__)])
 
 
@@ -61,13 +64,43 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
+def _torch_root() -> str:
+    """torch's folder, without importing it."""
+    import importlib.util
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch not found")
+    return list(spec.submodule_search_locations)[0]
+
+
+def build_binding(verbose: bool = False) -> str:
+    import sysconfig
+    torch = _torch_root()
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = BINDING_LIB + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "c++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-Wno-attributes", os.path.join(CSRC, BINDING), "-o", tmp,
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(torch, "include"),
+           "-I" + os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-I" + os.path.join(cuda, "include"), "-I/usr/local/cuda/include",
+           "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ldl"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_LIB)
+    return BINDING_LIB
+
+
 def build_test_lib(force: bool = False, verbose: bool = False) -> str:
     return build(force=force, verbose=verbose, extra=TEST_DEFINES, lib=TEST_LIB)
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None,
           lib: str = LIB) -> str:
-    if not force and up_to_date(lib):
+    binding = lib == LIB  # the tests' library needs none
+    if not force and up_to_date(lib) and (not binding or up_to_date(BINDING_LIB)):
         return lib
     out_dir = os.path.dirname(lib)
     os.makedirs(out_dir, exist_ok=True)
@@ -87,8 +120,11 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             print(r.stderr, file=sys.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(len(UNITS), max(2, os.cpu_count() or 2))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(UNITS) + 1, max(2, os.cpu_count() or 2))) as ex:
+        native = ex.submit(build_binding, verbose) if binding else None
         objs = list(ex.map(compile_one, UNITS))
+        if native:
+            native.result()
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)

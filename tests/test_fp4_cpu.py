@@ -19,27 +19,47 @@ def kvq():
     return m
 
 
-def test_exports(kvq):
+_vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+SIGNATURES = {
+    "kvq_fp4_write": (_i32, [_vp, _vp, _i64, _vp, _i64, _i32, _i32, _vp, _vp, _i64, _i32, _vp, _i32, _vp, _i32, _i32, _vp, _vp]),
+    "kvq_fp4_read": (_i32, [_vp, _vp, _i64, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _i32, _i64, _vp, _i32, _vp, _i32, _i32, _vp,
+                            _vp, _i64, _vp, _vp]),
+    "kvq_fp4_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+    "kvq_fp4_decode_attn": (_i32, [_vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i64, _i32, _vp, _i32, _vp, _i32, _i32,
+                                   _i32, _i32, _vp, _sz, _vp, _vp, _vp]),
+    "kvq_fp4_prefill_attn": (_i32, [_vp, _vp, _i64, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i64, _i32, _vp, _i32,
+                                    _vp, _i32, _i32, _i32, _i32, _vp, _sz, _vp, _vp, _vp]),
+}
+
+
+@pytest.fixture(scope="module")
+def clib(kvq):
+    """The C ABI, past the binding."""
+    raw = ctypes.CDLL(kvq.LIB_PATH)
+    for name, (res, args) in SIGNATURES.items():
+        getattr(raw, name).restype, getattr(raw, name).argtypes = res, args
+    return raw
+
+
+def test_exports(kvq, clib):
     from fp8_quantized_paged_gb300 import fp4
     text = open(os.path.join(ROOT, "include", "kvq_fp4.h")).read()
     declared = set(re.findall(r"KVQ_API\s+[\w\s\*]+?\b(kvq_\w+)\s*\(", text))
-    assert declared == set(fp4.SIGNATURES)
-    raw = ctypes.CDLL(kvq.LIB_PATH)
+    assert declared == set(SIGNATURES)
     for name in declared:
-        assert getattr(raw, name) is not None and getattr(kvq, name) is getattr(fp4, name)
+        assert getattr(clib, name) is not None and getattr(kvq, name) is getattr(fp4, name)
 
 
-def _call(kvq, name, order, base, **kw):
+def _call(clib, name, order, base, **kw):
     args = dict(base, **kw)
     assert set(args) == set(order)
     p = lambda x: ctypes.c_void_p(x) if x else None  # noqa: E731
     ptr = {"k", "v", "slots", "kc", "vc", "ks", "vs", "status", "bt", "starts", "cu", "ko", "vo", "q", "sl", "ws", "out", "stream"}
-    return getattr(kvq.lib(), name)(*[p(args[n]) if n in ptr else args[n] for n in order])
+    return getattr(clib, name)(*[p(args[n]) if n in ptr else args[n] for n in order])
 
 
 @pytest.fixture(scope="module")
-def calls(kvq):
-    kvq.kvq_fp4_write  # sets the signatures
+def calls(clib):
     worder = "k v stride slots n hkv dh kc vc nb bs ks ksl vs vsl gran status stream".split()
     wbase = dict(k=A, v=A, stride=1024, slots=A, n=4, hkv=8, dh=128, kc=A, vc=A, nb=10, bs=16, ks=A, ksl=8, vs=A, vsl=8, gran=1,
                  status=0, stream=0)
@@ -49,10 +69,10 @@ def calls(kvq):
     tail = "sl B hq hkv dh nb bs ks ksl vs vsl gran window sinks ws wsb out status stream".split()
     tbase = dict(sl=A, B=2, hq=32, hkv=8, dh=128, nb=10, bs=16, ks=A, ksl=8, vs=A, vsl=8, gran=1, window=0, sinks=0, ws=A,
                  wsb=1 << 40, out=A, status=0, stream=0, kc=A, vc=A, bt=A, mb=4, q=A)
-    return {"write": lambda **k: _call(kvq, "kvq_fp4_write", worder, wbase, **k),
-            "read": lambda **k: _call(kvq, "kvq_fp4_read", rorder, rbase, **k),
-            "decode": lambda **k: _call(kvq, "kvq_fp4_decode_attn", "q kc vc bt mb".split() + tail, tbase, **k),
-            "prefill": lambda **k: _call(kvq, "kvq_fp4_prefill_attn", "q cu n maxq kc vc bt mb".split() + tail,
+    return {"write": lambda **k: _call(clib, "kvq_fp4_write", worder, wbase, **k),
+            "read": lambda **k: _call(clib, "kvq_fp4_read", rorder, rbase, **k),
+            "decode": lambda **k: _call(clib, "kvq_fp4_decode_attn", "q kc vc bt mb".split() + tail, tbase, **k),
+            "prefill": lambda **k: _call(clib, "kvq_fp4_prefill_attn", "q cu n maxq kc vc bt mb".split() + tail,
                                          dict(tbase, cu=A, n=20, maxq=10), **k)}
 
 
@@ -103,19 +123,11 @@ def test_workspace_size(kvq):
 B, HQ, HKV, DH, NB = 2, 8, 2, 64, 6
 
 
-@pytest.fixture()
-def fp4(kvq, monkeypatch):
-    """The binding with host tensors taken for the current device's: every case
-    below is refused before the library is reached."""
+@pytest.fixture(scope="module")
+def fp4(kvq):
+    """The binding.  It looks at the device last, so a host tensor is refused for
+    anything else that is wrong with it first, and no call reaches the library."""
     from fp8_quantized_paged_gb300 import fp4 as m
-    monkeypatch.setattr(m, "_device", lambda where, t: -1)
-
-    class NoLib:
-        def __getattr__(self, name):
-            def called(*args):
-                raise AssertionError("a refused call reached the library")
-            return called
-    monkeypatch.setattr(m, "_lib", NoLib())
     return m
 
 
@@ -146,7 +158,7 @@ def t(*s, d=torch.bfloat16):
     return torch.zeros(s, dtype=d)
 
 
-BOTH = [(dict(kc=t(NB, HKV, 9 * DH)), ARG, "k_cache"), (dict(vc=t(NB + 1, HKV, 9 * DH, d=torch.uint8)), SHAPE, "v_cache"),
+BOTH = [(dict(kc=t(NB, HKV, 9 * DH)), ARG, "k_cache"), (dict(kc=t(NB, 9 * DH, d=torch.uint8)), SHAPE, "caches"), (dict(vc=t(NB + 1, HKV, 9 * DH, d=torch.uint8)), SHAPE, "v_cache"),
         (dict(kc=t(NB, HKV, 16, DH, d=torch.uint8)), SHAPE, "caches"), (dict(kc=t(NB, HKV, 500, d=torch.uint8)), SHAPE, "page"),
         (dict(kc=t(NB, 9 * DH, HKV, d=torch.uint8).transpose(1, 2)), SHAPE, "contiguous"),
         (dict(ks=t(HKV)), ARG, "k_scale"), (dict(vs=t(HKV, d=torch.float64)), ARG, "v_scale"),
@@ -178,39 +190,27 @@ def test_binding_refusals(fp4, op, over, status, word):
     assert e.value.status == status and word in str(e.value)
 
 
-def test_binding_wants_cuda_tensors(kvq):
+def test_binding_wants_cuda_tensors(kvq, fp4):
     for op in ("write", "read", "decode", "prefill"):
         with pytest.raises(kvq.KvqError) as e:
-            from fp8_quantized_paged_gb300 import fp4
             _run(fp4, op, _args())
         assert e.value.status == ARG and "CUDA" in str(e.value)
 
 
-class _Elsewhere:
-    """A tensor that says it is on another device."""
-
-    def __init__(self, t, at):
-        self._t, self._at = t, at
-
-    def __getattr__(self, name):
-        return getattr(self._t, name)
-
-    def get_device(self):
-        return self._at
-
-
-def test_binding_refuses_other_devices(kvq, fp4, monkeypatch):
-    for op, names in (("write", "v slots kc vc ks vs"), ("read", "vc bt starts cu ks vs ko vo"), ("decode", "kc vc bt sl ks vs ws out"),
-                      ("prefill", "cu kc vc bt sl ks vs ws out")):
-        for n in names.split():
-            a = _args()
-            a[n] = _Elsewhere(a[n], 1)
-            with pytest.raises(fp4.KvqError) as e:
-                _run(fp4, op, a)
-            assert e.value.status == ARG and "device" in str(e.value), (op, n)
-    monkeypatch.undo()
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    with pytest.raises(kvq.KvqError) as e:
-        from fp8_quantized_paged_gb300 import fp4 as m
-        _run(m, "decode", _args(q=_Elsewhere(t(B, HQ, DH), 1)))
-    assert e.value.status == ARG and "current device" in str(e.value)
+def test_binding_arguments(fp4):
+    a = _args()
+    pos = (a["k"], a["v"], a["slots"], a["kc"], a["vc"], a["ks"], a["vs"])
+    for call in (lambda: fp4.kvq_fp4_write(*pos), lambda: fp4.kvq_fp4_write(*pos, 1, None, None, 3),
+                 lambda: fp4.kvq_fp4_write(*pos, 1, other=3), lambda: fp4.kvq_fp4_write(*pos, 1, k=a["k"]),
+                 lambda: fp4.kvq_fp4_write(7, *pos[1:], 1), lambda: fp4.kvq_fp4_write(None, *pos[1:], 1)):
+        with pytest.raises(TypeError):
+            call()
+    for bad in ("one", 1.5, None, 1 << 40, -(1 << 70)):
+        with pytest.raises(fp4.KvqError) as e:
+            fp4.kvq_fp4_write(*pos, bad)
+        assert e.value.status == ARG and "scale_granularity" in str(e.value)
+    # by name, in any order: as far as the device check
+    with pytest.raises(fp4.KvqError) as e:
+        fp4.kvq_fp4_write(scale_granularity=1, v_scale=a["vs"], k=a["k"], v=a["v"], slot_mapping=a["slots"], k_cache=a["kc"],
+                          v_cache=a["vc"], k_scale=a["ks"], stream=None, dev_status=None)
+    assert "CUDA" in str(e.value)
