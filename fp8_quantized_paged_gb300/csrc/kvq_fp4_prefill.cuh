@@ -97,7 +97,7 @@ struct PreSmem {
   static constexpr int v = k + kBufs * kTile;
   static constexpr int stage = v + kBufs * kTile;
   static constexpr int bars = stage + kPreStages * kStage;
-  static constexpr int kBars = 2 * kPreStages + 4 * kBufs + 5 * kTiles + 2;
+  static constexpr int kBars = 2 * kPreStages + 4 * kBufs + 6 * kTiles + 2;
   static constexpr int misc = bars + kBars * 8;
   // tmem address, abort flag, V NaN flag, merge flag, page flags [stages][8], issued [stages], masks [4]
   static constexpr int total = misc + (4 + kPreStages * 9 + 4) * 4 + 1024;
@@ -110,6 +110,91 @@ KVQ_DEVI uint32_t tile_off(int row, int col) {
   const int blk = col >> 6, c16 = (col & 63) >> 3;
   return static_cast<uint32_t>(blk * (128 * 128) + (row >> 3) * 1024 + (row & 7) * 128 +
                                ((c16 ^ (row & 7)) << 4) + ((col & 7) << 1));
+}
+
+// 64 consecutive TMEM columns of this thread's lane (warp-collective); the load and
+// its wait are one statement, so that nothing uses the registers early.
+KVQ_DEVI void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]),
+        "=f"(v[1]),
+        "=f"(v[2]),
+        "=f"(v[3]),
+        "=f"(v[4]),
+        "=f"(v[5]),
+        "=f"(v[6]),
+        "=f"(v[7]),
+        "=f"(v[8]),
+        "=f"(v[9]),
+        "=f"(v[10]),
+        "=f"(v[11]),
+        "=f"(v[12]),
+        "=f"(v[13]),
+        "=f"(v[14]),
+        "=f"(v[15]),
+        "=f"(v[16]),
+        "=f"(v[17]),
+        "=f"(v[18]),
+        "=f"(v[19]),
+        "=f"(v[20]),
+        "=f"(v[21]),
+        "=f"(v[22]),
+        "=f"(v[23]),
+        "=f"(v[24]),
+        "=f"(v[25]),
+        "=f"(v[26]),
+        "=f"(v[27]),
+        "=f"(v[28]),
+        "=f"(v[29]),
+        "=f"(v[30]),
+        "=f"(v[31]),
+        "=f"(v[32]),
+        "=f"(v[33]),
+        "=f"(v[34]),
+        "=f"(v[35]),
+        "=f"(v[36]),
+        "=f"(v[37]),
+        "=f"(v[38]),
+        "=f"(v[39]),
+        "=f"(v[40]),
+        "=f"(v[41]),
+        "=f"(v[42]),
+        "=f"(v[43]),
+        "=f"(v[44]),
+        "=f"(v[45]),
+        "=f"(v[46]),
+        "=f"(v[47]),
+        "=f"(v[48]),
+        "=f"(v[49]),
+        "=f"(v[50]),
+        "=f"(v[51]),
+        "=f"(v[52]),
+        "=f"(v[53]),
+        "=f"(v[54]),
+        "=f"(v[55]),
+        "=f"(v[56]),
+        "=f"(v[57]),
+        "=f"(v[58]),
+        "=f"(v[59]),
+        "=f"(v[60]),
+        "=f"(v[61]),
+        "=f"(v[62]),
+        "=f"(v[63])
+      : "r"(taddr)
+      : "memory");
+}
+
+// 8 consecutive columns of this thread's lane (no wait).
+KVQ_DEVI void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 // The pages that a CTA's rows see, as a list: the first tokens' pages [0, sink),
@@ -125,8 +210,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
   using PG = Page<DH>;
   constexpr int S = kPreStages;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_u32(smem);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::bars);  // [S] a stage landed
   uint64_t* empty = full + S;            // [S] a stage converted (128 arrivals)
@@ -140,6 +224,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
   uint64_t* pdone = phalf + kTiles;      // [kTiles] a block's PVs done (commit, and the issuer's arrival)
   uint64_t* fin = pdone + kTiles;        // every matrix step done (a commit of each issuer)
   uint64_t* qready = fin + 1;            // both Q tiles written (256)
+  uint64_t* turn = qready + 1;           // [kTiles] a tile's softmax is half through a block
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + SM::misc);
   volatile uint32_t* tmem_slot = misc;
   volatile uint32_t* abort_flag = misc + 1;
@@ -181,6 +266,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
       mbar_init(&pfull[2 * t + 1], 128);
       mbar_init(&phalf[t], 1);
       mbar_init(&pdone[t], 2);
+      mbar_init(&turn[t], 1);
     }
     mbar_init(fin, kTiles);
     mbar_init(qready, kTiles * 128);
@@ -303,6 +389,13 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
         const int i = j - jb[t], x = (j - c0) % kBufs, ph = (j - c0) / kBufs;
         const bool active = j >= jb[t] && j < je[t];
         if (!(ok = wait(&conv_k[x], ph))) break;
+        // The tiles take turns: a tile's S waits until the other's softmax has begun
+        // the block before, so that one's softmax runs beside the other's matrix
+        // steps.  (Left alone they fall into step: steps issued together end
+        // together, and both softmaxes then run against each other.)
+        if ((t == 1 || j > c0) && !(ok = wait(&turn[1 - t], j - c0 - (t == 0 ? 1 : 0)))) break;
+        // P of the block before read: this S may overwrite it
+        if (active && i > 0 && !(ok = wait(&pdone[t], i - 1))) break;
         if (active) {
           tc::tc_fence_after();
           const uint32_t a = sbase + SM::q + t * kRows * DH * 2, bk = sbase + SM::k + x * SM::kTile;
@@ -313,6 +406,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
           }
           mbar_arrive(&sfull[t]);  // hands on what conv_k's arrival showed (bmask)
           tc::mma_commit(&sfull[t]);
+        } else {
+          mbar_arrive(&turn[t]);
         }
         tc::mma_commit(&done_k[x]);
         if (!(ok = wait(&conv_v[x], ph))) break;
@@ -330,7 +425,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
         }
         if (!ok) break;
         tc::mma_commit(&done_v[x]);
-        if (active) ok = wait(&pdone[t], i);  // P read: the next S may overwrite it
       }
       if (!ok) fail();
       tc::mma_commit(fin);
@@ -352,39 +446,44 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
 #pragma unroll
       for (int e = 0; e < kBlkPages; ++e) bm |= (pg_bad[s * 8 + e] ? 1u : 0u) << e;
       if (ct == 0 && !is_v) bmask[(c0 + i) & 3] = bm;
-      const uint32_t stg = sbase + SM::stage + s * SM::kStage;
-      const uint32_t dst = sbase + (is_v ? SM::v : SM::k) + x * SM::kTile;
-      // Block of 16 dims e of the tile: 4 of a 64-column block of row r, rows in
-      // turn, so that eight lanes' 16-byte stores (two rows, four swizzled
-      // columns each) cover all banks.
-      constexpr int kIter = kKeys * (DH / 16) / 128;
+      // Thread ct converts 16 dims of rows r0, r0 + 32, r0 + 64, r0 + 96 (pages p0, p0 + 2, ...,
+      // all at row r0 % 16 of theirs), for each 64 dims of the head: block ct % 4 of the 64.  Eight
+      // lanes' 16-byte stores (two rows, four swizzled columns each) cover all banks.
+      const int r0 = ct >> 2, c4 = ct & 3, tr = r0 & 15, p0 = r0 >> 4;
+      const uint8_t* src = smem + SM::stage + s * SM::kStage + p0 * PG::kBytes;
+      const uint8_t* code = src + tr * PG::kRow + c4 * 8;
+      const uint8_t* scale = src + PG::kScaleOff + tr * PG::kScales + c4;
+      uint8_t* dst = smem + (is_v ? SM::v : SM::k) + x * SM::kTile + (r0 >> 3) * 1024 + (r0 & 7) * 128;
+      uint8_t* lo = dst + (((2 * c4) ^ (r0 & 7)) << 4);
+      uint8_t* hi = dst + (((2 * c4 + 1) ^ (r0 & 7)) << 4);
+      // Masked pages may hold anything.  Their keys are masked later; values count as 0, like
+      // those past the sequence (weights of 0 do not clear a NaN), and so do NaN blocks, which
+      // the epilogue puts back where they are seen.
+      uint32_t keep = 0xFu;  // bit y: row r0 + 32 y
+      if (is_v) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if ((bm >> (p0 + 2 * y) & 1u) || list.col(kBlkPages * (c0 + i) + p0 + 2 * y) * kTok + tr >= L) keep &= ~(1u << y);
+      }
       bool nan = false;
-#pragma unroll 4
-      for (int y = 0; y < kIter; ++y) {
-        const int e = ct + 128 * y;
-        const int c = (e & 3) + 4 * (e >> 9), r = (e >> 2) & 127;
-        const uint32_t page = stg + (r >> 4) * PG::kBytes, tr = r & 15;
-        uint32_t sb = 0;
-        uint2 w = make_uint2(0u, 0u);
-        if (!(bm >> (r >> 4) & 1u)) {
-          asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(page + tr * PG::kRow + c * 8));
-          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sb) : "r"(page + PG::kScaleOff + tr * PG::kScales + c));
-        }
+#pragma unroll
+      for (int y = 0; y < 4 * (DH / 64); ++y) {
+        const int yr = y & 3, yc = y >> 2;
+        const uint2 w = *reinterpret_cast<const uint2*>(code + yr * 2 * PG::kBytes + yc * 32);
+        uint32_t sb = scale[yr * 2 * PG::kBytes + yc * 4];
         if (is_v) {
-          // weights of 0 do not clear a NaN: tokens past the sequence count as 0,
-          // and so do NaN blocks, which the epilogue puts back where they are seen
-          if (list.col(kBlkPages * (c0 + i) + (r >> 4)) * kTok + static_cast<int>(tr) >= L) sb = 0;
-          if ((sb & 0x7Fu) == 0x7Fu) {
-            sb = 0;
-            nan = true;
-          }
+          const bool bad = (sb & 0x7Fu) == 0x7Fu, in = keep >> yr & 1u;
+          nan |= bad && in;
+          sb = bad || !in ? 0u : sb;
         }
         const uint32_t f = fp8x2_to_f16x2<KVQ_FMT_E4M3>(static_cast<uint16_t>(sb * 0x101u));
         uint32_t a[4], d[4];
         e2m1x8_to_f16x2x4(w.x, a);
         e2m1x8_to_f16x2x4(w.y, d);
-        tc::sts128(dst + tile_off(r, 16 * c), hmul2(a[0], f), hmul2(a[1], f), hmul2(a[2], f), hmul2(a[3], f));
-        tc::sts128(dst + tile_off(r, 16 * c + 8), hmul2(d[0], f), hmul2(d[1], f), hmul2(d[2], f), hmul2(d[3], f));
+        *reinterpret_cast<uint4*>(lo + yr * 4096 + yc * 16384) =
+            make_uint4(hmul2(a[0], f), hmul2(a[1], f), hmul2(a[2], f), hmul2(a[3], f));
+        *reinterpret_cast<uint4*>(hi + yr * 4096 + yc * 16384) =
+            make_uint4(hmul2(d[0], f), hmul2(d[1], f), hmul2(d[2], f), hmul2(d[3], f));
       }
       if (nan) *vnan = 1u;
       fence_proxy_async_smem();  // generic writes -> the tensor core's reads
@@ -443,32 +542,18 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
       if (!(ok = wait_w(&sfull[t], i))) break;
       const uint32_t bm8 = bmask[j & 3];
       tc::tc_fence_after();
+      if (r == 0) mbar_arrive(&turn[t]);
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         float x[64];
-        {
-          float a[32], d[32];
-          tc::tmem_ld32(tm_s + h * 64, a);
-          tc::tmem_ld32(tm_s + h * 64 + 32, d);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            x[e] = a[e];
-            x[32 + e] = d[e];
-          }
-        }
+        tmem_ld64(tm_s + h * 64, x);
         const int lp = j * kBlkPages + h * 4;  // list page of the half's first key
         const uint32_t bm = (bm8 >> (4 * h)) & 15u;
         const int k0 = list.col(lp) * kTok;
-        float mx8[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) mx8[e] = -INFINITY;
         // the row sees all 64 keys: four consecutive pages inside its window, or of its first tokens
         const bool whole = live && bm == 0u && k0 + 63 <= pos &&
                            (lp >= list.sink ? k0 >= lo : lp + 3 < list.sink && k0 + 63 < p.sinks);
-        if (whole) {
-#pragma unroll
-          for (int e = 0; e < 64; ++e) mx8[e & 7] = fmaxf(mx8[e & 7], x[e]);
-        } else {
+        if (!whole) {
 #pragma unroll
           for (int e4 = 0; e4 < 4; ++e4) {
             const int kp0 = list.col(lp + e4) * kTok;
@@ -478,12 +563,35 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
               const int kp = kp0 + e;
               const bool seen = page && kp <= pos && (kp >= lo || kp < p.sinks);
               x[16 * e4 + e] = seen ? x[16 * e4 + e] : -INFINITY;
-              mx8[e & 7] = fmaxf(mx8[e & 7], x[16 * e4 + e]);
             }
           }
         }
-        const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                               fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))) * lscale;
+        // Weights against the maximum so far, which grows rarely, and the half's own maximum
+        // beside them (no wait of one for the other); where it grew by over 8, O and l are
+        // rescaled and the weights formed again.
+        float sum, mx;
+        auto weights = [&] {
+          // while every key so far is masked m is -inf: any finite value keeps 2^-inf = 0 (and a NaN)
+          const float mb = m == -INFINITY ? 0.f : m - kPreBias;
+          float l4[4] = {0.f, 0.f, 0.f, 0.f}, mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t ph[8];
+#pragma unroll
+            for (int e2 = 0; e2 < 8; ++e2) {
+              const int e = 16 * c + 2 * e2;
+              const float p0 = fast_exp2(fmaf(x[e], lscale, -mb));
+              const float p1 = fast_exp2(fmaf(x[e + 1], lscale, -mb));
+              l4[e2 & 3] += p0 + p1;
+              mx4[e2 & 3] = fmaxf(mx4[e2 & 3], fmaxf(x[e], x[e + 1]));
+              ph[e2] = f32x2_to_f16x2(p0, p1);
+            }
+            tmem_st8(tm_s + h * 64 + 8 * c, ph);
+          }
+          sum = (l4[0] + l4[1]) + (l4[2] + l4[3]);
+          mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * lscale;
+        };
+        weights();
         const bool grow = mx > m + kRescaleThreshold;
         if (__any_sync(kFull, grow)) {
           // O's last writer: the first half's PV of this block, or (done before S came) block i - 1
@@ -503,24 +611,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
           }
           if (grow) l *= a;
           m = nm;
+          weights();
         }
-        // while every key so far is masked m is -inf: any finite value keeps 2^-inf = 0 (and a NaN)
-        const float mb = m == -INFINITY ? 0.f : m - kPreBias;
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t ph[4];
-#pragma unroll
-          for (int e2 = 0; e2 < 4; ++e2) {
-            const int e = 8 * c + 2 * e2;
-            const float p0 = fast_exp2(fmaf(x[e], lscale, -mb));
-            const float p1 = fast_exp2(fmaf(x[e + 1], lscale, -mb));
-            l4[e2] += p0 + p1;
-            ph[e2] = f32x2_to_f16x2(p0, p1);
-          }
-          tc::tmem_st4(tm_s + h * 64 + 4 * c, ph[0], ph[1], ph[2], ph[3]);
-        }
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        l += sum;
         tc::tmem_st_wait();
         tc::tc_fence_before();
         mbar_arrive(&pfull[2 * t + h]);
