@@ -5,6 +5,8 @@
 // one (token, KV head) row, the unit that shares a scale: the write loads two
 // 16-byte words per tensor and stores 8 bytes of codes and one of scale, the
 // read the reverse, so a row's lanes move whole contiguous runs.
+#include <algorithm>
+
 #include "kvq_fp4.cuh"
 #include "kvq_fp4_host.h"
 
@@ -49,10 +51,8 @@ KVQ_DEVI Divider divider(float d) {
   return v;
 }
 
-// The two bf16 of a word over v.d.
+// The two bf16 of a word over v.d, v.fast.
 KVQ_DEVI float2 quotient2(uint32_t w, const Divider& v) {
-  if (!v.fast)
-    return make_float2(__fdiv_rn(bf16lo_to_f32(w), v.d), __fdiv_rn(bf16hi_to_f32(w), v.d));
   uint32_t c;  // sign(x) min(|x|, L)
   asm("min.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(w), "r"(v.L2));
   const float2 x = make_float2(bf16lo_to_f32(c), bf16hi_to_f32(c));
@@ -77,43 +77,57 @@ KVQ_DEVI uint2 quantize_block(const uint4& a, const uint4& b, float s, const Div
     return make_uint2(0u, 0u);
   }
   const uint32_t amax = min(m, 0x7F7Fu);
-  scale = f32x2_to_fp8x2<KVQ_FMT_E4M3>(quotient2(amax, six).x, 0.f) & 0xFFu;
+  const float top = six.fast ? quotient2(amax, six).x : __fdiv_rn(bf16lo_to_f32(amax), six.d);
+  scale = f32x2_to_fp8x2<KVQ_FMT_E4M3>(top, 0.f) & 0xFFu;
   const float r = __fmul_rn(e4m3_to_f32(scale), s);
   if (!(r > 0.f)) return make_uint2(0u, 0u);
   const Divider div = divider(r);
-  uint2 o;
+  float q[16];
+  if (div.fast) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float q[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 v = quotient2(w[4 * h + i], div);
+    for (int i = 0; i < 8; ++i) {
+      const float2 v = quotient2(w[i], div);
       q[2 * i] = v.x;
       q[2 * i + 1] = v.y;
     }
-    uint32_t c = f32x8_to_e2m1x8(q);
-    // the residual form loses the sign of a zero quotient: take all signs
-    // (bits 15 and 31 of word i) from the inputs, to bits 8i + 3 and 8i + 7
+  } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t x = w[4 * h + i];
-      c |= (((x >> 12) & 8u) | ((x >> 24) & 0x80u)) << (8 * i);
+    for (int i = 0; i < 8; ++i) {
+      q[2 * i] = __fdiv_rn(bf16lo_to_f32(w[i]), r);
+      q[2 * i + 1] = __fdiv_rn(bf16hi_to_f32(w[i]), r);
     }
-    (h ? o.y : o.x) = c;
+  }
+  uint2 o;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float e[8] = {q[8 * h], q[8 * h + 1], q[8 * h + 2], q[8 * h + 3],
+                        q[8 * h + 4], q[8 * h + 5], q[8 * h + 6], q[8 * h + 7]};
+    // The residual form loses the sign of a zero quotient: all signs are taken from the inputs,
+    // bits 15 and 31 of word i to bits 8 i + 3 and 8 i + 7.
+    const uint32_t lo = prmt(w[4 * h], w[4 * h + 1], 0x7531u), hi = prmt(w[4 * h + 2], w[4 * h + 3], 0x7531u);
+    const uint32_t even = prmt(lo, hi, 0x6420u), odd = prmt(lo, hi, 0x7531u);
+    (h ? o.y : o.x) = f32x8_to_e2m1x8(e) | ((even >> 4) & 0x08080808u) | (odd & 0x80808080u);
   }
   return o;
 }
 
-// The grid's thread count is a multiple of the Hkv * DH / 16 blocks of a token
-// (token_row_shape), so a thread keeps its block and its head's scales and
-// strides over the tokens; the next token's loads are issued before the
-// current one is converted.
+// Blocks of 256 threads per SM: at 5 (51 registers) the conversion spills.
+// 32768 tokens of 8 heads of 128: 3 blocks 35.8 us, 4 34.9, 5 51.2.
+constexpr int kWriteCtas = 4;
+
+// K and V are two rows of the grid.  The grid's thread count is a multiple of
+// the Hkv * DH / 16 blocks of a token (token_row_shape), so a thread keeps its
+// block and its head's scale and strides over the tokens; the next token's loads
+// are issued before the current one is converted.
 template <int DH>
-__global__ void __launch_bounds__(256, 3) write_kernel(const WriteParams p) {
+__global__ void __launch_bounds__(256, kWriteCtas) write_kernel(const WriteParams p) {
   using P = Page<DH>;
   constexpr int CH = DH / 16;
   pdl_allow_next();
   pdl_wait();  // the inputs may come from the kernel before this one
+  const bool is_v = blockIdx.y != 0;
+  const uint16_t* in = is_v ? p.v : p.k;
+  uint8_t* cache = is_v ? p.vc : p.kc;
   const int row_units = p.hkv * CH;
   const int64_t gtid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   const int rem = static_cast<int>(gtid % row_units);
@@ -121,44 +135,35 @@ __global__ void __launch_bounds__(256, 3) write_kernel(const WriteParams p) {
   const int64_t tstride = static_cast<int64_t>(gridDim.x) * blockDim.x / row_units;
   int64_t t = gtid / row_units;
   if (t >= p.num_tokens) return;
-  const float sk = __ldg(p.ks + (p.per_head ? h : 0)), sv = __ldg(p.vs + (p.per_head ? h : 0));
-  const Divider dk = divider(__fmul_rn(6.f, sk)), dv = divider(__fmul_rn(6.f, sv));
-  uint4 k[2], v[2];
+  const float s = __ldg((is_v ? p.vs : p.ks) + (p.per_head ? h : 0));
+  const Divider six = divider(__fmul_rn(6.f, s));
+  uint4 x[2];
   int64_t slot;
-  auto load = [&](int64_t tt, uint4 (&kk)[2], uint4 (&vv)[2], int64_t& s) {
-    const int64_t src = tt * p.token_stride + rem * 16;
-    const uint4* kp = reinterpret_cast<const uint4*>(p.k + src);
-    const uint4* vp = reinterpret_cast<const uint4*>(p.v + src);
-    kk[0] = __ldcs(kp);
-    kk[1] = __ldcs(kp + 1);
-    vv[0] = __ldcs(vp);
-    vv[1] = __ldcs(vp + 1);
-    s = __ldg(p.slots + tt);
+  auto load = [&](int64_t tt, uint4 (&xx)[2], int64_t& sl) {
+    const uint4* src = reinterpret_cast<const uint4*>(in + tt * p.token_stride + rem * 16);
+    xx[0] = __ldcs(src);
+    xx[1] = __ldcs(src + 1);
+    sl = __ldg(p.slots + tt);
   };
-  load(t, k, v, slot);
+  load(t, x, slot);
   while (true) {
     const int64_t tn = t + tstride;
-    uint4 kn[2], vn[2];
+    uint4 xn[2];
     int64_t sn = -1;
-    if (tn < p.num_tokens) load(tn, kn, vn, sn);
+    if (tn < p.num_tokens) load(tn, xn, sn);
     if (slot >= p.capacity) {
       if (rem == 0) flag_status(p.status, KVQ_DEV_BAD_SLOT);
     } else if (slot >= 0) {  // a negative slot is a padding token
-      const int64_t page = ((slot >> 4) * p.hkv + h) * P::kBytes;
+      uint8_t* page = cache + ((slot >> 4) * p.hkv + h) * P::kBytes;
       const int row = static_cast<int>(slot & 15);
-      const int64_t code = page + row * P::kRow + c * 8, sc = page + P::kScaleOff + row * P::kScales + c;
-      uint32_t bk, bv;
-      *reinterpret_cast<uint2*>(p.kc + code) = quantize_block(k[0], k[1], sk, dk, bk);
-      *reinterpret_cast<uint2*>(p.vc + code) = quantize_block(v[0], v[1], sv, dv, bv);
-      p.kc[sc] = static_cast<uint8_t>(bk);
-      p.vc[sc] = static_cast<uint8_t>(bv);
+      uint32_t sb;
+      *reinterpret_cast<uint2*>(page + row * P::kRow + c * 8) = quantize_block(x[0], x[1], s, six, sb);
+      page[P::kScaleOff + row * P::kScales + c] = static_cast<uint8_t>(sb);
     }
     if (tn >= p.num_tokens) break;
     t = tn;
-    k[0] = kn[0];
-    k[1] = kn[1];
-    v[0] = vn[0];
-    v[1] = vn[1];
+    x[0] = xn[0];
+    x[1] = xn[1];
     slot = sn;
   }
 }
@@ -181,13 +186,13 @@ struct ReadParams {
   uint16_t* vo;
   int64_t out_stride;
   uint32_t* status;
+  int warp_rows;  // output rows that a warp takes
 };
 
 // 16 values of one block: (code * block scale) exact in f16 and binary32, one
 // binary32 product with s, then bf16.
-KVQ_DEVI void read_block(const uint8_t* cache, int64_t code, int64_t sc, float s, uint16_t* dst) {
-  const uint2 w = __ldg(reinterpret_cast<const uint2*>(cache + code));
-  const float sb = e4m3_to_f32(__ldg(cache + sc));
+KVQ_DEVI void read_block(uint2 w, uint32_t sb8, float s, uint16_t* dst) {
+  const float sb = e4m3_to_f32(sb8);
   uint32_t o[8];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -203,53 +208,83 @@ KVQ_DEVI void read_block(const uint8_t* cache, int64_t code, int64_t sc, float s
   __stcs(d + 1, make_uint4(o[4], o[5], o[6], o[7]));
 }
 
+// A warp takes p.warp_rows output rows at a time: a lane looks up one row's
+// sequence and page, then the lanes go through the rows' blocks in order, so
+// that the stores run on and kReadDeep blocks of K and of V are in flight a lane.
+constexpr int kReadDeep = 4;
+constexpr int kMaxReadRows = 8;
+
 template <int DH>
 __global__ void __launch_bounds__(256) read_kernel(const ReadParams p) {
   using P = Page<DH>;
   constexpr int CH = DH / 16;
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
   pdl_allow_next();
   pdl_wait();
-  const int row_units = p.hkv * CH;
-  const int64_t gtid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int rem = static_cast<int>(gtid % row_units);
-  const int h = rem / CH, c = rem % CH;
-  const int64_t tstride = static_cast<int64_t>(gridDim.x) * blockDim.x / row_units;
+  const int lane = threadIdx.x & 31;
+  const int units = p.hkv * CH;  // blocks of a row
   const int64_t rows = min(p.num_rows, static_cast<int64_t>(__ldg(p.cu + p.num_seqs)));
-  const float sk = __ldg(p.ks + (p.per_head ? h : 0)), sv = __ldg(p.vs + (p.per_head ? h : 0));
-  for (int64_t r = gtid / row_units; r < rows; r += tstride) {
-    int lo = 0, hi = p.num_seqs - 1;  // last b with cu[b] <= r
+  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5)) * p.warp_rows;
+  if (r0 < rows) {
+    const int n = static_cast<int>(min(static_cast<int64_t>(p.warp_rows), rows - r0));
+    // the first row's sequence, the last b with cu[b] <= r0, by all lanes: 32 probes a step
+    int lo = 0, hi = p.num_seqs - 1;
     while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (__ldg(p.cu + mid) <= r)
-        lo = mid;
-      else
-        hi = mid - 1;
+      const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
+      const int below = __popc(__ballot_sync(kAll, at <= hi && __ldg(p.cu + at) <= r0));
+      lo += below * step;
+      hi = min(hi, lo + step - 1);
     }
-    const int64_t pos = r - __ldg(p.cu + lo) + (p.starts ? __ldg(p.starts + lo) : 0);
-    int64_t blk = -1;
-    if (pos < 0 || pos >= static_cast<int64_t>(p.max_blocks) * kTok) {
-      if (rem == 0) flag_status(p.status, KVQ_DEV_BAD_SEQLEN);
-    } else {
-      blk = __ldg(p.block_tables + static_cast<int64_t>(lo) * p.max_blocks + pos / kTok);
-      if (blk < 0 || blk >= p.num_blocks) {
-        if (rem == 0) flag_status(p.status, KVQ_DEV_BAD_BLOCK);
-        blk = -1;
+    int my_blk = -1, my_tok = 0;
+    if (lane < n) {
+      const int64_t r = r0 + lane;
+      while (lo < p.num_seqs - 1 && __ldg(p.cu + lo + 1) <= r) ++lo;
+      const int64_t pos = r - __ldg(p.cu + lo) + (p.starts ? __ldg(p.starts + lo) : 0);
+      if (pos < 0 || pos >= static_cast<int64_t>(p.max_blocks) * kTok) {
+        flag_status(p.status, KVQ_DEV_BAD_SEQLEN);
+      } else {
+        my_tok = static_cast<int>(pos % kTok);
+        my_blk = __ldg(p.block_tables + static_cast<int64_t>(lo) * p.max_blocks + pos / kTok);
+        if (my_blk < 0 || my_blk >= p.num_blocks) {
+          flag_status(p.status, KVQ_DEV_BAD_BLOCK);
+          my_blk = -1;
+        }
       }
     }
-    const int64_t dst = r * p.out_stride + rem * 16;
-    if (blk < 0) {
-      const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-      uint4* kd = reinterpret_cast<uint4*>(p.ko + dst);
-      uint4* vd = reinterpret_cast<uint4*>(p.vo + dst);
-      kd[0] = kd[1] = z;
-      vd[0] = vd[1] = z;
-      continue;
+    __syncwarp();
+    const int total = n * units;
+    for (int i0 = 0; i0 < total; i0 += 32 * kReadDeep) {
+      uint2 wk[kReadDeep], wv[kReadDeep];
+      uint32_t sk[kReadDeep], sv[kReadDeep];
+      int row[kReadDeep], rem[kReadDeep];
+#pragma unroll
+      for (int y = 0; y < kReadDeep; ++y) {
+        const int i = i0 + 32 * y + lane;
+        row[y] = i < total ? i / units : -1;
+        rem[y] = i - row[y] * units;
+        const int from = row[y] < 0 ? 0 : row[y];
+        const int blk = __shfl_sync(kAll, my_blk, from), tok = __shfl_sync(kAll, my_tok, from);
+        wk[y] = wv[y] = make_uint2(0u, 0u);
+        sk[y] = sv[y] = 0u;
+        if (row[y] >= 0 && blk >= 0) {
+          const int h = rem[y] / CH, c = rem[y] % CH;
+          const int64_t page = (static_cast<int64_t>(blk) * p.hkv + h) * P::kBytes;
+          const int64_t code = page + tok * P::kRow + c * 8, sc = page + P::kScaleOff + tok * P::kScales + c;
+          wk[y] = __ldg(reinterpret_cast<const uint2*>(p.kc + code));
+          wv[y] = __ldg(reinterpret_cast<const uint2*>(p.vc + code));
+          sk[y] = __ldg(p.kc + sc);
+          sv[y] = __ldg(p.vc + sc);
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < kReadDeep; ++y) {
+        if (row[y] < 0) continue;
+        const int h = p.per_head ? rem[y] / CH : 0;
+        const int64_t dst = (r0 + row[y]) * p.out_stride + rem[y] * 16;
+        read_block(wk[y], sk[y], __ldg(p.ks + h), p.ko + dst);
+        read_block(wv[y], sv[y], __ldg(p.vs + h), p.vo + dst);
+      }
     }
-    const int row = static_cast<int>(pos % kTok);
-    const int64_t page = (blk * p.hkv + h) * P::kBytes;
-    const int64_t code = page + row * P::kRow + c * 8, sc = page + P::kScaleOff + row * P::kScales + c;
-    read_block(p.kc, code, sc, sk, p.ko + dst);
-    read_block(p.vc, code, sc, sv, p.vo + dst);
   }
 }
 
@@ -296,11 +331,11 @@ extern "C" int kvq_fp4_write(const void* k, const void* v, int64_t token_stride,
   p.per_head = scale_granularity == KVQ_SCALE_PER_HEAD;
   p.status = dev_status;
   int grid = 0, block = 0;
-  token_row_shape(num_tokens, num_kv_heads * (head_dim / 16), 3, grid, block);
+  token_row_shape(num_tokens, num_kv_heads * (head_dim / 16), fp4::kWriteCtas, grid, block);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = head_dim == 128
-                            ? launch_pdl(fp4::write_kernel<128>, dim3(grid), dim3(block), 0, s, p)
-                            : launch_pdl(fp4::write_kernel<64>, dim3(grid), dim3(block), 0, s, p);
+                            ? launch_pdl(fp4::write_kernel<128>, dim3(grid, 2), dim3(block), 0, s, p)
+                            : launch_pdl(fp4::write_kernel<64>, dim3(grid, 2), dim3(block), 0, s, p);
   if (e != cudaSuccess) return KVQ_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
@@ -351,8 +386,15 @@ extern "C" int kvq_fp4_read(const void* k_cache, const void* v_cache, int64_t nu
   p.vo = static_cast<uint16_t*>(v_out);
   p.out_stride = out_stride;
   p.status = dev_status;
-  int grid = 0, block = 0;
-  token_row_shape(num_rows, num_kv_heads * (head_dim / 16), 8, grid, block);
+  // Rows of a warp, for rows of 64 blocks (more of them where a row has fewer).  Few rows go one
+  // to a warp, for the shortest chain of loads (32 rows: 4.3 us, two a warp 5.1); 2049 rows take
+  // 5.1 us two to a warp and 5.7 one; 262144 take 165 us at four, 172 at two, 187 at one.
+  const int units = num_kv_heads * (head_dim / 16);
+  const int base = num_rows < 1024 ? 1 : (num_rows < 65536 ? 2 : 4);
+  p.warp_rows = std::min(fp4::kMaxReadRows, base * std::max(1, 64 / units));
+  const int64_t need = (num_rows + 8 * p.warp_rows - 1) / (8 * p.warp_rows);
+  if (need > 0x7FFFFFFF) return KVQ_ERR_UNSUPPORTED;
+  const int grid = static_cast<int>(need), block = 256;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = head_dim == 128
                             ? launch_pdl(fp4::read_kernel<128>, dim3(grid), dim3(block), 0, s, p)
