@@ -6,16 +6,12 @@
 namespace kvq {
 namespace fp4 {
 
-// Segments of at most this many pages, each with an SM to itself, go whole to
-// one CTA.
-#ifndef KVQ_FP4_SEG
-#define KVQ_FP4_SEG 128
-#endif
-constexpr int kSegPages = KVQ_FP4_SEG;
+// Segments of at most this many pages, with an SM each, go whole to one CTA.
+constexpr int kSegPages = 128;
 constexpr int kMaxSmem = 227 * 1024 - 1024;  // the static part and the system's
 
 template <int DH>
-static int launch_decode(DecParams p, bool seg, int grid, cudaStream_t s) {
+static int launch_decode(DecParams p, bool fix, int grid, cudaStream_t s) {
   static DeviceOnce once;
   if (!once.run(current_device(), [] {
         auto configure = [](auto kernel) {
@@ -27,11 +23,14 @@ static int launch_decode(DecParams p, bool seg, int grid, cudaStream_t s) {
         return configure(decode_kernel<DH, true>) && configure(decode_kernel<DH, false>);
       }))
     return KVQ_ERR_CUDA;
-  p.S = kMaxStages;
-  while (p.S > 2 && dec_smem<DH>(p.S, p.G, p.B, seg).total > kMaxSmem / kDecCtas) --p.S;
-  const size_t smem = dec_smem<DH>(p.S, p.G, p.B, seg).total;
+  const int rings = kDecWarps / p.HG;
+  const int fixed = dec_smem<DH>(0, p.HG, p.G, p.B, fix).total + 32;  // (all but the slots, and their rounding)
+  const int slot = 2 * p.HG * Page<DH>::kBytes + 24;
+  p.depth = std::min(kMaxDepth, (kMaxSmem / kDecCtas - fixed) / slot / rings);
+  if (p.depth < KVQ_FP4_NP) return KVQ_ERR_UNSUPPORTED;  // (a step holds so many slots; not reached)
+  const size_t smem = dec_smem<DH>(p.depth * rings, p.HG, p.G, p.B, fix).total;
   const cudaError_t e =
-      seg ? launch_pdl(decode_kernel<DH, true>, dim3(grid), dim3(kDecThreads), smem, s, p)
+      fix ? launch_pdl(decode_kernel<DH, true>, dim3(grid), dim3(kDecThreads), smem, s, p)
           : launch_pdl(decode_kernel<DH, false>, dim3(grid), dim3(kDecThreads), smem, s, p);
   if (e != cudaSuccess) return KVQ_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
@@ -83,9 +82,30 @@ extern "C" int kvq_fp4_decode_attn(const void* q, const void* k_cache, const voi
   if (sliding_window > 0)
     pages = std::min<int64_t>(pages, (static_cast<int64_t>(sliding_window) + fp4::kTok - 1) / fp4::kTok + 1 +
                                          (static_cast<int64_t>(num_sinks) + fp4::kTok - 1) / fp4::kTok);
+  // One sequence, or short ones with an SM for each KV head: a number of CTAs for each, one head
+  // a unit.  Else the units are split at equal cost, with as many heads a unit as leave a segment
+  // ten pieces or fewer.
   const int segs = num_seqs * num_kv_heads;
-  const bool seg = segs <= P && pages <= fp4::kSegPages;
-  const int64_t ctas = seg ? segs : (segs * pages + fp4::kDecWarps - 1) / fp4::kDecWarps;
+  const bool fix = segs <= P && (num_seqs == 1 || pages <= fp4::kSegPages);
+  int HG = 1, cps = 1;
+#ifdef X_HG
+  HG = fix ? 1 : X_HG;
+#endif
+  if (fix) {
+    if (num_seqs == 1)
+      cps = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(P / segs, pages / fp4::kMinUnits)));
+  } else if (HG == 1) {
+#ifndef X_HG
+    for (int h = fp4::kMaxHeads; h > 1; h /= 2)
+      if (num_kv_heads % h == 0 && segs / h * 10 >= P) {
+        HG = h;
+        break;
+      }
+#endif
+  }
+  const int64_t units = static_cast<int64_t>(segs / HG) * pages;
+  const int64_t ctas = fix ? static_cast<int64_t>(segs) * cps
+                           : std::min<int64_t>(P, (units * HG + fp4::kDecWarps - 1) / fp4::kDecWarps);
 
   fp4::DecParams p;
   p.q = static_cast<const uint16_t*>(q);
@@ -105,16 +125,19 @@ extern "C" int kvq_fp4_decode_attn(const void* q, const void* k_cache, const voi
   p.vs = v_scale;
   p.per_head = scale_granularity == KVQ_SCALE_PER_HEAD;
   p.logit_scale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(head_dim)));
+  p.HG = HG;
+  p.NG = num_kv_heads / HG;
   p.P = P;
-  p.S = 0;
+  p.cps = cps;
+  p.depth = 0;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.ws_cnt = reinterpret_cast<uint32_t*>(ws);
   p.ws_ml = reinterpret_cast<float2*>(ws + wl.ml);
   p.ws_o = reinterpret_cast<float*>(ws + wl.o);
   p.out = static_cast<uint16_t*>(out);
   p.status = dev_status;
-  const int grid = static_cast<int>(std::min<int64_t>(ctas, seg ? ctas : P));
+  const int grid = static_cast<int>(ctas);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return head_dim == 128 ? fp4::launch_decode<128>(p, seg, grid, s)
-                         : fp4::launch_decode<64>(p, seg, grid, s);
+  return head_dim == 128 ? fp4::launch_decode<128>(p, fix, grid, s)
+                         : fp4::launch_decode<64>(p, fix, grid, s);
 }

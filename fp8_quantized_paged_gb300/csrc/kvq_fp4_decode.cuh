@@ -5,23 +5,25 @@
 // sK goes into the logits' scale and sV to the normalised output; the inner
 // loop works on code * block scale, which is exact in f16.
 //
-// A unit of work is one KV head's page: 16 tokens of K and of V, 2304 (1152)
-// bytes.  The units of all (sequence, KV head) segments, in order, are cut
-// into one contiguous run per CTA, of equal cost (kvq_decode.cuh: CostSplit,
-// a segment costing kPc pages beside its own); a segment cut over CTAs leaves
-// partial states (m, l, o) in the workspace, and the CTA that completes it
-// merges them.  Where the host can tell that every segment is short and each
-// has an SM to itself, a CTA takes one whole segment, with no plan to build
-// and nothing to merge (SEG).
+// A unit of work is the page of HG neighbouring KV heads: 16 tokens of K and of
+// V, HG * 1152 (576) contiguous bytes each.  The units of all (sequence, HG
+// heads) segments, in order, are cut into one contiguous run per CTA, of equal
+// cost (kvq_decode.cuh: CostSplit, a segment costing kPc units beside its own);
+// a segment cut over CTAs leaves partial states (m, l, o) in the workspace, and
+// the CTA that completes it merges them.  Where every segment is as long as the
+// others (one sequence) or short, the host gives each a number of CTAs of its
+// own and there is no plan to build (FIX).
 //
-// A CTA's run is cut once more into one contiguous run per warp, and each warp
-// goes through its own: its lanes copy the warp's next pages (codes and scales
-// of K, then of V: one bulk copy each) into the warp's own ring of shared
-// memory, and it works through them two at a time, with no barrier between
-// warps before the end.  A segment that lies whole in a warp's run is written
-// by that warp; the others' states (a warp has at most two: of the segment
-// that its run begins in and of the one that it ends in) are merged after one
-// barrier.
+// Consumer warp w of a CTA's 16 works on head w % HG of every (16 / HG)th unit
+// from w / HG on.  The HG warps of a unit share a ring of shared memory, which a
+// producer warp fills (one bulk copy for the heads' K, one for their V) as they
+// let go of its slots; there is no other barrier before a segment ends.  Then the
+// 16 / HG warps of a head merge their states.  HG trades the two ends: eight heads
+// a unit make few, long copies and states that two warps share; one head makes the
+// fewest pieces per segment where few sequences are cut over many CTAs.
+// The producer has a warpgroup of its own and leaves its registers to the
+// consumers (setmaxnreg: 640 threads launch with 96 each; the loop needs 112).
+//
 // Per page, 16 tokens against the group's G <= 8 query heads:
 //   S = K^ Q^T  m16n8k16 f16 matrix steps: lane (g, t) converts the codes of
 //               token rows g and g + 8, dims t dh/4 .. (t + 1) dh/4, and
@@ -35,6 +37,8 @@
 //               matrix step wants
 #pragma once
 
+#include <type_traits>
+
 #include "kvq_decode.cuh"
 #include "kvq_fp4.cuh"
 
@@ -42,22 +46,25 @@ namespace kvq {
 namespace fp4 {
 
 #ifndef KVQ_FP4_WARPS
-#define KVQ_FP4_WARPS 16
+#define KVQ_FP4_WARPS 8
 #endif
 #ifndef KVQ_FP4_CTAS
 #define KVQ_FP4_CTAS 1
 #endif
 #ifndef KVQ_FP4_NP
-#define KVQ_FP4_NP 2
+#define KVQ_FP4_NP 4
 #endif
 #ifndef KVQ_FP4_PC
 #define KVQ_FP4_PC 16
 #endif
 constexpr int kDecWarps = KVQ_FP4_WARPS;
-constexpr int kDecThreads = kDecWarps * 32;
+constexpr int kDecThreads = kDecWarps * 32 + 128;  // consumers, the producer's warpgroup
+constexpr int kConsumerRegs = 224, kProducerRegs = 40;  // 256 x 224 + 128 x 40 <= 384 x 168
 constexpr int kDecCtas = KVQ_FP4_CTAS;  // CTAs per SM
 constexpr int kPc = KVQ_FP4_PC;         // fixed cost of a piece, in pages
-constexpr int kMaxStages = 8;
+constexpr int kMaxHeads = 8;            // most KV heads of a unit
+constexpr int kMaxDepth = 12;           // most slots of a ring
+constexpr int kMinUnits = 32;           // least units of a CTA that shares a segment: two a warp
 constexpr float kPBias = 7.f;           // log2 of the factor that the weights carry
 
 struct DecParams {
@@ -73,8 +80,10 @@ struct DecParams {
   const float* vs;
   int per_head;
   float logit_scale;  // log2(e) / sqrt(dh)
+  int HG, NG;         // KV heads of a unit, and units side by side (Hkv / HG)
   int P;              // CTAs that share the units
-  int S;              // ring stages of a warp
+  int cps;            // FIX: CTAs of a segment
+  int depth;          // slots of a ring
   uint32_t* ws_cnt;   // [B * Hkv] arrivals (zero between calls)
   float2* ws_ml;      // [slots][G]
   float* ws_o;        // [slots][G][DH]
@@ -83,13 +92,14 @@ struct DecParams {
 };
 
 // Workspace: kvq_decode_attn's table of arrival counters, then per partial
-// slot the (m, l) and o of a group's heads.  The piece of segment sigma =
-// b Hkv + g that CTA c holds has slot c + sigma (CTA ranges are ordered).
+// slot the (m, l) and o of one KV head's query heads.  CTA c's piece of segment
+// s = b NG + (group of heads) has slots (c + s) HG .. + HG - 1, one a head: unique,
+// as the CTAs' runs are ordered (FIX: c HG .. + HG - 1).
 struct DecWs {
   size_t ml, o, total;
 };
 inline DecWs dec_ws(int B, int G, int Hkv, int DH, int P) {
-  const size_t slots = static_cast<size_t>(P) + static_cast<size_t>(B) * Hkv;
+  const size_t slots = static_cast<size_t>(P) * kMaxHeads + static_cast<size_t>(B) * Hkv;
   DecWs w;
   w.ml = KVQ_WS_COUNTER_BYTES;
   w.o = w.ml + round256(slots * G * sizeof(float2));
@@ -97,24 +107,24 @@ inline DecWs dec_ws(int B, int G, int Hkv, int DH, int P) {
   return w;
 }
 
-// Dynamic shared memory (byte offsets).
+// Dynamic shared memory (byte offsets); S: slots of all rings.
 struct DecSmem {
   int bars, bad, ml, o, plan, total;
 };
 template <int DH>
-__host__ __device__ inline DecSmem dec_smem(int S, int G, int B, bool seg) {
+__host__ __device__ inline DecSmem dec_smem(int S, int HG, int G, int B, bool fix) {
   DecSmem s;
-  s.bars = kDecWarps * S * 2 * Page<DH>::kBytes;  // the rings are at 0
-  s.bad = s.bars + kDecWarps * S * 8;
-  s.ml = (s.bad + kDecWarps * S * 4 + 15) & ~15;  // [warps][2][G] (m, l) of a warp's first and last piece
-  s.o = s.ml + kDecWarps * 2 * G * 8;             // [warps][G][DH] o of the first; the last's is in the ring
+  s.bars = S * 2 * HG * Page<DH>::kBytes;  // the ring is at 0; full[S], empty[S]
+  s.bad = s.bars + 2 * S * 8;
+  s.ml = (s.bad + 2 * S * 4 + 15) & ~15;   // (bad[S], last[S]); [warps][G] (m, l)
+  s.o = s.ml + kDecWarps * G * 8;          // [warps][G][DH] o
   s.plan = s.o + kDecWarps * G * DH * 4;
-  s.total = s.plan + (seg ? 0 : (3 * B + 2) * 4);
+  s.total = s.plan + (fix ? 0 : (3 * B + 2) * 4);
   return s;
 }
 
 // The pages' and costs' exclusive prefix sums over the sequences, in units of
-// (sequence, all KV heads): off[0 .. B], voff[0 .. B], and the checked lengths.
+// (sequence, all its segments): off[0 .. B], voff[0 .. B], and the checked lengths.
 KVQ_DEVI void dec_plan(const DecParams& p, int32_t* off, int32_t* len, int32_t* voff,
                        uint64_t* warp_tot) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -140,20 +150,21 @@ KVQ_DEVI void dec_plan(const DecParams& p, int32_t* off, int32_t* len, int32_t* 
   }
   if (lane == 31) warp_tot[warp] = incl;
   __syncthreads();
-  uint64_t base = 0;
-  for (int w = 0; w < warp; ++w) base += warp_tot[w];
+  uint64_t base = lane < warp ? warp_tot[lane] : 0;  // (at most 32 warps)
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) base += __shfl_xor_sync(kFull, base, d);
   uint64_t at = base + incl - local;
   for (int b = b0; b < b1; ++b) {
     const int n = off[b];
-    const int pages = static_cast<int>(at & 0xFFFFFFFFu) * p.Hkv;
+    const int pages = static_cast<int>(at & 0xFFFFFFFFu) * p.NG;
     off[b] = pages;
-    voff[b] = pages + static_cast<int>(at >> 32) * p.Hkv * kPc;
+    voff[b] = pages + static_cast<int>(at >> 32) * p.NG * kPc;
     at += (static_cast<uint64_t>(n > 0) << 32) + static_cast<uint32_t>(n);
   }
   if (tid == kDecThreads - 1) {
-    const int pages = static_cast<int>(at & 0xFFFFFFFFu) * p.Hkv;
+    const int pages = static_cast<int>(at & 0xFFFFFFFFu) * p.NG;
     off[p.B] = pages;
-    voff[p.B] = pages + static_cast<int>(at >> 32) * p.Hkv * kPc;
+    voff[p.B] = pages + static_cast<int>(at >> 32) * p.NG * kPc;
   }
   __syncthreads();
 }
@@ -174,9 +185,9 @@ struct Running {
 };
 
 // NP staged pages of one warp: dot products, online softmax, weighted sum.
-//   page[i]: K page, V page behind it; tok0[i]: first token; skip[i]: masked out
+//   kpage[i], vpage[i]: the head's pages; tok0[i]: first token; skip[i]: masked out
 template <int DH, int NP>
-KVQ_DEVI void dec_pages(const uint8_t* const (&page)[NP], const int (&tok0)[NP], const bool (&skip)[NP],
+KVQ_DEVI void dec_pages(const uint8_t* const (&kpage)[NP], const uint8_t* const (&vpage)[NP], const int (&tok0)[NP], const bool (&skip)[NP],
                         const PieceView& pv, int g, int t, const uint32_t (&qb)[DH / 16][2],
                         float (&o)[DH / 16][4], Running& st) {
   using P = Page<DH>;
@@ -186,7 +197,7 @@ KVQ_DEVI void dec_pages(const uint8_t* const (&page)[NP], const int (&tok0)[NP],
   float x[NP][4];
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
-    const uint8_t* kp = page[i];
+    const uint8_t* kp = kpage[i];
     uint32_t k0[KW], k1[KW], sc0[2], sc1[2];  // codes, block scales (in both halves) of rows g, g + 8
     if (DH == 128) {
       const uint4 a = *reinterpret_cast<const uint4*>(kp + g * P::kRow + t * 16);
@@ -230,7 +241,7 @@ KVQ_DEVI void dec_pages(const uint8_t* const (&page)[NP], const int (&tok0)[NP],
   uint32_t v[NP][4][VW], vs[NP][2];
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
-    const uint8_t* vp = page[i] + P::kBytes;
+    const uint8_t* vp = vpage[i];
     uint32_t s4[4];
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
@@ -331,188 +342,252 @@ KVQ_DEVI void dec_pages(const uint8_t* const (&page)[NP], const int (&tok0)[NP],
   }
 }
 
-// A segment that warps share, or CTAs: units [a, z) of it in this CTA.
-struct Shared {
-  int b, gkv, first, pages;  // first unit of the whole segment, its pages
-  int wa, wz;                // first and last warp that hold some of it
-  int np, c_lo;              // pieces over CTAs (1: all of it is here), the first one's CTA
+// Sums of states j = 0 .. n - 1 (m, l, four dims of o) for E outputs, U states at a time
+// with their loads together: l and o scaled by 2^(m - M), M the largest m.  A state with
+// m of -inf has l and o of 0, or NaN.
+struct State {
+  float m, l;
+  float4 o;
 };
-
-template <int DH, bool SEG>
-__global__ void __launch_bounds__(kDecThreads, kDecCtas) decode_kernel(const __grid_constant__ DecParams p) {
-  using PG = Page<DH>;
-  constexpr int MT = DH / 16;
-  constexpr int kSlot = 2 * PG::kBytes;
-  constexpr int kNP = KVQ_FP4_NP;  // pages of a step
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t warp_tot[kDecWarps];
-  __shared__ int32_t bounds[2];
-  __shared__ Shared list[kDecWarps + 1];
-  __shared__ int list_n;
-  __shared__ int32_t wstart[kDecWarps + 1];  // first unit of each warp's run
-  __shared__ uint32_t merge_s[kDecWarps + 1];
-  const DecSmem sm = dec_smem<DH>(p.S, p.G, p.B, SEG);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, t = lane & 3;
-  uint8_t* ring = smem + warp * p.S * kSlot;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + sm.bars) + warp * p.S;
-  uint32_t* bad_s = reinterpret_cast<uint32_t*>(smem + sm.bad) + warp * p.S;
-  float2* cml = reinterpret_cast<float2*>(smem + sm.ml);
-  float* co = reinterpret_cast<float*>(smem + sm.o);
-  int32_t* off = reinterpret_cast<int32_t*>(smem + sm.plan);  // [B + 1]
-  int32_t* len = off + p.B + 1;                               // [B]
-  int32_t* voff = len + p.B;                                  // [B + 1]
-
-  if (lane < p.S) mbar_init(&full[lane], 1);
-  if (tid == 0) list_n = 0;
-  fence_mbar_init();
-  __syncwarp();
-  pdl_wait();
-  pdl_allow_next();
-
-  const int c = blockIdx.x;
-  int u0 = 0, u1 = 0, seg_b = 0, seg_g = 0, seg_len = 0;
-  int V = 0, Pe = 1;
-  if (SEG) {
-    seg_b = c / p.Hkv;
-    seg_g = c - seg_b * p.Hkv;
-    seg_len = __ldg(p.seq_lens + seg_b);
-    if (seg_len < 0 || seg_len > p.max_blocks * kTok) {
-      if (seg_g == 0 && tid == 0) flag_status(p.status, KVQ_DEV_BAD_SEQLEN);
-      seg_len = 0;
-    }
-    u1 = visible(p.window, p.sinks, seg_len).count;
-    if (u1 == 0) {  // nothing to attend to
-      uint16_t* o = p.out + (static_cast<int64_t>(seg_b) * p.Hq + seg_g * p.G) * DH;
-      for (int i = tid; i < p.G * DH; i += kDecThreads) o[i] = 0;
-      return;
-    }
-  } else {
-    dec_plan(p, off, len, voff, warp_tot);
-    for (int b = c; b < p.B; b += gridDim.x) {  // sequences with nothing to attend to
-      if (off[b + 1] != off[b]) continue;
-      uint16_t* o = p.out + static_cast<int64_t>(b) * p.Hq * DH;
-      for (int i = tid; i < p.Hq * DH; i += kDecThreads) o[i] = 0;
-    }
-    const int W = off[p.B];
-    V = voff[p.B];
-    // a CTA has a step for every warp at least
-    Pe = min(p.P, (W + kDecWarps - 1) / kDecWarps);
-    const CostSplit split(V, Pe);
-    if ((tid == 0 || tid == 32) && c < Pe)
-      bounds[tid >> 5] = pages_before(off, voff, p.B, p.Hkv, split(c + (tid >> 5)), kPc);
-    __syncthreads();
-    if (c < Pe) {
-      u0 = bounds[0];
-      u1 = bounds[1];
+template <int E, int U, typename Load>
+KVQ_DEVI void merge_states(int n, State (&a)[E], const Load& load) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) a[e] = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int j = 0; j < n; j += U) {
+    State x[E][U];
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int y = 0; y < U; ++y) {
+        x[e][y] = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        if (j + y < n) load(j + y, e, x[e][y]);
+      }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      float m = a[e].m;
+#pragma unroll
+      for (int y = 0; y < U; ++y) m = fmaxf(m, x[e][y].m);
+      const float r = a[e].m == -INFINITY ? 1.f : fast_exp2(a[e].m - m);
+      a[e].l *= r;
+      a[e].o.x *= r;
+      a[e].o.y *= r;
+      a[e].o.z *= r;
+      a[e].o.w *= r;
+      a[e].m = m;
+#pragma unroll
+      for (int y = 0; y < U; ++y) {
+        const float w = x[e][y].m == -INFINITY ? 1.f : fast_exp2(x[e][y].m - m);
+        a[e].l += x[e][y].l * w;
+        a[e].o.x += x[e][y].o.x * w;
+        a[e].o.y += x[e][y].o.y * w;
+        a[e].o.z += x[e][y].o.z * w;
+        a[e].o.w += x[e][y].o.w * w;
+      }
     }
   }
+}
 
-  // ---- this warp's run of pages [w0, w1)
+KVQ_DEVI void store_out(uint16_t* dst, const State& a, float sv) {
+  const float f = a.l > 0.f ? sv / a.l : 0.f;
+  *reinterpret_cast<uint2*>(dst) =
+      make_uint2(f32x2_to_bf16x2(a.o.x * f, a.o.y * f), f32x2_to_bf16x2(a.o.z * f, a.o.w * f));
+}
+
+KVQ_DEVI void head_barrier(int head, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(head + 1), "r"(threads) : "memory");
+}
+
+// The producer: copies the CTA's units into the rings.  Unit i of the run belongs to
+// ring i % (16 / HG), as its unit k = i / (16 / HG), in slot k % depth.  Lane j takes
+// units j, j + 32, ..., each as soon as its slot is free, the block ids looked up 32
+// units ahead.  A lane looks at its slot's phase only once the unit that the slot held
+// last has been copied (all units below the first pending one have): the phase before
+// is then complete, and the parity cannot stand for one two back.
+template <int DH, typename Segment>
+KVQ_DEVI void decode_copies(const DecParams& p, uint8_t* smem, uint64_t* full, uint64_t* empty, volatile uint32_t* bad_s,
+                            volatile int32_t* last_s, volatile uint32_t* abort_flag, int u0, int u1,
+                            const Segment& segment) {
+  const int lane = threadIdx.x & 31;
+  const int rings = kDecWarps / p.HG, S = rings * p.depth;
+  const int half = p.HG * Page<DH>::kBytes;
   const int total = u1 - u0;
-  auto run_start = [&](int w) { return u0 + static_cast<int>(static_cast<int64_t>(total) * w / kDecWarps); };
-  auto warp_of = [&](int u) {  // the warp whose run holds unit u
-    return static_cast<int>((static_cast<int64_t>(u - u0 + 1) * kDecWarps - 1) / total);
-  };
-  const int w0 = run_start(warp), w1 = run_start(warp + 1);
-  const int mine = w1 - w0;
-  if (lane < 2) wstart[warp + lane] = lane ? w1 : w0;  // (neighbours write the same)
-  // the (sequence, KV head) segment of unit u
-  auto segment = [&](int u, int& b, int& gkv, int& pages, int& p0, int& L) {
-    if (SEG) {
-      b = seg_b;
-      gkv = seg_g;
-      pages = total;
-      p0 = u;
-      L = seg_len;
-    } else {
-      b = find_seq(off, p.B, u);
-      pages = (off[b + 1] - off[b]) / p.Hkv;
-      gkv = (u - off[b]) / pages;
-      p0 = u - off[b] - gkv * pages;
-      L = len[b];
-    }
-  };
-  // lane j holds the block id (and KV head) of the warp's page 32 i + j, fetched 32 pages ahead
-  int blk_now = -1, head_now = 0, blk_next = -1, head_next = 0;
-  auto fetch = [&](int k, int& blk, int& head) {
+  auto fetch = [&](int i, int& blk, int& gr) {
     blk = -1;
-    head = 0;
-    if (k >= mine) return;
+    gr = 0;
+    if (i >= total) return;
     int b, pages, p0, L;
-    segment(w0 + k, b, head, pages, p0, L);
+    segment(u0 + i, b, gr, pages, p0, L);
     const Visible vis = visible(p.window, p.sinks, L);
     const int col = p0 < vis.sink ? p0 : vis.first + p0 - vis.sink;
     if (col >= 0 && col < p.max_blocks)
       blk = __ldg(p.block_tables + static_cast<int64_t>(b) * p.max_blocks + col);
   };
-  // The warp's next n pages into stages s, s + 1, ...: lanes 2i and 2i + 1 copy
-  // K and V of page i.
-  fetch(lane, blk_now, head_now);
-  fetch(32 + lane, blk_next, head_next);
-  int issued = 0;
-  auto issue = [&](int s, int n) {
-    const int k = issued + (lane >> 1);
-    const int ba = __shfl_sync(kFull, blk_now, k & 31), ha = __shfl_sync(kFull, head_now, k & 31);
-    int blk = ba, head = ha;
-    if (((issued + n - 1) ^ issued) & 32) {  // the last of them are of the next 32
-      const int bb = __shfl_sync(kFull, blk_next, k & 31), hb = __shfl_sync(kFull, head_next, k & 31);
-      if ((k ^ issued) & 32) {
-        blk = bb;
-        head = hb;
-      }
-    }
-    if (((issued + n) ^ issued) & 32) {
-      blk_now = blk_next;
-      head_now = head_next;
-      fetch(((issued + n) | 31) + 1 + lane, blk_next, head_next);
-    }
-    if (lane < 2 * n) {
-      int st = s + (lane >> 1);
-      if (st >= p.S) st -= p.S;
-      const bool bad = blk < 0 || blk >= p.num_blocks;
-      if (!(lane & 1)) {
-        bad_s[st] = bad;
+  int blk_next, gr_next;
+  fetch(lane, blk_next, gr_next);
+  uint32_t idle = 0;
+  for (int base = 0; base < total; base += 32) {
+    const int i = base + lane;
+    const int ring = i % rings, k = i / rings, s = ring * p.depth + k % p.depth, round = k / p.depth;
+    const int blk = blk_next, gr = gr_next;
+    fetch(i + 32, blk_next, gr_next);
+    bool pending = i < total;
+    while (true) {
+      const uint32_t left = __ballot_sync(kFull, pending);
+      if (left == 0) break;
+      bool moved = false;
+      if (pending && i - S < base + __ffs(left) - 1 &&
+          (round == 0 || mbar_test_wait(&empty[s], static_cast<uint32_t>((round - 1) & 1)))) {
+        const bool bad = blk < 0 || blk >= p.num_blocks;
+        bad_s[s] = bad;
         if (bad) {
           flag_status(p.status, KVQ_DEV_BAD_BLOCK);
-          mbar_arrive(&full[st]);
+          mbar_arrive(&full[s]);
         } else {
-          mbar_arrive_expect_tx(&full[st], kSlot);
+          const int64_t at = (static_cast<int64_t>(blk) * p.Hkv + gr * p.HG) * Page<DH>::kBytes;
+          uint8_t* dst = smem + s * 2 * half;
+          last_s[s] = k;
+          mbar_arrive_expect_tx(&full[s], 2 * half);
+          bulk_load(dst, p.kc + at, half, &full[s]);
+          bulk_load(dst + half, p.vc + at, half, &full[s]);
         }
+        pending = false;
+        moved = true;
       }
-      __syncwarp((1u << (2 * n)) - 1u);  // (n <= 8)
-      if (!bad)
-        bulk_load(ring + st * kSlot + (lane & 1) * PG::kBytes,
-                  ((lane & 1) ? p.vc : p.kc) + (static_cast<int64_t>(blk) * p.Hkv + head) * PG::kBytes,
-                  PG::kBytes, &full[st]);
+      if (__any_sync(kFull, moved)) {
+        idle = 0;
+      } else if (++idle > kMaxPolls || (((idle & 63u) == 0u) && __any_sync(kFull, *abort_flag != 0u))) {
+        if (lane == 0 && !*abort_flag) {
+          *abort_flag = 1u;
+          flag_status(p.status, KVQ_DEV_WAIT_TIMEOUT);
+        }
+        return;
+      }
     }
-    issued += n;
-  };
-  if (mine > 0) issue(0, min(p.S, mine));
+  }
+}
 
-  int done = 0, stage = 0;
-  uint32_t parity = 0;
+// The CTA's run, unit by unit (see the head of the file).
+template <int DH, bool FIX, typename Segment>
+KVQ_DEVI void decode_run(const DecParams& p, uint8_t* smem, const DecSmem& sm, uint64_t* full, uint64_t* empty,
+                         volatile uint32_t* bad_s, volatile uint32_t* abort_flag, uint32_t* merge_s,
+                         const int32_t* voff, int u0, int u1, int V, int Pe, int fix_np, const Segment& segment) {
+  using PG = Page<DH>;
+  constexpr int MT = DH / 16;
+  constexpr int kNP = KVQ_FP4_NP;  // units of a step
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int half = p.HG * PG::kBytes, slot_bytes = 2 * half;
+  const int g = lane >> 2, t = lane & 3;
+  const int wph = kDecWarps / p.HG;          // warps of a head
+  const int head = warp % p.HG, po = warp / p.HG;
+  const int hthreads = wph * 32, htid = po * 32 + lane;  // the head's threads
+  float2* cml = reinterpret_cast<float2*>(smem + sm.ml) + head * wph * p.G;      // [wph][G]
+  float* co = reinterpret_cast<float*>(smem + sm.o) + head * wph * p.G * DH;     // [wph][G][DH]
+  // the ring of this warp's group (the HG warps of unit w / HG)
+  uint8_t* ring = smem + po * p.depth * slot_bytes;
+  full += po * p.depth;
+  empty += po * p.depth;
+  bad_s += po * p.depth;
   bool dead = false;
-  for (int u = w0; u < w1;) {
-    // ---- a piece: the part of one segment inside the warp's run
-    int b, gkv, pages, p0;
+  auto timed_out = [&] {  // no more copies, the rest is skipped
+    dead = true;
+    if (lane == 0 && !*abort_flag) {
+      *abort_flag = 1u;
+      flag_status(p.status, KVQ_DEV_WAIT_TIMEOUT);
+    }
+  };
+  // The queries of the piece that begins at unit u: head g, dims t dh/4 .. (t + 1) dh/4.  They
+  // are asked for before the piece before is merged, the first ones before the first pages
+  // arrive (behind those 28 MB they took 3.8 us).
+  uint32_t raw[DH / 8];
+  auto load_q = [&](int u) {
+    int b, gr, pages, p0, L;
+    segment(u, b, gr, pages, p0, L);
+    const uint4* src = reinterpret_cast<const uint4*>(
+        p.q + (static_cast<int64_t>(b) * p.Hq + (gr * p.HG + head) * p.G + (g < p.G ? g : 0)) * DH + t * (DH / 4));
+#pragma unroll
+    for (int k = 0; k < DH / 32; ++k) {
+      const uint4 w = g < p.G ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
+      raw[4 * k] = w.x; raw[4 * k + 1] = w.y; raw[4 * k + 2] = w.z; raw[4 * k + 3] = w.w;
+    }
+  };
+  if (u0 < u1) load_q(u0);
+  // Merges a segment's np pieces (the first in partial slot `first`, the next HG slots on),
+  // by this head's warps: thread (y, e) takes pieces y, y + K, ... of output float4 e.
+  const int n4 = p.G * DH / 4;
+  auto merge_pieces = [&](int np, int64_t first, int sigma, uint16_t* orow, float sv) {
+    const int K = max(1, min(hthreads / n4, wph));  // [K][n4] fits co
+    const float2* ml = p.ws_ml + first * p.G;
+    const float4* ob = reinterpret_cast<const float4*>(p.ws_o) + first * n4;
+    auto piece = [&](int j, int e, State& v) {
+      const int64_t at = static_cast<int64_t>(j) * p.HG;
+      const float2 z = __ldcg(ml + at * p.G + 4 * e / DH);
+      v.m = z.x;
+      v.l = z.y;
+      v.o = __ldcg(ob + at * n4 + e);
+    };
+    if (K == 1) {  // four outputs of a thread together
+      for (int e0 = htid; e0 < n4; e0 += 4 * hthreads) {
+        State a[4];
+        merge_states<4, 4>(np, a, [&](int j, int y, State& v) { if (e0 + y * hthreads < n4) piece(j, e0 + y * hthreads, v); });
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if (e0 + y * hthreads < n4) store_out(orow + 4 * (e0 + y * hthreads), a[y], sv);
+      }
+      if (htid == 0) p.ws_cnt[sigma] = 0u;
+      return;
+    }
+    float4* part = reinterpret_cast<float4*>(co);
+    for (int x = htid; x < K * n4; x += hthreads) {
+      const int y0 = x / n4, e = x - y0 * n4;
+      State a[1];
+      merge_states<1, 8>((np - y0 + K - 1) / K, a, [&](int j, int, State& v) { piece(y0 + j * K, e, v); });
+      part[x] = a[0].o;
+      if (4 * e % DH == 0) cml[y0 * p.G + 4 * e / DH] = make_float2(a[0].m, a[0].l);
+    }
+    if (htid == 0) p.ws_cnt[sigma] = 0u;
+    head_barrier(head, hthreads);
+    for (int e = htid; e < n4; e += hthreads) {
+      State a[1];
+      merge_states<1, 4>(K, a, [&](int y, int, State& v) {
+        const float2 z = cml[y * p.G + 4 * e / DH];
+        v.m = z.x;
+        v.l = z.y;
+        v.o = part[y * n4 + e];
+      });
+      store_out(orow + 4 * e, a[0], sv);
+    }
+    head_barrier(head, hthreads);
+  };
+  // The run's first piece where others go on with its segment and this run goes on too: its
+  // arrival is looked at when the run ends (a CTA that ends with the segment mostly comes later).
+  int held_np = 0, held_c = 0, held_b = 0, held_gr = 0;
+  uint32_t held_count = 0;
+
+  int i = po;    // this warp's next unit of the run, its slot
+  int slot = 0;
+  uint32_t parity = 0;
+  for (int u = u0; u < u1;) {
+    // ---- a piece: the part of one segment inside the run
+    int b, gr, pages, p0;
     PieceView pv;
-    segment(u, b, gkv, pages, p0, pv.L);
+    segment(u, b, gr, pages, p0, pv.L);
     const Visible vis = visible(p.window, p.sinks, pv.L);
     pv.lo = vis.lo;
     pv.sinks = p.sinks;
-    const int n = min(w1 - u, pages - p0);
-    // the group's queries: head g, dims t dh/4 .. (t + 1) dh/4, scaled by a power of two to f16
+    const int n = min(u1 - u, pages - p0);
+    const int end = u - u0 + n;
+    const int gkv = gr * p.HG + head;
+    int np = FIX ? fix_np : 1, c_lo = FIX ? c / p.cps * p.cps : c;  // CTAs that hold the segment, the first
+    if (!FIX && n < pages) {
+      const CostSplit split(V, Pe);
+      const int v_first = voff[b] + gr * (pages + kPc) + kPc;
+      c_lo = split.cta_of(v_first);
+      np = split.cta_of(v_first + pages - 1) - c_lo + 1;
+    }
+    // the group's queries, scaled by a power of two to f16
+    const float sv = __ldg(p.vs + (p.per_head ? gkv : 0));
     uint32_t qb[MT][2];
     {
-      uint32_t raw[DH / 8];
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.q + (static_cast<int64_t>(b) * p.Hq + gkv * p.G + (g < p.G ? g : 0)) * DH + t * (DH / 4));
-#pragma unroll
-      for (int i = 0; i < DH / 32; ++i) {
-        const uint4 w = g < p.G ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-        raw[4 * i] = w.x; raw[4 * i + 1] = w.y; raw[4 * i + 2] = w.z; raw[4 * i + 3] = w.w;
-      }
       const float ls = __ldg(p.ks + (p.per_head ? gkv : 0)) * p.logit_scale;
       const int qa = q_fragments<KVQ_FMT_E4M3, DH>(raw, qb);
       // (kept above 0 where it would underflow, so that it times -inf stays -inf)
@@ -526,237 +601,214 @@ __global__ void __launch_bounds__(kDecThreads, kDecCtas) decode_kernel(const __g
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
 
-    for (int j = 0; j < n; j += kNP) {
-      const uint8_t* page[kNP];
-      int tok0[kNP];
-      bool skip[kNP];
-      const int first = stage, have = min(kNP, n - j);
+    auto step = [&](auto units) {
+      constexpr int NP = decltype(units)::value;
+      const uint8_t *kpage[NP], *vpage[NP];
+      int tok0[NP], slots[NP];
+      bool skip[NP];
 #pragma unroll
-      for (int i = 0; i < kNP; ++i) {
-        const int pg = p0 + j + i;
-        tok0[i] = (pg < vis.sink ? pg : vis.first + pg - vis.sink) * kTok;
-        page[i] = ring + stage * kSlot;
-        skip[i] = true;
-        if (i < have) {
-          if (!dead && !__all_sync(kFull, mbar_wait(&full[stage], parity))) {
-            dead = true;  // the wait ran out: no more copies, the rest is skipped
-            if (lane == 0) flag_status(p.status, KVQ_DEV_WAIT_TIMEOUT);
-          }
-          skip[i] = bad_s[stage] != 0;
-          if (++stage == p.S) {
-            stage = 0;
-            parity ^= 1u;
-          }
+      for (int k = 0; k < NP; ++k) {
+        const int pg = p0 + i + u0 - u;
+        tok0[k] = (pg < vis.sink ? pg : vis.first + pg - vis.sink) * kTok;
+        kpage[k] = ring + slot * slot_bytes + head * PG::kBytes;
+        vpage[k] = kpage[k] + half;
+        slots[k] = slot;
+        if (!dead && !__all_sync(kFull, wait_or_abort(&full[slot], parity, abort_flag))) timed_out();
+        skip[k] = bad_s[slot] != 0u;
+        i += wph;
+        if (++slot == p.depth) {
+          slot = 0;
+          parity ^= 1u;
         }
       }
       if (!dead) {
-        dec_pages<DH, kNP>(page, tok0, skip, pv, g, t, qb, o, st);
+        dec_pages<DH, NP>(kpage, vpage, tok0, skip, pv, g, t, qb, o, st);
         __syncwarp();
-        const int more = min(have, mine - issued);
-        if (more > 0) issue(first, more);
+        if (lane == 0) {
+#pragma unroll
+          for (int k = 0; k < NP; ++k) mbar_arrive(&empty[slots[k]]);
+        }
       }
-      if (!dead) done += have;
-    }
+    };
+    while (i + (kNP - 1) * wph < end) step(std::integral_constant<int, kNP>());
+    while (i < end) step(std::integral_constant<int, 1>());
+    if (u + n < u1) load_q(u + n);
 
+    // ---- the head's warps merge their states
 #pragma unroll
     for (int d = 4; d < 32; d <<= 1) {
       st.l[0] += __shfl_xor_sync(kFull, st.l[0], d);
       st.l[1] += __shfl_xor_sync(kFull, st.l[1], d);
     }
-    if (n == pages) {  // the whole segment: its output
-      const float sv = __ldg(p.vs + (p.per_head ? gkv : 0));
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int h = 2 * t + e;
-        if (h >= p.G) continue;
-        const float f = st.l[e] > 0.f ? sv / st.l[e] : 0.f;
-        uint4* dst = reinterpret_cast<uint4*>(
-            p.out + (static_cast<int64_t>(b) * p.Hq + gkv * p.G + h) * DH + g * (DH / 8));
+    for (int e = 0; e < 2; ++e) {
+      const int h = 2 * t + e;
+      if (h >= p.G) continue;
+      if (g == 0)  // m in log2 units
+        cml[po * p.G + h] = make_float2(st.m[e] == -INFINITY ? -INFINITY : st.m[e] * pv.ls[e], st.l[e]);
+      float* dst = co + (po * p.G + h) * DH + g * (DH / 8);
 #pragma unroll
-        for (int mt = 0; mt < MT; mt += 4)
-          dst[mt / 4] = make_uint4(f32x2_to_bf16x2(o[mt][e] * f, o[mt][2 + e] * f),
-                                   f32x2_to_bf16x2(o[mt + 1][e] * f, o[mt + 1][2 + e] * f),
-                                   f32x2_to_bf16x2(o[mt + 2][e] * f, o[mt + 2][2 + e] * f),
-                                   f32x2_to_bf16x2(o[mt + 3][e] * f, o[mt + 3][2 + e] * f));
+      for (int mt = 0; mt < MT; ++mt)
+        *reinterpret_cast<float2*>(dst + 2 * mt) = make_float2(o[mt][e], o[mt][2 + e]);
+    }
+    head_barrier(head, hthreads);
+    uint16_t* orow = p.out + (static_cast<int64_t>(b) * p.Hq + gkv * p.G) * DH;
+    const int sigma = b * p.Hkv + gkv;
+    const int64_t seg = FIX ? 0 : static_cast<int64_t>(b) * p.NG + gr;
+    const int64_t mine = (c + seg) * p.HG + head;  // partial slot
+    for (int e = htid; e < n4; e += hthreads) {  // a float4 of one query head's output
+      const int h = 4 * e / DH;
+      State a[1];
+      merge_states<1, 4>(wph, a, [&](int w, int, State& v) {
+        const float2 z = cml[w * p.G + h];
+        v.m = z.x;
+        v.l = z.y;
+        v.o = *reinterpret_cast<const float4*>(co + w * p.G * DH + 4 * e);
+      });
+      if (np == 1) {
+        store_out(orow + 4 * e, a[0], sv);
+      } else {
+        reinterpret_cast<float4*>(p.ws_o)[mine * n4 + e] = a[0].o;
+        if (4 * e % DH == 0) p.ws_ml[mine * p.G + h] = make_float2(a[0].m, a[0].l);
       }
-    } else {
-      // its state: the warp's first piece, or its last (all of the ring's pages are used by then)
-      const int k = u == w0 ? 0 : 1;
-      float* dst0 = k == 0 ? co + warp * p.G * DH : reinterpret_cast<float*>(ring);
-      __syncwarp();
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int h = 2 * t + e;
-        if (h >= p.G) continue;
-        // m in log2 units
-        if (g == 0)
-          cml[(warp * 2 + k) * p.G + h] = make_float2(st.m[e] == -INFINITY ? -INFINITY : st.m[e] * pv.ls[e], st.l[e]);
-        float* dst = dst0 + h * DH + g * (DH / 8);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-          *reinterpret_cast<float2*>(dst + 2 * mt) = make_float2(o[mt][e], o[mt][2 + e]);
-      }
-      const int a = u - p0;  // the segment's first unit
-      if (lane == 0 && u == max(a, u0)) {  // the first of its pieces in the CTA announces it
-        Shared s;
-        s.b = b;
-        s.gkv = gkv;
-        s.first = a;
-        s.pages = pages;
-        s.wa = warp;
-        s.wz = warp_of(min(a + pages, u1) - 1);
-        s.np = 1;
-        s.c_lo = 0;
-        if (!SEG && (a < u0 || a + pages > u1)) {
-          const CostSplit split(V, Pe);
-          const int v_first = voff[b] + gkv * (pages + kPc) + kPc;
-          s.c_lo = split.cta_of(v_first);
-          s.np = split.cta_of(v_first + pages - 1) - s.c_lo + 1;
-        }
-        list[atomicAdd(&list_n, 1)] = s;
+    }
+    head_barrier(head, hthreads);
+    if (np > 1) {
+      // Publish the piece: the barrier above orders the threads' stores before the
+      // acquire-release arrival, and an arrival that completes the count makes all
+      // pieces visible to this head's warps.
+      uint32_t count = 0;
+      if (htid == 0) count = atom_add_acq_rel_gpu(p.ws_cnt + sigma, 1u) + 1;
+      if (u + n < u1) {
+        held_np = np;
+        held_c = c_lo;
+        held_b = b;
+        held_gr = gr;
+        held_count = count;
+      } else {
+        if (htid == 0) merge_s[head] = count == static_cast<uint32_t>(np);
+        head_barrier(head, hthreads);
+        if (merge_s[head]) merge_pieces(np, (c_lo + seg) * p.HG + head, sigma, orow, sv);
       }
     }
     u += n;
   }
-  __syncthreads();
+  if (!FIX && held_np) {
+    head_barrier(head, hthreads);
+    if (htid == 0) merge_s[head] = held_count == static_cast<uint32_t>(held_np);
+    head_barrier(head, hthreads);
+    if (merge_s[head]) {
+      const int gkv = held_gr * p.HG + head;
+      merge_pieces(held_np, (held_c + static_cast<int64_t>(held_b) * p.NG + held_gr) * p.HG + head,
+                   held_b * p.Hkv + gkv, p.out + (static_cast<int64_t>(held_b) * p.Hq + gkv * p.G) * DH,
+                   __ldg(p.vs + (p.per_head ? gkv : 0)));
+    }
+  }
+}
 
-  // ---- the shared segments: a float4 of one head's output a thread
-  const int n4 = p.G * DH / 4, shared = list_n;
-  bool split_any = false;
-  for (int i = tid; i < shared * n4; i += kDecThreads) {
-    const int k = i / n4, e = i - k * n4, h = 4 * e / DH;
-    const Shared s = list[k];
-    float M = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int w0_ = s.wa; w0_ <= s.wz; w0_ += 4) {  // four warps at a time, their loads together
-      float2 ml[4];
-      float4 v[4];
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int w = w0_ + y;
-        ml[y] = make_float2(-INFINITY, 0.f);
-        v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (w <= s.wz && wstart[w] < wstart[w + 1]) {
-          const bool head = wstart[w] >= s.first;
-          ml[y] = cml[(w * 2 + (head ? 0 : 1)) * p.G + h];
-          v[y] = *reinterpret_cast<const float4*>(
-              (head ? co + w * p.G * DH : reinterpret_cast<const float*>(smem + w * p.S * kSlot)) + 4 * e);
-        }
-      }
-      const float nm = fmaxf(fmaxf(M, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
-      const float r = M == -INFINITY ? 1.f : fast_exp2(M - nm);
-      l *= r;
-      acc.x *= r;
-      acc.y *= r;
-      acc.z *= r;
-      acc.w *= r;
-      M = nm;
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const float a = ml[y].x == -INFINITY ? 1.f : fast_exp2(ml[y].x - M);  // (-inf: l and o are 0, or NaN)
-        l += ml[y].y * a;
-        acc.x += v[y].x * a;
-        acc.y += v[y].y * a;
-        acc.z += v[y].z * a;
-        acc.w += v[y].w * a;
-      }
+template <int DH, bool FIX>
+__global__ void __launch_bounds__(kDecThreads, kDecCtas) decode_kernel(const __grid_constant__ DecParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t warp_tot[kDecThreads / 32];
+  __shared__ int32_t bounds[2];
+  __shared__ uint32_t merge_s[kDecWarps];
+  __shared__ uint32_t abort_s;
+  const int S = p.depth * (kDecWarps / p.HG);  // slots of all rings
+  const DecSmem sm = dec_smem<DH>(S, p.HG, p.G, p.B, FIX);
+  const int tid = threadIdx.x;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + sm.bars);  // [S] a unit landed
+  uint64_t* empty = full + S;                                    // [S] its HG warps are done with it
+  volatile uint32_t* bad_s = reinterpret_cast<volatile uint32_t*>(smem + sm.bad);
+  volatile int32_t* last_s = reinterpret_cast<volatile int32_t*>(bad_s + S);  // [S] last unit copied there
+  volatile uint32_t* abort_flag = &abort_s;
+  int32_t* off = reinterpret_cast<int32_t*>(smem + sm.plan);  // [B + 1]
+  int32_t* len = off + p.B + 1;                               // [B]
+  int32_t* voff = len + p.B;                                  // [B + 1]
+
+  if (tid < S) {
+    mbar_init(&full[tid], 1);
+    mbar_init(&empty[tid], p.HG);
+    last_s[tid] = -1;
+    fence_mbar_init();
+  }
+  if (tid == 0) abort_s = 0u;
+  pdl_wait();
+  pdl_allow_next();
+
+  const int c = blockIdx.x;
+  int u0 = 0, u1 = 0, fix_b = 0, fix_g = 0, fix_len = 0, fix_pages = 0, fix_np = 1;
+  int V = 0, Pe = 1;
+  if (FIX) {
+    const int seg = c / p.cps, part = c - seg * p.cps;
+    fix_b = seg / p.NG;
+    fix_g = seg - fix_b * p.NG;
+    fix_len = __ldg(p.seq_lens + fix_b);
+    if (fix_len < 0 || fix_len > p.max_blocks * kTok) {
+      if (fix_g == 0 && part == 0 && tid == 0) flag_status(p.status, KVQ_DEV_BAD_SEQLEN);
+      fix_len = 0;
     }
-    if (s.np == 1) {
-      const float f = l > 0.f ? __ldg(p.vs + (p.per_head ? s.gkv : 0)) / l : 0.f;
-      *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(s.b) * p.Hq + s.gkv * p.G) * DH + 4 * e) =
-          make_uint2(f32x2_to_bf16x2(acc.x * f, acc.y * f), f32x2_to_bf16x2(acc.z * f, acc.w * f));
+    fix_pages = visible(p.window, p.sinks, fix_len).count;
+    fix_np = max(1, min(p.cps, fix_pages / kMinUnits));
+    if (part >= fix_np) return;
+    u0 = static_cast<int>(static_cast<int64_t>(fix_pages) * part / fix_np);
+    u1 = static_cast<int>(static_cast<int64_t>(fix_pages) * (part + 1) / fix_np);
+    if (fix_pages == 0) {  // nothing to attend to
+      uint16_t* o = p.out + (static_cast<int64_t>(fix_b) * p.Hq + fix_g * p.HG * p.G) * DH;
+      for (int i = tid; i < p.HG * p.G * DH; i += kDecThreads) o[i] = 0;
+      return;
+    }
+    __syncthreads();
+  } else {
+    dec_plan(p, off, len, voff, warp_tot);
+    for (int b = c; b < p.B; b += gridDim.x) {  // sequences with nothing to attend to
+      if (off[b + 1] != off[b]) continue;
+      uint16_t* o = p.out + static_cast<int64_t>(b) * p.Hq * DH;
+      for (int i = tid; i < p.Hq * DH; i += kDecThreads) o[i] = 0;
+    }
+    const int W = off[p.B];
+    V = voff[p.B];
+    // a CTA has a unit for every warp of a head at least
+    const int least = kDecWarps / p.HG;
+    Pe = min(p.P, (W + least - 1) / least);
+    const CostSplit split(V, Pe);
+    if ((tid == 0 || tid == 32) && c < Pe)
+      bounds[tid >> 5] = pages_before(off, voff, p.B, p.NG, split(c + (tid >> 5)), kPc);
+    __syncthreads();
+    if (c < Pe) {
+      u0 = bounds[0];
+      u1 = bounds[1];
+    }
+  }
+  // the segment of unit u: sequence, group of heads, its units, u's place in it, tokens
+  auto segment = [&](int u, int& b, int& gr, int& pages, int& p0, int& L) {
+    if (FIX) {
+      b = fix_b;
+      gr = fix_g;
+      pages = fix_pages;
+      p0 = u;
+      L = fix_len;
     } else {
-      const int64_t slot = c + static_cast<int64_t>(s.b) * p.Hkv + s.gkv;
-      *reinterpret_cast<float4*>(p.ws_o + slot * p.G * DH + 4 * e) = acc;
-      if (4 * e % DH == 0) p.ws_ml[slot * p.G + h] = make_float2(M, l);
+      b = find_seq(off, p.B, u);
+      pages = (off[b + 1] - off[b]) / p.NG;
+      gr = (u - off[b]) / pages;
+      p0 = u - off[b] - gr * pages;
+      L = len[b];
     }
+  };
+
+  if (tid < kDecWarps * 32) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
+    decode_run<DH, FIX>(p, smem, sm, full, empty, bad_s, abort_flag, merge_s, voff, u0, u1, V, Pe, fix_np, segment);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    if (tid < kDecWarps * 32 + 32)
+      decode_copies<DH>(p, smem, full, empty, bad_s, last_s, abort_flag, u0, u1, segment);
   }
-  if (!SEG) {
-    for (int k = 0; k < shared; ++k) split_any |= list[k].np > 1;
-    if (split_any) {  // the same for every thread
-      // Publish the pieces: the barrier orders every thread's stores before the
-      // acquire-release arrivals, and an arrival that completes a count makes all
-      // pieces of that segment visible to this CTA.
-      __syncthreads();
-      if (tid < shared) {
-        const Shared s = list[tid];
-        merge_s[tid] = s.np > 1 && atom_add_acq_rel_gpu(p.ws_cnt + static_cast<int64_t>(s.b) * p.Hkv + s.gkv, 1u) + 1 ==
-                                       static_cast<uint32_t>(s.np);
-      }
-      __syncthreads();
-      const int K = max(1, min(kDecThreads / n4, kDecWarps));  // [K][n4] fits co
-      float4* part = reinterpret_cast<float4*>(co);
-      for (int k = 0; k < shared; ++k) {
-        if (!merge_s[k]) continue;
-        const Shared s = list[k];
-        // thread (y, e): the pieces y, y + K, ... of output float4 e
-        const int64_t sigma = static_cast<int64_t>(s.b) * p.Hkv + s.gkv;
-        const float2* ml = p.ws_ml + (s.c_lo + sigma) * p.G;
-        const float4* ob = reinterpret_cast<const float4*>(p.ws_o + (s.c_lo + sigma) * p.G * DH);
-        for (int i = tid; i < K * n4; i += kDecThreads) {
-          const int y0 = i / n4, e = i - y0 * n4, h = 4 * e / DH;
-          float M = -INFINITY, l = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int j = y0; j < s.np; j += 8 * K) {  // eight pieces at a time, their loads together
-            float2 m8[8];
-            float4 v8[8];
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              const int x = j + y * K;
-              m8[y] = x < s.np ? __ldcg(ml + static_cast<int64_t>(x) * p.G + h) : make_float2(-INFINITY, 0.f);
-              v8[y] = x < s.np ? __ldcg(ob + static_cast<int64_t>(x) * n4 + e) : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            float nm = M;
-#pragma unroll
-            for (int y = 0; y < 8; ++y) nm = fmaxf(nm, m8[y].x);
-            const float a = M == -INFINITY ? 1.f : fast_exp2(M - nm);
-            l *= a;
-            acc.x *= a;
-            acc.y *= a;
-            acc.z *= a;
-            acc.w *= a;
-            M = nm;
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              const float w = m8[y].x == -INFINITY ? 1.f : fast_exp2(m8[y].x - M);
-              l += m8[y].y * w;
-              acc.x += v8[y].x * w;
-              acc.y += v8[y].y * w;
-              acc.z += v8[y].z * w;
-              acc.w += v8[y].w * w;
-            }
-          }
-          part[i] = acc;
-          if (4 * e % DH == 0) cml[y0 * p.G + h] = make_float2(M, l);
-        }
-        __syncthreads();
-        for (int e = tid; e < n4; e += kDecThreads) {
-          const int h = 4 * e / DH;
-          float M = -INFINITY, l = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int y = 0; y < K; ++y) M = fmaxf(M, cml[y * p.G + h].x);
-          for (int y = 0; y < K; ++y) {
-            const float2 x = cml[y * p.G + h];
-            const float4 v = part[y * n4 + e];
-            const float w = x.x == -INFINITY ? 1.f : fast_exp2(x.x - M);
-            l += x.y * w;
-            acc.x += v.x * w;
-            acc.y += v.y * w;
-            acc.z += v.z * w;
-            acc.w += v.w * w;
-          }
-          const float f = l > 0.f ? __ldg(p.vs + (p.per_head ? s.gkv : 0)) / l : 0.f;
-          *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(s.b) * p.Hq + s.gkv * p.G) * DH + 4 * e) =
-              make_uint2(f32x2_to_bf16x2(acc.x * f, acc.y * f), f32x2_to_bf16x2(acc.z * f, acc.w * f));
-        }
-        if (tid == 0) p.ws_cnt[sigma] = 0u;
-        __syncthreads();
-      }
-    }
-  }
+  __syncthreads();
   // after a timeout: the copies still in flight land (or the wait runs out) before the CTA leaves
-  for (; dead && done < issued; ++done)
-    mbar_wait(&full[done % p.S], static_cast<uint32_t>((done / p.S) & 1));
+  if (*abort_flag && tid == 0)
+    for (int s = 0; s < S; ++s)
+      if (last_s[s] >= 0) mbar_wait(&full[s], static_cast<uint32_t>((last_s[s] / p.depth) & 1));
 }
 
 }  // namespace fp4

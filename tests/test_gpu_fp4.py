@@ -247,6 +247,24 @@ def test_decode_splits(kvq, lens, hq, hkv, dh, window, sinks):
     assert torch.equal(first, g.out)
 
 
+@pytest.mark.parametrize("lens,hq,hkv,dh", [
+    ([2300] * 20, 8, 8, 128), ([1700] * 40, 16, 8, 64), ([2100, 5, 1900, 640] * 8, 8, 4, 128),
+    ([3100] * 16, 12, 6, 64), ([900, 4000, 17, 2500] * 5, 64, 8, 128)])
+def test_decode_long_runs(kvq, lens, hq, hkv, dh):
+    """Runs of many units per block, of 8, 4 and 2 heads each: the rings of shared pages
+    go round several times."""
+    b = f4.Batch(len(lens) + hkv, lens, hq, hkv, dh)
+    g = OnGpu(kvq, b, [1] * len(lens))
+    g.decode()
+    g.check(what="first")
+    first = g.out.clone()
+    for _ in range(5):
+        g.out.fill_(3.0)
+        g.decode()
+        torch.cuda.synchronize()
+        assert torch.equal(first, g.out)
+
+
 def test_decode_one_wide_query(kvq):
     """Logits up to hundreds (one token takes all) and queries of 1e-30 and 1e30."""
     b = f4.Batch(11, [300, 64], 8, 2, 128, amp=8.0)
