@@ -55,7 +55,7 @@ namespace fp4 {
 #define KVQ_FP4_NP 4
 #endif
 #ifndef KVQ_FP4_PC
-#define KVQ_FP4_PC 16
+#define KVQ_FP4_PC 8
 #endif
 constexpr int kDecWarps = KVQ_FP4_WARPS;
 constexpr int kDecThreads = kDecWarps * 32 + 128;  // consumers, the producer's warpgroup
@@ -461,6 +461,8 @@ KVQ_DEVI void decode_copies(const DecParams& p, uint8_t* smem, uint64_t* full, u
           flag_status(p.status, KVQ_DEV_WAIT_TIMEOUT);
         }
         return;
+      } else {
+        __nanosleep(40);
       }
     }
   }

@@ -12,17 +12,16 @@
 //     bulk copy a page: codes and scales), into a ring of 3 stages
 //   warps 8-11 (converters)  code * block scale as f16 (exact), K and V both
 //     token-major in the 128-byte-swizzled layout, two buffers each
-//   warps 13, 14 (one per tile)  one lane each issues, block by block,
-//     S = Q K^T (M 128, N 128) and, as the softmax delivers them, the two
-//     halves of O += P V (A = P from tensor memory, K 64 each)
+//   warps 13, 14 (one per tile)  one lane each issues, for each half (64 keys) of a
+//     block, S = Q K^T (M 128, N 64) and, as the softmax delivers P, O += P V
+//     (A = P from tensor memory, K 64), then the half's next S at once
 //   warps 0-3, 4-7 (softmax of tiles 0, 1; thread = row = TMEM lane)  64 keys
-//     at a time: S from TMEM, mask, running maximum with a lazy rescale of O,
-//     P = 2^(x - m + 7) as f16 over the S columns that it came from
-// 128 keys a block because a matrix step of M 128 takes about 76 cycles for any
-// N up to 128: with 64 the two tiles' steps alone took 1824 cycles per 64 keys.
-// S and P share columns (2 tiles x (128 S + 128 O) fill the 512), so a tile's
-// next S waits for its last P to be read; the other tile's softmax and matrix
-// steps fill that time.
+//     at a time: S from TMEM, mask, P = 2^(x - m + 7) as f16 over the S columns
+//     that it came from, with the running maximum m raised lazily (and O rescaled)
+// S and P share columns: 2 tiles x (2 halves of 64 + 128 of O) fill the 512.  A
+// half's next S waits for the PV that reads its P, while the softmax works on the
+// other half, so that the softmax (which bounds the loop: both tiles' 16384 weights
+// a block) hardly waits.
 //
 // Where the tiles are fewer than the SMs, the host splits each tile's blocks
 // over several CTAs; each leaves (m, l, O) of its rows in the workspace and the
@@ -218,13 +217,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
   uint64_t* conv_v = conv_k + kBufs;     // [kBufs]
   uint64_t* done_k = conv_v + kBufs;     // [kBufs] K buffer read by both tiles (a commit each)
   uint64_t* done_v = done_k + kBufs;     // [kBufs]
-  uint64_t* sfull = done_v + kBufs;      // [kTiles] S written (commit, and the issuer's arrival)
-  uint64_t* pfull = sfull + kTiles;      // [kTiles][2] a half of P written, of S read (128)
-  uint64_t* phalf = pfull + 2 * kTiles;  // [kTiles] the first half's PV done (commit)
-  uint64_t* pdone = phalf + kTiles;      // [kTiles] a block's PVs done (commit, and the issuer's arrival)
-  uint64_t* fin = pdone + kTiles;        // every matrix step done (a commit of each issuer)
+  uint64_t* sfull = done_v + kBufs;      // [kTiles][2] a half of S written (commit, and the issuer's arrival)
+  uint64_t* pfull = sfull + 2 * kTiles;  // [kTiles][2] the half of P written, of S read (128)
+  uint64_t* pdone = pfull + 2 * kTiles;  // [kTiles][2] its PV done (commit, and the issuer's arrival)
+  uint64_t* fin = pdone + 2 * kTiles;    // every matrix step done (a commit of each issuer)
   uint64_t* qready = fin + 1;            // both Q tiles written (256)
-  uint64_t* turn = qready + 1;           // [kTiles] a tile's softmax is half through a block
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + SM::misc);
   volatile uint32_t* tmem_slot = misc;
   volatile uint32_t* abort_flag = misc + 1;
@@ -238,9 +235,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
 
   // A parity wait for phase k of a barrier is sound while the barrier has
   // completed k or k + 1 phases.  Each waiter takes its barriers' phases in
-  // order, but for phalf (waited only where O is rescaled between the halves):
-  // S of block i comes after the PVs of block i - 1, so phase i - 1 is complete,
-  // and phase i + 1 needs this softmax's own later progress.
+  // order, but for the softmax's waits for pdone, where O is rescaled: S of half h
+  // of block i came after the PV of half h of block i - 1, and that PV's next phase
+  // needs this softmax's own later progress.
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.z, gkv = blockIdx.y;
@@ -260,13 +257,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
       mbar_init(&done_k[i], kTiles);
       mbar_init(&done_v[i], kTiles);
     }
-    for (int t = 0; t < kTiles; ++t) {
+    for (int t = 0; t < 2 * kTiles; ++t) {
       mbar_init(&sfull[t], 2);
-      mbar_init(&pfull[2 * t], 128);
-      mbar_init(&pfull[2 * t + 1], 128);
-      mbar_init(&phalf[t], 1);
+      mbar_init(&pfull[t], 128);
       mbar_init(&pdone[t], 2);
-      mbar_init(&turn[t], 1);
     }
     mbar_init(fin, kTiles);
     mbar_init(qready, kTiles * 128);
@@ -379,37 +373,36 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     // ------------------------------------------------------------ matrix steps of one tile
     const int t = warp - kMmaWarp;
     if (lane == 0) {
-      const uint32_t id_qk = tc::idesc_f16(kRows, kKeys), id_pv = tc::idesc_f16(kRows, DH) | (1u << 16);
+      const uint32_t id_qk = tc::idesc_f16(kRows, kKeys / 2), id_pv = tc::idesc_f16(kRows, DH) | (1u << 16);
       const uint32_t tm = tmem + t * kTileCols;
       auto wait = [&](uint64_t* bar, int phase) {
         return wait_or_abort(bar, static_cast<uint32_t>(phase & 1), abort_flag);
       };
+      // S of half h of block j
+      auto qk = [&](int j, int h) {
+        tc::tc_fence_after();
+        const uint32_t a = sbase + SM::q + t * kRows * DH * 2;
+        const uint32_t bk = sbase + SM::k + (j - c0) % kBufs * SM::kTile + h * 8192;
+#pragma unroll
+        for (int k = 0; k < DH / 16; ++k) {
+          const uint32_t o = (k >> 2) * (128 * 128) + (k & 3) * 32;
+          tc::mma_f16_ss(tm + h * 64, tc::sw128_desc(a + o), tc::sw128_desc(bk + o), id_qk, k > 0 ? 1u : 0u);
+        }
+        mbar_arrive(&sfull[2 * t + h]);  // hands on what conv_k's arrival showed (bmask)
+        tc::mma_commit(&sfull[2 * t + h]);
+      };
       bool ok = wait(qready, 0);
       for (int j = c0; j < c1 && ok; ++j) {
         const int i = j - jb[t], x = (j - c0) % kBufs, ph = (j - c0) / kBufs;
-        const bool active = j >= jb[t] && j < je[t];
-        if (!(ok = wait(&conv_k[x], ph))) break;
-        // The tiles take turns: a tile's S waits until the other's softmax has begun
-        // the block before, so that one's softmax runs beside the other's matrix
-        // steps.  (Left alone they fall into step: steps issued together end
-        // together, and both softmaxes then run against each other.)
-        if ((t == 1 || j > c0) && !(ok = wait(&turn[1 - t], j - c0 - (t == 0 ? 1 : 0)))) break;
-        // P of the block before read: this S may overwrite it
-        if (active && i > 0 && !(ok = wait(&pdone[t], i - 1))) break;
-        if (active) {
-          tc::tc_fence_after();
-          const uint32_t a = sbase + SM::q + t * kRows * DH * 2, bk = sbase + SM::k + x * SM::kTile;
-#pragma unroll
-          for (int k = 0; k < DH / 16; ++k) {
-            const uint32_t o = (k >> 2) * (128 * 128) + (k & 3) * 32;
-            tc::mma_f16_ss(tm, tc::sw128_desc(a + o), tc::sw128_desc(bk + o), id_qk, k > 0 ? 1u : 0u);
+        const bool active = j >= jb[t] && j < je[t], more = active && j + 1 < je[t];
+        if (!active || i == 0) {  // (later blocks' S was issued beside the block before)
+          if (!(ok = wait(&conv_k[x], ph))) break;
+          if (active) {
+            qk(j, 0);
+            qk(j, 1);
           }
-          mbar_arrive(&sfull[t]);  // hands on what conv_k's arrival showed (bmask)
-          tc::mma_commit(&sfull[t]);
-        } else {
-          mbar_arrive(&turn[t]);
+          tc::mma_commit(&done_k[x]);
         }
-        tc::mma_commit(&done_k[x]);
         if (!(ok = wait(&conv_v[x], ph))) break;
         for (int h = 0; h < 2 && active && ok; ++h) {
           if (!(ok = wait(&pfull[2 * t + h], i))) break;
@@ -420,8 +413,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
           for (int k = 0; k < 4; ++k)
             tc::mma_f16_ts(tm + 128, tm + h * 64 + k * 8, tc::sw128_desc(bv + k * 2048, 128 * 128, 1024),
                            id_pv, (i > 0 || h > 0 || k > 0) ? 1u : 0u);
-          if (h) mbar_arrive(&pdone[t]);  // hands on what conv_v's arrival showed (vnan)
-          tc::mma_commit(h ? &pdone[t] : &phalf[t]);
+          mbar_arrive(&pdone[2 * t + h]);  // hands on what conv_v's arrival showed (vnan)
+          tc::mma_commit(&pdone[2 * t + h]);
+          if (more) {  // the half's next S, over the P that this PV has read, beside the other half's softmax
+            const int xn = (j + 1 - c0) % kBufs;
+            if (h == 0 && !(ok = wait(&conv_k[xn], (j + 1 - c0) / kBufs))) break;
+            if (!(ok = wait(&pdone[2 * t + h], i))) break;
+            qk(j + 1, h);
+            if (h == 1) tc::mma_commit(&done_k[xn]);
+          }
         }
         if (!ok) break;
         tc::mma_commit(&done_v[x]);
@@ -539,12 +539,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     const int nI = je[t] - jb[t];
     for (int i = 0; i < nI && ok; ++i) {
       const int j = jb[t] + i;
-      if (!(ok = wait_w(&sfull[t], i))) break;
-      const uint32_t bm8 = bmask[j & 3];
-      tc::tc_fence_after();
-      if (r == 0) mbar_arrive(&turn[t]);
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
+        if (!(ok = wait_w(&sfull[2 * t + h], i))) break;
+        const uint32_t bm8 = bmask[j & 3];
+        tc::tc_fence_after();
         float x[64];
         tmem_ld64(tm_s + h * 64, x);
         const int lp = j * kBlkPages + h * 4;  // list page of the half's first key
@@ -594,8 +593,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
         weights();
         const bool grow = mx > m + kRescaleThreshold;
         if (__any_sync(kFull, grow)) {
-          // O's last writer: the first half's PV of this block, or (done before S came) block i - 1
-          if (h == 1 && !(ok = wait_w(&phalf[t], i))) break;
+          // O's last writer: the PV of the half before
+          if (h == 1 ? !(ok = wait_w(&pdone[2 * t], i)) : i > 0 && !(ok = wait_w(&pdone[2 * t + 1], i - 1))) break;
           tc::tc_fence_after();
           const float nm = grow ? mx : m;
           const float a = m == -INFINITY ? 0.f : fast_exp2(m - nm);
@@ -619,7 +618,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
         mbar_arrive(&pfull[2 * t + h]);
       }
     }
-    if (ok && nI > 0) ok = wait_w(&pdone[t], nI - 1);
+    if (ok && nI > 0) ok = wait_w(&pdone[2 * t], nI - 1) && wait_w(&pdone[2 * t + 1], nI - 1);
     if (!ok) fail();
     // ---- epilogue: the row of O, normalised, or (keys shared out) as it is
     const float sv = __ldg(p.vs + (p.per_head ? gkv : 0));
