@@ -42,8 +42,10 @@ constexpr int kRows = 128;   // query rows of a tile (MMA M)
 constexpr int kTiles = 2;    // tiles of a CTA
 constexpr int kKeys = 128;   // keys of a block
 constexpr int kBlkPages = kKeys / kTok;
-constexpr int kPreThreads = 480;
-constexpr int kConvWarp = 8, kProdWarp = 12, kMmaWarp = 13;
+constexpr int kPreThreads = 640;
+constexpr int kConvWarp = 8, kProdWarp = 16, kMmaWarp = 17;
+constexpr int kSoftRegs = 136, kConvRegs = 72, kIssueRegs = 64;  // of 96 at launch: 256, 256 and 128 threads
+static_assert(256 * kSoftRegs + 256 * kConvRegs + 128 * kIssueRegs <= kPreThreads * 96, "registers");
 constexpr uint32_t kTmemCols = 512, kTileCols = 256;  // per tile: S and P at +0, O at +128
 constexpr int kPreStages = 3, kBufs = 2;
 constexpr float kPreBias = 7.f;  // log2 of the factor that the weights carry
@@ -189,11 +191,43 @@ KVQ_DEVI void tmem_ld64(uint32_t taddr, float (&v)[64]) {
       : "memory");
 }
 
+// Two binary32 values in a register pair: one instruction for both.
+using f32x2 = unsigned long long;
+KVQ_DEVI f32x2 f32x2_pack(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+KVQ_DEVI void f32x2_unpack(f32x2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+KVQ_DEVI f32x2 f32x2_fma(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+KVQ_DEVI f32x2 f32x2_add(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+KVQ_DEVI float fmax3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // 8 consecutive columns of this thread's lane (no wait).
 KVQ_DEVI void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
                ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
+}
+
+// True in one lane of the (whole) warp.  Matrix instructions that the compiler sees issued
+// under elect.sync cost 12 cycles each to issue, under lane == 0 they cost 52.
+KVQ_DEVI bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // The pages that a CTA's rows see, as a list: the first tokens' pages [0, sink),
@@ -202,6 +236,18 @@ struct PageList {
   int sink, first, count;
   KVQ_DEVI int col(int i) const { return i < sink ? i : first + i - sink; }
 };
+
+// A CTA converts its nb blocks in the order K0 K1 V0 K2 V1 ... V(nb - 1): a K buffer is
+// free half a block before the V buffer.  Item `it` of these, and the last K up to it.
+struct PreTask {
+  int block, last_k;
+  bool v;
+};
+KVQ_DEVI PreTask pre_task(int it, int nb) {
+  const bool v = it == 2 * nb - 1 || (it > 0 && (it & 1) == 0);
+  const int k = min((it + 1) >> 1, nb - 1);
+  return {v ? (it == 2 * nb - 1 ? nb - 1 : (it >> 1) - 1) : k, k, v};
+}
 
 template <int DH>
 __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_constant__ PreParams p) {
@@ -297,6 +343,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
   // this CTA's blocks [c0, c1) and tile t's [jb, je) of them
   const int c0 = static_cast<int>(static_cast<int64_t>(nall) * share / p.ns);
   const int c1 = static_cast<int>(static_cast<int64_t>(nall) * (share + 1) / p.ns);
+  const int nb = c1 - c0;
   int jb[kTiles], je[kTiles];
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) {
@@ -327,15 +374,19 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     return __all_sync(kFull, wait_or_abort(bar, static_cast<uint32_t>(phase & 1), abort_flag));
   };
 
+  if (warp >= kProdWarp) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
   if (warp == kProdWarp) {
     // ------------------------------------------------------------ producer
-    // Item 2i is K of the CTA's block i, item 2i + 1 its V.  The 32 lanes look
-    // up the block ids of 4 blocks at once; lanes 0-7 copy a page each.
-    int64_t my_at = -1;  // byte offset of list page 8 (c0 + i - i % 4) + lane, -1: masked out
-    for (int it = 0; it < 2 * (c1 - c0); ++it) {
-      const int i = it >> 1, s = it % S;
-      if ((it & 7) == 0) {
+    // The 32 lanes look up the block ids of 4 blocks at once; lanes 0-7 copy a page each.
+    int64_t my_at = -1, old_at = -1;  // byte offset of list page 8 (c0 + i - i % 4) + lane, -1: masked out
+    for (int it = 0; it < 2 * nb; ++it) {
+      const int s = it % S;
+      const PreTask task = pre_task(it, nb);
+      const int i = task.block;
+      if (!task.v && (i & 3) == 0) {
         const int lp = kBlkPages * (c0 + i) + lane;
+        old_at = my_at;  // V is at most two blocks behind K
         my_at = -1;
         if (lp < list.count) {
           const int col = list.col(lp);
@@ -348,7 +399,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
             flag_status(p.status, KVQ_DEV_BAD_BLOCK);
         }
       }
-      const int64_t at = __shfl_sync(kFull, my_at, 8 * (i & 3) + (lane & 7));
+      const bool old = task.v && (i >> 2) != (task.last_k >> 2);
+      const int64_t at = __shfl_sync(kFull, old ? old_at : my_at, 8 * (i & 3) + (lane & 7));
       const bool ok = it < S || wait_w(&empty[s], it / S - 1);
       if (__any_sync(kFull, !ok || *abort_flag)) {
         if (lane == 0) fail();
@@ -366,15 +418,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
       }
       __syncwarp();
       if (lane < kBlkPages && at >= 0)
-        bulk_load(smem + SM::stage + s * SM::kStage + lane * PG::kBytes, ((it & 1) ? p.vc : p.kc) + at,
+        bulk_load(smem + SM::stage + s * SM::kStage + lane * PG::kBytes, (task.v ? p.vc : p.kc) + at,
                   PG::kBytes, &full[s]);
     }
-  } else if (warp >= kMmaWarp) {
+  } else if (warp < kMmaWarp + kTiles) {
     // ------------------------------------------------------------ matrix steps of one tile
-    const int t = warp - kMmaWarp;
-    if (lane == 0) {
+    const int t = __shfl_sync(kFull, warp, 0) - kMmaWarp;
+    const uint32_t tmem_u = __shfl_sync(kFull, tmem, 0);
+    if (elect_one()) {
       const uint32_t id_qk = tc::idesc_f16(kRows, kKeys / 2), id_pv = tc::idesc_f16(kRows, DH) | (1u << 16);
-      const uint32_t tm = tmem + t * kTileCols;
+      const uint32_t tm = tmem_u + t * kTileCols;
       auto wait = [&](uint64_t* bar, int phase) {
         return wait_or_abort(bar, static_cast<uint32_t>(phase & 1), abort_flag);
       };
@@ -430,12 +483,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
       tc::mma_commit(fin);
       if (!mbar_wait(fin, 0u)) fail();
     }
+  }
   } else if (warp >= kConvWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
     // ------------------------------------------------------------ converters
-    const int ct = tid - kConvWarp * 32;  // 0 .. 127
-    for (int it = 0; it < 2 * (c1 - c0); ++it) {
-      const int i = it >> 1, s = it % S, x = i % kBufs;
-      const bool is_v = it & 1;
+    const bool is_v = warp >= kConvWarp + 4;
+    const int ct = tid & 127;
+    for (int it = 0; it < 2 * nb; ++it) {
+      const PreTask task = pre_task(it, nb);
+      if (task.v != is_v) continue;
+      const int i = task.block, s = it % S, x = i % kBufs;
       bool ok = wait_w(&full[s], it / S);
       if (ok && i >= kBufs) ok = wait_w(is_v ? &done_v[x] : &done_k[x], i / kBufs - 1);
       if (!ok) {
@@ -460,7 +517,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
       // those past the sequence (weights of 0 do not clear a NaN), and so do NaN blocks, which
       // the epilogue puts back where they are seen.
       uint32_t keep = 0xFu;  // bit y: row r0 + 32 y
-      if (is_v) {
+      if (is_v && (bm || kBlkPages * (c0 + i + 1) >= list.count)) {  // (L ends in the list's last page)
 #pragma unroll
         for (int y = 0; y < 4; ++y)
           if ((bm >> (p0 + 2 * y) & 1u) || list.col(kBlkPages * (c0 + i) + p0 + 2 * y) * kTok + tr >= L) keep &= ~(1u << y);
@@ -492,6 +549,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     }
   } else {
     // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int t = warp >> 2, r = tid & 127;
     const int jr = j0 + t * TQ + r / p.G;  // query token of this row
     const bool live = t < p.tpc && r < TQ * p.G && jr < nc;
@@ -572,23 +630,29 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
         auto weights = [&] {
           // while every key so far is masked m is -inf: any finite value keeps 2^-inf = 0 (and a NaN)
           const float mb = m == -INFINITY ? 0.f : m - kPreBias;
-          float l4[4] = {0.f, 0.f, 0.f, 0.f}, mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          const f32x2 sc2 = f32x2_pack(lscale, lscale), nb2 = f32x2_pack(-mb, -mb);
+          f32x2 l2[2] = {f32x2_pack(0.f, 0.f), f32x2_pack(0.f, 0.f)};
+          float mx2[2] = {-INFINITY, -INFINITY};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t ph[8];
 #pragma unroll
             for (int e2 = 0; e2 < 8; ++e2) {
               const int e = 16 * c + 2 * e2;
-              const float p0 = fast_exp2(fmaf(x[e], lscale, -mb));
-              const float p1 = fast_exp2(fmaf(x[e + 1], lscale, -mb));
-              l4[e2 & 3] += p0 + p1;
-              mx4[e2 & 3] = fmaxf(mx4[e2 & 3], fmaxf(x[e], x[e + 1]));
+              float p0, p1;
+              f32x2_unpack(f32x2_fma(f32x2_pack(x[e], x[e + 1]), sc2, nb2), p0, p1);
+              p0 = fast_exp2(p0);
+              p1 = fast_exp2(p1);
+              l2[e2 & 1] = f32x2_add(l2[e2 & 1], f32x2_pack(p0, p1));
+              mx2[e2 & 1] = fmax3(mx2[e2 & 1], x[e], x[e + 1]);
               ph[e2] = f32x2_to_f16x2(p0, p1);
             }
             tmem_st8(tm_s + h * 64 + 8 * c, ph);
           }
-          sum = (l4[0] + l4[1]) + (l4[2] + l4[3]);
-          mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * lscale;
+          float s0, s1;
+          f32x2_unpack(f32x2_add(l2[0], l2[1]), s0, s1);
+          sum = s0 + s1;
+          mx = fmaxf(mx2[0], mx2[1]) * lscale;
         };
         weights();
         const bool grow = mx > m + kRescaleThreshold;
