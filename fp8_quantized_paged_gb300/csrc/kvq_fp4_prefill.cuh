@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     const int t = warp >> 2, r = tid & 127;
     const int jr = j0 + t * TQ + r / p.G;  // query token of this row
     const bool live = t < p.tpc && r < TQ * p.G && jr < nc;
-    const int pos = live ? base + jr : -1;
+    const int pos = base + jr;
     const int lo = live && p.window > 0 && pos >= p.window ? pos + 1 - p.window : 0;
     const int64_t qrow = live ? (static_cast<int64_t>(q0) + jr) * p.Hq + gkv * p.G + r % p.G : 0;
     const uint32_t tm_s = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * kTileCols;
@@ -595,7 +595,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     const int nI = je[t] - jb[t];
-    for (int i = 0; i < nI && ok; ++i) {
+    const bool some = __any_sync(kFull, live);
+    for (int i = 0; i < 2 * nI && ok && !some; ++i) {  // no row of the warp is asked for: any P does
+      if ((ok = wait_w(&sfull[2 * t + (i & 1)], i >> 1))) mbar_arrive(&pfull[2 * t + (i & 1)]);
+    }
+    for (int i = 0; i < nI && ok && some; ++i) {
       const int j = jb[t] + i;
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
@@ -608,19 +612,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
         const uint32_t bm = (bm8 >> (4 * h)) & 15u;
         const int k0 = list.col(lp) * kTok;
         // the row sees all 64 keys: four consecutive pages inside its window, or of its first tokens
-        const bool whole = live && bm == 0u && k0 + 63 <= pos &&
-                           (lp >= list.sink ? k0 >= lo : lp + 3 < list.sink && k0 + 63 < p.sinks);
+        const bool whole = (bm == 0u && k0 + 63 <= pos &&
+                                     (lp >= list.sink ? k0 >= lo : lp + 3 < list.sink && k0 + 63 < p.sinks));
         if (!whole) {
 #pragma unroll
           for (int e4 = 0; e4 < 4; ++e4) {
             const int kp0 = list.col(lp + e4) * kTok;
-            const bool page = live && !(bm >> e4 & 1u);
+            auto below = [&](int end) { return (1u << min(max(end - kp0, 0), kTok)) - 1u; };  // keys before `end`
+            const uint32_t seen = bm >> e4 & 1u ? 0u : below(pos + 1) & (~below(lo) | below(p.sinks));
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int kp = kp0 + e;
-              const bool seen = page && kp <= pos && (kp >= lo || kp < p.sinks);
-              x[16 * e4 + e] = seen ? x[16 * e4 + e] : -INFINITY;
-            }
+            for (int e = 0; e < 16; ++e)
+              x[16 * e4 + e] = seen >> e & 1u ? x[16 * e4 + e] : -INFINITY;
           }
         }
         // Weights against the maximum so far, which grows rarely, and the half's own maximum
