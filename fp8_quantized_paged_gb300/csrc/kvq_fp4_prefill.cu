@@ -5,17 +5,19 @@
 namespace kvq {
 namespace fp4 {
 
-constexpr int kMinBlocks = 2;  // least key blocks of a share
+constexpr int kMinShare = 2;    // least key blocks of a share where SMs would idle
+constexpr int kMinTail = 24;    // and where they would after the last whole wave
+constexpr int kOverhead = 6;    // a share's start, end and merge, in blocks
 
 template <int DH>
-static int launch_prefill(const PreParams& p, cudaStream_t s) {
+static int launch_prefill(const PreParams& p, int64_t ctas, cudaStream_t s) {
   static DeviceOnce once;
   if (!once.run(current_device(), [] {
         return cudaFuncSetAttribute(prefill_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     PreSmem<DH>::total) == cudaSuccess;
       }))
     return KVQ_ERR_CUDA;
-  const dim3 grid(p.groups * p.ns, p.Hkv, p.B), block(kPreThreads);
+  const dim3 grid(static_cast<unsigned>(ctas)), block(kPreThreads);
   if (launch_pdl(prefill_kernel<DH>, grid, block, PreSmem<DH>::total, s, p) != cudaSuccess)
     return KVQ_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
@@ -47,7 +49,7 @@ extern "C" int kvq_fp4_prefill_attn(const void* q, const int32_t* cu_q_lens, int
   if (num_seqs > 65535) return KVQ_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(max_blocks_per_seq) * fp4::kTok >= (int64_t(1) << 30))
     return KVQ_ERR_UNSUPPORTED;
-  if (num_q_tokens >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
+  if (num_q_tokens > (int64_t(1) << 30)) return KVQ_ERR_UNSUPPORTED;
   const int G = num_q_heads / num_kv_heads, sms = device_sm_count();
   if (sms <= 0) return KVQ_ERR_CUDA;
   const fp4::PreWs wl = fp4::pre_ws(head_dim, sms);
@@ -76,14 +78,35 @@ extern "C" int kvq_fp4_prefill_attn(const void* q, const int32_t* cu_q_lens, int
   // Two tiles a CTA share each converted block.
   p.tpc = p.tiles > 1 ? fp4::kTiles : 1;
   p.groups = (p.tiles + p.tpc - 1) / p.tpc;
-  // Fewer CTAs than SMs: their blocks are shared out, at least kMinBlocks each.
-  const int64_t ctas = static_cast<int64_t>(p.groups) * num_kv_heads * num_seqs;
+  const int64_t items = static_cast<int64_t>(p.groups) * num_kv_heads * num_seqs;
   int64_t pages = max_blocks_per_seq;
   if (sliding_window > 0)
     pages = std::min<int64_t>(pages, (static_cast<int64_t>(sliding_window) + static_cast<int64_t>(p.tpc) * TQ) / fp4::kTok +
                                          2 + (static_cast<int64_t>(num_sinks) + fp4::kTok - 1) / fp4::kTok);
   const int64_t blocks = (pages + fp4::kBlkPages - 1) / fp4::kBlkPages;
-  p.ns = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms / ctas, blocks / fp4::kMinBlocks)));
+  // Items are whole while they fill waves of a CTA per SM; the rest, where it would leave SMs
+  // idle, shares its keys out.  A single, partial wave takes what SMs there are; after whole
+  // waves the split is the one that ends first (a split's rounds times a share's length).
+  p.whole = items;
+  p.ns = 1;
+  p.min_share = fp4::kMinTail;
+  const int64_t rest = items % sms;
+  if (items < sms) {
+    p.ns = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms / items, blocks / fp4::kMinShare)));
+    p.min_share = fp4::kMinShare;
+  } else {
+    double best = static_cast<double>(blocks + fp4::kOverhead);
+    for (int64_t n = 2; rest > 0 && rest * n <= static_cast<int64_t>(fp4::kShares) * sms && n * fp4::kMinTail <= blocks; ++n) {
+      const double t = static_cast<double>((rest * n + sms - 1) / sms) * (static_cast<double>(blocks) / n + fp4::kOverhead);
+      if (t < best) {
+        best = t;
+        p.ns = static_cast<int>(n);
+      }
+    }
+  }
+  if (p.ns > 1) p.whole = items - rest;
+  const int64_t ctas = p.whole + (items - p.whole) * p.ns;
+  if (ctas >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
   p.ks = k_scale;
   p.vs = v_scale;
   p.per_head = scale_granularity == KVQ_SCALE_PER_HEAD;
@@ -95,5 +118,5 @@ extern "C" int kvq_fp4_prefill_attn(const void* q, const int32_t* cu_q_lens, int
   p.out = static_cast<uint16_t*>(out);
   p.status = dev_status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return head_dim == 128 ? fp4::launch_prefill<128>(p, s) : fp4::launch_prefill<64>(p, s);
+  return head_dim == 128 ? fp4::launch_prefill<128>(p, ctas, s) : fp4::launch_prefill<64>(p, ctas, s);
 }

@@ -62,26 +62,29 @@ struct PreParams {
   int window, sinks;
   int tiles;   // tiles of the longest chunk
   int tpc;     // tiles of a CTA
-  int groups;  // CTAs that cover the tiles
-  int ns;      // shares of the keys
+  int groups;  // items of a sequence and KV head: tpc tiles each
+  int64_t whole;   // items that one CTA each takes, the first ones
+  int ns;          // shares of the keys of the items after them, at most
+  int min_share;   // blocks of a share, at least
   const float* ks;
   const float* vs;
   int per_head;
   float logit_scale;  // log2(e) / sqrt(dh)
-  uint32_t* ws_cnt;   // [B * Hkv * groups] arrivals (ns > 1)
-  float2* ws_ml;      // [CTA][kTiles * kRows]
-  float* ws_o;        // [CTA][kTiles * kRows][DH]
+  uint32_t* ws_cnt;   // [shared item] arrivals
+  float2* ws_ml;      // [share][kTiles * kRows]
+  float* ws_o;        // [share][kTiles * kRows][DH]
   uint16_t* out;
   uint32_t* status;
 };
 
-// Workspace: the arrival counters (kvq_decode_attn's table), then per CTA of a
-// call that shares out its keys (at most one per SM) the states of its rows.
+// Workspace: the arrival counters (kvq_decode_attn's table), then the states of the rows
+// of each share, at most kShares per SM.
+constexpr int kShares = 3;
 struct PreWs {
   size_t ml, o, total;
 };
 inline PreWs pre_ws(int DH, int sms) {
-  const size_t rows = static_cast<size_t>(sms) * kTiles * kRows;
+  const size_t rows = static_cast<size_t>(sms) * kShares * kTiles * kRows;
   PreWs w;
   w.ml = KVQ_WS_COUNTER_BYTES;
   w.o = w.ml + round256(rows * sizeof(float2));
@@ -286,9 +289,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
   // needs this softmax's own later progress.
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.z, gkv = blockIdx.y;
-  const int share = static_cast<int>(blockIdx.x) % p.ns;
-  const int group = p.groups - 1 - static_cast<int>(blockIdx.x) / p.ns;  // longest first
+  const int64_t cta = blockIdx.x;
+  const int64_t shared = cta < p.whole ? 0 : (cta - p.whole) / p.ns;  // which of the shared items
+  const int64_t item = cta < p.whole ? cta : p.whole + shared;
+  const int share = cta < p.whole ? 0 : static_cast<int>((cta - p.whole) % p.ns);
+  const int group = p.groups - 1 - static_cast<int>(item % p.groups);  // longest first
+  const int b = static_cast<int>(item / p.groups / p.Hkv), gkv = static_cast<int>(item / p.groups % p.Hkv);
   const int TQ = kRows / p.G;  // query tokens of a tile
 
   if (tid == 0) {
@@ -320,7 +326,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
   const int q0 = __ldg(p.cu_q + b);
   const int n = __ldg(p.cu_q + b + 1) - q0;
   const int j0 = group * p.tpc * TQ;  // first query token of tile 0
-  if (blockIdx.x == 0 && gkv == 0 && tid == 0 && n > p.tiles * TQ)
+  if (group == 0 && share == 0 && gkv == 0 && tid == 0 && n > p.tiles * TQ)
     flag_status(p.status, KVQ_DEV_BAD_QLEN);
   if (n <= 0 || j0 >= min(n, p.tiles * TQ) || q0 < 0 || static_cast<int64_t>(q0) + n > p.total_q) return;
   const int nc = min(n, p.tiles * TQ);  // query tokens that the grid covers
@@ -340,9 +346,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
   const Visible v0 = visible(p.window, p.sinks, base + j0 + 1);
   const PageList list = {v0.sink, v0.first, v0.sink + (base + j1 - 1) / kTok - v0.first + 1};
   const int nall = (list.count + kBlkPages - 1) / kBlkPages;
+  // few blocks need fewer CTAs
+  const int ns = cta < p.whole ? 1 : max(1, min(p.ns, nall / p.min_share));
+  if (share >= ns) return;
   // this CTA's blocks [c0, c1) and tile t's [jb, je) of them
-  const int c0 = static_cast<int>(static_cast<int64_t>(nall) * share / p.ns);
-  const int c1 = static_cast<int>(static_cast<int64_t>(nall) * (share + 1) / p.ns);
+  const int c0 = static_cast<int>(static_cast<int64_t>(nall) * share / ns);
+  const int c1 = static_cast<int>(static_cast<int64_t>(nall) * (share + 1) / ns);
   const int nb = c1 - c0;
   int jb[kTiles], je[kTiles];
 #pragma unroll
@@ -688,12 +697,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     if (!ok) fail();
     // ---- epilogue: the row of O, normalised, or (keys shared out) as it is
     const float sv = __ldg(p.vs + (p.per_head ? gkv : 0));
-    const float f = p.ns > 1 ? 1.f : (l > 0.f ? sv / l : 0.f);
-    const int64_t cta = (static_cast<int64_t>(b) * p.Hkv + gkv) * gridDim.x + blockIdx.x;
-    const int64_t part = cta * (kTiles * kRows) + t * kRows + r;
+    const float f = ns > 1 ? 1.f : (l > 0.f ? sv / l : 0.f);
+    const int64_t part = (cta - p.whole) * (kTiles * kRows) + t * kRows + r;
     tc::tc_fence_after();
     if (ok) {
-      if (p.ns > 1 && live) p.ws_ml[part] = make_float2(m, l);
+      if (ns > 1 && live) p.ws_ml[part] = make_float2(m, l);
 #pragma unroll 1
       for (int c = 0; c < DH; c += 32) {
         float o[32];
@@ -720,7 +728,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
             }
           }
         }
-        if (live && p.ns == 1) {
+        if (live && ns == 1) {
           uint4* dst = reinterpret_cast<uint4*>(p.out + qrow * DH + c);
 #pragma unroll
           for (int y = 0; y < 4; ++y)
@@ -748,13 +756,13 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, kTmemCols);
   }
-  if (p.ns == 1) return;
+  if (ns == 1) return;
 
   // ---- the CTA that completes a tile group merges its shares: the barriers above
   // order every thread's stores before thread 0's acquire-release arrival
-  const int64_t first = (static_cast<int64_t>(b) * p.Hkv + gkv) * gridDim.x + (blockIdx.x - share);
-  uint32_t* cnt = p.ws_cnt + (static_cast<int64_t>(b) * p.Hkv + gkv) * p.groups + group;
-  if (tid == 0) *merge_s = atom_add_acq_rel_gpu(cnt, 1u) + 1 == static_cast<uint32_t>(p.ns);
+  const int64_t first = cta - p.whole - share;
+  uint32_t* cnt = p.ws_cnt + shared;
+  if (tid == 0) *merge_s = atom_add_acq_rel_gpu(cnt, 1u) + 1 == static_cast<uint32_t>(ns);
   __syncthreads();
   if (!*merge_s) return;
   if (tid == 0) *cnt = 0u;
@@ -767,7 +775,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     if (t >= p.tpc || r >= TQ * p.G || jr >= nc) continue;
     float M = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int y = 0; y < p.ns; ++y) {
+#pragma unroll 4
+    for (int y = 0; y < ns; ++y) {
       const int64_t at = (first + y) * rows + row;
       const float2 ml = __ldcg(p.ws_ml + at);
       const float4 v = __ldcg(reinterpret_cast<const float4*>(p.ws_o + at * DH) + e);

@@ -353,6 +353,22 @@ def test_prefill_chunks(kvq, lens, counts, hq, hkv, dh, window, sinks):
     assert torch.equal(first, g.out)
 
 
+@pytest.mark.parametrize("dh,longest_last", [(64, True), (64, False), (128, True)])
+def test_prefill_more_items_than_sms(kvq, dh, longest_last):
+    """160 sequences on shared pages: a whole wave, and a rest whose keys are shared out
+    where they are many."""
+    b = f4.Batch(21 + dh, [6300], 8, 1, dh)
+    b.table = np.repeat(b.table, 160, 0)
+    b.lens = (300 + 37 * np.arange(160)[:: 1 if longest_last else -1]).astype(np.int32)
+    g = OnGpu(kvq, b, [1 + i % 3 for i in range(160)])
+    g.prefill()
+    g.check(what="first")
+    first = g.out.clone()
+    g.prefill()
+    torch.cuda.synchronize()
+    assert torch.equal(first, g.out)
+
+
 def test_prefill_bad_blocks_lengths_and_rows_behind(kvq):
     b = f4.Batch(15, [100, 100, 40, 16], 8, 2, 128)
     g = OnGpu(kvq, b, [20, 100, 10, 16])
