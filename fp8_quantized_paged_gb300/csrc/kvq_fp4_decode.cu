@@ -6,8 +6,11 @@
 namespace kvq {
 namespace fp4 {
 
-// Segments of at most this many pages, with an SM each, go whole to one CTA.
+// Segments of at most this many pages, with an SM each, go whole to one CTA, without a plan.
 constexpr int kSegPages = 128;
+// Most pieces of a segment that units of several heads may leave.  One sequence of 32768 tokens,
+// 8 KV heads: one head a unit (19 pieces) 19.1 us, two 24.5, eight (152 pieces) 70.8.
+constexpr int kMaxPieces = 10;
 constexpr int kMaxSmem = 227 * 1024 - 1024;  // the static part and the system's
 
 template <int DH>
@@ -16,7 +19,7 @@ static int launch_decode(DecParams p, bool fix, int grid, cudaStream_t s) {
   if (!once.run(current_device(), [] {
         auto configure = [](auto kernel) {
           return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      kMaxSmem / kDecCtas) == cudaSuccess &&
+                                      kMaxSmem) == cudaSuccess &&
                  cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                                       cudaSharedmemCarveoutMaxShared) == cudaSuccess;
         };
@@ -26,8 +29,8 @@ static int launch_decode(DecParams p, bool fix, int grid, cudaStream_t s) {
   const int rings = kDecWarps / p.HG;
   const int fixed = dec_smem<DH>(0, p.HG, p.G, p.B, fix).total + 32;  // (all but the slots, and their rounding)
   const int slot = 2 * p.HG * Page<DH>::kBytes + 24;
-  p.depth = std::min(kMaxDepth, (kMaxSmem / kDecCtas - fixed) / slot / rings);
-  if (p.depth < KVQ_FP4_NP) return KVQ_ERR_UNSUPPORTED;  // (a step holds so many slots; not reached)
+  p.depth = std::min(kMaxDepth, (kMaxSmem - fixed) / slot / rings);
+  if (p.depth < kStepUnits) return KVQ_ERR_UNSUPPORTED;  // (a step holds so many slots; not reached)
   const size_t smem = dec_smem<DH>(p.depth * rings, p.HG, p.G, p.B, fix).total;
   const cudaError_t e =
       fix ? launch_pdl(decode_kernel<DH, true>, dim3(grid), dim3(kDecThreads), smem, s, p)
@@ -49,7 +52,7 @@ extern "C" size_t kvq_fp4_workspace_size(int num_seqs, int num_q_heads, int num_
   if (num_sms <= 0) num_sms = device_sm_count();
   if (num_sms <= 0) return 0;
   return std::max(fp4::dec_ws(num_seqs, num_q_heads / num_kv_heads, num_kv_heads, head_dim,
-                              fp4::kDecCtas * num_sms).total,
+                              num_sms).total,
                   fp4::pre_ws(head_dim, num_sms).total);
 }
 
@@ -69,11 +72,12 @@ extern "C" int kvq_fp4_decode_attn(const void* q, const void* k_cache, const voi
   if (st != KVQ_OK) return st;
   if (num_seqs > kMaxSeqs || num_seqs * num_kv_heads > kMaxSegments) return KVQ_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(num_seqs) * (static_cast<int64_t>(max_blocks_per_seq) + fp4::kPc) *
-          num_kv_heads >= (int64_t(1) << 31))
+          num_kv_heads >= (int64_t(1) << 31) ||
+      static_cast<int64_t>(max_blocks_per_seq) * fp4::kTok >= (int64_t(1) << 31))
     return KVQ_ERR_UNSUPPORTED;
   const int G = num_q_heads / num_kv_heads, sms = device_sm_count();
   if (sms <= 0) return KVQ_ERR_CUDA;
-  const int P = fp4::kDecCtas * sms;
+  const int P = sms;
   const fp4::DecWs wl = fp4::dec_ws(num_seqs, G, num_kv_heads, head_dim, P);
   if (workspace_bytes < wl.total) return KVQ_ERR_WORKSPACE;
 
@@ -84,24 +88,20 @@ extern "C" int kvq_fp4_decode_attn(const void* q, const void* k_cache, const voi
                                          (static_cast<int64_t>(num_sinks) + fp4::kTok - 1) / fp4::kTok);
   // One sequence, or short ones with an SM for each KV head: a number of CTAs for each, one head
   // a unit.  Else the units are split at equal cost, with as many heads a unit as leave a segment
-  // ten pieces or fewer.
+  // kMaxPieces pieces or fewer (32 sequences of 2049 tokens / 128 of mixed lengths: one head a unit
+  // 38.3 / 119 us, two 32.0 / 79.1, four 31.2 / 66.9, eight 30.7 / 62.9).
   const int segs = num_seqs * num_kv_heads;
   const bool fix = segs <= P && (num_seqs == 1 || pages <= fp4::kSegPages);
   int HG = 1, cps = 1;
-#ifdef X_HG
-  HG = fix ? 1 : X_HG;
-#endif
   if (fix) {
     if (num_seqs == 1)
       cps = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(P / segs, pages / fp4::kMinUnits)));
-  } else if (HG == 1) {
-#ifndef X_HG
+  } else {
     for (int h = fp4::kMaxHeads; h > 1; h /= 2)
-      if (num_kv_heads % h == 0 && segs / h * 10 >= P) {
+      if (num_kv_heads % h == 0 && segs / h * fp4::kMaxPieces >= P) {
         HG = h;
         break;
       }
-#endif
   }
   const int64_t units = static_cast<int64_t>(segs / HG) * pages;
   const int64_t ctas = fix ? static_cast<int64_t>(segs) * cps

@@ -14,15 +14,25 @@
 // others (one sequence) or short, the host gives each a number of CTAs of its
 // own and there is no plan to build (FIX).
 //
-// Consumer warp w of a CTA's 16 works on head w % HG of every (16 / HG)th unit
-// from w / HG on.  The HG warps of a unit share a ring of shared memory, which a
-// producer warp fills (one bulk copy for the heads' K, one for their V) as they
-// let go of its slots; there is no other barrier before a segment ends.  Then the
-// 16 / HG warps of a head merge their states.  HG trades the two ends: eight heads
-// a unit make few, long copies and states that two warps share; one head makes the
-// fewest pieces per segment where few sequences are cut over many CTAs.
+// Consumer warp w of a CTA's 8 works on head w % HG of every (8 / HG)th unit from
+// w / HG on, four units a step.  The HG warps of a unit share a ring of shared
+// memory, which a producer warp fills (one bulk copy for the heads' K, one for
+// their V) as they let go of its slots; there is no other barrier before a segment
+// ends.  Then the 8 / HG warps of a head merge their states.  HG trades the two
+// ends: eight heads a unit make few, long copies and no states to merge in a CTA; one
+// head makes the fewest pieces per segment where few sequences are cut over many CTAs.
 // The producer has a warpgroup of its own and leaves its registers to the
-// consumers (setmaxnreg: 640 threads launch with 96 each; the loop needs 112).
+// consumers (setmaxnreg: 384 threads launch with 168 each; a step of four pages
+// takes over 200).
+//
+// What bounds it: the conversions.  A page takes a warp about 265 instructions, half
+// of them at half rate (64 conversions of two values, 64 products by scales, 16 matrix
+// steps); the loop alone needs 296 cycles a page and SM quarter with two warps there
+// (411 with one page a step), and about 450 in place, among copies and waits.  32 sequences
+// of 2049 tokens, 8 KV heads: 30.7 us (11.2 us at the measured bandwidth); of them
+// 2.5 the plan and the block ids, 2.3 the first pages, 16 the loop, 5 the states of
+// cut segments.  128 sequences of 17 to 16384 tokens under a window: 63.0 us (31.5).
+// One of 32768: 19.1 us (5.6).
 //
 // Per page, 16 tokens against the group's G <= 8 query heads:
 //   S = K^ Q^T  m16n8k16 f16 matrix steps: lane (g, t) converts the codes of
@@ -45,26 +55,17 @@
 namespace kvq {
 namespace fp4 {
 
-#ifndef KVQ_FP4_WARPS
-#define KVQ_FP4_WARPS 8
-#endif
-#ifndef KVQ_FP4_CTAS
-#define KVQ_FP4_CTAS 1
-#endif
-#ifndef KVQ_FP4_NP
-#define KVQ_FP4_NP 4
-#endif
-#ifndef KVQ_FP4_PC
-#define KVQ_FP4_PC 8
-#endif
-constexpr int kDecWarps = KVQ_FP4_WARPS;
-constexpr int kDecThreads = kDecWarps * 32 + 128;  // consumers, the producer's warpgroup
+constexpr int kDecWarps = 8;                       // consumers: a step of four pages needs their registers
+constexpr int kDecThreads = kDecWarps * 32 + 128;  // and the producer's warpgroup
 constexpr int kConsumerRegs = 224, kProducerRegs = 40;  // 256 x 224 + 128 x 40 <= 384 x 168
-constexpr int kDecCtas = KVQ_FP4_CTAS;  // CTAs per SM
-constexpr int kPc = KVQ_FP4_PC;         // fixed cost of a piece, in pages
+// Units of a step, and the fixed cost of a piece in pages.  32 sequences of 2049 tokens / 128 of
+// mixed lengths: one unit 33.0 / 69.8 us, two 31.7 / 65.9, four 30.7 / 62.9, five 31.2 / 64.9;
+// a cost of 4 32.4 / 62.9, 8 30.7 / 62.9, 16 32.1 / 66.6.
+constexpr int kStepUnits = 4;
+constexpr int kPc = 8;
 constexpr int kMaxHeads = 8;            // most KV heads of a unit
 constexpr int kMaxDepth = 12;           // most slots of a ring
-constexpr int kMinUnits = 32;           // least units of a CTA that shares a segment: two a warp
+constexpr int kMinUnits = 32;           // least units of a CTA that shares a segment: a step a warp
 constexpr float kPBias = 7.f;           // log2 of the factor that the weights carry
 
 struct DecParams {
@@ -394,11 +395,14 @@ KVQ_DEVI void store_out(uint16_t* dst, const State& a, float sv) {
 }
 
 KVQ_DEVI void head_barrier(int head, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(head + 1), "r"(threads) : "memory");
+  if (threads == 32)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(head + 1), "r"(threads) : "memory");
 }
 
 // The producer: copies the CTA's units into the rings.  Unit i of the run belongs to
-// ring i % (16 / HG), as its unit k = i / (16 / HG), in slot k % depth.  Lane j takes
+// ring i % (8 / HG), as its unit k = i / (8 / HG), in slot k % depth.  Lane j takes
 // units j, j + 32, ..., each as soon as its slot is free, the block ids looked up 32
 // units ahead.  A lane looks at its slot's phase only once the unit that the slot held
 // last has been copied (all units below the first pending one have): the phase before
@@ -475,7 +479,7 @@ KVQ_DEVI void decode_run(const DecParams& p, uint8_t* smem, const DecSmem& sm, u
                          const int32_t* voff, int u0, int u1, int V, int Pe, int fix_np, const Segment& segment) {
   using PG = Page<DH>;
   constexpr int MT = DH / 16;
-  constexpr int kNP = KVQ_FP4_NP;  // units of a step
+  constexpr int kNP = kStepUnits;
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int half = p.HG * PG::kBytes, slot_bytes = 2 * half;
   const int g = lane >> 2, t = lane & 3;
@@ -642,6 +646,34 @@ KVQ_DEVI void decode_run(const DecParams& p, uint8_t* smem, const DecSmem& sm, u
       st.l[0] += __shfl_xor_sync(kFull, st.l[0], d);
       st.l[1] += __shfl_xor_sync(kFull, st.l[1], d);
     }
+    uint16_t* orow = p.out + (static_cast<int64_t>(b) * p.Hq + gkv * p.G) * DH;
+    const int sigma = b * p.Hkv + gkv;
+    const int64_t seg = FIX ? 0 : static_cast<int64_t>(b) * p.NG + gr;
+    const int64_t mine = (c + seg) * p.HG + head;  // partial slot
+    if (wph == 1) {  // a warp has the head to itself: its state is the piece's
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int h = 2 * t + e;
+        if (h >= p.G) continue;
+        if (np == 1) {
+          const float f = st.l[e] > 0.f ? sv / st.l[e] : 0.f;
+          uint4* dst = reinterpret_cast<uint4*>(orow + h * DH + g * (DH / 8));
+#pragma unroll
+          for (int mt = 0; mt < MT; mt += 4)
+            dst[mt / 4] = make_uint4(f32x2_to_bf16x2(o[mt][e] * f, o[mt][2 + e] * f),
+                                     f32x2_to_bf16x2(o[mt + 1][e] * f, o[mt + 1][2 + e] * f),
+                                     f32x2_to_bf16x2(o[mt + 2][e] * f, o[mt + 2][2 + e] * f),
+                                     f32x2_to_bf16x2(o[mt + 3][e] * f, o[mt + 3][2 + e] * f));
+        } else {
+          if (g == 0)  // m in log2 units
+            p.ws_ml[mine * p.G + h] = make_float2(st.m[e] == -INFINITY ? -INFINITY : st.m[e] * pv.ls[e], st.l[e]);
+          float4* dst = reinterpret_cast<float4*>(p.ws_o + (mine * p.G + h) * DH + g * (DH / 8));
+#pragma unroll
+          for (int mt = 0; mt < MT; mt += 2)
+            dst[mt / 2] = make_float4(o[mt][e], o[mt][2 + e], o[mt + 1][e], o[mt + 1][2 + e]);
+        }
+      }
+    } else {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int h = 2 * t + e;
@@ -654,10 +686,6 @@ KVQ_DEVI void decode_run(const DecParams& p, uint8_t* smem, const DecSmem& sm, u
         *reinterpret_cast<float2*>(dst + 2 * mt) = make_float2(o[mt][e], o[mt][2 + e]);
     }
     head_barrier(head, hthreads);
-    uint16_t* orow = p.out + (static_cast<int64_t>(b) * p.Hq + gkv * p.G) * DH;
-    const int sigma = b * p.Hkv + gkv;
-    const int64_t seg = FIX ? 0 : static_cast<int64_t>(b) * p.NG + gr;
-    const int64_t mine = (c + seg) * p.HG + head;  // partial slot
     for (int e = htid; e < n4; e += hthreads) {  // a float4 of one query head's output
       const int h = 4 * e / DH;
       State a[1];
@@ -673,6 +701,7 @@ KVQ_DEVI void decode_run(const DecParams& p, uint8_t* smem, const DecSmem& sm, u
         reinterpret_cast<float4*>(p.ws_o)[mine * n4 + e] = a[0].o;
         if (4 * e % DH == 0) p.ws_ml[mine * p.G + h] = make_float2(a[0].m, a[0].l);
       }
+    }
     }
     head_barrier(head, hthreads);
     if (np > 1) {
@@ -709,7 +738,7 @@ KVQ_DEVI void decode_run(const DecParams& p, uint8_t* smem, const DecSmem& sm, u
 }
 
 template <int DH, bool FIX>
-__global__ void __launch_bounds__(kDecThreads, kDecCtas) decode_kernel(const __grid_constant__ DecParams p) {
+__global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_constant__ DecParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t warp_tot[kDecThreads / 32];
   __shared__ int32_t bounds[2];

@@ -50,7 +50,13 @@ extern "C" int kvq_fp4_prefill_attn(const void* q, const int32_t* cu_q_lens, int
   if (static_cast<int64_t>(max_blocks_per_seq) * fp4::kTok >= (int64_t(1) << 30))
     return KVQ_ERR_UNSUPPORTED;
   if (num_q_tokens > (int64_t(1) << 30)) return KVQ_ERR_UNSUPPORTED;
-  const int G = num_q_heads / num_kv_heads, sms = device_sm_count();
+  const int G = num_q_heads / num_kv_heads, TQ = fp4::kRows / G;
+  const int64_t tiles = (std::min<int64_t>(max_q_len, num_q_tokens) + TQ - 1) / TQ;
+  // Two tiles a CTA share each converted block.
+  const int tpc = tiles > 1 ? fp4::kTiles : 1;
+  const int64_t groups = (tiles + tpc - 1) / tpc, items = groups * num_kv_heads * num_seqs;
+  if (items >= (int64_t(1) << 31) - 65536) return KVQ_ERR_UNSUPPORTED;  // (the grid)
+  const int sms = device_sm_count();
   if (sms <= 0) return KVQ_ERR_CUDA;
   const fp4::PreWs wl = fp4::pre_ws(head_dim, sms);
   if (workspace_bytes < wl.total) return KVQ_ERR_WORKSPACE;
@@ -72,16 +78,12 @@ extern "C" int kvq_fp4_prefill_attn(const void* q, const int32_t* cu_q_lens, int
   p.total_q = num_q_tokens;
   p.window = sliding_window;
   p.sinks = num_sinks;
-  const int64_t longest = std::min<int64_t>(max_q_len, num_q_tokens);
-  const int TQ = fp4::kRows / G;
-  p.tiles = static_cast<int>((longest + TQ - 1) / TQ);
-  // Two tiles a CTA share each converted block.
-  p.tpc = p.tiles > 1 ? fp4::kTiles : 1;
-  p.groups = (p.tiles + p.tpc - 1) / p.tpc;
-  const int64_t items = static_cast<int64_t>(p.groups) * num_kv_heads * num_seqs;
+  p.tiles = static_cast<int>(tiles);
+  p.tpc = tpc;
+  p.groups = static_cast<int>(groups);
   int64_t pages = max_blocks_per_seq;
   if (sliding_window > 0)
-    pages = std::min<int64_t>(pages, (static_cast<int64_t>(sliding_window) + static_cast<int64_t>(p.tpc) * TQ) / fp4::kTok +
+    pages = std::min<int64_t>(pages, (static_cast<int64_t>(sliding_window) + static_cast<int64_t>(tpc) * TQ) / fp4::kTok +
                                          2 + (static_cast<int64_t>(num_sinks) + fp4::kTok - 1) / fp4::kTok);
   const int64_t blocks = (pages + fp4::kBlkPages - 1) / fp4::kBlkPages;
   // Items are whole while they fill waves of a CTA per SM; the rest, where it would leave SMs
@@ -106,7 +108,6 @@ extern "C" int kvq_fp4_prefill_attn(const void* q, const int32_t* cu_q_lens, int
   }
   if (p.ns > 1) p.whole = items - rest;
   const int64_t ctas = p.whole + (items - p.whole) * p.ns;
-  if (ctas >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
   p.ks = k_scale;
   p.vs = v_scale;
   p.per_head = scale_granularity == KVQ_SCALE_PER_HEAD;

@@ -144,7 +144,8 @@ KVQ_API size_t kvq_fp4_workspace_size(int num_seqs, int num_q_heads, int num_kv_
  * power of two, as in kvq_decode_attn); each probability reaches the product
  * with V^ as one f16, within 2^-11 of its value or 2^-32 of the row's largest.
  * Limits: num_seqs <= 4096; num_seqs * num_kv_heads <= 65536; num_seqs *
- * (max_blocks_per_seq + 16) * num_kv_heads < 2^31; num_kv_heads <= 256.
+ * (max_blocks_per_seq + 8) * num_kv_heads < 2^31; num_kv_heads <= 256;
+ * max_blocks_per_seq * block_size < 2^31.
  */
 KVQ_API int kvq_fp4_decode_attn(const void* q, const void* k_cache, const void* v_cache,
                                 const int32_t* block_tables, int max_blocks_per_seq,
@@ -180,8 +181,9 @@ KVQ_API int kvq_fp4_decode_attn(const void* q, const void* k_cache, const void* 
  *   dev_status     optional; KVQ_DEV_BAD_BLOCK, KVQ_DEV_BAD_SEQLEN (L_b < n_b
  *                  or L_b > max_blocks_per_seq * block_size: zero rows),
  *                  KVQ_DEV_BAD_QLEN, KVQ_DEV_WAIT_TIMEOUT
- * Precision as for kvq_fp4_decode_attn.  Limits: num_seqs <= 65535,
- * num_kv_heads <= 256, max_blocks_per_seq * block_size < 2^30.
+ * Precision as for kvq_fp4_decode_attn.  Limits: num_seqs <= 65535;
+ * num_kv_heads <= 256; max_blocks_per_seq * block_size < 2^30; num_q_tokens
+ * <= 2^30; num_seqs * num_kv_heads * (max_q_len / 16 + 1) < 2^31.
  */
 KVQ_API int kvq_fp4_prefill_attn(const void* q, const int32_t* cu_q_lens, int64_t num_q_tokens,
                                  int max_q_len, const void* k_cache, const void* v_cache,

@@ -95,9 +95,11 @@ CASES = {
                       (dict(B=0), ARG), (dict(mb=0), ARG), (dict(stride=1016), SHAPE), (dict(stride=1026), ALIGN),
                       (dict(ko=A + 4), ALIGN), (dict(cu=A + 1), ALIGN), (dict(starts=A + 3), ALIGN), (dict(stride=1 << 60), SHAPE)],
     "decode": ATTN + [(dict(B=5000), UNSUPPORTED), (dict(B=4096, mb=1 << 20), UNSUPPORTED),
-                      (dict(B=4000, hkv=32, ksl=32, vsl=32), UNSUPPORTED)],
+                      (dict(B=4000, hkv=32, ksl=32, vsl=32), UNSUPPORTED),
+                      (dict(B=1, hkv=1, hq=8, ksl=1, vsl=1, mb=1 << 27), UNSUPPORTED)],
     "prefill": ATTN + [(dict(cu=0), NULL), (dict(cu=A + 2), ALIGN), (dict(n=-1), ARG), (dict(maxq=-1), ARG),
-                       (dict(B=70000), UNSUPPORTED), (dict(mb=1 << 27), UNSUPPORTED), (dict(n=1 << 40), UNSUPPORTED)],
+                       (dict(B=70000), UNSUPPORTED), (dict(mb=1 << 27), UNSUPPORTED), (dict(n=1 << 40), UNSUPPORTED),
+                       (dict(n=(1 << 30) + 1), UNSUPPORTED), (dict(B=65535, n=1 << 30, maxq=1 << 30), UNSUPPORTED)],
 }
 
 
