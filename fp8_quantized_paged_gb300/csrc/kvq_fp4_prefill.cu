@@ -5,9 +5,16 @@
 namespace kvq {
 namespace fp4 {
 
-constexpr int kMinShare = 2;    // least key blocks of a share where SMs would idle
-constexpr int kMinTail = 24;    // and where they would after the last whole wave
-constexpr int kOverhead = 6;    // a share's start, end and merge, in blocks
+// Least key blocks of a share where SMs would idle, by the tiles of an item: the merge of 256 rows
+// takes about 15 us, of a few rows 3.  One sequence, 8 KV heads, 4 queries over 1024 tokens (8
+// blocks): shares of 2 blocks 11.4 us, of 4 14.2, none 17.6; over 4096 13.5, 14.6, 31.2.  64 queries
+// (two tiles) over 1024: shares of 2 32.4, of 4 35.4, none 27.4; over 2048 39.0, 35.9, 41.4.
+constexpr int kMinShare[2] = {2, 5};
+// And where they would after the last whole wave.  Ragged chunks under a window (10 blocks, 220
+// items): whole 41.5 us, the rest in two 47.2.  2048 queries over 32768 tokens (256 blocks, 256
+// items): whole 919 us, the rest in four 858.
+constexpr int kMinTail = 24;
+constexpr int kOverhead = 6;  // a share's start, end and merge, in blocks
 
 template <int DH>
 static int launch_prefill(const PreParams& p, int64_t ctas, cudaStream_t s) {
@@ -94,8 +101,8 @@ extern "C" int kvq_fp4_prefill_attn(const void* q, const int32_t* cu_q_lens, int
   p.min_share = fp4::kMinTail;
   const int64_t rest = items % sms;
   if (items < sms) {
-    p.ns = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms / items, blocks / fp4::kMinShare)));
-    p.min_share = fp4::kMinShare;
+    p.ns = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms / items, blocks / fp4::kMinShare[tpc - 1])));
+    p.min_share = fp4::kMinShare[tpc - 1];
   } else {
     double best = static_cast<double>(blocks + fp4::kOverhead);
     for (int64_t n = 2; rest > 0 && rest * n <= static_cast<int64_t>(fp4::kShares) * sms && n * fp4::kMinTail <= blocks; ++n) {

@@ -3,16 +3,17 @@
 //
 //   O = softmax(q K^^T / sqrt(dh)) V^,  K^ = code * block scale * sK
 //
-// One CTA per (sequence, KV head, one or two tiles of query rows, share of the
-// keys).  A row is a (query token, query head of the group) pair, a tile 128
-// of them (128 / G tokens).  The visible pages of the CTA's rows (the first
-// tokens' pages, then the window's) form a list, taken in blocks of 8 pages =
-// 128 keys:
-//   warp 12 (producer)    copies a block's 8 K pages, then its 8 V pages (one
+// An item of work is one or two tiles of query rows of a sequence and KV head; a CTA
+// takes an item, or a share of its keys.  A row is a (query token, query head of the
+// group) pair, a tile 128 of them (128 / G tokens).  The visible pages of the CTA's
+// rows (the first tokens' pages, then the window's) form a list, taken in blocks of
+// 8 pages = 128 keys:
+//   warp 16 (producer)    copies a block's 8 K pages, then its 8 V pages (one
 //     bulk copy a page: codes and scales), into a ring of 3 stages
-//   warps 8-11 (converters)  code * block scale as f16 (exact), K and V both
-//     token-major in the 128-byte-swizzled layout, two buffers each
-//   warps 13, 14 (one per tile)  one lane each issues, for each half (64 keys) of a
+//   warps 8-11 and 12-15 (converters of K, of V)  code * block scale as f16 (exact),
+//     both token-major in the 128-byte-swizzled layout, two buffers each; K runs a
+//     block ahead, as its buffer is let go of half a block before V's
+//   warps 17, 18 (one per tile)  one lane each issues, for each half (64 keys) of a
 //     block, S = Q K^T (M 128, N 64) and, as the softmax delivers P, O += P V
 //     (A = P from tensor memory, K 64), then the half's next S at once
 //   warps 0-3, 4-7 (softmax of tiles 0, 1; thread = row = TMEM lane)  64 keys
@@ -20,12 +21,22 @@
 //     that it came from, with the running maximum m raised lazily (and O rescaled)
 // S and P share columns: 2 tiles x (2 halves of 64 + 128 of O) fill the 512.  A
 // half's next S waits for the PV that reads its P, while the softmax works on the
-// other half, so that the softmax (which bounds the loop: both tiles' 16384 weights
-// a block) hardly waits.
+// other half.  The softmax takes most registers (setmaxnreg).
 //
-// Where the tiles are fewer than the SMs, the host splits each tile's blocks
-// over several CTAs; each leaves (m, l, O) of its rows in the workspace and the
-// one that completes the tile merges them.
+// What bounds it: the matrix unit's operands.  An N 64 step reads 6 KB of shared
+// memory in 48 cycles (128 bytes a cycle, all there are), an N 128 step 8 KB in 64:
+// for the two tiles' block 32 x 48 + 16 x 64 = 2560 cycles, beside the converters'
+// stores and the copies; measured about 3600, with the unit 90% busy.  2048 queries
+// of 32 heads over 32768 tokens, 8 KV heads of 128 dims: 858 us, 1240 TFLOP/s (563 us
+// at the measured bf16 rate).  On the way: S in steps of N 128, tiles taking turns
+// 1201 us; halves 1106; issue under elect.sync, K and V converted by a warpgroup each
+// 927 (with one 1007); the rest after whole waves split 858.  S in one 64-column buffer with two
+// of P beside it 987.  Equal stretches of all items' keys for every SM instead of
+// whole items: 1107 where that was 1106, and small calls a third slower.
+//
+// Where items leave SMs idle the host splits their blocks over several CTAs; each
+// leaves (m, l, O) of its rows in the workspace and the one that completes the item
+// merges them.
 //
 // Every wait is bounded; a timeout sets KVQ_DEV_WAIT_TIMEOUT, the roles stop,
 // and the CTA waits (bounded) for copies and matrix steps in flight.
@@ -768,11 +779,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
   if (tid == 0) *cnt = 0u;
   const float sv = __ldg(p.vs + (p.per_head ? gkv : 0));
   const int rows = kTiles * kRows;
-  for (int i = tid; i < rows * (DH / 4); i += kPreThreads) {
-    const int row = i / (DH / 4), e = i - row * (DH / 4);
-    const int t = row / kRows, r = row - t * kRows;
+  const int live0 = min(TQ, nc - j0) * p.G;  // live rows of tile 0, then of both
+  const int live = live0 + (p.tpc > 1 ? max(0, min(TQ, nc - j0 - TQ)) * p.G : 0);
+  for (int i = tid; i < live * (DH / 4); i += kPreThreads) {
+    const int at = i / (DH / 4), e = i - at * (DH / 4);
+    const int t = at >= live0, r = t ? at - live0 : at, row = t * kRows + r;
     const int jr = j0 + t * TQ + r / p.G;
-    if (t >= p.tpc || r >= TQ * p.G || jr >= nc) continue;
     float M = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
