@@ -55,8 +55,10 @@ constexpr int kKeys = 128;   // keys of a block
 constexpr int kBlkPages = kKeys / kTok;
 constexpr int kPreThreads = 640;
 constexpr int kConvWarp = 8, kProdWarp = 16, kMmaWarp = 17;
-constexpr int kSoftRegs = 136, kConvRegs = 72, kIssueRegs = 64;  // of 96 at launch: 256, 256 and 128 threads
-static_assert(256 * kSoftRegs + 256 * kConvRegs + 128 * kIssueRegs <= kPreThreads * 96, "registers");
+// Registers of a thread at launch, of the 256 softmax, the 256 converter and the 128 other threads
+// while they have their parts, and again what all had for the merge, which all take part in.
+constexpr int kLaunchRegs = 96, kSoftRegs = 136, kConvRegs = 72, kIssueRegs = 64;
+static_assert(256 * kSoftRegs + 256 * kConvRegs + 128 * kIssueRegs <= kPreThreads * kLaunchRegs, "registers");
 constexpr uint32_t kTmemCols = 512, kTileCols = 256;  // per tile: S and P at +0, O at +128
 constexpr int kPreStages = 3, kBufs = 2;
 constexpr float kPreBias = 7.f;  // log2 of the factor that the weights carry
@@ -754,10 +756,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
         }
       }
     }
+    __syncwarp();
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLaunchRegs));
   }
 
   tc::tc_fence_before();
   __syncthreads();
+  // Every softmax warp has let go of its registers.  (A warp that took its own back any earlier
+  // could take them from a softmax warp that waits for them at its start.)
+  if (warp >= kConvWarp) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kLaunchRegs));
   // After an abort: wait (bounded) for the copies in flight; the issuers waited for their steps.
   if (*abort_flag && tid == 0)
     for (int s = 0; s < S; ++s)
