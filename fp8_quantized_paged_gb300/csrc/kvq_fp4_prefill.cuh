@@ -23,16 +23,18 @@
 // half's next S waits for the PV that reads its P, while the softmax works on the
 // other half.  The softmax takes most registers (setmaxnreg).
 //
-// What bounds it: the matrix unit's operands.  An N 64 step reads 6 KB of shared
-// memory in 48 cycles (128 bytes a cycle, all there are), an N 128 step 8 KB in 64:
-// for the two tiles' block 32 x 48 + 16 x 64 = 2560 cycles, beside the converters'
-// stores and the copies; measured about 3600, with the unit 90% busy.  2048 queries
-// of 32 heads over 32768 tokens, 8 KV heads of 128 dims: 858 us, 1240 TFLOP/s (563 us
-// at the measured bf16 rate).  On the way: S in steps of N 128, tiles taking turns
-// 1201 us; halves 1106; issue under elect.sync, K and V converted by a warpgroup each
-// 927 (with one 1007); the rest after whole waves split 858.  S in one 64-column buffer with two
-// of P beside it 987.  Equal stretches of all items' keys for every SM instead of
-// whole items: 1107 where that was 1106, and small calls a third slower.
+// What bounds it: an N 64 step reads 6 KB of shared memory in 48 cycles (128 bytes a
+// cycle, all there are), an N 128 step 8 KB in 64: for the two tiles' block 32 x 48 +
+// 16 x 64 = 2560 cycles beside the converters' loads and stores, of about 4000 measured.
+// Shared memory's bandwidth is 83% taken (51 operands, 32 converters); the rest is the
+// chain of a half, softmax, P V, next S.  2048 queries of 32 heads over 32768 tokens,
+// 8 KV heads of 128 dims: 857 us, 1240 TFLOP/s (563 us at the measured bf16 rate).
+// On the way: S in steps of N 128, tiles taking turns 1201 us; halves 1106; issue
+// under elect.sync, K and V converted by a warpgroup each 927 (by one 1007); the rest
+// after whole waves split 857.  S in one 64-column buffer with two of P beside it 987.
+// Equal stretches of all items' keys for every SM instead of whole items: 1107 where
+// whole ones took 1106, and small calls a third slower.  Codes read 16 bytes a lane,
+// free of bank conflicts: 855.
 //
 // Where items leave SMs idle the host splits their blocks over several CTAs; each
 // leaves (m, l, O) of its rows in the workspace and the one that completes the item
