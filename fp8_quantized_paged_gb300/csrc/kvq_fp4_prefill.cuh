@@ -30,8 +30,8 @@
 // chain of a half, softmax, P V, next S.  2048 queries of 32 heads over 32768 tokens,
 // 8 KV heads of 128 dims: 857 us, 1240 TFLOP/s (563 us at the measured bf16 rate).
 // On the way: S in steps of N 128, tiles taking turns 1201 us; halves 1106; issue
-// under elect.sync, K and V converted by a warpgroup each 927 (by one 1007); the rest
-// after whole waves split 857.  S in one 64-column buffer with two of P beside it 987.
+// under elect.sync, K and V converted by a warpgroup each 927; the rest after whole
+// waves split 857.  S in one 64-column buffer with two of P beside it 987.
 // Equal stretches of all items' keys for every SM instead of whole items: 1107 where
 // whole ones took 1106, and small calls a third slower.  Codes read 16 bytes a lane,
 // free of bank conflicts: 855.

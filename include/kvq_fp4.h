@@ -61,7 +61,7 @@ extern "C" {
  * largest magnitude: the E4M3 scale of kvq_calibrate_scales over 6) the
  * largest block scale is 448.
  *
- *   k, v, token_stride, slot_mapping   as for kvq_write
+ *   k, v, token_stride, slot_mapping   as for kvq_write (slots distinct)
  *   k_cache, v_cache   uint8, layout above, num_blocks blocks
  *   k_scale, v_scale   fp32 device arrays of 1 (KVQ_SCALE_PER_TENSOR) or
  *                      num_kv_heads (KVQ_SCALE_PER_HEAD) values, finite, > 0
