@@ -376,7 +376,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
       jb[t] = je[t] = c0;
     } else {
       const int lo = visible(p.window, p.sinks, base + a + 1).first;
-      jb[t] = max(c0, list.sink > 0 ? 0 : (lo - list.first) / kBlkPages);
+      // (where the first row still sees all tokens, the list has no first part, but tile 1 may
+      // need its first pages all the same)
+      jb[t] = max(c0, p.sinks > 0 ? 0 : (lo - list.first) / kBlkPages);
       je[t] = min(c1, (list.sink + (base + e - 1) / kTok - list.first) / kBlkPages + 1);
       if (je[t] < jb[t]) je[t] = jb[t];
     }

@@ -353,6 +353,18 @@ def test_prefill_chunks(kvq, lens, counts, hq, hkv, dh, window, sinks):
     assert torch.equal(first, g.out)
 
 
+@pytest.mark.parametrize("lens,counts,hkv,dh,window,sinks", [
+    ([260, 150], [233, 150], 4, 128, 16, 1), ([166, 196], [166, 186], 1, 64, 16, 5000), ([595], [255], 2, 128, 300, 17),
+    ([400], [400], 2, 64, 40, 20)])
+def test_prefill_second_tile_still_sees_the_first_tokens(kvq, lens, counts, hkv, dh, window, sinks):
+    """A tile whose window has left the first pages, beside one whose first row sees
+    every token there is."""
+    b = f4.Batch(22 + dh, lens, hkv, hkv, dh)
+    g = OnGpu(kvq, b, counts)
+    g.prefill(window, sinks)
+    g.check(window, sinks, "prefill")
+
+
 @pytest.mark.parametrize("dh,longest_last", [(64, True), (64, False), (128, True)])
 def test_prefill_more_items_than_sms(kvq, dh, longest_last):
     """160 sequences on shared pages: a whole wave, and a rest whose keys are shared out
