@@ -28,7 +28,7 @@
 // 16 x 64 = 2560 cycles beside the converters' loads and stores, of about 4000 measured.
 // Shared memory's bandwidth is 83% taken (51 operands, 32 converters); the rest is the
 // chain of a half, softmax, P V, next S.  2048 queries of 32 heads over 32768 tokens,
-// 8 KV heads of 128 dims: 857 us, 1240 TFLOP/s (563 us at the measured bf16 rate).
+// 8 KV heads of 128 dims: 860 us, 1240 TFLOP/s (563 us at the measured bf16 rate).
 // On the way: S in steps of N 128, tiles taking turns 1201 us; halves 1106; issue
 // under elect.sync, K and V converted by a warpgroup each 927; the rest after whole
 // waves split 857.  S in one 64-column buffer with two of P beside it 987.
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_u32(smem);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::bars);  // [S] a stage landed
-  uint64_t* empty = full + S;            // [S] a stage converted (128 arrivals)
+  uint64_t* empty = full + S;            // [S] a stage converted, and seen by the other converters (256 arrivals)
   uint64_t* conv_k = empty + S;          // [kBufs] K buffer filled (128)
   uint64_t* conv_v = conv_k + kBufs;     // [kBufs]
   uint64_t* done_k = conv_v + kBufs;     // [kBufs] K buffer read by both tiles (a commit each)
@@ -299,7 +299,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
 
   // A parity wait for phase k of a barrier is sound while the barrier has
   // completed k or k + 1 phases.  Each waiter takes its barriers' phases in
-  // order, but for the softmax's waits for pdone, where O is rescaled: S of half h
+  // order (the converters of K wait for V's copies too, and the other way round, and the stage
+  // waits for both: a waiter that skipped a phase could take the one before for its own), but for
+  // the softmax's waits for pdone, where O is rescaled: S of half h
   // of block i came after the PV of half h of block i - 1, and that PV's next phase
   // needs this softmax's own later progress.
 
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 128);
+      mbar_init(&empty[i], 256);
       issued[i] = -1;
     }
     for (int i = 0; i < kBufs; ++i) {
@@ -517,9 +519,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     const int ct = tid & 127;
     for (int it = 0; it < 2 * nb; ++it) {
       const PreTask task = pre_task(it, nb);
-      if (task.v != is_v) continue;
       const int i = task.block, s = it % S, x = i % kBufs;
       bool ok = wait_w(&full[s], it / S);
+      if (ok && task.v != is_v) {  // the other warpgroup's
+        mbar_arrive(&empty[s]);
+        continue;
+      }
       if (ok && i >= kBufs) ok = wait_w(is_v ? &done_v[x] : &done_k[x], i / kBufs - 1);
       if (!ok) {
         fail();
