@@ -56,6 +56,18 @@ KVQ_DEVI uint32_t hmul2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// ------------------------------------------------------------------ logits
+
+// The attentions keep a row's running maximum as a raw dot product of scaled f16 queries and
+// code * block scale, below 2^34, and its scale ls (to base-2 exponents) beside it: above 0, so
+// that it times -inf stays -inf, and finite.
+KVQ_DEVI float bounded_scale(float ls) { return fminf(fmaxf(ls, 0x1p-120f), 0x1p126f); }
+
+// States are merged on the maximum's exponent in units of 2^40: finite for every logit that a
+// binary32 scale below 2^24 gives (and bf16 queries), where the exponent itself passes binary32.
+constexpr float kMergeUnit = 0x1p40f;
+KVQ_DEVI float merge_max(float m, float ls) { return m == -INFINITY ? m : m * (ls * (1.f / kMergeUnit)); }
+
 // ------------------------------------------------------------------ visible pages
 
 // The pages that hold a visible token of a sequence of L tokens seen from its

@@ -179,8 +179,8 @@ struct PieceView {
   float ls[2];       // logit scale (log2 units) of heads 2t, 2t + 1
 };
 
-// Running maximum (of the raw dot products), the exponent's offset
-// 7 - max * ls, and the lane's share of the denominator, of heads 2t, 2t + 1.
+// Running maximum (of the raw dot products), what a dot product loses before its scale (the
+// maximum, 0 while that is -inf), and the lane's share of the denominator, of heads 2t, 2t + 1.
 struct Running {
   float m[2], c[2], l[2];
 };
@@ -302,15 +302,18 @@ KVQ_DEVI void dec_pages(const uint8_t* const (&kpage)[NP], const uint8_t* const 
     st.m[0] = n0;
     st.m[1] = n1;
     // with nothing seen any finite offset keeps 2^-inf = 0 (and a NaN a NaN)
-    st.c[0] = n0 == -INFINITY ? 0.f : fmaf(-n0, pv.ls[0], kPBias);
-    st.c[1] = n1 == -INFINITY ? 0.f : fmaf(-n1, pv.ls[1], kPBias);
+    st.c[0] = n0 == -INFINITY ? 0.f : n0;
+    st.c[1] = n1 == -INFINITY ? 0.f : n1;
   }
   // ---- P^T as the B operand: head g of tokens (t, t + 8) and (t + 4, t + 12)
   uint32_t pb[NP][2];
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
-    const float p0 = fast_exp2(fmaf(x[i][0], pv.ls[0], st.c[0])), p1 = fast_exp2(fmaf(x[i][1], pv.ls[1], st.c[1]));
-    const float p2 = fast_exp2(fmaf(x[i][2], pv.ls[0], st.c[0])), p3 = fast_exp2(fmaf(x[i][3], pv.ls[1], st.c[1]));
+    // The difference comes before the scale: the maximum's own exponent is then 7 however large the
+    // logits are (7 - m ls, rounded, leaves it the rounding of m ls, which passes f16's range from
+    // logits of 2^26 on).
+    const float p0 = fast_exp2(fmaf(x[i][0] - st.c[0], pv.ls[0], kPBias)), p1 = fast_exp2(fmaf(x[i][1] - st.c[1], pv.ls[1], kPBias));
+    const float p2 = fast_exp2(fmaf(x[i][2] - st.c[0], pv.ls[0], kPBias)), p3 = fast_exp2(fmaf(x[i][3] - st.c[1], pv.ls[1], kPBias));
     st.l[0] += p0 + p2;
     st.l[1] += p1 + p3;
     const uint32_t h0 = f32x2_to_f16x2(p0, p2), h1 = f32x2_to_f16x2(p1, p3);
@@ -344,8 +347,8 @@ KVQ_DEVI void dec_pages(const uint8_t* const (&kpage)[NP], const uint8_t* const 
 }
 
 // Sums of states j = 0 .. n - 1 (m, l, four dims of o) for E outputs, U states at a time
-// with their loads together: l and o scaled by 2^(m - M), M the largest m.  A state with
-// m of -inf has l and o of 0, or NaN.
+// with their loads together: l and o scaled by 2^(kMergeUnit (m - M)), M the largest m.  A
+// state with m of -inf has l and o of 0, or NaN.
 struct State {
   float m, l;
   float4 o;
@@ -368,7 +371,7 @@ KVQ_DEVI void merge_states(int n, State (&a)[E], const Load& load) {
       float m = a[e].m;
 #pragma unroll
       for (int y = 0; y < U; ++y) m = fmaxf(m, x[e][y].m);
-      const float r = a[e].m == -INFINITY ? 1.f : fast_exp2(a[e].m - m);
+      const float r = a[e].m == -INFINITY ? 1.f : fast_exp2((a[e].m - m) * kMergeUnit);
       a[e].l *= r;
       a[e].o.x *= r;
       a[e].o.y *= r;
@@ -377,7 +380,7 @@ KVQ_DEVI void merge_states(int n, State (&a)[E], const Load& load) {
       a[e].m = m;
 #pragma unroll
       for (int y = 0; y < U; ++y) {
-        const float w = x[e][y].m == -INFINITY ? 1.f : fast_exp2(x[e][y].m - m);
+        const float w = x[e][y].m == -INFINITY ? 1.f : fast_exp2((x[e][y].m - m) * kMergeUnit);
         a[e].l += x[e][y].l * w;
         a[e].o.x += x[e][y].o.x * w;
         a[e].o.y += x[e][y].o.y * w;
@@ -596,9 +599,8 @@ KVQ_DEVI void decode_run(const DecParams& p, uint8_t* smem, const DecSmem& sm, u
     {
       const float ls = __ldg(p.ks + (p.per_head ? gkv : 0)) * p.logit_scale;
       const int qa = q_fragments<KVQ_FMT_E4M3, DH>(raw, qb);
-      // (kept above 0 where it would underflow, so that it times -inf stays -inf)
-      pv.ls[0] = fmaxf(ls * __int_as_float((127 - __shfl_sync(kFull, qa, 8 * t)) << 23), 0x1p-120f);
-      pv.ls[1] = fmaxf(ls * __int_as_float((127 - __shfl_sync(kFull, qa, 8 * t + 4)) << 23), 0x1p-120f);
+      pv.ls[0] = bounded_scale(ls * __int_as_float((127 - __shfl_sync(kFull, qa, 8 * t)) << 23));
+      pv.ls[1] = bounded_scale(ls * __int_as_float((127 - __shfl_sync(kFull, qa, 8 * t + 4)) << 23));
     }
     Running st;
     st.m[0] = st.m[1] = -INFINITY;
@@ -665,8 +667,7 @@ KVQ_DEVI void decode_run(const DecParams& p, uint8_t* smem, const DecSmem& sm, u
                                      f32x2_to_bf16x2(o[mt + 2][e] * f, o[mt + 2][2 + e] * f),
                                      f32x2_to_bf16x2(o[mt + 3][e] * f, o[mt + 3][2 + e] * f));
         } else {
-          if (g == 0)  // m in log2 units
-            p.ws_ml[mine * p.G + h] = make_float2(st.m[e] == -INFINITY ? -INFINITY : st.m[e] * pv.ls[e], st.l[e]);
+          if (g == 0) p.ws_ml[mine * p.G + h] = make_float2(merge_max(st.m[e], pv.ls[e]), st.l[e]);
           float4* dst = reinterpret_cast<float4*>(p.ws_o + (mine * p.G + h) * DH + g * (DH / 8));
 #pragma unroll
           for (int mt = 0; mt < MT; mt += 2)
@@ -678,8 +679,7 @@ KVQ_DEVI void decode_run(const DecParams& p, uint8_t* smem, const DecSmem& sm, u
     for (int e = 0; e < 2; ++e) {
       const int h = 2 * t + e;
       if (h >= p.G) continue;
-      if (g == 0)  // m in log2 units
-        cml[po * p.G + h] = make_float2(st.m[e] == -INFINITY ? -INFINITY : st.m[e] * pv.ls[e], st.l[e]);
+      if (g == 0) cml[po * p.G + h] = make_float2(merge_max(st.m[e], pv.ls[e]), st.l[e]);
       float* dst = co + (po * p.G + h) * DH + g * (DH / 8);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
