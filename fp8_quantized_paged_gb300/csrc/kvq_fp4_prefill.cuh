@@ -64,6 +64,7 @@ static_assert(256 * kSoftRegs + 256 * kConvRegs + 128 * kIssueRegs <= kPreThread
 constexpr uint32_t kTmemCols = 512, kTileCols = 256;  // per tile: S and P at +0, O at +128
 constexpr int kPreStages = 3, kBufs = 2;
 constexpr float kPreBias = 7.f;  // log2 of the factor that the weights carry
+constexpr float kFarMax = 0x1p16f;  // maxima (in exponents) from which keys lose them before the scale
 
 struct PreParams {
   const uint16_t* q;
@@ -591,7 +592,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     const uint32_t tm_o = tm_s + 128;
     // the query row times a power of two 2^a, its largest value in [2^14, 2^15): f16, exact
     // but for values 2^38 times smaller than that
-    // (kept above 0 where it would underflow, so that it times -inf stays -inf)
     float lscale = __ldg(p.ks + (p.per_head ? gkv : 0)) * p.logit_scale;
     {
       const uint4* src = reinterpret_cast<const uint4*>(p.q + qrow * DH);
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
         a = a > 126 ? 126 : (a < -126 ? -126 : a);
       }
       const float up = __int_as_float((a + 127) << 23);
-      lscale = fmaxf(lscale * __int_as_float((127 - a) << 23), 0x1p-120f);
+      lscale = bounded_scale(lscale * __int_as_float((127 - a) << 23));
 #pragma unroll
       for (int c = 0; c < DH / 8; ++c) {
         const uint4 w = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
@@ -623,7 +623,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     }
     fence_proxy_async_smem();
     mbar_arrive(qready);
-    float m = -INFINITY, l = 0.f;
+    // m, a raw dot product; the exponents' offset 7 - m lscale (7 while every key so far is masked and
+    // m is -inf: any finite value keeps 2^-inf = 0, and a NaN)
+    float m = -INFINITY, l = 0.f, off = kPreBias;
+    const float rise = kRescaleThreshold / lscale;
+    bool far = false;  // a row of the warp has a maximum past kFarMax
     bool ok = true;
     const int nI = je[t] - jb[t];
     const bool some = __any_sync(kFull, live);
@@ -660,10 +664,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
         // beside them (no wait of one for the other); where it grew by over 8, O and l are
         // rescaled and the weights formed again.
         float sum, mx;
-        auto weights = [&] {
-          // while every key so far is masked m is -inf: any finite value keeps 2^-inf = 0 (and a NaN)
-          const float mb = m == -INFINITY ? 0.f : m - kPreBias;
-          const f32x2 sc2 = f32x2_pack(lscale, lscale), nb2 = f32x2_pack(-mb, -mb);
+        auto weights = [&](float off) {
+          const f32x2 sc2 = f32x2_pack(lscale, lscale), off2 = f32x2_pack(off, off);
           f32x2 l2[2] = {f32x2_pack(0.f, 0.f), f32x2_pack(0.f, 0.f)};
           float mx2[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -673,7 +675,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
             for (int e2 = 0; e2 < 8; ++e2) {
               const int e = 16 * c + 2 * e2;
               float p0, p1;
-              f32x2_unpack(f32x2_fma(f32x2_pack(x[e], x[e + 1]), sc2, nb2), p0, p1);
+              f32x2_unpack(f32x2_fma(f32x2_pack(x[e], x[e + 1]), sc2, off2), p0, p1);
               p0 = fast_exp2(p0);
               p1 = fast_exp2(p1);
               l2[e2 & 1] = f32x2_add(l2[e2 & 1], f32x2_pack(p0, p1));
@@ -685,16 +687,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
           float s0, s1;
           f32x2_unpack(f32x2_add(l2[0], l2[1]), s0, s1);
           sum = s0 + s1;
-          mx = fmaxf(mx2[0], mx2[1]) * lscale;
+          mx = fmaxf(mx2[0], mx2[1]);
         };
-        weights();
-        const bool grow = mx > m + kRescaleThreshold;
-        if (__any_sync(kFull, grow)) {
+        weights(off);
+        const bool grow = mx > m + rise;
+        if (__any_sync(kFull, grow) || far) {
           // O's last writer: the PV of the half before
           if (h == 1 ? !(ok = wait_w(&pdone[2 * t], i)) : i > 0 && !(ok = wait_w(&pdone[2 * t + 1], i - 1))) break;
           tc::tc_fence_after();
           const float nm = grow ? mx : m;
-          const float a = m == -INFINITY ? 0.f : fast_exp2(m - nm);
+          const float a = m == -INFINITY ? 0.f : fast_exp2((m - nm) * lscale);
           if (i > 0 || h > 0) {
 #pragma unroll 1
             for (int c = 0; c < DH; c += 16) {
@@ -707,7 +709,18 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
           }
           if (grow) l *= a;
           m = nm;
-          weights();
+          // The offset's rounding, up to 2^-24 of the maximum's exponent, is common to all keys and
+          // cancels, but from about 2^27 on it takes the weights out of f16's range.  Rows far below
+          // that already subtract the maximum itself: its key's exponent is exactly 7.  (In place of
+          // the offset for all rows: 918 us where this takes 861, 2048 queries over 32768 tokens.)
+          const float fm = m == -INFINITY ? 0.f : m;
+          off = fmaf(-fm, lscale, kPreBias);
+          far = __any_sync(kFull, fabsf(fm) * lscale > kFarMax);
+          if (far) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e) x[e] -= fm;
+          }
+          weights(far ? kPreBias : off);
         }
         l += sum;
         tc::tmem_st_wait();
@@ -723,7 +736,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     const int64_t part = (cta - p.whole) * (kTiles * kRows) + t * kRows + r;
     tc::tc_fence_after();
     if (ok) {
-      if (ns > 1 && live) p.ws_ml[part] = make_float2(m, l);
+      if (ns > 1 && live) p.ws_ml[part] = make_float2(merge_max(m, lscale), l);
 #pragma unroll 1
       for (int c = 0; c < DH; c += 32) {
         float o[32];
@@ -809,7 +822,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
       const float2 ml = __ldcg(p.ws_ml + at);
       const float4 v = __ldcg(reinterpret_cast<const float4*>(p.ws_o + at * DH) + e);
       const float nm = fmaxf(M, ml.x);
-      const float a = M == -INFINITY ? 1.f : fast_exp2(M - nm), w = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - nm);
+      const float a = M == -INFINITY ? 1.f : fast_exp2((M - nm) * kMergeUnit);
+      const float w = ml.x == -INFINITY ? 1.f : fast_exp2((ml.x - nm) * kMergeUnit);
       l = l * a + ml.y * w;
       acc.x = acc.x * a + v.x * w;
       acc.y = acc.y * a + v.y * w;

@@ -77,3 +77,26 @@ def test_decode_large_logits(kvq, lens, hq, hkv, dh, window, sinks):  # noqa: F8
     widen(g)
     g.decode(window, sinks)
     check_one_hot(g, window, sinks)
+
+
+@pytest.mark.parametrize("lens,counts,hq,hkv,dh", [
+    ([300, 64, 5, 1], [40, 64, 5, 1], 8, 2, 128), ([300, 64, 5, 1], [30, 20, 1, 1], 8, 2, 64), ([2500], [3], 32, 8, 128),
+    ([3001, 1700], [9, 4], 16, 4, 128), ([1000] * 6, [64, 7, 1, 30, 33, 16], 8, 2, 64), ([900, 20, 500], [70, 20, 40], 14, 2, 128)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (200, 5)])
+def test_prefill_large_logits(kvq, lens, counts, hq, hkv, dh, window, sinks):  # noqa: F811
+    b = f4.Batch(sum(lens) + dh + window, lens, hq, hkv, dh)
+    g = OnGpu(kvq, b, counts)
+    widen(g)
+    g.prefill(window, sinks)
+    check_one_hot(g, window, sinks)
+
+
+@pytest.mark.parametrize("dh", [64, 128])
+def test_small_and_zero_queries(kvq, dh):  # noqa: F811
+    """Queries down to bf16's subnormals, and of zero: the mean of the values, or nearly."""
+    b = f4.Batch(5 + dh, [300, 64, 17], 8, 2, dh)
+    for counts, call in (([1, 1, 1], "decode"), ([40, 64, 3], "prefill")):
+        g = OnGpu(kvq, b, counts)
+        widen(g, [1.0, 0.0, 1e-10, 1e-30, 1e-37, 3e-39, 30.0])
+        getattr(g, call)()
+        g.check(what=call)
