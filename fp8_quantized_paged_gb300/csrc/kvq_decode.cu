@@ -101,6 +101,7 @@ static bool make_cache_map(CUtensorMap* m, const void* base, int fmt, int dh, ui
 #ifdef KVQ_TEST_HOOKS
 // Test builds only: the stream position CTA 0's producer withholds (-1: none).
 static std::atomic<int> g_withhold{-1};
+int test_withheld() { return g_withhold.load(); }
 #endif
 
 }  // namespace kvq
@@ -108,8 +109,8 @@ static std::atomic<int> g_withhold{-1};
 using namespace kvq;
 
 #ifdef KVQ_TEST_HOOKS
-// Test builds only (not declared in kvq.h): make the next decodes withhold the
-// copy of CTA 0's page at stream position `position` (-1: none), so that a
+// Test builds only (not declared in kvq.h): make the next decodes, and the 4-bit
+// cache's attentions, withhold CTA 0's copy at stream position `position` (-1: none), so that a
 // bounded wait runs out and reports KVQ_DEV_WAIT_TIMEOUT.
 extern "C" __attribute__((visibility("default"))) void kvq_test_withhold_page(int position) {
   g_withhold.store(position);
@@ -241,7 +242,7 @@ extern "C" int kvq_decode_attn(const void* q, const void* k_cache, const void* v
   p.clu = 0;
   p.ncl = 0;
 #ifdef KVQ_TEST_HOOKS
-  p.withhold = g_withhold.load();
+  p.withhold = test_withheld();
 #else
   p.withhold = -1;
 #endif

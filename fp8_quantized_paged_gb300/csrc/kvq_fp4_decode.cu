@@ -136,6 +136,11 @@ extern "C" int kvq_fp4_decode_attn(const void* q, const void* k_cache, const voi
   p.ws_o = reinterpret_cast<float*>(ws + wl.o);
   p.out = static_cast<uint16_t*>(out);
   p.status = dev_status;
+#ifdef KVQ_TEST_HOOKS
+  p.withhold = test_withheld();
+#else
+  p.withhold = -1;
+#endif
   const int grid = static_cast<int>(ctas);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return head_dim == 128 ? fp4::launch_decode<128>(p, fix, grid, s)

@@ -90,6 +90,7 @@ struct DecParams {
   float* ws_o;        // [slots][G][DH]
   uint16_t* out;
   uint32_t* status;
+  int withhold;       // test builds: unit of CTA 0's run that is never copied; -1
 };
 
 // Workspace: kvq_decode_attn's table of arrival counters, then per partial
@@ -445,14 +446,22 @@ KVQ_DEVI void decode_copies(const DecParams& p, uint8_t* smem, uint64_t* full, u
       if (pending && i - S < base + __ffs(left) - 1 &&
           (round == 0 || mbar_test_wait(&empty[s], static_cast<uint32_t>((round - 1) & 1)))) {
         const bool bad = blk < 0 || blk >= p.num_blocks;
-        bad_s[s] = bad;
-        if (bad) {
+#ifdef KVQ_TEST_HOOKS
+        const bool held = blockIdx.x == 0 && i == p.withhold;  // its full barrier never completes
+#else
+        constexpr bool held = false;
+#endif
+        if (!held) {
+          bad_s[s] = bad;
+          last_s[s] = k;  // (a bad page completes its phase too)
+        }
+        if (held) {
+        } else if (bad) {
           flag_status(p.status, KVQ_DEV_BAD_BLOCK);
           mbar_arrive(&full[s]);
         } else {
           const int64_t at = (static_cast<int64_t>(blk) * p.Hkv + gr * p.HG) * Page<DH>::kBytes;
           uint8_t* dst = smem + s * 2 * half;
-          last_s[s] = k;
           mbar_arrive_expect_tx(&full[s], 2 * half);
           bulk_load(dst, p.kc + at, half, &full[s]);
           bulk_load(dst + half, p.vc + at, half, &full[s]);
@@ -750,7 +759,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_kernel(const __grid_con
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + sm.bars);  // [S] a unit landed
   uint64_t* empty = full + S;                                    // [S] its HG warps are done with it
   volatile uint32_t* bad_s = reinterpret_cast<volatile uint32_t*>(smem + sm.bad);
-  volatile int32_t* last_s = reinterpret_cast<volatile int32_t*>(bad_s + S);  // [S] last unit copied there
+  volatile int32_t* last_s = reinterpret_cast<volatile int32_t*>(bad_s + S);  // [S] last unit put there
   volatile uint32_t* abort_flag = &abort_s;
   int32_t* off = reinterpret_cast<int32_t*>(smem + sm.plan);  // [B + 1]
   int32_t* len = off + p.B + 1;                               // [B]

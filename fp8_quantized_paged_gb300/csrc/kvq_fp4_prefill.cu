@@ -125,6 +125,11 @@ extern "C" int kvq_fp4_prefill_attn(const void* q, const int32_t* cu_q_lens, int
   p.ws_o = reinterpret_cast<float*>(ws + wl.o);
   p.out = static_cast<uint16_t*>(out);
   p.status = dev_status;
+#ifdef KVQ_TEST_HOOKS
+  p.withhold = test_withheld();
+#else
+  p.withhold = -1;
+#endif
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return head_dim == 128 ? fp4::launch_prefill<128>(p, ctas, s) : fp4::launch_prefill<64>(p, ctas, s);
 }

@@ -91,6 +91,7 @@ struct PreParams {
   float* ws_o;        // [share][kTiles * kRows][DH]
   uint16_t* out;
   uint32_t* status;
+  int withhold;       // test builds: stage of CTA 0's run that is never copied; -1
 };
 
 // Workspace: the arrival counters (kvq_decode_attn's table), then the states of the rows
@@ -435,6 +436,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
         if (lane == 0) fail();
         break;
       }
+#ifdef KVQ_TEST_HOOKS
+      if (cta == 0 && it == p.withhold) continue;  // its full barrier never completes
+#endif
       const uint32_t good = __ballot_sync(kFull, lane < kBlkPages && at >= 0);
       if (lane < kBlkPages) pg_bad[s * 8 + lane] = at < 0;
       __syncwarp();
@@ -729,7 +733,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
       }
     }
     if (ok && nI > 0) ok = wait_w(&pdone[2 * t], nI - 1) && wait_w(&pdone[2 * t + 1], nI - 1);
-    if (!ok) fail();
+    if (!ok) {
+      tc::tmem_st_wait();  // (weights of the half that was given up)
+      fail();
+    }
     // ---- epilogue: the row of O, normalised, or (keys shared out) as it is
     const float sv = __ldg(p.vs + (p.per_head ? gkv : 0));
     const float f = ns > 1 ? 1.f : (l > 0.f ? sv / l : 0.f);

@@ -51,6 +51,12 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 // SM count of the current device (cached per device); 0 if no device.
 int device_sm_count();
 
+#ifdef KVQ_TEST_HOOKS
+// Test builds only: the position in CTA 0's stream of copies that its producer withholds, so that
+// the wait for it runs out (-1: none; kvq_test_withhold_page).
+int test_withheld();
+#endif
+
 // Launch shape of a kernel whose threads each keep one of the row_units
 // chunks of a token row and stride over tokens: a block is the largest
 // multiple of row_units that fits 256 threads (or 256 threads, with the grid
