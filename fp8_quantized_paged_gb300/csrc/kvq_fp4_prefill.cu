@@ -61,13 +61,14 @@ extern "C" int kvq_fp4_prefill_attn(const void* q, const int32_t* cu_q_lens, int
   const int64_t tiles = (std::min<int64_t>(max_q_len, num_q_tokens) + TQ - 1) / TQ;
   // Two tiles a CTA share each converted block.
   const int tpc = tiles > 1 ? fp4::kTiles : 1;
-  const int64_t groups = (tiles + tpc - 1) / tpc, items = groups * num_kv_heads * num_seqs;
+  // (with a bound of 0 there are no tiles: the CTAs only look for chunks past it)
+  const int64_t groups = std::max<int64_t>(1, (tiles + tpc - 1) / tpc), items = groups * num_kv_heads * num_seqs;
   if (items >= (int64_t(1) << 31) - 65536) return KVQ_ERR_UNSUPPORTED;  // (the grid)
   const int sms = device_sm_count();
   if (sms <= 0) return KVQ_ERR_CUDA;
   const fp4::PreWs wl = fp4::pre_ws(head_dim, sms);
   if (workspace_bytes < wl.total) return KVQ_ERR_WORKSPACE;
-  if (num_q_tokens == 0 || max_q_len == 0) return KVQ_OK;
+  if (num_q_tokens == 0) return KVQ_OK;
 
   fp4::PreParams p;
   p.q = static_cast<const uint16_t*>(q);

@@ -343,11 +343,13 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
   pdl_allow_next();
 
   const int q0 = __ldg(p.cu_q + b);
-  const int n = __ldg(p.cu_q + b + 1) - q0;
+  const int q1 = __ldg(p.cu_q + b + 1);
+  const bool bad_q = q0 < 0 || q1 < q0 || q1 > p.total_q;  // no rows of its own
+  const int n = bad_q ? 0 : q1 - q0;
   const int j0 = group * p.tpc * TQ;  // first query token of tile 0
-  if (group == 0 && share == 0 && gkv == 0 && tid == 0 && n > p.tiles * TQ)
+  if (group == 0 && share == 0 && gkv == 0 && tid == 0 && (bad_q || n > p.tiles * TQ))
     flag_status(p.status, KVQ_DEV_BAD_QLEN);
-  if (n <= 0 || j0 >= min(n, p.tiles * TQ) || q0 < 0 || static_cast<int64_t>(q0) + n > p.total_q) return;
+  if (n == 0 || j0 >= min(n, p.tiles * TQ)) return;
   const int nc = min(n, p.tiles * TQ);  // query tokens that the grid covers
   const int j1 = min(nc, j0 + p.tpc * TQ);
   const int L = __ldg(p.seq_lens + b);

@@ -175,13 +175,16 @@ KVQ_API int kvq_fp4_decode_attn(const void* q, const void* k_cache, const void* 
  *                  cu_q_lens[num_seqs] <= num_q_tokens; rows of out from
  *                  cu_q_lens[num_seqs] on are left as they were
  *   max_q_len      host: an upper bound of every n_b; the rows of a longer
- *                  chunk past it are left unwritten (rounded up to whole
- *                  tiles) and KVQ_DEV_BAD_QLEN is raised
+ *                  chunk past it, rounded up to whole tiles of 128 /
+ *                  (num_q_heads / num_kv_heads) queries (0: all its rows), are
+ *                  left as they were and KVQ_DEV_BAD_QLEN is raised
  *   workspace      as for kvq_fp4_decode_attn
  *   out            bf16 [num_q_tokens][num_q_heads][head_dim]
  *   dev_status     optional; KVQ_DEV_BAD_BLOCK, KVQ_DEV_BAD_SEQLEN (L_b < n_b
  *                  or L_b > max_blocks_per_seq * block_size: zero rows),
- *                  KVQ_DEV_BAD_QLEN, KVQ_DEV_WAIT_TIMEOUT
+ *                  KVQ_DEV_BAD_QLEN (rows past max_q_len, or a chunk whose
+ *                  cu_q_lens are negative, decrease or pass num_q_tokens: its
+ *                  rows are left as they were), KVQ_DEV_WAIT_TIMEOUT
  * Precision as for kvq_fp4_decode_attn.  Limits: num_seqs <= 65535;
  * num_kv_heads <= 256; max_blocks_per_seq * block_size < 2^30; num_q_tokens
  * <= 2^30; num_seqs * num_kv_heads * (max_q_len / 16 + 1) < 2^31.

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import fp4_testlib as f4
-from test_gpu_fp4 import OnGpu, _pages_equal, dev, kvq, status  # noqa: F401
+from test_gpu_fp4 import OnGpu, _pages_equal, bits, dev, kvq, status  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +69,39 @@ def test_prefill_two_tiles_shared_out(kvq, B, chunk, hq, dh):  # noqa: F811
         g.prefill(window, sinks)
         torch.cuda.synchronize()
         assert torch.equal(first, g.out)
+
+
+@pytest.mark.parametrize("cu", [[0, 5, 14], [0, 8, 5], [-2, 3, 10], [-(1 << 31), (1 << 31) - 1, 10], [0, 4, 4 + (1 << 30)]])
+def test_prefill_bad_chunk_bounds(kvq, cu):  # noqa: F811
+    """Chunks that end past the queries, or whose bounds decrease or are negative, are
+    reported, and their rows left alone; the others are right."""
+    b = f4.Batch(3, [40, 33], 8, 2, 64)
+    g = OnGpu(kvq, b, [5, 5])
+    cu = np.array(cu, np.int64)
+    bad = (cu[:-1] < 0) | (cu[1:] < cu[:-1]) | (cu[1:] > 10)
+    g.dcu = dev(cu.astype(np.int32))
+    g.prefill(max_q=10)
+    torch.cuda.synchronize()
+    assert int(g.st.item()) == kvq.KVQ_DEV_BAD_QLEN
+    # the good chunks alone, beside sequences without queries
+    mine = np.zeros(10, bool)
+    for s in np.nonzero(~bad)[0]:
+        lens = np.where(np.arange(2) == s, b.lens, 0)
+        one = np.where(np.arange(3) <= s, 0, cu[s + 1] - cu[s])
+        want, tol = f4.attention(g.q[cu[s]:cu[s + 1]], g.K, g.V, b.ks, b.vs, b.table, lens, one, 0, 0)
+        f4.check(bits(g.out[cu[s]:cu[s + 1]]), want, tol, f"sequence {s}")
+        mine[cu[s]:cu[s + 1]] = True
+    assert bool((g.out[torch.from_numpy(~mine).cuda()] == 7).all())
+
+
+def test_prefill_bound_of_zero(kvq):  # noqa: F811
+    """No queries at all are fine (the rows are padding); any chunk is past the bound."""
+    b = f4.Batch(4, [40, 33], 8, 2, 64)
+    g = OnGpu(kvq, b, [5, 5])
+    for cu, want in (([0, 0, 0], 0), ([0, 0, 1], kvq.KVQ_DEV_BAD_QLEN), ([0, 10, 10], kvq.KVQ_DEV_BAD_QLEN)):
+        g.st.zero_()
+        g.dcu = dev(np.array(cu, np.int32))
+        g.prefill(max_q=0)
+        torch.cuda.synchronize()
+        assert int(g.st.item()) == want
+        assert bool((g.out == 7).all())
