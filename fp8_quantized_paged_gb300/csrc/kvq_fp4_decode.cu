@@ -65,7 +65,7 @@ extern "C" int kvq_fp4_decode_attn(const void* q, const void* k_cache, const voi
                                    int sliding_window, int num_sinks, void* workspace,
                                    size_t workspace_bytes, void* out, uint32_t* dev_status,
                                    kvq_stream_t stream) {
-  const int st = fp4::check_attn(q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens,
+  const int st = fp4::check_attn(true, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens,
                                  num_seqs, num_q_heads, num_kv_heads, head_dim, num_blocks,
                                  block_size, k_scale, k_scale_len, v_scale, v_scale_len,
                                  scale_granularity, sliding_window, num_sinks, workspace, out);

@@ -28,8 +28,8 @@ inline int check_caches(int64_t num_blocks, int block_size, int num_kv_heads, in
   return KVQ_OK;
 }
 
-// What the two attentions check alike.
-inline int check_attn(const void* q, const void* k_cache, const void* v_cache,
+// What the two attentions check alike.  Without rows q and out may be NULL, as empty tensors' are.
+inline int check_attn(bool rows, const void* q, const void* k_cache, const void* v_cache,
                       const int32_t* block_tables, int max_blocks, const int32_t* seq_lens,
                       int num_seqs, int hq, int hkv, int dh, int64_t num_blocks, int block_size,
                       const float* k_scale, int k_len, const float* v_scale, int v_len, int gran,
@@ -39,7 +39,7 @@ inline int check_attn(const void* q, const void* k_cache, const void* v_cache,
     return KVQ_ERR_ARG;
   int st = check_scales(k_scale, k_len, v_scale, v_len, gran, hkv);
   if (st != KVQ_OK) return st;
-  if (!q || !k_cache || !v_cache || !block_tables || !seq_lens || !workspace || !out)
+  if (!k_cache || !v_cache || !block_tables || !seq_lens || !workspace || (rows && (!q || !out)))
     return KVQ_ERR_NULL;
   st = check_caches(num_blocks, block_size, hkv, dh);
   if (st != KVQ_OK) return st;

@@ -45,7 +45,7 @@ extern "C" int kvq_fp4_prefill_attn(const void* q, const int32_t* cu_q_lens, int
                                     int sliding_window, int num_sinks, void* workspace,
                                     size_t workspace_bytes, void* out, uint32_t* dev_status,
                                     kvq_stream_t stream) {
-  const int st = fp4::check_attn(q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens,
+  const int st = fp4::check_attn(num_q_tokens != 0, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens,
                                  num_seqs, num_q_heads, num_kv_heads, head_dim, num_blocks,
                                  block_size, k_scale, k_scale_len, v_scale, v_scale_len,
                                  scale_granularity, sliding_window, num_sinks, workspace, out);
@@ -64,11 +64,11 @@ extern "C" int kvq_fp4_prefill_attn(const void* q, const int32_t* cu_q_lens, int
   // (with a bound of 0 there are no tiles: the CTAs only look for chunks past it)
   const int64_t groups = std::max<int64_t>(1, (tiles + tpc - 1) / tpc), items = groups * num_kv_heads * num_seqs;
   if (items >= (int64_t(1) << 31) - 65536) return KVQ_ERR_UNSUPPORTED;  // (the grid)
+  if (num_q_tokens == 0) return KVQ_OK;
   const int sms = device_sm_count();
   if (sms <= 0) return KVQ_ERR_CUDA;
   const fp4::PreWs wl = fp4::pre_ws(head_dim, sms);
   if (workspace_bytes < wl.total) return KVQ_ERR_WORKSPACE;
-  if (num_q_tokens == 0) return KVQ_OK;
 
   fp4::PreParams p;
   p.q = static_cast<const uint16_t*>(q);

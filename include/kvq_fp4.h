@@ -188,6 +188,7 @@ KVQ_API int kvq_fp4_decode_attn(const void* q, const void* k_cache, const void* 
  * Precision as for kvq_fp4_decode_attn.  Limits: num_seqs <= 65535;
  * num_kv_heads <= 256; max_blocks_per_seq * block_size < 2^30; num_q_tokens
  * <= 2^30; num_seqs * num_kv_heads * (max_q_len / 16 + 1) < 2^31.
+ * num_q_tokens == 0 is a no-op.
  */
 KVQ_API int kvq_fp4_prefill_attn(const void* q, const int32_t* cu_q_lens, int64_t num_q_tokens,
                                  int max_q_len, const void* k_cache, const void* v_cache,

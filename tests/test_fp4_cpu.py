@@ -113,6 +113,13 @@ def test_abi_nothing_to_do(calls):
     assert calls["read"](n=0, ko=0, vo=0) == 0
 
 
+def test_abi_prefill_of_no_queries(calls):
+    assert calls["prefill"](n=0, q=0, out=0) == 0
+    assert calls["prefill"](n=0, q=0, out=0, maxq=0) == 0
+    assert calls["prefill"](n=0, q=0, out=0, cu=0) == NULL
+    assert calls["prefill"](n=1, q=0) == NULL and calls["prefill"](n=1, out=0) == NULL
+
+
 def test_workspace_size(kvq):
     f = kvq.kvq_fp4_workspace_size
     assert f(1, 8, 2, 64, 152) >= kvq.KVQ_WS_COUNTER_BYTES

@@ -105,3 +105,13 @@ def test_prefill_bound_of_zero(kvq):  # noqa: F811
         torch.cuda.synchronize()
         assert int(g.st.item()) == want
         assert bool((g.out == 7).all())
+
+
+def test_prefill_of_no_queries(kvq):  # noqa: F811
+    """A step in which no sequence has new tokens, with empty tensors."""
+    b = f4.Batch(5, [40, 33], 8, 2, 64)
+    g = OnGpu(kvq, b, [0, 0])
+    for max_q in (0, 16):
+        g.prefill(max_q=max_q)
+    torch.cuda.synchronize()
+    assert int(g.st.item()) == 0
