@@ -4,6 +4,10 @@ Each CUDA source compiles to an object in parallel (the decode kernels once
 per cache format and head size), then nvcc links the
 shared library (static CUDA runtime, no libcuda link: the tensor-map encoder
 is looked up through the runtime's driver entry-point query).
+
+The 4-bit cache's Python binding is a library of its own, built with g++ against
+Python's and torch's headers.  libkvq.so needs nvcc alone: where the binding does
+not build, build() says so on stderr and links the library all the same.
 """
 from __future__ import annotations
 
@@ -44,10 +48,17 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _inputs():
+def _inputs(sources):
     inc = os.path.join(os.path.dirname(HERE), "include")
-    return ([os.path.join(CSRC, s) for s in SOURCES + HEADERS + [BINDING]] +
+    return ([os.path.join(CSRC, s) for s in sources] +
             [os.path.join(inc, h) for h in ("kvq.h", "kvq_fp4.h")] + [os.path.abspath(__file__)])
+
+
+def _newer(lib: str, sources) -> bool:
+    if not os.path.exists(lib):
+        return False
+    t = os.path.getmtime(lib)
+    return all(os.path.getmtime(p) <= t for p in _inputs(sources))
 
 
 # The tests' timeout build: the same sources with the test hooks compiled in
@@ -58,10 +69,7 @@ TEST_DEFINES = ["-DKVQ_TEST_HOOKS", "-DKVQ_MAX_POLLS=65536u"]
 
 
 def up_to_date(lib: str = LIB) -> bool:
-    if not os.path.exists(lib):
-        return False
-    t = os.path.getmtime(lib)
-    return all(os.path.getmtime(p) <= t for p in _inputs())
+    return _newer(lib, SOURCES + HEADERS)
 
 
 def _torch_root() -> str:
@@ -73,9 +81,26 @@ def _torch_root() -> str:
     return list(spec.submodule_search_locations)[0]
 
 
+def _binding_stamp() -> str:
+    """What the binding is compiled against: this Python and torch's version file."""
+    with open(os.path.join(_torch_root(), "version.py")) as f:
+        return sys.version + "\n" + f.read()
+
+
+def binding_up_to_date() -> bool:
+    if not _newer(BINDING_LIB, [BINDING]) or not os.path.exists(BINDING_LIB + ".stamp"):
+        return False
+    with open(BINDING_LIB + ".stamp") as f:
+        return f.read() == _binding_stamp()
+
+
 def build_binding(verbose: bool = False) -> str:
     import sysconfig
     torch = _torch_root()
+    os.makedirs(BUILD, exist_ok=True)
+    for old in (BINDING_LIB, BINDING_LIB + ".stamp"):  # a failure leaves no binding of other headers behind
+        if os.path.exists(old):
+            os.remove(old)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     tmp = BINDING_LIB + f".tmp{os.getpid()}"
     cmd = [shutil.which("g++") or "c++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
@@ -90,7 +115,17 @@ def build_binding(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING_LIB)
+    with open(BINDING_LIB + ".stamp", "w") as f:
+        f.write(_binding_stamp())
     return BINDING_LIB
+
+
+def _try_binding(force: bool, verbose: bool) -> None:
+    try:
+        if force or not binding_up_to_date():
+            build_binding(verbose)
+    except (RuntimeError, OSError) as e:
+        print(f"the 4-bit cache's Python binding is not built: {e}", file=sys.stderr)
 
 
 def build_test_lib(force: bool = False, verbose: bool = False) -> str:
@@ -99,9 +134,13 @@ def build_test_lib(force: bool = False, verbose: bool = False) -> str:
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None,
           lib: str = LIB) -> str:
-    binding = lib == LIB  # the tests' library needs none
-    if not force and up_to_date(lib) and (not binding or up_to_date(BINDING_LIB)):
-        return lib
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        if lib == LIB:  # the tests' library needs no binding
+            ex.submit(_try_binding, force, verbose)
+        return lib if not force and up_to_date(lib) else _build_lib(verbose, extra, lib)
+
+
+def _build_lib(verbose: bool, extra: list[str] | None, lib: str) -> str:
     out_dir = os.path.dirname(lib)
     os.makedirs(out_dir, exist_ok=True)
     nvcc = _nvcc()
@@ -120,11 +159,8 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             print(r.stderr, file=sys.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(len(UNITS) + 1, max(2, os.cpu_count() or 2))) as ex:
-        native = ex.submit(build_binding, verbose) if binding else None
+    with cf.ThreadPoolExecutor(max_workers=min(len(UNITS), max(2, os.cpu_count() or 2))) as ex:
         objs = list(ex.map(compile_one, UNITS))
-        if native:
-            native.result()
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
