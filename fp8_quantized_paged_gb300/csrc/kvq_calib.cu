@@ -98,8 +98,8 @@ __global__ void calib_zero(uint32_t* kbits, uint32_t* vbits, int n) {
 // In place: scale = amax / fmt_max (binary32, round to nearest even); 1.0
 // where that is 0 (no finite non-zero value, or a quotient that underflows).
 __global__ void calib_finalize(uint32_t* kbits, uint32_t* vbits, int n, float fmt_max) {
-  pdl_allow_next();
   pdl_wait();
+  pdl_allow_next();
   for (int i = threadIdx.x; i < 2 * n; i += blockDim.x) {
     uint32_t* b = i < n ? kbits + i : vbits + (i - n);
     const float amax = __uint_as_float(*b);

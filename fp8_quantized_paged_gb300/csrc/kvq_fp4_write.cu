@@ -123,8 +123,8 @@ template <int DH>
 __global__ void __launch_bounds__(256, kWriteCtas) write_kernel(const WriteParams p) {
   using P = Page<DH>;
   constexpr int CH = DH / 16;
-  pdl_allow_next();
   pdl_wait();  // the inputs may come from the kernel before this one
+  pdl_allow_next();
   const bool is_v = blockIdx.y != 0;
   const uint16_t* in = is_v ? p.v : p.k;
   uint8_t* cache = is_v ? p.vc : p.kc;
@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(256) read_kernel(const ReadParams p) {
   using P = Page<DH>;
   constexpr int CH = DH / 16;
   constexpr uint32_t kAll = 0xFFFFFFFFu;
-  pdl_allow_next();
   pdl_wait();
+  pdl_allow_next();
   const int lane = threadIdx.x & 31;
   const int units = p.hkv * CH;  // blocks of a row
   const int64_t rows = min(p.num_rows, static_cast<int64_t>(__ldg(p.cu + p.num_seqs)));

@@ -250,8 +250,8 @@ struct DequantParams {
 // product with the head's scale, RNE to bf16.
 template <int FMT>
 __global__ void __launch_bounds__(256) dequant_kernel(const DequantParams p) {
-  pdl_allow_next();
   pdl_wait();
+  pdl_allow_next();
   const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
   for (int64_t u = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; u < p.units;
        u += stride) {

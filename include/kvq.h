@@ -258,7 +258,10 @@ KVQ_API size_t kvq_decode_workspace_size(int num_seqs, int num_q_heads, int num_
  *                   before writing anything: the caller promises that the
  *                   preceding kernel writes none of the early inputs (true
  *                   when it is the kvq_write of one new token per sequence,
- *                   or a decode of another layer).
+ *                   or a decode of another layer).  A kvq_write or
+ *                   kvq_write_token_head lets the next kernel start before
+ *                   its own wait, so where one precedes, the promise covers
+ *                   the kernel before it too.
  *   workspace       device scratch of at least
  *                   kvq_decode_workspace_size(num_seqs, ...) bytes, 256-byte
  *                   aligned.  Its first KVQ_WS_COUNTER_BYTES bytes are
