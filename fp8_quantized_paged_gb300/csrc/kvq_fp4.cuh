@@ -63,6 +63,12 @@ KVQ_DEVI uint32_t hmul2(uint32_t a, uint32_t b) {
 // that it times -inf stays -inf, and finite.
 KVQ_DEVI float bounded_scale(float ls) { return fminf(fmaxf(ls, 0x1p-120f), 0x1p126f); }
 
+// An output from its weighted sum o, inv = 1 / l (0 where l is), and the values' scale: in this order
+// no intermediate leaves binary32's normal range before the output does.
+KVQ_DEVI uint32_t output2(float o0, float o1, float inv, float sv) {
+  return f32x2_to_bf16x2(o0 * inv * sv, o1 * inv * sv);
+}
+
 // States are merged on the maximum's exponent in units of 2^40: finite for every logit that a
 // binary32 scale below 2^24 gives (and bf16 queries), where the exponent itself passes binary32.
 constexpr float kMergeUnit = 0x1p40f;

@@ -393,9 +393,8 @@ KVQ_DEVI void merge_states(int n, State (&a)[E], const Load& load) {
 }
 
 KVQ_DEVI void store_out(uint16_t* dst, const State& a, float sv) {
-  const float f = a.l > 0.f ? sv / a.l : 0.f;
-  *reinterpret_cast<uint2*>(dst) =
-      make_uint2(f32x2_to_bf16x2(a.o.x * f, a.o.y * f), f32x2_to_bf16x2(a.o.z * f, a.o.w * f));
+  const float inv = a.l > 0.f ? 1.f / a.l : 0.f;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(output2(a.o.x, a.o.y, inv, sv), output2(a.o.z, a.o.w, inv, sv));
 }
 
 KVQ_DEVI void head_barrier(int head, int threads) {
@@ -606,10 +605,10 @@ KVQ_DEVI void decode_run(const DecParams& p, uint8_t* smem, const DecSmem& sm, u
     const float sv = __ldg(p.vs + (p.per_head ? gkv : 0));
     uint32_t qb[MT][2];
     {
-      const float ls = __ldg(p.ks + (p.per_head ? gkv : 0)) * p.logit_scale;
+      const float sk = __ldg(p.ks + (p.per_head ? gkv : 0));
       const int qa = q_fragments<KVQ_FMT_E4M3, DH>(raw, qb);
-      pv.ls[0] = bounded_scale(ls * __int_as_float((127 - __shfl_sync(kFull, qa, 8 * t)) << 23));
-      pv.ls[1] = bounded_scale(ls * __int_as_float((127 - __shfl_sync(kFull, qa, 8 * t + 4)) << 23));
+      pv.ls[0] = bounded_scale(sk * __int_as_float((127 - __shfl_sync(kFull, qa, 8 * t)) << 23) * p.logit_scale);
+      pv.ls[1] = bounded_scale(sk * __int_as_float((127 - __shfl_sync(kFull, qa, 8 * t + 4)) << 23) * p.logit_scale);
     }
     Running st;
     st.m[0] = st.m[1] = -INFINITY;
@@ -667,14 +666,14 @@ KVQ_DEVI void decode_run(const DecParams& p, uint8_t* smem, const DecSmem& sm, u
         const int h = 2 * t + e;
         if (h >= p.G) continue;
         if (np == 1) {
-          const float f = st.l[e] > 0.f ? sv / st.l[e] : 0.f;
+          const float inv = st.l[e] > 0.f ? 1.f / st.l[e] : 0.f;
           uint4* dst = reinterpret_cast<uint4*>(orow + h * DH + g * (DH / 8));
 #pragma unroll
           for (int mt = 0; mt < MT; mt += 4)
-            dst[mt / 4] = make_uint4(f32x2_to_bf16x2(o[mt][e] * f, o[mt][2 + e] * f),
-                                     f32x2_to_bf16x2(o[mt + 1][e] * f, o[mt + 1][2 + e] * f),
-                                     f32x2_to_bf16x2(o[mt + 2][e] * f, o[mt + 2][2 + e] * f),
-                                     f32x2_to_bf16x2(o[mt + 3][e] * f, o[mt + 3][2 + e] * f));
+            dst[mt / 4] = make_uint4(output2(o[mt][e], o[mt][2 + e], inv, sv),
+                                     output2(o[mt + 1][e], o[mt + 1][2 + e], inv, sv),
+                                     output2(o[mt + 2][e], o[mt + 2][2 + e], inv, sv),
+                                     output2(o[mt + 3][e], o[mt + 3][2 + e], inv, sv));
         } else {
           if (g == 0) p.ws_ml[mine * p.G + h] = make_float2(merge_max(st.m[e], pv.ls[e]), st.l[e]);
           float4* dst = reinterpret_cast<float4*>(p.ws_o + (mine * p.G + h) * DH + g * (DH / 8));

@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     const uint32_t tm_o = tm_s + 128;
     // the query row times a power of two 2^a, its largest value in [2^14, 2^15): f16, exact
     // but for values 2^38 times smaller than that
-    float lscale = __ldg(p.ks + (p.per_head ? gkv : 0)) * p.logit_scale;
+    float lscale = __ldg(p.ks + (p.per_head ? gkv : 0));
     {
       const uint4* src = reinterpret_cast<const uint4*>(p.q + qrow * DH);
       float amax = 0.f;
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
         a = a > 126 ? 126 : (a < -126 ? -126 : a);
       }
       const float up = __int_as_float((a + 127) << 23);
-      lscale = bounded_scale(lscale * __int_as_float((127 - a) << 23));
+      lscale = bounded_scale(lscale * __int_as_float((127 - a) << 23) * p.logit_scale);
 #pragma unroll
       for (int c = 0; c < DH / 8; ++c) {
         const uint4 w = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     }
     // ---- epilogue: the row of O, normalised, or (keys shared out) as it is
     const float sv = __ldg(p.vs + (p.per_head ? gkv : 0));
-    const float f = ns > 1 ? 1.f : (l > 0.f ? sv / l : 0.f);
+    const float inv = l > 0.f ? 1.f / l : 0.f;
     const int64_t part = (cta - p.whole) * (kTiles * kRows) + t * kRows + r;
     tc::tc_fence_after();
     if (ok) {
@@ -776,10 +776,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
           uint4* dst = reinterpret_cast<uint4*>(p.out + qrow * DH + c);
 #pragma unroll
           for (int y = 0; y < 4; ++y)
-            dst[y] = make_uint4(f32x2_to_bf16x2(o[8 * y] * f, o[8 * y + 1] * f),
-                                f32x2_to_bf16x2(o[8 * y + 2] * f, o[8 * y + 3] * f),
-                                f32x2_to_bf16x2(o[8 * y + 4] * f, o[8 * y + 5] * f),
-                                f32x2_to_bf16x2(o[8 * y + 6] * f, o[8 * y + 7] * f));
+            dst[y] = make_uint4(output2(o[8 * y], o[8 * y + 1], inv, sv), output2(o[8 * y + 2], o[8 * y + 3], inv, sv),
+                                output2(o[8 * y + 4], o[8 * y + 5], inv, sv), output2(o[8 * y + 6], o[8 * y + 7], inv, sv));
         } else if (live) {
           float4* dst = reinterpret_cast<float4*>(p.ws_o + part * DH + c);
 #pragma unroll
@@ -840,10 +838,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
       acc.w = acc.w * a + v.w * w;
       M = nm;
     }
-    const float f = l > 0.f ? sv / l : 0.f;
-    uint2 o;
-    o.x = f32x2_to_bf16x2(acc.x * f, acc.y * f);
-    o.y = f32x2_to_bf16x2(acc.z * f, acc.w * f);
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const uint2 o = make_uint2(output2(acc.x, acc.y, inv, sv), output2(acc.z, acc.w, inv, sv));
     const int64_t qrow = (static_cast<int64_t>(q0) + jr) * p.Hq + gkv * p.G + r % p.G;
     *reinterpret_cast<uint2*>(p.out + qrow * DH + 4 * e) = o;
   }

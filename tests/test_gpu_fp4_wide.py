@@ -100,3 +100,37 @@ def test_small_and_zero_queries(kvq, dh):  # noqa: F811
         widen(g, [1.0, 0.0, 1e-10, 1e-30, 1e-37, 3e-39, 30.0])
         getattr(g, call)()
         g.check(what=call)
+
+
+@pytest.mark.parametrize("log2v", [-126, -118, 100])
+@pytest.mark.parametrize("lens,counts,hq,hkv,dh", [
+    ([300, 64, 17], [40, 64, 3], 8, 2, 64), ([2500], [3], 32, 8, 128), ([900] * 21, [5] * 21, 8, 8, 128),
+    ([20000], [2], 8, 1, 64)])
+def test_scales_near_the_ends(kvq, log2v, lens, counts, hq, hkv, dh):  # noqa: F811
+    """Scales of V down to binary32's least normal one, and of K as far down with queries as
+    far up.  Compared in units of V's scale, beside half of bf16's least step."""
+    for n, call in (([1] * len(lens), "decode"), (counts, "prefill")):
+        b = f4.Batch(len(lens) + dh, lens, hq, hkv, dh, per_head=False)
+        g = OnGpu(kvq, b, n)
+        b.vs = np.array([2.0 ** log2v], np.float32)
+        if log2v < 0:
+            g.q = f4.to_bf16(f4.bf16_to_f32(g.q) * np.float32(2.0 ** 111))  # (near-equal weights: large sums)
+            b.ks = (b.ks * np.float32(2.0 ** -118)).astype(np.float32)
+        g.ks, g.vs, g.dq = dev(b.ks), dev(b.vs), dev(g.q)
+        getattr(g, call)()
+        want, tol = f4.attention(g.q, g.K, g.V, b.ks, 1.0, b.table, b.lens, g.cu, 0, 0)
+        torch.cuda.synchronize()
+        assert int(g.st.item()) == 0
+        off = np.abs(f4.bf16_to_f32(bits(g.out)).astype(np.float64) * 2.0 ** -log2v - want)
+        bad = int((off > tol + 2.0 ** (-134 - log2v)).sum())
+        assert bad == 0, f"{call}: {bad} of {off.size} values off, by up to {off.max():.3g}"
+
+
+def test_decode_of_nothing(kvq):  # noqa: F811
+    """Batches whose sequences are all empty, few of them and many."""
+    for n, hkv in ((1, 1), (3, 2), (200, 8)):
+        b = f4.Batch(n, [0] * n, 8, hkv, 128)
+        g = OnGpu(kvq, b, [1] * n)
+        g.decode()
+        torch.cuda.synchronize()
+        assert int(g.st.item()) == 0 and not bool(g.out.any())
