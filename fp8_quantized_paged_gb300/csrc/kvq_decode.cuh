@@ -691,8 +691,9 @@ KVQ_DEVI void load_q_raw(const DecodeParams& p, int b, int gkv, int hq, int t,
 
 // For the FP8 caches the f16 operand is the query times a per-head power of
 // two 2^a (a returned; the four lanes of a head agree) that puts the head's
-// largest |q| in [2^14, 2^15): exact, and every bf16 query fits f16's range
-// (elements below 2^-38 of the head's largest lose bits as f16 subnormals).
+// largest |q| in [2^14, 2^15): every bf16 query fits f16's range, elements
+// within 2^31 of the head's largest exactly (8 significant bits down to
+// 2^-17), smaller ones off by half of f16's least step, 2^-25, at most.
 // The caller folds 2^-a into the head's logit scale.
 template <int FMT, int DH>
 KVQ_DEVI int q_fragments(const uint32_t (&w)[DH / 8], uint32_t (&qb)[DH / 16][2]) {

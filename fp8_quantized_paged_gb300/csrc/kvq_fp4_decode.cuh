@@ -25,21 +25,24 @@
 // consumers (setmaxnreg: 384 threads launch with 168 each; a step of four pages
 // takes over 200).
 //
-// What bounds it: the conversions.  A page takes a warp about 265 instructions, half
+// What bounds it: the conversions.  A page takes a warp about 270 instructions, half
 // of them at half rate (64 conversions of two values, 64 products by scales, 16 matrix
 // steps); the loop alone needs 296 cycles a page and SM quarter with two warps there
 // (411 with one page a step), and about 450 in place, among copies and waits.  32 sequences
-// of 2049 tokens, 8 KV heads: 30.7 us (11.2 us at the measured bandwidth); of them
+// of 2049 tokens, 8 KV heads: 31.1 us (11.2 us at the measured bandwidth); of them
 // 2.5 the plan and the block ids, 2.3 the first pages, 16 the loop, 5 the states of
-// cut segments.  128 sequences of 17 to 16384 tokens under a window: 63.0 us (31.5).
-// One of 32768: 19.1 us (5.6).
+// cut segments.  128 sequences of 17 to 16384 tokens under a window: 63.4 us (31.5).
+// One of 32768: 19.0 us (5.6).
 //
 // Per page, 16 tokens against the group's G <= 8 query heads:
 //   S = K^ Q^T  m16n8k16 f16 matrix steps: lane (g, t) converts the codes of
 //               token rows g and g + 8, dims t dh/4 .. (t + 1) dh/4, and
 //               multiplies them by their block scales (exact)
 //   P = 2^(x - m + 7) in binary32, rounded once to f16 (the 2^7 keeps small
-//               weights out of f16's subnormals; it cancels in the division)
+//               weights out of f16's subnormals; it cancels in the division).  One f16
+//               a weight: within 2^-11, which bf16's 2^-8 in the output covers (error
+//               against 64 bits 0.0017 relative, with binary32 weights 0.0016 to 0.0017);
+//               a second part would take half as many matrix steps again
 //   O^T += V^T P^T  lane (g, t) holds dims g dh/8 .. (g + 1) dh/8 of tokens
 //               t, t + 8, t + 4, t + 12: two tokens' codes are interleaved
 //               four bits by four with two shifts and two selects per eight

@@ -12,7 +12,10 @@ namespace fp4 {
 constexpr int kMinShare[2] = {2, 5};
 // And where they would after the last whole wave.  Ragged chunks under a window (10 blocks, 220
 // items): whole 41.5 us, the rest in two 47.2.  2048 queries over 32768 tokens (256 blocks, 256
-// items): whole 919 us, the rest in four 858.
+// items): whole 919 us, the rest in four 858.  In between, one sequence and 8 KV heads, whole / with
+// a least share of 12 / 24 blocks: 160 items of 32 blocks 114 / 111 / 114 us, of 48 171 / 142 / 171, of
+// 64 227 / 169 / 192, of 128 453 / 296 / 312; 200 items of 48 180 / 154 / 181, of 96 349 / 267 / 267; 256
+// items of 64 242 / 265 / 241, of 96 354 / 364 / 379, of 128 467 / 462 / 463.
 constexpr int kMinTail = 24;
 constexpr int kOverhead = 6;  // a share's start, end and merge, in blocks
 

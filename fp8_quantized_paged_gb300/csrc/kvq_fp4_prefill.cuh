@@ -18,7 +18,10 @@
 //     (A = P from tensor memory, K 64), then the half's next S at once
 //   warps 0-3, 4-7 (softmax of tiles 0, 1; thread = row = TMEM lane)  64 keys
 //     at a time: S from TMEM, mask, P = 2^(x - m + 7) as f16 over the S columns
-//     that it came from, with the running maximum m raised lazily (and O rescaled)
+//     that it came from, with the running maximum m raised lazily (and O rescaled).
+//     One f16 a weight: within 2^-11, which bf16's 2^-8 in the output covers (error against 64
+//     bits 0.0017 relative, with binary32 weights 0.0016 to 0.0017); a second part would double P V,
+//     and the operands' share of shared memory with it
 // S and P share columns: 2 tiles x (2 halves of 64 + 128 of O) fill the 512.  A
 // half's next S waits for the PV that reads its P, while the softmax works on the
 // other half.  The softmax takes most registers (setmaxnreg).
@@ -26,9 +29,9 @@
 // What bounds it: an N 64 step reads 6 KB of shared memory in 48 cycles (128 bytes a
 // cycle, all there are), an N 128 step 8 KB in 64: for the two tiles' block 32 x 48 +
 // 16 x 64 = 2560 cycles beside the converters' loads and stores, of about 4000 measured.
-// Shared memory's bandwidth is 83% taken (51 operands, 32 converters); the rest is the
+// Shared memory's bandwidth is 82% taken (50 operands, 32 converters); the rest is the
 // chain of a half, softmax, P V, next S.  2048 queries of 32 heads over 32768 tokens,
-// 8 KV heads of 128 dims: 860 us, 1240 TFLOP/s (563 us at the measured bf16 rate).
+// 8 KV heads of 128 dims: 859 to 865 us, 1240 TFLOP/s (563 us at the measured bf16 rate).
 // On the way: S in steps of N 128, tiles taking turns 1201 us; halves 1106; issue
 // under elect.sync, K and V converted by a warpgroup each 927; the rest after whole
 // waves split 857.  S in one 64-column buffer with two of P beside it 987.
@@ -596,8 +599,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) prefill_kernel(const __grid_co
     const int64_t qrow = live ? (static_cast<int64_t>(q0) + jr) * p.Hq + gkv * p.G + r % p.G : 0;
     const uint32_t tm_s = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * kTileCols;
     const uint32_t tm_o = tm_s + 128;
-    // the query row times a power of two 2^a, its largest value in [2^14, 2^15): f16, exact
-    // but for values 2^38 times smaller than that
+    // the query row times a power of two 2^a, its largest value in [2^14, 2^15): f16, exact for
+    // values down to 2^-17 (8 significant bits over a least step of 2^-24), off by 2^-25 at most below
     float lscale = __ldg(p.ks + (p.per_head ? gkv : 0));
     {
       const uint4* src = reinterpret_cast<const uint4*>(p.q + qrow * DH);

@@ -387,8 +387,10 @@ extern "C" int kvq_fp4_read(const void* k_cache, const void* v_cache, int64_t nu
   p.out_stride = out_stride;
   p.status = dev_status;
   // Rows of a warp, for rows of 64 blocks (more of them where a row has fewer).  Few rows go one
-  // to a warp, for the shortest chain of loads (32 rows: 4.3 us, two a warp 5.1); 2049 rows take
-  // 5.1 us two to a warp and 5.7 one; 262144 take 165 us at four, 172 at two, 187 at one.
+  // to a warp, for the shortest chain of loads.  One sequence of 8 heads of 128, graph replay over
+  // tensors past L2, one / two / four a warp: 32 rows 2.7 / 3.4 / 5.2 us, 1023 3.4 / 4.0 / 5.8, 2049
+  // 4.7 / 4.4 / 6.1, 32768 35.2 / 35.5 / 34.6, 65535 65.5 / 61.4 / 62.0, 262144 242 / 215 / 222; 64
+  // sequences of 512 to 8192 tokens, new inputs every time, 180 / 165 / 160.
   const int units = num_kv_heads * (head_dim / 16);
   const int base = num_rows < 1024 ? 1 : (num_rows < 65536 ? 2 : 4);
   p.warp_rows = std::min(fp4::kMaxReadRows, base * std::max(1, 64 / units));

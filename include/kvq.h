@@ -221,7 +221,9 @@ KVQ_API size_t kvq_decode_workspace_size(int num_seqs, int num_q_heads, int num_
  *
  *   q               bf16 [num_seqs][num_q_heads][head_dim], any finite values
  *                   (for the FP8 caches each head's query is scaled by a power
- *                   of two, exactly, before its f16 tensor-core conversion).
+ *                   of two before its f16 tensor-core conversion, which is
+ *                   exact for values within 2^31 of the head's largest and
+ *                   off by 2^-39 of that at most for smaller ones).
  *   block_tables    int32 [num_seqs][max_blocks_per_seq]; entries past
  *                   ceil(L_b / block_size) are never read.
  *   seq_lens        int32 [num_seqs]; 0 gives a zero output row.

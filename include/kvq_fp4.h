@@ -141,9 +141,12 @@ KVQ_API size_t kvq_fp4_workspace_size(int num_seqs, int num_q_heads, int num_kv_
  *   dev_status     optional; KVQ_DEV_BAD_BLOCK (the page is masked out),
  *                  KVQ_DEV_BAD_SEQLEN (L_b < 0 or > max_blocks_per_seq *
  *                  block_size: a zero row), KVQ_DEV_WAIT_TIMEOUT
- * Statistics and sums are binary32.  The logits use q exactly (scaled by a
- * power of two, as in kvq_decode_attn); each probability reaches the product
- * with V^ as one f16, within 2^-11 of its value or 2^-32 of the row's largest.
+ * Statistics and sums are binary32.  The logits use q as f16 after a scaling by
+ * a power of two: exact for values within 2^31 of the query head's largest, off
+ * by 2^-39 of that at most for smaller ones, as in kvq_decode_attn.  Finite
+ * queries of any magnitude are fine: logits past binary32's integers leave the
+ * largest one's token.  Each probability reaches the product with V^ as one f16,
+ * within 2^-11 of its value or 2^-32 of the row's largest.
  * Limits: num_seqs <= 4096; num_seqs * num_kv_heads <= 65536; num_seqs *
  * (max_blocks_per_seq + 8) * num_kv_heads < 2^31; num_kv_heads <= 256;
  * max_blocks_per_seq * block_size < 2^31.
