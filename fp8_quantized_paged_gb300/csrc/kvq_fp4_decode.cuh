@@ -456,17 +456,16 @@ KVQ_DEVI void decode_copies(const DecParams& p, uint8_t* smem, uint64_t* full, u
         if (!held) {
           bad_s[s] = bad;
           last_s[s] = k;  // (a bad page completes its phase too)
-        }
-        if (held) {
-        } else if (bad) {
-          flag_status(p.status, KVQ_DEV_BAD_BLOCK);
-          mbar_arrive(&full[s]);
-        } else {
-          const int64_t at = (static_cast<int64_t>(blk) * p.Hkv + gr * p.HG) * Page<DH>::kBytes;
-          uint8_t* dst = smem + s * 2 * half;
-          mbar_arrive_expect_tx(&full[s], 2 * half);
-          bulk_load(dst, p.kc + at, half, &full[s]);
-          bulk_load(dst + half, p.vc + at, half, &full[s]);
+          if (bad) {
+            flag_status(p.status, KVQ_DEV_BAD_BLOCK);
+            mbar_arrive(&full[s]);
+          } else {
+            const int64_t at = (static_cast<int64_t>(blk) * p.Hkv + gr * p.HG) * Page<DH>::kBytes;
+            uint8_t* dst = smem + s * 2 * half;
+            mbar_arrive_expect_tx(&full[s], 2 * half);
+            bulk_load(dst, p.kc + at, half, &full[s]);
+            bulk_load(dst + half, p.vc + at, half, &full[s]);
+          }
         }
         pending = false;
         moved = true;
