@@ -115,3 +115,19 @@ def test_prefill_of_no_queries(kvq):  # noqa: F811
         g.prefill(max_q=max_q)
     torch.cuda.synchronize()
     assert int(g.st.item()) == 0
+
+
+@pytest.mark.parametrize("lens,counts,hq,hkv,dh", [([2500], [3], 32, 8, 128), ([5000], [40], 16, 4, 64), ([2300] * 20, [2] * 20, 8, 8, 128)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1500, 7)])
+def test_nan_in_shared_out_keys(kvq, lens, counts, hq, hkv, dh, window, sinks):  # noqa: F811
+    """NaN keys and values in tokens of one piece of a sequence reach the rows that see them
+    through the merge, and no others; a sequence that is NaN alone, too."""
+    b = f4.Batch(len(lens) + dh + window, lens, hq, hkv, dh)
+    b.k[2, 0, 3] = b.v[5, 1, 40] = b.v[1200, 2, 17] = b.k[lens[0] - 2, 3, 50] = 0x7FC0
+    if len(lens) > 1:
+        b.k[lens[0]:2 * lens[0], 4, 0] = 0x7FC0
+    for n, call in (([1] * len(lens), "decode"), (counts, "prefill")):
+        g = OnGpu(kvq, b, n)
+        getattr(g, call)(window, sinks)
+        g.check(window, sinks, call)
+        assert bool(torch.isnan(g.out.float()).any()) and not bool(torch.isnan(g.out.float()).all())

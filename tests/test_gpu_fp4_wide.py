@@ -134,3 +134,22 @@ def test_decode_of_nothing(kvq):  # noqa: F811
         g.decode()
         torch.cuda.synchronize()
         assert int(g.st.item()) == 0 and not bool(g.out.any())
+
+
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("lens,counts,hq,hkv", [([300, 150], [70, 40], 8, 2), ([2500], [4], 32, 8), ([700] * 20, [3] * 20, 8, 8)])
+def test_bad_queries_stay_in_their_rows(kvq, dh, lens, counts, hq, hkv):  # noqa: F811
+    """A NaN or an infinity in a query head is that head's output; its neighbours, which share
+    matrix steps and decisions of a warp with it, are right."""
+    for n, call in (([1] * len(lens), "decode"), (counts, "prefill")):
+        b = f4.Batch(len(lens) + dh + 1, lens, hq, hkv, dh)
+        g = OnGpu(kvq, b, n)
+        q = f4.bf16_to_f32(g.q).copy()
+        q[0, 0, 3], q[-1, hq - 1, dh - 1], q[-1, 1, 0] = np.nan, np.inf, -np.inf
+        g.q = f4.to_bf16(q)
+        g.dq = dev(g.q)
+        getattr(g, call)()
+        with np.errstate(invalid="ignore"):
+            g.check(what=call)
+        nan = torch.isnan(g.out.float())
+        assert int(nan.any(-1).sum()) == 3 and bool(nan[0, 0].all())
