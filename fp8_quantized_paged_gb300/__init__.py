@@ -361,17 +361,24 @@ def new_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, device="cuda"):
 
 
 # --------------------------------------------------------------------------
-# the microscaled 4-bit cache
+# the microscaled 4-bit cache, and the operators around a serving step
 # --------------------------------------------------------------------------
 
 _FP4 = ("kvq_fp4_write", "kvq_fp4_read", "kvq_fp4_workspace_size", "kvq_fp4_decode_attn",
         "kvq_fp4_prefill_attn", "new_fp4_cache", "new_fp4_workspace")
+_STEP = ("kvq_rope_write", "kvq_tree_commit", "kvq_copy_pages", "kvq_pages_init", "kvq_pages_alloc",
+         "kvq_pages_free", "kvq_pages_fork", "new_page_pool", "rope_turns", "KVQ_DEV_NO_PAGES",
+         "KVQ_DEV_BAD_TREE")
 
 
 def __getattr__(name):
-    """The names of ``fp4``, which needs torch at import where this module does not."""
+    """The names of ``fp4`` and ``step``, which need torch at import where this module does not."""
     if name in _FP4:
         from . import fp4
         globals().update({n: getattr(fp4, n) for n in _FP4})
+        return globals()[name]
+    if name in _STEP:
+        from . import step
+        globals().update({n: getattr(step, n) for n in _STEP})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

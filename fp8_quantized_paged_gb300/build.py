@@ -5,8 +5,8 @@ per cache format and head size), then nvcc links the
 shared library (static CUDA runtime, no libcuda link: the tensor-map encoder
 is looked up through the runtime's driver entry-point query).
 
-The 4-bit cache's Python binding is a library of its own, built with g++ against
-Python's and torch's headers.  libkvq.so needs nvcc alone: where the binding does
+The native Python binding (the 4-bit cache, the operators around a serving step) is
+a library of its own, built with g++ against Python's and torch's headers.  libkvq.so needs nvcc alone: where the binding does
 not build, build() says so on stderr and links the library all the same.
 """
 from __future__ import annotations
@@ -23,18 +23,19 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libkvq.so")
 SOURCES = ["kvq_host.cu", "kvq_write.cu", "kvq_decode.cu", "kvq_decode_tc.cu", "kvq_decode_blk.cu",
            "kvq_static.cu", "kvq_calib.cu", "kvq_prefill.cu", "kvq_decode_variant.cu",
-           "kvq_fp4_write.cu", "kvq_fp4_decode.cu", "kvq_fp4_prefill.cu"]
+           "kvq_fp4_write.cu", "kvq_fp4_decode.cu", "kvq_fp4_prefill.cu", "kvq_rope.cu", "kvq_pages.cu"]
 HEADERS = ["kvq_common.cuh", "kvq_host.h", "kvq_decode.cuh", "kvq_tc.cuh", "kvq_decode_tc.cuh",
            "kvq_decode_blk.cuh", "kvq_prefill_tc.cuh", "kvq_fp4.cuh", "kvq_fp4_host.h", "kvq_fp4_decode.cuh",
-           "kvq_fp4_prefill.cuh"]
+           "kvq_fp4_prefill.cuh", "kvq_quant.cuh"]
 # (object, source, defines): one object per translation unit, the decode
 # variants once per (format, head size); kvq_fmt 0 = BF16, 1 = E4M3, 2 = E5M2
 UNITS = [(os.path.splitext(s)[0], s, []) for s in SOURCES if s != "kvq_decode_variant.cu"] + [
     (f"kvq_decode_f{fmt}_d{dh}", "kvq_decode_variant.cu",
      [f"-DKVQ_VARIANT_FMT={fmt}", f"-DKVQ_VARIANT_DH={dh}"])
     for fmt in (1, 2, 0) for dh in (128, 64)]
-# the 4-bit cache's Python binding: host code against torch's headers
-BINDING = "fp4_binding.cpp"
+# the Python binding of the 4-bit cache and of the operators around a step: host code against torch's headers
+BINDING = ["fp4_binding.cpp", "step_binding.cpp"]
+BINDING_HEADERS = ["binding.h"]
 BINDING_LIB = os.path.join(BUILD, "_kvq_fp4.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -51,7 +52,7 @@ def _nvcc() -> str:
 def _inputs(sources):
     inc = os.path.join(os.path.dirname(HERE), "include")
     return ([os.path.join(CSRC, s) for s in sources] +
-            [os.path.join(inc, h) for h in ("kvq.h", "kvq_fp4.h")] + [os.path.abspath(__file__)])
+            [os.path.join(inc, h) for h in ("kvq.h", "kvq_fp4.h", "kvq_step.h")] + [os.path.abspath(__file__)])
 
 
 def _newer(lib: str, sources) -> bool:
@@ -88,7 +89,7 @@ def _binding_stamp() -> str:
 
 
 def binding_up_to_date() -> bool:
-    if not _newer(BINDING_LIB, [BINDING]) or not os.path.exists(BINDING_LIB + ".stamp"):
+    if not _newer(BINDING_LIB, BINDING + BINDING_HEADERS) or not os.path.exists(BINDING_LIB + ".stamp"):
         return False
     with open(BINDING_LIB + ".stamp") as f:
         return f.read() == _binding_stamp()
@@ -104,7 +105,7 @@ def build_binding(verbose: bool = False) -> str:
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     tmp = BINDING_LIB + f".tmp{os.getpid()}"
     cmd = [shutil.which("g++") or "c++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
-           "-Wno-attributes", os.path.join(CSRC, BINDING), "-o", tmp,
+           "-Wno-attributes", *[os.path.join(CSRC, s) for s in BINDING], "-o", tmp,
            "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(torch, "include"),
            "-I" + os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            "-I" + os.path.join(cuda, "include"), "-I/usr/local/cuda/include",
@@ -113,7 +114,7 @@ def build_binding(verbose: bool = False) -> str:
         print(" ".join(cmd), file=sys.stderr)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on {BINDING}:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"g++ failed on {' '.join(BINDING)}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING_LIB)
     with open(BINDING_LIB + ".stamp", "w") as f:
         f.write(_binding_stamp())

@@ -1,0 +1,633 @@
+// kvq_pages.cu -- rows and pages of the caches moved, and the pool that pages
+// are taken from: kvq_tree_commit, kvq_copy_pages, kvq_pages_*.
+//
+// Nothing here computes: each kernel is a chain of a few dependent loads
+// (lengths, then a path or a table, then rows) and then a copy, so the work
+// is laid out to have all of a warp's rows in flight behind one such chain.
+//
+// The pool takes the lowest free pages first.  A bit for each free page makes
+// that a prefix sum over num_blocks / 32 words (200 000 pages are 25 KB, where
+// their counts are 800 KB) whose result depends on nothing but the pool:
+// giving pages back in any order, by atomics, leaves the same pool.
+#include "../../include/kvq_step.h"
+#include "kvq_common.cuh"
+#include "kvq_host.h"
+
+namespace kvq {
+namespace pages {
+
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+constexpr int kTok = 16;
+constexpr int kMaxRowsCaches = 128;  // caches of one launch (their descriptions are kernel parameters)
+constexpr int kMaxTables = 4096;     // sequences of a pool's call
+
+struct Caches {
+  kvq_rows c[kMaxRowsCaches];
+};
+
+// ------------------------------------------------------------------ commit
+
+struct CommitParams {
+  int caches, B, hkv, max_blocks, max_path, first;  // first: this launch writes new_lens
+  int64_t num_blocks;
+  const int32_t* cu_q;
+  const int32_t* tables;
+  const int32_t* seq_lens;
+  const int32_t* path;
+  const int32_t* taken;
+  int32_t* new_lens;
+  uint32_t* status;
+};
+
+constexpr int kUnits = 8;  // 16-byte (4-byte) units that a lane has in flight
+
+// Rows [i0, i0 + c) of the path in every head, a T a unit: all of a head's rows are read before
+// the first is written.  A path rises, so rows of later chunks come from at or behind their own places.
+template <typename T>
+KVQ_DEVI void move_rows(const CommitParams& p, uint8_t* data, int64_t page_bytes, int part_off, int row_bytes,
+                        const int32_t* path, const int32_t* table, int before, int taken) {
+  const int lane = threadIdx.x & 31;
+  const int u = row_bytes / static_cast<int>(sizeof(T));  // units of a row
+  if (u == 0) return;
+  const int most = max(1, 32 * kUnits / u);
+  for (int i0 = 0; i0 < taken; i0 += most) {
+    const int c = min(most, taken - i0), per_head = c * u;
+    const int hb = max(1, 32 * kUnits / per_head);  // heads of a batch
+    for (int h0 = 0; h0 < p.hkv; h0 += hb) {
+      const int n = min(hb, p.hkv - h0) * per_head;
+      T val[kUnits];
+      T* dst[kUnits];
+#pragma unroll
+      for (int y = 0; y < kUnits; ++y) {
+        const int x = lane + 32 * y;
+        dst[y] = nullptr;
+        if (x >= n) continue;
+        const int h = x / per_head, r = (x - h * per_head) / u, e = x % u, i = i0 + r;
+        const int from = path[i];
+        if (from == i) continue;  // in its place already
+        const int s = before + from, d = before + i;
+        const int ps = __ldg(table + s / kTok), pd = __ldg(table + d / kTok);
+        if (ps < 0 || ps >= p.num_blocks || pd < 0 || pd >= p.num_blocks) {
+          flag_status(p.status, KVQ_DEV_BAD_BLOCK);
+          continue;
+        }
+        const int64_t head = h0 + h;
+        const uint8_t* src = data + (ps * static_cast<int64_t>(p.hkv) + head) * page_bytes + part_off + (s % kTok) * row_bytes;
+        dst[y] = reinterpret_cast<T*>(data + (pd * static_cast<int64_t>(p.hkv) + head) * page_bytes + part_off +
+                                      (d % kTok) * row_bytes) + e;
+        val[y] = reinterpret_cast<const T*>(src)[e];
+      }
+      __syncwarp();
+#pragma unroll
+      for (int y = 0; y < kUnits; ++y)
+        if (dst[y]) *dst[y] = val[y];
+      __syncwarp();
+    }
+  }
+}
+
+// A warp takes a sequence and a cache, all heads: 4 KB of rows in flight behind one chain of
+// lengths, path and table.
+__global__ void __launch_bounds__(128) commit_kernel(const __grid_constant__ CommitParams p,
+                                                     const __grid_constant__ Caches cs) {
+  pdl_wait();
+  pdl_allow_next();
+  const int lane = threadIdx.x & 31;
+  const int per = max(1, p.caches);
+  const int64_t items = static_cast<int64_t>(p.B) * per, warps = static_cast<int64_t>(gridDim.x) * 4;
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5); it < items; it += warps) {
+    const int b = static_cast<int>(it / per), c = static_cast<int>(it - static_cast<int64_t>(b) * per);
+    const int L = __ldg(p.seq_lens + b), q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1);
+    const int taken = __ldg(p.taken + b);
+    const int32_t* path = p.path + static_cast<int64_t>(b) * p.max_path;
+    const bool bad_q = q0 < 0 || q1 < q0;
+    const int n = bad_q ? 0 : q1 - q0;
+    const bool bad_len = L < n || L > p.max_blocks * kTok;
+    bool good = taken >= 0 && taken <= min(n, p.max_path);
+    if (good && !bad_q && !bad_len) {
+      bool rises = true;
+      for (int i = lane; i < taken; i += 32) {
+        const int at = __ldg(path + i);
+        rises = rises && at >= 0 && at < n && (i == 0 || __ldg(path + i - 1) < at);
+      }
+      good = __all_sync(kAll, rises);
+    }
+    const bool moves = good && !bad_q && !bad_len;
+    if (c == 0 && p.first && lane == 0) {
+      p.new_lens[b] = moves ? L - n + taken : L;
+      if (!moves) flag_status(p.status, bad_q ? KVQ_DEV_BAD_QLEN : bad_len ? KVQ_DEV_BAD_SEQLEN : KVQ_DEV_BAD_TREE);
+    }
+    if (!moves || p.caches == 0) continue;
+    const kvq_rows r = cs.c[c];
+    const int32_t* table = p.tables + static_cast<int64_t>(b) * p.max_blocks;
+    const int64_t page = static_cast<int64_t>(kTok) * (r.row_bytes + r.sub_bytes);
+    uint8_t* data = static_cast<uint8_t*>(r.data);
+    if (r.row_bytes % 16 == 0 && r.sub_bytes % 4 == 0)
+      move_rows<uint4>(p, data, page, 0, r.row_bytes, path, table, L - n, taken);
+    else
+      move_rows<uint32_t>(p, data, page, 0, r.row_bytes, path, table, L - n, taken);
+    move_rows<uint32_t>(p, data, page, kTok * r.row_bytes, r.sub_bytes, path, table, L - n, taken);
+  }
+}
+
+// ------------------------------------------------------------------ copies of pages
+
+struct CopyParams {
+  int caches, hkv, n;
+  int64_t num_blocks;
+  const int32_t* copies;
+  uint32_t* status;
+};
+
+constexpr int kCopyThreads = 256;
+
+// A CTA a page of a cache, all its heads: one run of 16 Hkv (row + sub) bytes.
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyParams p,
+                                                            const __grid_constant__ Caches cs) {
+  pdl_wait();
+  pdl_allow_next();
+  const int64_t items = static_cast<int64_t>(p.n) * p.caches;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int i = static_cast<int>(it / p.caches), c = static_cast<int>(it - static_cast<int64_t>(i) * p.caches);
+    const int s = __ldg(p.copies + 2 * i), d = __ldg(p.copies + 2 * i + 1);
+    if (s < 0 || d < 0) continue;
+    if (s >= p.num_blocks || d >= p.num_blocks) {
+      if (threadIdx.x == 0) flag_status(p.status, KVQ_DEV_BAD_BLOCK);
+      continue;
+    }
+    const kvq_rows r = cs.c[c];
+    const int64_t bytes = static_cast<int64_t>(kTok) * p.hkv * (r.row_bytes + r.sub_bytes);
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(r.data) + s * bytes);
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(r.data) + d * bytes);
+    const int64_t n = bytes / 16;
+    for (int64_t x = threadIdx.x; x < n; x += 4 * kCopyThreads) {
+      uint4 v[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        if (x + y * kCopyThreads < n) v[y] = __ldcs(src + x + y * kCopyThreads);
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        if (x + y * kCopyThreads < n) dst[x + y * kCopyThreads] = v[y];
+    }
+  }
+}
+
+// ------------------------------------------------------------------ the pool
+
+struct PoolParams {
+  int32_t* pool;
+  int num_blocks;
+  int32_t* tables;
+  int max_blocks;
+  const int32_t* old_lens;
+  const int32_t* new_lens;
+  int B;
+  uint32_t* status;
+};
+
+KVQ_DEVI int pages_of(int len) { return len / kTok + (len % kTok != 0); }
+KVQ_DEVI bool length_ok(int len, int max_blocks) { return len >= 0 && pages_of(len) <= max_blocks; }
+
+constexpr int kPoolThreads = 1024;
+
+// Block-wide exclusive scan; warp_sum: a word for each warp.
+template <int NT>
+KVQ_DEVI int64_t block_scan(int64_t v, int64_t& total, int64_t* warp_sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t incl = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t t = __shfl_up_sync(kAll, incl, off);
+    if (lane >= off) incl += t;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  int64_t base = 0;
+  total = 0;
+  for (int w = 0; w < NT / 32; ++w) {
+    const int64_t s = warp_sum[w];
+    base += w < warp ? s : 0;
+    total += s;
+  }
+  __syncthreads();
+  return base + incl - v;
+}
+
+// Page after page of the pool's free ones, lowest first, to take(rank, page) for the ranks below
+// `wanted`: each thread counts four words' bits, a scan gives their ranks.  One CTA.
+template <typename F>
+KVQ_DEVI void take_lowest(int32_t* pool, int num_blocks, int64_t wanted, int64_t* warp_sum, F&& take) {
+  uint32_t* bits = reinterpret_cast<uint32_t*>(pool + KVQ_POOL_HEADER + num_blocks);
+  const int words = (num_blocks + 31) / 32;
+  int64_t base = 0;
+  for (int w0 = 0; w0 < words && base < wanted; w0 += 4 * kPoolThreads) {
+    uint32_t w[4];
+    int n = 0;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const int at = w0 + 4 * static_cast<int>(threadIdx.x) + y;
+      w[y] = at < words ? bits[at] : 0u;
+      n += __popc(w[y]);
+    }
+    int64_t total;
+    int64_t rank = base + block_scan<kPoolThreads>(n, total, warp_sum);
+    base += total;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const int at = w0 + 4 * static_cast<int>(threadIdx.x) + y;
+      uint32_t left = w[y];
+      while (left && rank < wanted) {
+        const int bit = __ffs(left) - 1;
+        left &= left - 1;
+        const int page = 32 * at + bit;
+        if (page < num_blocks) take(rank, page);
+        ++rank;
+      }
+      if (left != w[y]) bits[at] = left;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kPoolThreads) alloc_kernel(const __grid_constant__ PoolParams p) {
+  __shared__ int32_t off[kMaxTables + 1];
+  __shared__ int64_t warp_sum[kPoolThreads / 32];
+  pdl_wait();
+  pdl_allow_next();
+  // what each sequence wants, and where its pages' ranks begin
+  constexpr int kPer = kMaxTables / kPoolThreads;
+  int need[kPer];
+  int64_t mine = 0;
+#pragma unroll
+  for (int y = 0; y < kPer; ++y) {
+    const int b = kPer * static_cast<int>(threadIdx.x) + y;
+    need[y] = 0;
+    if (b < p.B) {
+      const int a = p.old_lens[b], z = p.new_lens[b];
+      if (!length_ok(a, p.max_blocks) || !length_ok(z, p.max_blocks))
+        flag_status(p.status, KVQ_DEV_BAD_SEQLEN);
+      else
+        need[y] = max(0, pages_of(z) - pages_of(a));
+    }
+    mine += need[y];
+  }
+  int64_t total;
+  int64_t at = block_scan<kPoolThreads>(mine, total, warp_sum);
+  if (total > p.pool[1]) {
+    if (threadIdx.x == 0) flag_status(p.status, KVQ_DEV_NO_PAGES);
+    return;
+  }
+#pragma unroll
+  for (int y = 0; y < kPer; ++y) {
+    const int b = kPer * static_cast<int>(threadIdx.x) + y;
+    if (b <= p.B) off[b] = static_cast<int32_t>(at);
+    at += need[y];
+  }
+  if (threadIdx.x == 0) off[p.B] = static_cast<int32_t>(total);
+  __syncthreads();
+  int b = -1;
+  take_lowest(p.pool, p.num_blocks, total, warp_sum, [&](int64_t rank, int page) {
+    if (b < 0 || rank >= off[b + 1] || rank < off[b]) {  // the last b with off[b] <= rank
+      int lo = 0, hi = p.B - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (off[mid] <= rank)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      b = lo;
+    }
+    p.pool[KVQ_POOL_HEADER + page] = 1;
+    p.tables[static_cast<int64_t>(b) * p.max_blocks + pages_of(p.old_lens[b]) + (rank - off[b])] = page;
+  });
+  __syncthreads();
+  if (threadIdx.x == 0) p.pool[1] -= static_cast<int32_t>(total);
+}
+
+// One holder less; the last one's page is free.  False where nothing held it.
+KVQ_DEVI bool let_go(int32_t* pool, int num_blocks, int page) {
+  int32_t* refs = pool + KVQ_POOL_HEADER;
+  const int32_t old = atomicSub(refs + page, 1);
+  if (old <= 0) {
+    atomicAdd(refs + page, 1);
+    return false;
+  }
+  if (old == 1) {
+    atomicOr(reinterpret_cast<uint32_t*>(refs + num_blocks) + page / 32, 1u << (page % 32));
+    atomicAdd(pool + 1, 1);
+  }
+  return true;
+}
+
+constexpr int kRowThreads = 128;
+
+__global__ void __launch_bounds__(kRowThreads) free_kernel(const __grid_constant__ PoolParams p) {
+  pdl_wait();
+  pdl_allow_next();
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const int a = p.old_lens[b], z = p.new_lens[b];
+    if (!length_ok(a, p.max_blocks) || !length_ok(z, p.max_blocks)) {
+      if (threadIdx.x == 0) flag_status(p.status, KVQ_DEV_BAD_SEQLEN);
+      continue;
+    }
+    int32_t* row = p.tables + static_cast<int64_t>(b) * p.max_blocks;
+    for (int i = pages_of(z) + threadIdx.x; i < pages_of(a); i += kRowThreads) {
+      const int page = row[i];
+      row[i] = -1;
+      if (page < 0 || page >= p.num_blocks || !let_go(p.pool, p.num_blocks, page))
+        flag_status(p.status, KVQ_DEV_BAD_BLOCK);
+    }
+  }
+}
+
+struct ForkParams {
+  int32_t* pool;
+  int num_blocks;
+  const int32_t* tables;
+  const int32_t* lens;
+  int num_src, max_blocks;
+  const int32_t* parents;
+  int num_out;
+  int32_t* out_tables;
+  int32_t* out_lens;
+  int32_t* copies;
+  uint32_t* status;
+};
+
+struct ForkRow {
+  int src, len;  // -1: an empty row
+  int last;      // the last page, where it is not full and can be copied; -1
+  bool bad_len, bad_page;
+};
+
+// What row b goes on from.  A page that nothing holds stays so until the last CTA is done, one that is
+// held is held throughout, so every CTA sees the same.
+KVQ_DEVI ForkRow fork_row(const ForkParams& p, int b) {
+  ForkRow r = {-1, 0, -1, false, false};
+  const int s = __ldg(p.parents + b);
+  if (s < 0) return r;
+  const int len = s < p.num_src ? __ldg(p.lens + s) : -1;
+  if (!length_ok(len, p.max_blocks)) {
+    r.bad_len = true;
+    return r;
+  }
+  r.src = s;
+  r.len = len;
+  if (len % kTok) {
+    const int page = __ldg(p.tables + static_cast<int64_t>(s) * p.max_blocks + len / kTok);
+    if (page >= 0 && page < p.num_blocks && __ldcg(p.pool + KVQ_POOL_HEADER + page) > 0)
+      r.last = page;
+    else
+      r.bad_page = true;
+  }
+  return r;
+}
+
+// CTA 0 takes the pages, the others write the rows; all of them first count the pages wanted, and
+// the last one that is done changes what the others compare with: the count of free pages, and the
+// counts of those taken.
+__global__ void __launch_bounds__(kPoolThreads) fork_kernel(const __grid_constant__ ForkParams p) {
+  __shared__ int32_t off[kMaxTables + 1];  // the row that takes the k-th page
+  __shared__ int64_t warp_sum[kPoolThreads / 32];
+  __shared__ bool is_last;
+  pdl_wait();
+  pdl_allow_next();
+  constexpr int kPer = kMaxTables / kPoolThreads;
+  uint32_t wants = 0;
+#pragma unroll
+  for (int y = 0; y < kPer; ++y) {
+    const int b = kPer * static_cast<int>(threadIdx.x) + y;
+    if (b < p.num_out && fork_row(p, b).last >= 0) wants |= 1u << y;
+  }
+  int64_t total;
+  int64_t at = block_scan<kPoolThreads>(__popc(wants), total, warp_sum);
+  const bool enough = total <= __ldcg(p.pool + 1);
+  if (!enough && blockIdx.x == 0 && threadIdx.x == 0) flag_status(p.status, KVQ_DEV_NO_PAGES);
+  if (enough && blockIdx.x == 0) {
+#pragma unroll
+    for (int y = 0; y < kPer; ++y)
+      if (wants >> y & 1u) off[at++] = kPer * static_cast<int>(threadIdx.x) + y;
+    __syncthreads();
+    take_lowest(p.pool, p.num_blocks, total, warp_sum, [&](int64_t rank, int page) {
+      const int b = off[rank];
+      const ForkRow r = fork_row(p, b);
+      p.out_tables[static_cast<int64_t>(b) * p.max_blocks + r.len / kTok] = page;
+      p.copies[2 * b] = r.last;
+      p.copies[2 * b + 1] = page;
+    });
+  }
+  if (enough && (blockIdx.x > 0 || gridDim.x == 1)) {
+    const int first = gridDim.x == 1 ? 0 : blockIdx.x - 1, step = gridDim.x == 1 ? 1 : gridDim.x - 1;
+    for (int b = first; b < p.num_out; b += step) {
+      const ForkRow r = fork_row(p, b);
+      if (threadIdx.x == 0) {
+        if (r.bad_len) flag_status(p.status, KVQ_DEV_BAD_SEQLEN);
+        if (r.bad_page) flag_status(p.status, KVQ_DEV_BAD_BLOCK);
+        p.out_lens[b] = r.len;
+        if (r.last < 0) p.copies[2 * b] = p.copies[2 * b + 1] = -1;
+      }
+      int32_t* out = p.out_tables + static_cast<int64_t>(b) * p.max_blocks;
+      const int full = r.len / kTok;
+      for (int i = threadIdx.x; i < p.max_blocks; i += kPoolThreads) {
+        if (i == full && r.last >= 0) continue;  // the new page
+        int page = -1;
+        if (i < full) {
+          page = __ldg(p.tables + static_cast<int64_t>(r.src) * p.max_blocks + i);
+          if (page >= 0 && page < p.num_blocks && __ldcg(p.pool + KVQ_POOL_HEADER + page) > 0) {
+            atomicAdd(p.pool + KVQ_POOL_HEADER + page, 1);
+          } else {
+            page = -1;
+            flag_status(p.status, KVQ_DEV_BAD_BLOCK);
+          }
+        }
+        out[i] = page;
+      }
+    }
+  }
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) is_last = atomicAdd(p.pool, 1) + 1 == static_cast<int>(gridDim.x);
+  __syncthreads();
+  if (!is_last) return;
+  __threadfence();
+  if (threadIdx.x == 0) {
+    p.pool[0] = 0;
+    if (enough) p.pool[1] -= static_cast<int32_t>(total);
+  }
+  for (int b = threadIdx.x; enough && b < p.num_out; b += kPoolThreads) {
+    const int page = __ldcg(p.copies + 2 * b + 1);
+    if (page >= 0) p.pool[KVQ_POOL_HEADER + page] = 1;
+  }
+}
+
+__global__ void __launch_bounds__(256) init_kernel(int32_t* pool, const int num_blocks) {
+  pdl_wait();
+  pdl_allow_next();
+  const int words = (num_blocks + 31) / 32, n = KVQ_POOL_HEADER + num_blocks + words;
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
+    int32_t v = 0;
+    if (i == 1) v = num_blocks;
+    if (i >= KVQ_POOL_HEADER + num_blocks) {
+      const int left = num_blocks - 32 * (i - KVQ_POOL_HEADER - num_blocks);
+      v = left >= 32 ? -1 : static_cast<int32_t>((1u << left) - 1u);
+    }
+    pool[i] = v;
+  }
+}
+
+static int done(cudaError_t e) {
+  if (e != cudaSuccess) return KVQ_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static int check_rows(const kvq_rows* caches, int num_caches, int64_t num_blocks, int num_kv_heads, int block_size) {
+  if (num_caches < 0 || num_blocks <= 0 || num_kv_heads <= 0) return KVQ_ERR_ARG;
+  if (num_caches > 0 && !caches) return KVQ_ERR_NULL;
+  if (block_size != kTok || num_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;
+  for (int i = 0; i < num_caches; ++i) {
+    const kvq_rows& r = caches[i];
+    if (!r.data) return KVQ_ERR_NULL;
+    if (r.row_bytes <= 0 || r.row_bytes > 512 || r.row_bytes % 4 || r.sub_bytes < 0 || r.sub_bytes > 512 || r.sub_bytes % 4)
+      return KVQ_ERR_SHAPE;
+    if (!aligned16(r.data)) return KVQ_ERR_ALIGN;
+    if (num_blocks > INT64_MAX / (static_cast<int64_t>(kTok) * 1024 * num_kv_heads)) return KVQ_ERR_SHAPE;
+  }
+  return KVQ_OK;
+}
+
+static int check_pool(const int32_t* pool, int64_t num_blocks, int max_blocks, int n) {
+  if (num_blocks <= 0 || max_blocks <= 0 || n < 0) return KVQ_ERR_ARG;
+  if (!pool) return KVQ_ERR_NULL;
+  if (num_blocks > (1 << 24) || n > kMaxTables || max_blocks > INT32_MAX / kTok) return KVQ_ERR_UNSUPPORTED;
+  return aligned4(pool) ? KVQ_OK : KVQ_ERR_ALIGN;
+}
+
+static int pool_call(void (*kernel)(PoolParams), bool rows, int32_t* pool, int64_t num_blocks, int32_t* tables,
+                     int max_blocks, const int32_t* old_lens, const int32_t* new_lens, int B, uint32_t* status,
+                     kvq_stream_t stream) {
+  const int st = check_pool(pool, num_blocks, max_blocks, B);
+  if (st != KVQ_OK) return st;
+  if (B > 0 && (!tables || !old_lens || !new_lens)) return KVQ_ERR_NULL;
+  if (!aligned4(tables) || !aligned4(old_lens) || !aligned4(new_lens)) return KVQ_ERR_ALIGN;
+  if (B == 0) return KVQ_OK;
+  PoolParams p = {pool, static_cast<int>(num_blocks), tables, max_blocks, old_lens, new_lens, B, status};
+  return done(launch_pdl(kernel, dim3(rows ? B : 1), dim3(rows ? kRowThreads : kPoolThreads), 0,
+                         reinterpret_cast<cudaStream_t>(stream), p));
+}
+
+}  // namespace pages
+}  // namespace kvq
+
+using namespace kvq;
+using namespace kvq::pages;
+
+extern "C" int kvq_tree_commit(const kvq_rows* caches, int num_caches, int64_t num_blocks,
+                               int num_kv_heads, int block_size, const int32_t* cu_q_lens,
+                               const int32_t* block_tables, int max_blocks_per_seq,
+                               const int32_t* seq_lens, int num_seqs, const int32_t* accepted,
+                               int max_path, const int32_t* num_accepted, int32_t* new_lens,
+                               uint32_t* dev_status, kvq_stream_t stream) {
+  const int st = check_rows(caches, num_caches, num_blocks, num_kv_heads, block_size);
+  if (st != KVQ_OK) return st;
+  if (num_seqs < 0 || max_path < 0 || max_blocks_per_seq <= 0) return KVQ_ERR_ARG;
+  if (num_seqs > 0 && (!cu_q_lens || !block_tables || !seq_lens || !num_accepted || !new_lens || (max_path > 0 && !accepted)))
+    return KVQ_ERR_NULL;
+  if (num_seqs > 65535 || max_path > 4096 || max_blocks_per_seq > INT32_MAX / kTok) return KVQ_ERR_UNSUPPORTED;
+  if (!aligned4(cu_q_lens) || !aligned4(block_tables) || !aligned4(seq_lens) || !aligned4(accepted) ||
+      !aligned4(num_accepted) || !aligned4(new_lens))
+    return KVQ_ERR_ALIGN;
+  if (num_seqs > 0 && new_lens == seq_lens) return KVQ_ERR_ARG;
+  if (num_seqs == 0) return KVQ_OK;
+  const int sms = device_sm_count();
+  if (sms <= 0) return KVQ_ERR_CUDA;
+  CommitParams p = {0, num_seqs, num_kv_heads, max_blocks_per_seq, max_path, 1, num_blocks, cu_q_lens, block_tables,
+                    seq_lens, accepted, num_accepted, new_lens, dev_status};
+  int at = 0;
+  do {
+    Caches cs = {};
+    p.caches = num_caches - at < kMaxRowsCaches ? num_caches - at : kMaxRowsCaches;
+    for (int i = 0; i < p.caches; ++i) cs.c[i] = caches[at + i];
+    const int64_t warps = static_cast<int64_t>(num_seqs) * (p.caches > 0 ? p.caches : 1);
+    const int64_t ctas = (warps + 3) / 4, cap = static_cast<int64_t>(sms) * 64;
+    const int r = done(launch_pdl(commit_kernel, dim3(static_cast<unsigned>(ctas < cap ? ctas : cap)), dim3(128), 0,
+                                  reinterpret_cast<cudaStream_t>(stream), p, cs));
+    if (r != KVQ_OK) return r;
+    at += p.caches;
+    p.first = 0;
+  } while (at < num_caches);
+  return KVQ_OK;
+}
+
+extern "C" int kvq_copy_pages(const kvq_rows* caches, int num_caches, int64_t num_blocks,
+                              int num_kv_heads, int block_size, const int32_t* copies,
+                              int num_copies, uint32_t* dev_status, kvq_stream_t stream) {
+  const int st = check_rows(caches, num_caches, num_blocks, num_kv_heads, block_size);
+  if (st != KVQ_OK) return st;
+  if (num_copies < 0) return KVQ_ERR_ARG;
+  if (num_copies > 0 && !copies) return KVQ_ERR_NULL;
+  if (num_copies > (1 << 20)) return KVQ_ERR_UNSUPPORTED;
+  if (!aligned4(copies)) return KVQ_ERR_ALIGN;
+  const int sms = num_copies > 0 && num_caches > 0 ? device_sm_count() : 1;
+  if (sms <= 0) return KVQ_ERR_CUDA;
+  for (int at = 0; at < num_caches && num_copies > 0; at += kMaxRowsCaches) {
+    Caches cs = {};
+    CopyParams p = {num_caches - at < kMaxRowsCaches ? num_caches - at : kMaxRowsCaches, num_kv_heads, num_copies,
+                    num_blocks, copies, dev_status};
+    for (int i = 0; i < p.caches; ++i) cs.c[i] = caches[at + i];
+    const int64_t items = static_cast<int64_t>(num_copies) * p.caches, cap = static_cast<int64_t>(sms) * 64;
+    const int r = done(launch_pdl(copy_kernel, dim3(static_cast<unsigned>(items < cap ? items : cap)), dim3(kCopyThreads), 0,
+                                  reinterpret_cast<cudaStream_t>(stream), p, cs));
+    if (r != KVQ_OK) return r;
+  }
+  return KVQ_OK;
+}
+
+extern "C" int kvq_pages_init(int32_t* pool, int64_t num_blocks, kvq_stream_t stream) {
+  const int st = check_pool(pool, num_blocks, 1, 0);
+  if (st != KVQ_OK) return st;
+  const int64_t ctas = (KVQ_POOL_WORDS(num_blocks) + 255) / 256;
+  return done(launch_pdl(init_kernel, dim3(static_cast<unsigned>(ctas < 1024 ? ctas : 1024)), dim3(256), 0,
+                         reinterpret_cast<cudaStream_t>(stream), pool, static_cast<int>(num_blocks)));
+}
+
+extern "C" int kvq_pages_alloc(int32_t* pool, int64_t num_blocks, int32_t* block_tables,
+                               int max_blocks_per_seq, const int32_t* old_lens,
+                               const int32_t* new_lens, int num_seqs, uint32_t* dev_status,
+                               kvq_stream_t stream) {
+  return pool_call(alloc_kernel, false, pool, num_blocks, block_tables, max_blocks_per_seq, old_lens, new_lens, num_seqs,
+                   dev_status, stream);
+}
+
+extern "C" int kvq_pages_free(int32_t* pool, int64_t num_blocks, int32_t* block_tables,
+                              int max_blocks_per_seq, const int32_t* old_lens,
+                              const int32_t* new_lens, int num_seqs, uint32_t* dev_status,
+                              kvq_stream_t stream) {
+  return pool_call(free_kernel, true, pool, num_blocks, block_tables, max_blocks_per_seq, old_lens, new_lens, num_seqs,
+                   dev_status, stream);
+}
+
+extern "C" int kvq_pages_fork(int32_t* pool, int64_t num_blocks, const int32_t* tables,
+                              const int32_t* lens, int num_src, int max_blocks_per_seq,
+                              const int32_t* parents, int num_out, int32_t* out_tables,
+                              int32_t* out_lens, int32_t* copies, uint32_t* dev_status,
+                              kvq_stream_t stream) {
+  int st = check_pool(pool, num_blocks, max_blocks_per_seq, num_out);
+  if (st == KVQ_OK) st = check_pool(pool, num_blocks, max_blocks_per_seq, num_src);
+  if (st != KVQ_OK) return st;
+  if ((num_src > 0 && (!tables || !lens)) || (num_out > 0 && (!parents || !out_tables || !out_lens || !copies)))
+    return KVQ_ERR_NULL;
+  if (!aligned4(tables) || !aligned4(lens) || !aligned4(parents) || !aligned4(out_tables) || !aligned4(out_lens) ||
+      !aligned4(copies))
+    return KVQ_ERR_ALIGN;
+  if (num_out > 0 && (out_tables == tables || out_lens == lens || out_lens == parents)) return KVQ_ERR_ARG;
+  if (num_out == 0) return KVQ_OK;
+  const int sms = device_sm_count();
+  if (sms <= 0) return KVQ_ERR_CUDA;
+  ForkParams p = {pool, static_cast<int>(num_blocks), tables, lens, num_src, max_blocks_per_seq, parents, num_out,
+                  out_tables, out_lens, copies, dev_status};
+  const int rows = num_out < sms - 1 ? num_out : sms - 1;  // CTAs that write rows
+  return done(launch_pdl(fork_kernel, dim3(1 + (rows > 0 ? rows : 0)), dim3(kPoolThreads), 0,
+                         reinterpret_cast<cudaStream_t>(stream), p));
+}

@@ -1,0 +1,337 @@
+// kvq_rope.cu -- norm, rotation and quantize-and-scatter in one pass.
+//
+// Per head row x of q and k, in binary32: y = x rsqrt(mean x^2 + eps) w, then
+// (y_a, y_b) turned by the angle of their pair; q leaves as bf16, k and v as
+// the cache's codes (cast_fp8(x / s), kvq_quant.cuh) in the row of the token's
+// slot.  What it saves against a norm, a rotation and a write of their own is
+// the rows' way to memory and back between them.
+//
+// A stream: (2 Hq + 2 Hkv) dh bf16 values in or out and 2 Hkv dh codes out a
+// token.  DH / 16 lanes share a row, 16 dims a lane in two runs of 8: the two
+// halves of its pairs, so that a pair's dims meet in one lane.  A warp takes a
+// token (or a share of its rows, where the tokens are few), so the lane's 8
+// angles are formed once for all of the token's rows: their turns are a 64-bit
+// integer product modulo 2^64, exact at any position, of which the upper 32
+// bits go to sincospif.  The next rows are loaded before the present ones are
+// worked on.
+#include "../../include/kvq_step.h"
+#include "kvq_host.h"
+#include "kvq_quant.cuh"
+
+namespace kvq {
+namespace rope {
+
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+constexpr int kThreads = 256;
+constexpr int kCtasPerSM = 3;
+
+struct RopeParams {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t q_stride, k_stride, v_stride, out_stride;
+  int64_t tokens;
+  int hq, hkv;
+  const int32_t* pos;
+  int axes;
+  const unsigned long long* turns;
+  const uint8_t* axis;
+  int pairs;  // a multiple of 8
+  int interleaved;
+  const uint16_t* wq;
+  const uint16_t* wk;
+  float eps;
+  const int64_t* slots;
+  void* kc;
+  void* vc;
+  int64_t capacity;  // num_blocks * 16
+  float* ks;         // scales, or (TS) scale caches
+  float* vs;
+  int per_head;
+  uint16_t* out;
+  uint32_t* status;
+  int split;  // warps that share a token's rows
+};
+
+KVQ_DEVI void unpack8(const uint4& a, float (&x)[8]) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf16lo_to_f32(w[i]);
+    x[2 * i + 1] = bf16hi_to_f32(w[i]);
+  }
+}
+
+KVQ_DEVI uint4 pack8(const float (&x)[8]) {
+  return make_uint4(f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3]), f32x2_to_bf16x2(x[4], x[5]),
+                    f32x2_to_bf16x2(x[6], x[7]));
+}
+
+// Eight binary32 values -> eight codes of cast_fp8(x / s).  The quotient is the IEEE one: as in
+// quantize2, but x has 24 significant bits where a bf16 has 8, so q0 = RN(x r) may be off by two
+// units; one correction takes it within one, and from there Markstein's second is exact.
+template <int FMT>
+KVQ_DEVI uint2 quantize8(const float (&x)[8], const HeadScale& h) {
+  uint32_t o[4];
+  const float L = __uint_as_float(h.L2 & 0xFFFF0000u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 q;
+    if (h.fast) {
+      float2 c;
+      asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(c.x) : "f"(x[2 * i]), "f"(L));
+      asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(c.y) : "f"(x[2 * i + 1]), "f"(L));
+      q = __fmul2_rn(c, h.r2);
+      q = __ffma2_rn(__ffma2_rn(q, h.ns2, c), h.r2, q);
+      q = __ffma2_rn(__ffma2_rn(q, h.ns2, c), h.r2, q);
+    } else {
+      q = make_float2(__fdiv_rn(x[2 * i], h.s), __fdiv_rn(x[2 * i + 1], h.s));
+    }
+    const uint32_t signs = ((__float_as_uint(x[2 * i]) >> 24) & 0x80u) | ((__float_as_uint(x[2 * i + 1]) >> 16) & 0x8000u);
+    o[i] = f32x2_to_fp8x2<FMT>(q.x, q.y) | signs;
+  }
+  return make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+}
+
+template <int FMT, int DH, bool TS>
+__global__ void __launch_bounds__(kThreads, kCtasPerSM) rope_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int CH = DH / 16;      // lanes of a row
+  constexpr int RW = 32 / CH;      // rows of a warp
+  constexpr bool BF = FMT == KVQ_FMT_BF16;
+  pdl_wait();
+  pdl_allow_next();
+  const int lane = threadIdx.x & 31, g = lane / CH, l = lane % CH;
+  const uint32_t row_mask = (CH == 8 ? 0xFFu : 0xFu) << (lane & ~(CH - 1));
+  const int pc = p.pairs >> 3;
+  const bool turned = l < pc;
+  // the lane's runs of 8 dims: both halves of its pairs, or (interleaved, or past the pairs) neighbours
+  const bool apart = !p.interleaved && turned;
+  const int d0 = 8 * (apart ? l : 2 * l), d1 = 8 * (apart ? l + pc : 2 * l + 1);
+  const int rows = p.hq + 2 * p.hkv, steps = (rows + RW - 1) / RW;
+  unsigned long long turns[8];
+  uint32_t axes = 0;  // four bits each
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    turns[i] = turned ? __ldg(p.turns + 8 * l + i) : 0ull;
+    const uint32_t a = turned && p.axis ? __ldg(p.axis + 8 * l + i) : 0u;
+    axes |= (a < static_cast<uint32_t>(p.axes) ? a : 0u) << (4 * i);
+  }
+  const int64_t items = p.tokens * p.split;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); it < items; it += warps) {
+    const int64_t t = it / p.split;
+    const int first = static_cast<int>(it - t * p.split);
+    auto load = [&](int row, uint4& a, uint4& b) {
+      if (row >= rows) return;
+      const uint16_t* src = row < p.hq            ? p.q + t * p.q_stride + row * DH
+                            : row < p.hq + p.hkv ? p.k + t * p.k_stride + (row - p.hq) * DH
+                                                  : p.v + t * p.v_stride + (row - p.hq - p.hkv) * DH;
+      a = __ldcs(reinterpret_cast<const uint4*>(src + d0));
+      b = __ldcs(reinterpret_cast<const uint4*>(src + d1));
+    };
+    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+    load(first * RW + g, a, b);
+    const int64_t slot = __ldg(p.slots + t);
+    float cs[8], sn[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t at = __ldg(p.pos + static_cast<int64_t>((axes >> (4 * i)) & 15u) * p.tokens + t);
+      const unsigned long long turn = static_cast<unsigned long long>(at) * turns[i];
+      // the upper 32 bits as [-2^31, 2^31) of 2^32 to a turn; sincospif takes half turns
+      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sn[i], &cs[i]);
+    }
+    if (slot >= p.capacity && first == 0 && lane == 0) flag_status(p.status, KVQ_DEV_BAD_SLOT);
+    const bool kept = slot >= 0 && slot < p.capacity;
+    for (int s = first; s < steps; s += p.split) {
+      uint4 an = make_uint4(0u, 0u, 0u, 0u), bn = an;
+      if (s + p.split < steps) load((s + p.split) * RW + g, an, bn);
+      const int row = s * RW + g;
+      const bool is_q = row < p.hq, is_v = row >= p.hq + p.hkv;
+      float x[8], y[8];
+      unpack8(a, x);
+      unpack8(b, y);
+      const uint16_t* w = is_q ? p.wq : p.wk;
+      if (p.wq || p.wk) {
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), make_float2(x[2 * i], x[2 * i + 1]), sum);
+          sum = __ffma2_rn(make_float2(y[2 * i], y[2 * i + 1]), make_float2(y[2 * i], y[2 * i + 1]), sum);
+        }
+        float sq = sum.x + sum.y;
+#pragma unroll
+        for (int off = 1; off < CH; off <<= 1) sq += __shfl_xor_sync(kAll, sq, off);
+        if (!is_v && w) {
+          const float f = rsqrtf(sq * (1.f / DH) + p.eps);
+          float u[8], v[8];
+          unpack8(__ldg(reinterpret_cast<const uint4*>(w + d0)), u);
+          unpack8(__ldg(reinterpret_cast<const uint4*>(w + d1)), v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x[i] *= f * u[i];
+            y[i] *= f * v[i];
+          }
+        }
+      }
+      if (!is_v && turned) {
+        if (p.interleaved) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x0 = x[2 * i], x1 = x[2 * i + 1], y0 = y[2 * i], y1 = y[2 * i + 1];
+            x[2 * i] = x0 * cs[i] - x1 * sn[i];
+            x[2 * i + 1] = x0 * sn[i] + x1 * cs[i];
+            y[2 * i] = y0 * cs[4 + i] - y1 * sn[4 + i];
+            y[2 * i + 1] = y0 * sn[4 + i] + y1 * cs[4 + i];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float x0 = x[i], y0 = y[i];
+            x[i] = x0 * cs[i] - y0 * sn[i];
+            y[i] = x0 * sn[i] + y0 * cs[i];
+          }
+        }
+      }
+      float amax = 0.f;
+      if (TS) {  // every lane of the row takes part, whatever its slot
+        uint32_t m = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t u = __float_as_uint(x[i]) & 0x7FFFFFFFu, v = __float_as_uint(y[i]) & 0x7FFFFFFFu;
+          m = max(m, max(u < 0x7F800000u ? u : 0u, v < 0x7F800000u ? v : 0u));
+        }
+#pragma unroll
+        for (int off = 1; off < CH; off <<= 1) m = max(m, __shfl_xor_sync(row_mask, m, off));
+        amax = __uint_as_float(m);
+      }
+      if (is_q) {
+        uint16_t* dst = p.out + t * p.out_stride + static_cast<int64_t>(row) * DH;
+        *reinterpret_cast<uint4*>(dst + d0) = pack8(x);
+        *reinterpret_cast<uint4*>(dst + d1) = pack8(y);
+      } else if (row < rows && kept) {
+        const int h = row - p.hq - (is_v ? p.hkv : 0);
+        const int64_t at = ((slot >> 4) * p.hkv + h) * 16 + (slot & 15);
+        void* cache = is_v ? p.vc : p.kc;
+        if constexpr (BF) {
+          uint16_t* dst = static_cast<uint16_t*>(cache) + at * DH;
+          *reinterpret_cast<uint4*>(dst + d0) = is_v ? a : pack8(x);
+          *reinterpret_cast<uint4*>(dst + d1) = is_v ? b : pack8(y);
+        } else {
+          float* scale = is_v ? p.vs : p.ks;
+          const HeadScale hs = head_scale(TS ? scale_of_amax<FMT>(amax) : __ldg(scale + (p.per_head ? h : 0)));
+          uint8_t* dst = static_cast<uint8_t*>(cache) + at * DH;
+          *reinterpret_cast<uint2*>(dst + d0) = quantize8<FMT>(x, hs);
+          *reinterpret_cast<uint2*>(dst + d1) = quantize8<FMT>(y, hs);
+          if (TS && l == 0) scale[at] = hs.s;
+        }
+      }
+      a = an;
+      b = bn;
+    }
+  }
+}
+
+template <int FMT, int DH, bool TS>
+static cudaError_t launch_rope(RopeParams& p, cudaStream_t s) {
+  const int rw = 32 / (DH / 16), steps = (p.hq + 2 * p.hkv + rw - 1) / rw;
+  const int64_t warps = static_cast<int64_t>(device_sm_count()) * kCtasPerSM * (kThreads / 32);
+  // Few tokens are spread over several warps each, as far as those are idle.
+  int64_t split = warps / p.tokens;
+  split = split < 1 ? 1 : (split > steps ? steps : split);
+  p.split = static_cast<int>(split);
+  const int64_t need = (p.tokens * split + kThreads / 32 - 1) / (kThreads / 32);
+  const int64_t cap = static_cast<int64_t>(device_sm_count()) * kCtasPerSM;
+  const dim3 grid(static_cast<unsigned>(need < cap ? need : cap));
+  return launch_pdl(rope_kernel<FMT, DH, TS>, grid, dim3(kThreads), 0, s, p);
+}
+
+template <int FMT, bool TS>
+static cudaError_t launch_rope_dh(RopeParams& p, int dh, cudaStream_t s) {
+  return dh == 128 ? launch_rope<FMT, 128, TS>(p, s) : launch_rope<FMT, 64, TS>(p, s);
+}
+
+}  // namespace rope
+}  // namespace kvq
+
+using namespace kvq;
+
+extern "C" int kvq_rope_write(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                              const void* v, int64_t v_stride, int64_t num_tokens, int num_q_heads,
+                              int num_kv_heads, int head_dim, const int32_t* positions, int num_axes,
+                              const int64_t* turns, const uint8_t* axis, int num_pairs,
+                              int interleaved, const void* q_weight, const void* k_weight, float eps,
+                              const int64_t* slot_mapping, void* k_cache, void* v_cache,
+                              int64_t num_blocks, int block_size, float* k_scale, int k_scale_len,
+                              float* v_scale, int v_scale_len, int scale_granularity, int fmt,
+                              void* q_out, int64_t q_out_stride, uint32_t* dev_status,
+                              kvq_stream_t stream) {
+  if (fmt < KVQ_FMT_BF16 || fmt > KVQ_FMT_E5M2) return KVQ_ERR_ARG;
+  if (scale_granularity < KVQ_SCALE_PER_TENSOR || scale_granularity > KVQ_SCALE_PER_TOKEN_HEAD) return KVQ_ERR_ARG;
+  const bool ts = scale_granularity == KVQ_SCALE_PER_TOKEN_HEAD;
+  if (ts && fmt == KVQ_FMT_BF16) return KVQ_ERR_UNSUPPORTED;
+  if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_blocks <= 0 || num_axes <= 0 || num_pairs < 0 ||
+      !(eps >= 0.f))
+    return KVQ_ERR_ARG;
+  if (!k_cache || !v_cache || (num_pairs > 0 && !turns)) return KVQ_ERR_NULL;
+  if (num_tokens > 0 && (!q || !k || !v || !q_out || !slot_mapping || !positions)) return KVQ_ERR_NULL;
+  if (head_dim != 64 && head_dim != 128) return KVQ_ERR_UNSUPPORTED;
+  if (block_size != 16 || num_axes > 16) return KVQ_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_q_heads) + num_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;
+  if (num_pairs % 8 || num_pairs > head_dim / 2) return KVQ_ERR_SHAPE;
+  const int64_t nq = static_cast<int64_t>(num_q_heads) * head_dim, nk = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (q_stride < nq || q_out_stride < nq || k_stride < nk || v_stride < nk) return KVQ_ERR_SHAPE;
+  if (q == q_out && q_stride != q_out_stride) return KVQ_ERR_SHAPE;
+  if ((q_stride | q_out_stride | k_stride | v_stride) % 8) return KVQ_ERR_ALIGN;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned16(q_weight) || !aligned16(k_weight) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) ||
+      (reinterpret_cast<uintptr_t>(turns) & 7u) || (reinterpret_cast<uintptr_t>(positions) & 3u) ||
+      ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & (ts ? 15u : 3u)))
+    return KVQ_ERR_ALIGN;
+  if (num_blocks > (INT64_MAX / 16) / nk) return KVQ_ERR_SHAPE;
+  if (fmt != KVQ_FMT_BF16) {
+    if (!k_scale || !v_scale) return KVQ_ERR_NULL;
+    const int64_t want = ts ? num_blocks * num_kv_heads * 16 : scale_granularity == KVQ_SCALE_PER_HEAD ? num_kv_heads : 1;
+    if (k_scale_len != want || v_scale_len != want) return KVQ_ERR_SHAPE;
+  }
+  if (num_tokens == 0) return KVQ_OK;
+  if (device_sm_count() <= 0) return KVQ_ERR_CUDA;
+  rope::RopeParams p = {};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.out_stride = q_out_stride;
+  p.tokens = num_tokens;
+  p.hq = num_q_heads;
+  p.hkv = num_kv_heads;
+  p.pos = positions;
+  p.axes = num_axes;
+  p.turns = reinterpret_cast<const unsigned long long*>(turns);
+  p.axis = axis;
+  p.pairs = num_pairs;
+  p.interleaved = interleaved != 0;
+  p.wq = static_cast<const uint16_t*>(q_weight);
+  p.wk = static_cast<const uint16_t*>(k_weight);
+  p.eps = eps;
+  p.slots = slot_mapping;
+  p.kc = k_cache;
+  p.vc = v_cache;
+  p.capacity = num_blocks * block_size;
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.per_head = scale_granularity == KVQ_SCALE_PER_HEAD;
+  p.out = static_cast<uint16_t*>(q_out);
+  p.status = dev_status;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (fmt == KVQ_FMT_BF16)
+    e = rope::launch_rope_dh<KVQ_FMT_BF16, false>(p, head_dim, s);
+  else if (fmt == KVQ_FMT_E4M3)
+    e = ts ? rope::launch_rope_dh<KVQ_FMT_E4M3, true>(p, head_dim, s) : rope::launch_rope_dh<KVQ_FMT_E4M3, false>(p, head_dim, s);
+  else
+    e = ts ? rope::launch_rope_dh<KVQ_FMT_E5M2, true>(p, head_dim, s) : rope::launch_rope_dh<KVQ_FMT_E5M2, false>(p, head_dim, s);
+  if (e != cudaSuccess) return KVQ_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
