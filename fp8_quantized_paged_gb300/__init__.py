@@ -366,9 +366,10 @@ def new_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, device="cuda"):
 
 _FP4 = ("kvq_fp4_write", "kvq_fp4_read", "kvq_fp4_workspace_size", "kvq_fp4_decode_attn",
         "kvq_fp4_prefill_attn", "new_fp4_cache", "new_fp4_workspace")
-_STEP = ("kvq_rope_write", "kvq_tree_commit", "kvq_copy_pages", "kvq_pages_init", "kvq_pages_alloc",
-         "kvq_pages_free", "kvq_pages_fork", "new_page_pool", "rope_turns", "KVQ_DEV_NO_PAGES",
-         "KVQ_DEV_BAD_TREE")
+_STEP = ("kvq_rope_write", "kvq_tree_attn", "kvq_tree_workspace_size", "kvq_tree_commit",
+         "kvq_copy_pages", "kvq_pages_init", "kvq_pages_alloc", "kvq_pages_free", "kvq_pages_fork",
+         "new_tree_workspace", "new_page_pool", "rope_turns", "KVQ_DEV_NO_PAGES",
+         "KVQ_DEV_BAD_TREE", "KVQ_TREE_MAX_NODES")
 
 
 def __getattr__(name):

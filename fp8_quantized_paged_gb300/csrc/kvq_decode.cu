@@ -78,8 +78,8 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // decode kernels' fragment reads are free of bank conflicts and the tensor
 // cores read the 128-byte rows directly; a 256-byte bf16 row takes two
 // boxes (x = 0 and x = 64).
-static bool make_cache_map(CUtensorMap* m, const void* base, int fmt, int dh, uint64_t rows,
-                           int box_rows = kBS) {
+bool make_cache_map(CUtensorMap* m, const void* base, int fmt, int dh, uint64_t rows,
+                    int box_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (!enc) return false;
   const int elem = fmt == KVQ_FMT_BF16 ? 2 : 1;

@@ -193,6 +193,9 @@ inline WsLayout ws_layout(int B, int G, int Hkv, int DH, int P) {
   return w;
 }
 
+// Tensor map of one cache tensor, its pages' rows (kvq_decode.cu); false where it cannot be made.
+bool make_cache_map(CUtensorMap* m, const void* base, int fmt, int dh, uint64_t rows, int box_rows = kBS);
+
 KVQ_DEVI uint32_t swz(uint32_t logical, uint32_t mask) {
   return logical ^ (((logical >> 7) & mask) << 4);
 }

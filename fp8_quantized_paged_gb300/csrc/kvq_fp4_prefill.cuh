@@ -214,44 +214,14 @@ KVQ_DEVI void tmem_ld64(uint32_t taddr, float (&v)[64]) {
       : "memory");
 }
 
-// Two binary32 values in a register pair: one instruction for both.
-using f32x2 = unsigned long long;
-KVQ_DEVI f32x2 f32x2_pack(float a, float b) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-KVQ_DEVI void f32x2_unpack(f32x2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-KVQ_DEVI f32x2 f32x2_fma(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-KVQ_DEVI f32x2 f32x2_add(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-KVQ_DEVI float fmax3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-// 8 consecutive columns of this thread's lane (no wait).
-KVQ_DEVI void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-               ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-
-// True in one lane of the (whole) warp.  Matrix instructions that the compiler sees issued
-// under elect.sync cost 12 cycles each to issue, under lane == 0 they cost 52.
-KVQ_DEVI bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
+using tc::elect_one;
+using tc::f32x2;
+using tc::f32x2_add;
+using tc::f32x2_fma;
+using tc::f32x2_pack;
+using tc::f32x2_unpack;
+using tc::fmax3;
+using tc::tmem_st8;
 
 // The pages that a CTA's rows see, as a list: the first tokens' pages [0, sink),
 // then [first, last].

@@ -13,6 +13,7 @@ namespace {
 using namespace binding;
 
 decltype(&kvq_rope_write) p_rope = nullptr;
+decltype(&kvq_tree_attn) p_tree = nullptr;
 decltype(&kvq_tree_commit) p_commit = nullptr;
 decltype(&kvq_copy_pages) p_copy = nullptr;
 decltype(&kvq_pages_init) p_init = nullptr;
@@ -133,6 +134,47 @@ PyObject* rope_write(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObjec
     Py_BEGIN_ALLOW_THREADS
     r = p_rope(qp, sq, kp, sk, vp, sv, n, h, g, d, pp, axes, turns, axis, np, inter, w[0], w[1], static_cast<float>(eps), slots,
                c.k, c.v, c.blocks, kBlockSize, ks, nk, vs, nv, gran, fmt, op, so, st, stream);
+    Py_END_ALLOW_THREADS
+    return result(where, r);
+  });
+}
+
+PyObject* tree_attn(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kw) {
+  static const char* const names[] = {"q", "cu_q_lens", "parents", "k_cache", "v_cache", "block_tables", "seq_lens", "k_scale",
+                                      "v_scale", "scale_granularity", "fmt", "sliding_window", "workspace", "out", "dev_status",
+                                      "stream", "q_scale", "flags"};
+  const char* where = "kvq_tree_attn";
+  return guarded([&]() -> PyObject* {
+    bound(where);
+    auto a = take(where, names, 14, args, nargs, kw);
+    Tensors ts(where);
+    const at::Tensor& q = ts.tensor("q", a[0]);
+    void* qp = ts.dense("q", q, at::kBFloat16);
+    if (q.dim() != 3) fail(where, "q must have shape [num_q_tokens][Hq][head_dim]", KVQ_ERR_SHAPE);
+    const int64_t n = q.size(0);
+    const int fmt = int32(where, "fmt", a[10]);
+    const Paged c = paged(where, ts, a[3], a[4], fmt);
+    if (c.dh != q.size(2)) fail(where, "the caches and q must have the same head_dim", KVQ_ERR_SHAPE);
+    const Table bt = table(where, ts, "block_tables", a[5], -1);
+    const int64_t B1 = bt.rows + 1;
+    int32_t *lens = ints(ts, "seq_lens", a[6], at::IntArrayRef(&bt.rows, 1)), *cu = ints(ts, "cu_q_lens", a[1], at::IntArrayRef(&B1, 1));
+    int32_t* parents = given(a[2]) ? ints(ts, "parents", a[2], at::IntArrayRef(&n, 1)) : nullptr;
+    int nq, nk, nv;
+    float *ks = scale(where, ts, "k_scale", a[7], nk), *vs = scale(where, ts, "v_scale", a[8], nv);
+    float* qs = scale(where, ts, "q_scale", a[16], nq);
+    const int gran = int32(where, "scale_granularity", a[9]), window = int32(where, "sliding_window", a[11]);
+    int64_t ws_bytes;
+    void* ws = ts.dense("workspace", a[12], at::kByte, &ws_bytes);
+    void* out = ts.dense("out", a[13], at::kBFloat16, q.sizes());
+    uint32_t* st = ts.status(a[14]);
+    const int flags = a[17] ? int32(where, "flags", a[17]) : 0;
+    const int hq = narrow(where, "query heads", q.size(1)), h = narrow(where, "KV heads", c.heads), d = narrow(where, "head dims", c.dh);
+    const int B = narrow(where, "sequences", bt.rows), mb = narrow(where, "blocks per sequence", bt.columns);
+    kvq_stream_t stream = ts.stream(a[15]);
+    int r;
+    Py_BEGIN_ALLOW_THREADS
+    r = p_tree(qp, cu, n, parents, c.k, c.v, bt.p, mb, lens, B, hq, h, d, c.blocks, kBlockSize, qs, nq, ks, nk, vs, nv, gran, fmt,
+               window, static_cast<unsigned>(flags), ws, static_cast<size_t>(ws_bytes), out, st, stream);
     Py_END_ALLOW_THREADS
     return result(where, r);
   });
@@ -326,6 +368,7 @@ bool step_bind(void* handle, const char* path) {
     f = reinterpret_cast<std::remove_reference_t<decltype(f)>>(dlsym(handle, name));
     all = all && f;
   };
+  sym(p_tree, "kvq_tree_attn");
   sym(p_commit, "kvq_tree_commit");
   sym(p_copy, "kvq_copy_pages");
   sym(p_init, "kvq_pages_init");
@@ -347,6 +390,11 @@ PyMethodDef step_methods[] = {
      "k_scale, v_scale, scale_granularity, fmt, q_out, dev_status=None, stream=None)\n\nNorm (with a weight of [head_dim], None: "
      "none) and rotate q and k bf16 [N][heads][dh], write q to q_out and quantize k and v into their slots.  positions int32 [N] "
      "or [axes][N]; turns int64 [pairs] (rope_turns); axis uint8 [pairs] or None.  q_out may be q."},
+    {"kvq_tree_attn", KVQ_FAST(tree_attn), METH_FASTCALL | METH_KEYWORDS,
+     "kvq_tree_attn(q, cu_q_lens, parents, k_cache, v_cache, block_tables, seq_lens, k_scale, v_scale, scale_granularity, fmt, "
+     "sliding_window, workspace, out, dev_status=None, stream=None, q_scale=None, flags=0)\n\nAttention of trees of drafted tokens, "
+     "each sequence's last ones: q bf16 [total_q][Hq][dh], cu_q_lens int32 [B + 1], parents int32 [total_q] (a node of the same "
+     "tree before it, -1: none; None: drafts in a row).  A node sees the tokens before the tree, its ancestors and itself."},
     {"kvq_tree_commit", KVQ_FAST(tree_commit), METH_FASTCALL | METH_KEYWORDS,
      "kvq_tree_commit(caches, cu_q_lens, block_tables, seq_lens, accepted, num_accepted, new_lens, dev_status=None, stream=None)"
      "\n\nMove the rows of each sequence's accepted path (int32 [B][max_path] nodes, the first num_accepted[b] of them) together "

@@ -12,13 +12,15 @@ import math
 
 import torch
 
-from . import KVQ_ERR_ARG, KvqError
+from . import KVQ_ERR_ARG, KvqError, _i32, _sz, lib
 from .fp4 import _native
 
 KVQ_DEV_NO_PAGES, KVQ_DEV_BAD_TREE = 64, 128
+KVQ_TREE_MAX_NODES = 256
 KVQ_POOL_HEADER = 4
 
 kvq_rope_write = _native.kvq_rope_write
+kvq_tree_attn = _native.kvq_tree_attn
 kvq_tree_commit = _native.kvq_tree_commit
 kvq_copy_pages = _native.kvq_copy_pages
 kvq_pages_init = _native.kvq_pages_init
@@ -26,10 +28,25 @@ kvq_pages_alloc = _native.kvq_pages_alloc
 kvq_pages_free = _native.kvq_pages_free
 kvq_pages_fork = _native.kvq_pages_fork
 
+_size = lib().kvq_tree_workspace_size
+_size.restype, _size.argtypes = _sz, [_i32] * 4
+
+
+def kvq_tree_workspace_size(num_q_heads, num_kv_heads, head_dim, num_sms=0) -> int:
+    return int(_size(num_q_heads, num_kv_heads, head_dim, num_sms))
+
 
 # --------------------------------------------------------------------------
 # allocation helpers (torch memory; no compute)
 # --------------------------------------------------------------------------
+
+def new_tree_workspace(num_q_heads, num_kv_heads, head_dim, device="cuda"):
+    """A workspace of kvq_tree_attn; what it holds means nothing."""
+    n = kvq_tree_workspace_size(num_q_heads, num_kv_heads, head_dim)
+    if n == 0:
+        raise KvqError(KVQ_ERR_ARG, "kvq_tree_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
 
 def new_page_pool(num_blocks, device="cuda"):
     """A pool of num_blocks pages, all free: int32 words, of which [1] counts the free pages

@@ -90,6 +90,79 @@ KVQ_API int kvq_rope_write(const void* q, int64_t q_stride, const void* k, int64
                            void* q_out, int64_t q_out_stride, uint32_t* dev_status,
                            kvq_stream_t stream);
 
+/* Most nodes of one sequence's tree. */
+#define KVQ_TREE_MAX_NODES 256
+
+/*
+ * kvq_tree_workspace_size -- bytes of device workspace that kvq_tree_attn
+ * needs for any batch of these heads; its contents before a call and after it
+ * mean nothing.  num_sms <= 0 queries the current device.  Returns 0 for
+ * invalid sizes.
+ */
+KVQ_API size_t kvq_tree_workspace_size(int num_q_heads, int num_kv_heads, int head_dim, int num_sms);
+
+/*
+ * kvq_tree_attn -- attention of trees of drafted tokens over the paged cache,
+ * dequantization fused.
+ *
+ * Sequence b holds L_b = seq_lens[b] tokens in the cache, of which the last
+ * n_b = cu_q_lens[b+1] - cu_q_lens[b] are the nodes of its tree (written
+ * there before the call); P_b = L_b - n_b tokens precede the tree.  Query row
+ * cu_q_lens[b] + j is node j.  Its parent is node parents[cu_q_lens[b] + j] <
+ * j, or -1 where it follows the tokens before the tree directly; its depth is
+ * the number of its ancestors and its position P_b + depth.  It attends to
+ * the tokens t < P_b with t > position - sliding_window (all of them where
+ * sliding_window is 0), and to itself and its ancestors (with a window the
+ * nearest sliding_window of these):
+ *   O = softmax(q K^T / sqrt(head_dim)) V^
+ * A row that sees nothing whose page is good is zero.
+ *
+ *   q               bf16 [num_q_tokens][num_q_heads][head_dim]
+ *   cu_q_lens       int32 [num_seqs + 1], device: 0 = cu_q_lens[0] <= ... <=
+ *                   cu_q_lens[num_seqs] <= num_q_tokens; rows of out from
+ *                   cu_q_lens[num_seqs] on are left as they were
+ *   parents         int32 [num_q_tokens], or NULL: every node's parent is the
+ *                   node before it (drafts in a row, causal)
+ *   caches, block_tables, seq_lens, scales, scale_granularity, fmt, q_scale
+ *                   as for kvq_prefill_attn, every granularity included
+ *   flags           0 or KVQ_Q_FP8, as for kvq_prefill_attn
+ *   workspace       device scratch of kvq_tree_workspace_size bytes, 256-byte
+ *                   aligned; calls that may run at the same time (two graphs
+ *                   among them) need one each
+ *   out             bf16 [num_q_tokens][num_q_heads][head_dim]
+ *   dev_status      optional; KVQ_DEV_BAD_BLOCK (the page is masked out),
+ *                   KVQ_DEV_BAD_SEQLEN (L_b < n_b or L_b > max_blocks_per_seq
+ *                   * block_size: zero rows), KVQ_DEV_BAD_QLEN (n_b past
+ *                   KVQ_TREE_MAX_NODES, or cu_q_lens that are negative,
+ *                   decrease or pass num_q_tokens: the rows are left as they
+ *                   were), KVQ_DEV_BAD_TREE (a parent that is not before its
+ *                   node, or below -1, counts as -1), KVQ_DEV_WAIT_TIMEOUT
+ * Statistics and sums are binary32, the output is rounded once.  Over FP8
+ * caches the query row is scaled by a power of two that takes its largest
+ * value to [2^7, 2^8) and enters the products as two E4M3 parts: exact for
+ * values within 2^8 of the row's largest, off by 2^-18 of that at most
+ * below; finite queries of any magnitude are fine.  A weight enters the
+ * product with V^ as three E5M2 parts: within 2^-9 of its value or 2^-24 of
+ * the row's largest.  Over a bf16 cache the query is taken as it is and a
+ * weight as two bf16 parts, within 2^-17.  With KVQ_SCALE_PER_TOKEN_HEAD the
+ * weight carries its value's scale relative to the largest so far.
+ * Limits: num_seqs <= 4096; num_kv_heads <= 256; num_q_heads / num_kv_heads
+ * <= 8; num_blocks * num_kv_heads * block_size < 2^31; max_blocks_per_seq *
+ * block_size < 2^30; num_seqs * num_kv_heads * T * (max_blocks_per_seq / 4 +
+ * 4) < 2^31 with T = 1 where num_q_tokens * num_q_heads / num_kv_heads <=
+ * 128, else 16; beyond them KVQ_ERR_UNSUPPORTED.  num_q_tokens == 0 is a no-op.
+ */
+KVQ_API int kvq_tree_attn(const void* q, const int32_t* cu_q_lens, int64_t num_q_tokens,
+                          const int32_t* parents, const void* k_cache, const void* v_cache,
+                          const int32_t* block_tables, int max_blocks_per_seq,
+                          const int32_t* seq_lens, int num_seqs, int num_q_heads,
+                          int num_kv_heads, int head_dim, int64_t num_blocks, int block_size,
+                          const float* q_scale, int q_scale_len, const float* k_scale,
+                          int k_scale_len, const float* v_scale, int v_scale_len,
+                          int scale_granularity, int fmt, int sliding_window, unsigned flags,
+                          void* workspace, size_t workspace_bytes, void* out,
+                          uint32_t* dev_status, kvq_stream_t stream);
+
 /*
  * One cache tensor of one layer, for the calls that move rows or pages.  A
  * page of one KV head is 16 rows of row_bytes, then 16 rows of sub_bytes:
