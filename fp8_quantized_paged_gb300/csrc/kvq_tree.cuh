@@ -115,7 +115,7 @@ struct TreeSmem {
   static constexpr int S = C::kSlots;
   static constexpr int q = 0;
   static constexpr int ring = q + C::kQParts * C::kQTile;
-  static constexpr int tsc = ring + kRing;  // per-(token, head) scales of a slot
+  static constexpr int tsc = ring + kRing;  // per-(token, head) scales, K's and V's, that land with a V
   static constexpr int bars = tsc + (TS ? S * C::kKeys * 4 : 0);
   static constexpr int kBars = 2 * S + 9;
   static constexpr int misc = bars + kBars * 8;  // tmem address, abort, NaN mark, -, bad[S], issued[S], warp sums
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
   // Position 2 g of the stream is the K of the CTA's block g, 2 g + 1 its V; slot: position % S.
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::bars);  // [S] a slot landed
   uint64_t* empty = full + S;     // [S] read by the matrix steps (commit)
-  uint64_t* sfull = empty + S;    // S of a block written (commit)
+  uint64_t* sfull = empty + S;    // S of a block written (commit, and the issuer's arrival)
   uint64_t* pfull = sfull + 1;    // P of a block written, O rescaled (8 warps)
   uint64_t* pdone = pfull + 1;    // O += P V of a block done (commit, and the issuer's arrival)
   uint64_t* qready = pdone + 1;   // Q of a piece written (8 warps)
@@ -290,7 +290,8 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
   // A parity wait for phase k of a barrier is sound while it has completed k or k + 1 phases.  The
   // issuer, the producer and the softmax take their barriers' phases in order, one a block (a piece:
   // qready).  The softmax also looks at a V slot's full barrier, for some blocks only: all earlier
-  // phases of it are complete then, as the S of block g comes after the PV of block g - 1.
+  // phases of it are complete then, as the S of block g comes after the PV of block g - 1, and the
+  // next one waits for this softmax.  (Not at a K slot's: the next K may land while a warp is late.)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
@@ -299,7 +300,7 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
       mbar_init(&empty[i], 1);
       issued[i] = -1;
     }
-    mbar_init(sfull, 1);
+    mbar_init(sfull, 2);
     mbar_init(pfull, kSoftWarps);
     mbar_init(pdone, 2);
     mbar_init(qready, kSoftWarps);
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
             if (goods == 0)
               mbar_arrive(&full[s]);  // nothing to copy
             else
-              mbar_arrive_expect_tx(&full[s], __popc(goods) * (C::kPageBytes + (TS ? kBS * 4 : 0)));
+              mbar_arrive_expect_tx(&full[s], __popc(goods) * (C::kPageBytes + (TS && t == 1 ? 2 * kBS * 4 : 0)));
           }
           __syncwarp();
           if (good) {
@@ -438,8 +439,11 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
             const CUtensorMap* map = t ? &tmv : &tmk;
             tma_load_2d(dst, map, 0, row, &full[s]);
             if (C::kRow > 128) tma_load_2d(dst + KEYS * 128, map, 64, row, &full[s]);
-            if (TS)
-              bulk_load(smem + SM::tsc + (s * KEYS + lane * kBS) * 4, (t ? p.vs : p.ks) + row, kBS * 4, &full[s]);
+            if (TS && t == 1) {  // (K's own slot goes on to the next K before the softmax is done)
+              uint8_t* sc = smem + SM::tsc + (g % (S / 2) * 2 * KEYS + lane * kBS) * 4;
+              bulk_load(sc, p.ks + row, kBS * 4, &full[s]);
+              bulk_load(sc + KEYS * 4, p.vs + row, kBS * 4, &full[s]);
+            }
           }
         }
       }
@@ -478,6 +482,7 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
               if (parts > 1) tc::mma_f8_ss(tm, desc(a + C::kQTile + oa), desc(bk + ob), id_qk, 1u);
             }
           }
+          mbar_arrive(sfull);  // hands on what the K slot's arrival showed (bad)
           tc::mma_commit(sfull);
           tc::mma_commit(&empty[ks]);
           if (!(ok = wait(&full[vs], (2 * g + 1) / S) && wait(pfull, g))) break;
@@ -640,8 +645,8 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
       const float rise = kRescaleThreshold / lscale;
       for (int i = pc.i0; i < pc.i1; ++i, ++g) {
         const int k0 = pc.s.first + i * KEYS;
-        const int vslot = (2 * g + 1) % S, kslot = 2 * g % S;
-        if (!(ok = wait_w(&full[kslot], 2 * g / S))) break;
+        const int vslot = (2 * g + 1) % S;
+        if (!(ok = wait_w(sfull, g))) break;
         const uint32_t bm = bad[g % S];
         const bool edge = bm != 0u || k0 + KEYS > P || k0 < lo_most;
         if (edge || TS)
@@ -666,12 +671,11 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
           }
           fence_proxy_async_smem();  // generic writes -> the tensor core's reads
         }
-        if (!(ok = wait_w(sfull, g))) break;
         tc::tc_fence_after();
         if (some) {
           const int kh = half * (KEYS / 2);
-          const float* sk = reinterpret_cast<const float*>(smem + SM::tsc) + kslot * KEYS + kh;
-          const float* sv = reinterpret_cast<const float*>(smem + SM::tsc) + vslot * KEYS + kh;
+          const float* sk = reinterpret_cast<const float*>(smem + SM::tsc) + g % (S / 2) * 2 * KEYS + kh;
+          const float* sv = sk + KEYS;
           // 32 logits (as raw products) of the half's chunk c, masked
           auto load = [&](int c, float (&x)[32]) {
             tc::tmem_ld32(tm + kh + 32 * c, x);
@@ -717,7 +721,7 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
 #pragma unroll
             for (int y = 0; y < KEYS / 32; ++y) {
               const int key = lane + 32 * y;
-              const float v = *(reinterpret_cast<const float*>(smem + SM::tsc) + vslot * KEYS + key);
+              const float v = sv[key - kh];
               if (k0 + key < pc.s.L && !(bm >> (key / kBS) & 1u)) s = fmaxf(s, v);
             }
 #pragma unroll
