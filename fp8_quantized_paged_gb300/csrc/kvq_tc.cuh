@@ -222,6 +222,84 @@ KVQ_DEVI uint32_t lds32(uint32_t addr) {
   return r;
 }
 
+// 64 consecutive TMEM columns of this thread's lane (warp-collective); the load and
+// its wait are one statement, so that nothing uses the registers early.
+KVQ_DEVI void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]),
+        "=f"(v[1]),
+        "=f"(v[2]),
+        "=f"(v[3]),
+        "=f"(v[4]),
+        "=f"(v[5]),
+        "=f"(v[6]),
+        "=f"(v[7]),
+        "=f"(v[8]),
+        "=f"(v[9]),
+        "=f"(v[10]),
+        "=f"(v[11]),
+        "=f"(v[12]),
+        "=f"(v[13]),
+        "=f"(v[14]),
+        "=f"(v[15]),
+        "=f"(v[16]),
+        "=f"(v[17]),
+        "=f"(v[18]),
+        "=f"(v[19]),
+        "=f"(v[20]),
+        "=f"(v[21]),
+        "=f"(v[22]),
+        "=f"(v[23]),
+        "=f"(v[24]),
+        "=f"(v[25]),
+        "=f"(v[26]),
+        "=f"(v[27]),
+        "=f"(v[28]),
+        "=f"(v[29]),
+        "=f"(v[30]),
+        "=f"(v[31]),
+        "=f"(v[32]),
+        "=f"(v[33]),
+        "=f"(v[34]),
+        "=f"(v[35]),
+        "=f"(v[36]),
+        "=f"(v[37]),
+        "=f"(v[38]),
+        "=f"(v[39]),
+        "=f"(v[40]),
+        "=f"(v[41]),
+        "=f"(v[42]),
+        "=f"(v[43]),
+        "=f"(v[44]),
+        "=f"(v[45]),
+        "=f"(v[46]),
+        "=f"(v[47]),
+        "=f"(v[48]),
+        "=f"(v[49]),
+        "=f"(v[50]),
+        "=f"(v[51]),
+        "=f"(v[52]),
+        "=f"(v[53]),
+        "=f"(v[54]),
+        "=f"(v[55]),
+        "=f"(v[56]),
+        "=f"(v[57]),
+        "=f"(v[58]),
+        "=f"(v[59]),
+        "=f"(v[60]),
+        "=f"(v[61]),
+        "=f"(v[62]),
+        "=f"(v[63])
+      : "r"(taddr)
+      : "memory");
+}
+
 // Two binary32 values in a register pair: one instruction for both.
 using f32x2 = unsigned long long;
 KVQ_DEVI f32x2 f32x2_pack(float a, float b) {

@@ -11,18 +11,19 @@
 // leaves its rows' states in the workspace, which a second, dependent launch merges.  (A last
 // arriver would read a piece of 64 KB for each of, say, 38 CTAs alone.)
 //
-//   warp 8 (producer)  copies a block's K pages, then its V pages, by TMA into a ring of 64 KB
-//   warp 9 (issuer)    one lane: S = Q K^T (M 128, N kKeys); when the softmax has made P of it,
-//     O += P V with P from tensor memory, V as it lies (token-major: an MN-major operand)
-//   warps 0-7 (softmax)  thread = row (TMEM lane) and half of the block's keys: mask, running
-//     maximum (raised lazily, exchanged between a row's two threads), P over the S columns
-//     that it came from
+//   warp 4 (producer)  copies a block's K pages, then its V pages, by TMA into a ring of 64 KB
+//   warp 5 (issuer)    one lane: S = Q K^T (M 128, N 64) a block ahead, into two buffers in turn;
+//     when the softmax has made P of one, O += P V with P from tensor memory, V as it lies
+//     (token-major: an MN-major operand)
+//   warps 0-3 (softmax)  thread = row (TMEM lane): mask, running maximum (raised lazily), P over the
+//     S columns that it came from
 // The products run on the codes as they are: no conversion, no registers between memory and the
 // tensor cores.  For that Q and P are split into parts that 8 bits hold:
 //   q  2^a q = q1 + q2, E4M3 both, 2^a taking the row's largest to [2^7, 2^8): bf16's 8 bits are
 //     4 + 4, so exact within 2^8 of the largest; the parts add in one accumulator
-//   P  weights times 2^7 as f16, then p1 + p2 + p3, E5M2 each (f16's upper byte, so a part is
-//     subtracted exactly in f16): 2^-9 of the weight, or 2^-24 of the row's largest.  Three
+//   P  weights times 2^7 as f16, then p1 + p2 + p3, E5M2 each: f16's upper byte is an E5M2 number,
+//     so a part is a byte of what the parts before left, subtracted exactly in f16, the last one
+//     rounded: 2^-9 of the weight, or 2^-24 of the row's largest.  Three
 //     E5M2 parts and not two E4M3 ones, whose range of 2^17 would drop a long context's small
 //     weights beside one large one
 // Over bf16 caches the operands are bf16: q itself, P as two parts.
@@ -47,14 +48,15 @@ namespace kvq {
 namespace tree {
 
 constexpr int kRows = 128;  // rows of a tile (MMA M)
-constexpr int kSoftWarps = 8, kProdWarp = 8, kMmaWarp = 9;
-constexpr int kTreeThreads = 320;
+constexpr int kSoftWarps = 4, kProdWarp = 4, kMmaWarp = 5;
+constexpr int kTreeThreads = 192;
 constexpr int kTreeCtas = 2;                          // CTAs of an SM
-constexpr uint32_t kTmemCols = 256, kOutCol = 128;    // S and P at 0, O at 128
+constexpr int kKeys = 64;                             // keys of a block
+constexpr uint32_t kTmemCols = 256, kOutCol = 128;    // S and P at 0 and 64, O at 128
 constexpr int kRing = 64 * 1024;
 constexpr int kEntries = 1024;  // prefix sums of the plan: of every ceil(B / 1024)th sequence
-constexpr int kSegCost = 2;     // a segment's start and end, in blocks
-constexpr int kMinShare = 2;    // least cost of a CTA's stretch
+constexpr int kSegCost = 4;     // a segment's start and end, in blocks
+constexpr int kMinShare = 4;    // least cost of a CTA's stretch
 constexpr float kBias = 7.f;    // log2 of the factor that the weights carry
 constexpr int kMaskWords = KVQ_TREE_MAX_NODES / 32;
 
@@ -99,13 +101,11 @@ struct TreeCfg {
   static constexpr int kElem = kBf ? 2 : 1;
   static constexpr int kRow = DH * kElem;                 // bytes of a token's row
   static constexpr int kSpan = kRow > 128 ? 128 : kRow;   // of a tile's row; wider rows take two tiles side by side
-  static constexpr int kKeys = kRow > 128 ? 64 : 128;     // keys of a block
   static constexpr int kPages = kKeys / kBS;
   static constexpr int kTile = kKeys * kRow;              // a block's K or V
-  static constexpr int kSlots = kRing / kTile;            // 4 or 8
+  static constexpr int kSlots = kRing / kTile;            // 4, 8 or 16
   static constexpr int kQTile = kRows * kRow;             // one part of Q
   static constexpr int kQParts = kBf ? 1 : 2;
-  static constexpr int kChunks = kKeys / 64;              // of 32 keys, of a half block
   static constexpr int kPageBytes = kBS * kRow;
 };
 
@@ -116,12 +116,10 @@ struct TreeSmem {
   static constexpr int q = 0;
   static constexpr int ring = q + C::kQParts * C::kQTile;
   static constexpr int tsc = ring + kRing;  // per-(token, head) scales, K's and V's, that land with a V
-  static constexpr int bars = tsc + (TS ? S * C::kKeys * 4 : 0);
-  static constexpr int kBars = 2 * S + 9;
+  static constexpr int bars = tsc + (TS ? S * kKeys * 4 : 0);
+  static constexpr int kBars = 2 * S + 8;
   static constexpr int misc = bars + kBars * 8;  // tmem address, abort, NaN mark, -, bad[S], issued[S], warp sums
-  static constexpr int mx = misc + (4 + 2 * S + kTreeThreads / 32) * 4;  // [2][2][kRows] maxima, [2][kRows] sums
-  static constexpr int lo = mx + 6 * kRows * 4;                          // [kRows] first visible token
-  static constexpr int anc = lo + kRows * 4;                             // [kMaskWords][kRows] ancestors
+  static constexpr int anc = misc + (4 + 2 * S + kTreeThreads / 32) * 4;  // [kMaskWords][kRows] ancestors
   static constexpr int plan = anc + kMaskWords * kRows * 4;
   static constexpr int total = plan + (kEntries + 1) * 4 + 1024;
   static_assert(total <= 113 * 1024, "two CTAs an SM");
@@ -137,7 +135,6 @@ struct Seq {
   bool bad_q, bad_len;
 };
 
-template <int KEYS>
 KVQ_DEVI Seq seq_of(const TreeParams& p, int b) {
   Seq s;
   s.q0 = __ldg(p.cu_q + b);
@@ -152,7 +149,7 @@ KVQ_DEVI Seq seq_of(const TreeParams& p, int b) {
     s.tiles = (s.n + tq - 1) / tq;
     const int lo = p.window > 0 ? s.L - s.n - p.window + 1 : 0;  // of the nodes without ancestors
     s.first = lo > 0 ? lo / kBS * kBS : 0;
-    s.blocks = (s.L - s.first + KEYS - 1) / KEYS;
+    s.blocks = (s.L - s.first + kKeys - 1) / kKeys;
     s.cost = s.tiles * p.Hkv * (s.blocks + kSegCost);
   }
   return s;
@@ -168,7 +165,6 @@ struct Piece {
 
 // The pieces of a stretch [v, end) of cost positions, in order.  A segment of n blocks takes
 // kSegCost + n positions; block i is the CTA's that has position base + kSegCost + i.
-template <int KEYS>
 struct Pieces {
   const int32_t* plan;
   int per, entries;  // sequences of an entry
@@ -185,10 +181,10 @@ struct Pieces {
         const int e = find_seq(plan, entries, v);
         b = e * per;
         at = plan[e];
-        s = seq_of<KEYS>(p, b);
+        s = seq_of(p, b);
         while (v >= at + s.cost) {
           at += s.cost;
-          s = seq_of<KEYS>(p, ++b);
+          s = seq_of(p, ++b);
         }
       }
       const int len = s.blocks + kSegCost, seg = (v - at) / len;
@@ -228,22 +224,11 @@ KVQ_DEVI uint32_t hsub2(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// Two f16 -> two E5M2 codes in the low half.
-KVQ_DEVI uint32_t f16x2_to_e5m2x2(uint32_t h) {
-  uint16_t c;
-  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(c) : "r"(h));
-  return c;
-}
-// And back: an E5M2 code is the upper byte of its f16.
-KVQ_DEVI uint32_t e5m2x2_to_f16x2(uint32_t c) { return prmt(c, 0u, 0x1404u); }
-
-// The three E5M2 parts of two weights (f16), each in the low half of c[k].
+// The E5M2 parts of two weights (f16, not negative), each the upper byte of a half of c[k].
 KVQ_DEVI void weight_parts(uint32_t h, uint32_t (&c)[3]) {
-  c[0] = f16x2_to_e5m2x2(h);
-  h = hsub2(h, e5m2x2_to_f16x2(c[0]));
-  c[1] = f16x2_to_e5m2x2(h);
-  h = hsub2(h, e5m2x2_to_f16x2(c[1]));
-  c[2] = f16x2_to_e5m2x2(h);
+  c[0] = h;
+  c[1] = hsub2(h, h & 0xFF00FF00u);
+  c[2] = hsub2(c[1], c[1] & 0xFF00FF00u) + 0x00800080u;  // (rounds; no carry leaves a half)
 }
 
 // Byte `b` of row r in a tile of swizzled rows; rows past 128 bytes go on in a second tile.
@@ -259,7 +244,7 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
                 const __grid_constant__ CUtensorMap tmv) {
   using C = TreeCfg<FMT, DH>;
   using SM = TreeSmem<FMT, DH, TS>;
-  constexpr int S = C::kSlots, KEYS = C::kKeys;
+  constexpr int S = C::kSlots;
   constexpr bool BF = C::kBf;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -267,31 +252,28 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
   // Position 2 g of the stream is the K of the CTA's block g, 2 g + 1 its V; slot: position % S.
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::bars);  // [S] a slot landed
   uint64_t* empty = full + S;     // [S] read by the matrix steps (commit)
-  uint64_t* sfull = empty + S;    // S of a block written (commit, and the issuer's arrival)
-  uint64_t* pfull = sfull + 1;    // P of a block written, O rescaled (8 warps)
-  uint64_t* pdone = pfull + 1;    // O += P V of a block done (commit, and the issuer's arrival)
-  uint64_t* qready = pdone + 1;   // Q of a piece written (8 warps)
-  uint64_t* xch = qready + 1;     // [4] a row quarter's two warps have left words for each other
-  uint64_t* fin = xch + 4;        // every matrix step done (commit)
+  uint64_t* sfull = empty + S;    // [2] S of a block written (commit, and the issuer's arrival)
+  uint64_t* pfull = sfull + 2;    // [2] P of a block written, O rescaled (4 warps)
+  uint64_t* pdone = pfull + 2;    // [2] O += P V of a block done (commit, and the issuer's arrival)
+  uint64_t* qready = pdone + 2;   // Q of a piece written (4 warps)
+  uint64_t* fin = qready + 1;     // every matrix step done (commit)
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + SM::misc);
   volatile uint32_t* tmem_slot = misc;
   volatile uint32_t* abort_flag = misc + 1;
   volatile uint32_t* vnan = misc + 2;   // 1 + the last piece that met a NaN or infinity to put back
   volatile uint32_t* bad = misc + 4;    // [S] masked pages of block g at [g % S]: rewritten for block
-                                        // g + S, whose K waits for the S of a block after g
+                                        // g + S, whose K waits for the softmax of block g
   volatile int32_t* issued = reinterpret_cast<volatile int32_t*>(misc + 4 + S);  // [S] last position
   volatile int32_t* warp_sum = reinterpret_cast<volatile int32_t*>(misc + 4 + 2 * S);
-  float* mx_s = reinterpret_cast<float*>(smem + SM::mx);
-  float* l_s = mx_s + 4 * kRows;
-  int32_t* lo_s = reinterpret_cast<int32_t*>(smem + SM::lo);
   uint32_t* anc = reinterpret_cast<uint32_t*>(smem + SM::anc);
   int32_t* plan = reinterpret_cast<int32_t*>(smem + SM::plan);
 
   // A parity wait for phase k of a barrier is sound while it has completed k or k + 1 phases.  The
-  // issuer, the producer and the softmax take their barriers' phases in order, one a block (a piece:
-  // qready).  The softmax also looks at a V slot's full barrier, for some blocks only: all earlier
-  // phases of it are complete then, as the S of block g comes after the PV of block g - 1, and the
-  // next one waits for this softmax.  (Not at a K slot's: the next K may land while a warp is late.)
+  // issuer, the producer and the softmax take their barriers' phases in order, one every other block
+  // (a block; a piece: qready).  The softmax also looks at a V slot's full barrier and at pdone, for
+  // some blocks only: all earlier phases of them are complete then, as the S of block g comes after
+  // the PV of block g - 2, and the next ones wait for this softmax.  (Not at a K slot's: the next K may
+  // land while a warp is late.)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
@@ -300,11 +282,12 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
       mbar_init(&empty[i], 1);
       issued[i] = -1;
     }
-    mbar_init(sfull, 2);
-    mbar_init(pfull, kSoftWarps);
-    mbar_init(pdone, 2);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sfull[i], 2);
+      mbar_init(&pfull[i], kSoftWarps);
+      mbar_init(&pdone[i], 2);
+    }
     mbar_init(qready, kSoftWarps);
-    for (int i = 0; i < 4; ++i) mbar_init(&xch[i], 2);
     mbar_init(fin, 1);
     *abort_flag = 0u;
     *vnan = 0u;
@@ -331,7 +314,7 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
       sum[y] = 0;
       const int e = tid * each + y;
       if (y < each && e < entries)
-        for (int b = e * per; b < min(p.B, (e + 1) * per); ++b) sum[y] += seq_of<KEYS>(p, b).cost;
+        for (int b = e * per; b < min(p.B, (e + 1) * per); ++b) sum[y] += seq_of(p, b).cost;
       mine += sum[y];
     }
     int incl = mine;
@@ -360,7 +343,7 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
   }
   // sequences without work: errors, and zero rows
   for (int b = cta; b < p.B; b += gridDim.x) {
-    const Seq s = seq_of<KEYS>(p, b);
+    const Seq s = seq_of(p, b);
     if (tid == 0 && s.bad_q) flag_status(p.status, KVQ_DEV_BAD_QLEN);
     if (!s.bad_len) continue;
     if (tid == 0) flag_status(p.status, KVQ_DEV_BAD_SEQLEN);
@@ -387,7 +370,7 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
   if (warp == kProdWarp) {
     // ------------------------------------------------------------ producer
     constexpr int kAhead = 32 / C::kPages;  // blocks of which the lanes hold the block ids
-    Pieces<KEYS> it(plan, p.B, v0, v1);
+    Pieces it(plan, p.B, v0, v1);
     Piece pc;
     int g = 0;
     bool ok = true;
@@ -438,11 +421,11 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
             uint8_t* dst = smem + SM::ring + s * C::kTile + lane * (kBS * C::kSpan);
             const CUtensorMap* map = t ? &tmv : &tmk;
             tma_load_2d(dst, map, 0, row, &full[s]);
-            if (C::kRow > 128) tma_load_2d(dst + KEYS * 128, map, 64, row, &full[s]);
+            if (C::kRow > 128) tma_load_2d(dst + kKeys * 128, map, 64, row, &full[s]);
             if (TS && t == 1) {  // (K's own slot goes on to the next K before the softmax is done)
-              uint8_t* sc = smem + SM::tsc + (g % (S / 2) * 2 * KEYS + lane * kBS) * 4;
+              uint8_t* sc = smem + SM::tsc + (g % (S / 2) * 2 * kKeys + lane * kBS) * 4;
               bulk_load(sc, p.ks + row, kBS * 4, &full[s]);
-              bulk_load(sc + KEYS * 4, p.vs + row, kBS * 4, &full[s]);
+              bulk_load(sc + kKeys * 4, p.vs + row, kBS * 4, &full[s]);
             }
           }
         }
@@ -453,61 +436,67 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
     const uint32_t tm = __shfl_sync(kFull, tmem, 0);
     if (tc::elect_one()) {
       const bool qf8 = !BF && p.qs != nullptr;
-      const uint32_t id_qk = BF ? tc::idesc_bf16(kRows, KEYS)
-                                : tc::idesc_f8(kRows, KEYS, qf8 ? tc::tc_type(FMT) : tc::kTcE4M3, tc::tc_type(FMT), false, false);
+      const uint32_t id_qk = BF ? tc::idesc_bf16(kRows, kKeys)
+                                : tc::idesc_f8(kRows, kKeys, qf8 ? tc::tc_type(FMT) : tc::kTcE4M3, tc::tc_type(FMT), false, false);
       const uint32_t id_pv = BF ? tc::idesc_bf16(kRows, DH) | (1u << 16)
                                 : tc::idesc_f8(kRows, DH, tc::kTcE5M2, tc::tc_type(FMT), false, true);
       const int parts = BF || qf8 ? 1 : 2;
       auto wait = [&](uint64_t* bar, int phase) { return wait_or_abort(bar, static_cast<uint32_t>(phase & 1), abort_flag); };
       auto desc = [&](uint32_t a) { return C::kSpan == 64 ? tc::sw64_desc(a) : tc::sw128_desc(a); };
-      Pieces<KEYS> it(plan, p.B, v0, v1);
+      // S of block g, over the P that the PV of block g - 2 has read
+      auto qk = [&](int g) {
+        const int ks = 2 * g % S, buf = g & 1;
+        if (!wait(&full[ks], 2 * g / S) || (g > 1 && !wait(&pdone[buf], (g - 2) >> 1))) return false;
+        tc::tc_fence_after();
+        const uint32_t a = sbase + SM::q, bk = sbase + SM::ring + ks * C::kTile;
+#pragma unroll
+        for (int k = 0; k < C::kRow / 32; ++k) {  // 32 bytes of a row a step
+          const uint32_t oa = (k >> 2) * (kRows * 128) + (k & 3) * 32, ob = (k >> 2) * (kKeys * 128) + (k & 3) * 32;
+          if (BF) {
+            tc::mma_f16_ss(tm + buf * kKeys, desc(a + oa), desc(bk + ob), id_qk, k > 0 ? 1u : 0u);
+          } else {
+            tc::mma_f8_ss(tm + buf * kKeys, desc(a + oa), desc(bk + ob), id_qk, k > 0 ? 1u : 0u);
+            if (parts > 1) tc::mma_f8_ss(tm + buf * kKeys, desc(a + C::kQTile + oa), desc(bk + ob), id_qk, 1u);
+          }
+        }
+        mbar_arrive(&sfull[buf]);  // hands on what the K slot's arrival showed (bad)
+        tc::mma_commit(&sfull[buf]);
+        tc::mma_commit(&empty[ks]);
+        return true;
+      };
+      Pieces it(plan, p.B, v0, v1);
       Piece pc;
-      int g = 0, piece = 0;
+      int g = 0, piece = 0, next = 0;  // next: the block whose S comes next
       bool ok = true;
       while (ok && it.next(p, pc)) {
+        const int first = g, end = g + pc.i1 - pc.i0;
         if (!(ok = wait(qready, piece++))) break;
-        for (int i = pc.i0; i < pc.i1; ++i, ++g) {
-          const int ks = 2 * g % S, vs = (2 * g + 1) % S;
-          if (!(ok = wait(&full[ks], 2 * g / S))) break;
-          if (g > 0 && !(ok = wait(pdone, g - 1))) break;  // S's columns hold the P that this has read
+        for (; g < end; ++g) {
+          while (ok && next < end && next <= g + 1) ok = qk(next++);
+          const int vs = (2 * g + 1) % S, buf = g & 1;
+          if (!(ok = ok && wait(&full[vs], (2 * g + 1) / S) && wait(&pfull[buf], g >> 1))) break;
           tc::tc_fence_after();
-          const uint32_t a = sbase + SM::q, bk = sbase + SM::ring + ks * C::kTile;
-#pragma unroll
-          for (int k = 0; k < C::kRow / 32; ++k) {  // 32 bytes of a row a step
-            const uint32_t oa = (k >> 2) * (kRows * 128) + (k & 3) * 32, ob = (k >> 2) * (KEYS * 128) + (k & 3) * 32;
-            if (BF) {
-              tc::mma_f16_ss(tm, desc(a + oa), desc(bk + ob), id_qk, k > 0 ? 1u : 0u);
-            } else {
-              tc::mma_f8_ss(tm, desc(a + oa), desc(bk + ob), id_qk, k > 0 ? 1u : 0u);
-              if (parts > 1) tc::mma_f8_ss(tm, desc(a + C::kQTile + oa), desc(bk + ob), id_qk, 1u);
-            }
-          }
-          mbar_arrive(sfull);  // hands on what the K slot's arrival showed (bad)
-          tc::mma_commit(sfull);
-          tc::mma_commit(&empty[ks]);
-          if (!(ok = wait(&full[vs], (2 * g + 1) / S) && wait(pfull, g))) break;
-          tc::tc_fence_after();
-          const uint32_t bv = sbase + SM::ring + vs * C::kTile;
-          const uint32_t more = i > pc.i0 ? 1u : 0u;
+          const uint32_t bv = sbase + SM::ring + vs * C::kTile, tp = tm + buf * kKeys;
+          const uint32_t more = g > first ? 1u : 0u;
           if (BF) {
 #pragma unroll
-            for (int k = 0; k < KEYS / 16; ++k) {
-              const uint64_t d = tc::sw128_desc(bv + k * 2048, KEYS * 128, 1024);
-              const uint32_t at = tm + (k >> 1) * 32 + (k & 1) * 8;
+            for (int k = 0; k < kKeys / 16; ++k) {
+              const uint64_t d = tc::sw128_desc(bv + k * 2048, kKeys * 128, 1024);
+              const uint32_t at = tp + (k >> 1) * 32 + (k & 1) * 8;
               tc::mma_f16_ts(tm + kOutCol, at, d, id_pv, k > 0 ? 1u : more);
               tc::mma_f16_ts(tm + kOutCol, at + 16, d, id_pv, 1u);
             }
           } else {
 #pragma unroll
-            for (int k = 0; k < KEYS / 32; ++k) {
+            for (int k = 0; k < kKeys / 32; ++k) {
               const uint64_t d = desc(bv + k * 32 * C::kSpan);
 #pragma unroll
               for (int y = 0; y < 3; ++y)
-                tc::mma_f8_ts(tm + kOutCol, tm + k * 32 + y * 8, d, id_pv, k > 0 || y > 0 ? 1u : more);
+                tc::mma_f8_ts(tm + kOutCol, tp + k * 32 + y * 8, d, id_pv, k > 0 || y > 0 ? 1u : more);
             }
           }
-          mbar_arrive(pdone);  // hands on what the softmax warps' arrivals showed (vnan)
-          tc::mma_commit(pdone);
+          mbar_arrive(&pdone[buf]);  // hands on what the softmax warps' arrivals showed (vnan)
+          tc::mma_commit(&pdone[buf]);
           tc::mma_commit(&empty[vs]);
         }
       }
@@ -517,104 +506,103 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const int quad = warp & 3, half = warp >> 2, r = quad * 32 + lane;
-    const uint32_t tm = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    Pieces<KEYS> it(plan, p.B, v0, v1);
-    Piece pc;
-    int g = 0, piece = 0, xphase = 0;
-    bool ok = true;
-    // the two warps of a row quarter wait for each other
-    auto exchange = [&] {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&xch[quad]);
-      return wait_w(&xch[quad], xphase++);
-    };
-    while (ok && it.next(p, pc)) {
-      const int TQ = kRows / p.G, j0 = pc.tile * TQ;
-      const int rows = min(pc.s.n - j0, TQ) * p.G;
-      const bool live = r < rows, some = quad * 32 < rows;
-      const int node = j0 + (live ? r / p.G : 0), hq = pc.head * p.G + (live ? r % p.G : 0);
-      const int64_t qrow = (static_cast<int64_t>(pc.s.q0) + node) * p.Hq + hq;
-      const int P = pc.s.L - pc.s.n;  // tokens before the tree
+    // Lane t of tensor memory is row (t - turn) mod 128: the SM's two CTAs begin at different
+    // quarters, each of which is one scheduler's, so that tiles of few rows do not share one.
+    const int turn = (tmem & 0xFFFFu) ? 64 : 0;
+    const int t0 = warp * 32 + lane, r = (t0 - turn) & (kRows - 1);
+    const uint32_t tm = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    // The query row of a piece into the Q tile, scaled; its logits' scale.
+    auto write_q = [&](const Piece& pc) {
+      const int TQ = kRows / p.G, j0 = pc.tile * TQ, rows = min(pc.s.n - j0, TQ) * p.G;
       float lscale = (BF || TS ? 1.f : __ldg(p.ks + (p.per_head ? pc.head : 0))) * p.logit_scale;
-      // ---- the query row: its half of the dims
-      if (some) {
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + qrow * DH);
+      if (r < rows) {
+        const int hq = pc.head * p.G + r % p.G;
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + ((static_cast<int64_t>(pc.s.q0) + j0 + r / p.G) * p.Hq + hq) * DH);
+        uint4 w[DH / 8];
+#pragma unroll
+        for (int c = 0; c < DH / 8; ++c) w[c] = __ldg(src + c);
         if (BF) {
-#pragma unroll 4
-          for (int c = half * (DH / 16); c < (half + 1) * (DH / 16); ++c) {
-            const uint4 w = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-            tc::sts128(sbase + SM::q + tile_at<C::kSpan>(r, 16 * c), w.x, w.y, w.z, w.w);
+#pragma unroll
+          for (int c = 0; c < DH / 8; ++c) tc::sts128(sbase + SM::q + tile_at<C::kSpan>(t0, 16 * c), w[c].x, w[c].y, w[c].z, w[c].w);
+        } else if (p.qs) {
+          constexpr int F = FMT == KVQ_FMT_E5M2 ? KVQ_FMT_E5M2 : KVQ_FMT_E4M3;
+          const float sq = __ldg(p.qs + (p.q_per_head ? hq : 0));
+          lscale *= sq;
+#pragma unroll
+          for (int c = 0; c < DH / 16; ++c) {
+            uint32_t code[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint4& v = w[2 * c + (e >> 1)];
+              const uint32_t u0 = e & 1 ? v.z : v.x, u1 = e & 1 ? v.w : v.y;
+              code[e] = f32x2_to_fp8x2<F>(__fdiv_rn(bf16lo_to_f32(u0), sq), __fdiv_rn(bf16hi_to_f32(u0), sq)) |
+                        (static_cast<uint32_t>(f32x2_to_fp8x2<F>(__fdiv_rn(bf16lo_to_f32(u1), sq), __fdiv_rn(bf16hi_to_f32(u1), sq))) << 16);
+            }
+            tc::sts128(sbase + SM::q + tile_at<C::kSpan>(t0, 16 * c), code[0], code[1], code[2], code[3]);
           }
         } else {
-          float up = 1.f, sq = 1.f;
-          if (p.qs) {
-            sq = __ldg(p.qs + (p.q_per_head ? hq : 0));
-            lscale *= sq;
-          } else {
-            float amax = 0.f;
+          float amax = 0.f;
 #pragma unroll
-            for (int c = 0; c < DH / 8; ++c) {
-              const uint4 w = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-              const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+          for (int c = 0; c < DH / 8; ++c) {
+            const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16lo_to_f32(u[e])), fabsf(bf16hi_to_f32(u[e]))));
-            }
-            int a = 0;
-            if (amax > 0.f) {
-              a = 7 - (static_cast<int>((__float_as_uint(amax) >> 23) & 0xFFu) - 127);
-              a = a > 126 ? 126 : (a < -126 ? -126 : a);
-            }
-            up = __int_as_float((a + 127) << 23);
-            lscale *= __int_as_float((127 - a) << 23);
+            for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16lo_to_f32(u[e])), fabsf(bf16hi_to_f32(u[e]))));
           }
-#pragma unroll 2
-          for (int c = half * (DH / 32); c < (half + 1) * (DH / 32); ++c) {  // 16 dims
-            uint32_t lo[4], hi[4];
+          int a = 0;
+          if (amax > 0.f) {
+            a = 7 - (static_cast<int>((__float_as_uint(amax) >> 23) & 0xFFu) - 127);
+            a = a > 126 ? 126 : (a < -126 ? -126 : a);
+          }
+          const float up = __int_as_float((a + 127) << 23);  // exact: a power of two, no overflow
+          lscale *= __int_as_float((127 - a) << 23);
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint4 w = live ? __ldg(src + 2 * c + y) : make_uint4(0u, 0u, 0u, 0u);
-              const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+          for (int c = 0; c < DH / 16; ++c) {
+            uint32_t hi[4], lo[4];
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float x[4] = {bf16lo_to_f32(u[2 * e]), bf16hi_to_f32(u[2 * e]), bf16lo_to_f32(u[2 * e + 1]), bf16hi_to_f32(u[2 * e + 1])};
-                if (p.qs) {
-                  constexpr int F = FMT == KVQ_FMT_E5M2 ? KVQ_FMT_E5M2 : KVQ_FMT_E4M3;
-#pragma unroll
-                  for (int z = 0; z < 4; ++z) x[z] = __fdiv_rn(x[z], sq);
-                  hi[2 * y + e] = f32x2_to_fp8x2<F>(x[0], x[1]) | (static_cast<uint32_t>(f32x2_to_fp8x2<F>(x[2], x[3])) << 16);
-                  lo[2 * y + e] = 0u;
-                } else {
-#pragma unroll
-                  for (int z = 0; z < 4; ++z) x[z] *= up;  // exact: a power of two, no overflow
-                  const uint32_t c0 = f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[0], x[1]), c1 = f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[2], x[3]);
-                  const uint32_t h0 = fp8x2_to_f16x2<KVQ_FMT_E4M3>(static_cast<uint16_t>(c0));
-                  const uint32_t h1 = fp8x2_to_f16x2<KVQ_FMT_E4M3>(static_cast<uint16_t>(c1));
-                  const uint32_t d0 = f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[0] - f16lo_to_f32(h0), x[1] - f16hi_to_f32(h0));
-                  const uint32_t d1 = f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[2] - f16lo_to_f32(h1), x[3] - f16hi_to_f32(h1));
-                  hi[2 * y + e] = c0 | (c1 << 16);
-                  lo[2 * y + e] = d0 | (d1 << 16);
-                }
-              }
+            for (int e = 0; e < 4; ++e) {
+              const uint4& v = w[2 * c + (e >> 1)];
+              const uint32_t u0 = e & 1 ? v.z : v.x, u1 = e & 1 ? v.w : v.y;
+              const float x[4] = {bf16lo_to_f32(u0) * up, bf16hi_to_f32(u0) * up, bf16lo_to_f32(u1) * up, bf16hi_to_f32(u1) * up};
+              const uint32_t c0 = f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[0], x[1]), c1 = f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[2], x[3]);
+              const uint32_t h0 = fp8x2_to_f16x2<KVQ_FMT_E4M3>(static_cast<uint16_t>(c0));
+              const uint32_t h1 = fp8x2_to_f16x2<KVQ_FMT_E4M3>(static_cast<uint16_t>(c1));
+              hi[e] = c0 | (c1 << 16);
+              lo[e] = f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[0] - f16lo_to_f32(h0), x[1] - f16hi_to_f32(h0)) |
+                      (static_cast<uint32_t>(f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[2] - f16lo_to_f32(h1), x[3] - f16hi_to_f32(h1))) << 16);
             }
-            const uint32_t at = sbase + SM::q + tile_at<C::kSpan>(r, 16 * c);
+            const uint32_t at = sbase + SM::q + tile_at<C::kSpan>(t0, 16 * c);
             tc::sts128(at, hi[0], hi[1], hi[2], hi[3]);
-            if (!p.qs) tc::sts128(at + C::kQTile, lo[0], lo[1], lo[2], lo[3]);
+            tc::sts128(at + C::kQTile, lo[0], lo[1], lo[2], lo[3]);
           }
         }
         fence_proxy_async_smem();
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(qready);
-      lscale = fp4::bounded_scale(lscale);
+      return fp4::bounded_scale(lscale);
+    };
+    Pieces it(plan, p.B, v0, v1);
+    Piece nx;
+    int g = 0, piece = 0;
+    bool ok = true, more = it.next(p, nx);
+    float lscale_nx = more ? write_q(nx) : 1.f;
+    while (more) {
+      const Piece pc = nx;
+      const float lscale = lscale_nx;
+      const int TQ = kRows / p.G, j0 = pc.tile * TQ;
+      const int rows = min(pc.s.n - j0, TQ) * p.G;
+      const bool live = r < rows, some = ((warp * 32 - turn) & (kRows - 1)) < rows;
+      const int node = j0 + (live ? r / p.G : 0);
+      const int P = pc.s.L - pc.s.n;  // tokens before the tree
       // ---- the row's ancestors, and the first token that it sees
-      const int far = p.window > 0 ? p.window : INT_MAX;
-      if (some && half == 0 && live && (p.window > 0 || pc.s.first + pc.i1 * KEYS > P)) {
+      int lo = 0;
+      if (live && (p.window > 0 || pc.s.first + pc.i1 * kKeys > P)) {
+        const int far = p.window > 0 ? p.window : INT_MAX;
 #pragma unroll
-        for (int w = 0; w < kMaskWords; ++w) anc[w * kRows + r] = 0u;
+        for (int w = 0; w < kMaskWords; ++w) anc[w * kRows + t0] = 0u;
         int depth = -1;
         for (int at = node; at >= 0; ++depth) {
-          if (depth + 1 < far) anc[(at >> 5) * kRows + r] |= 1u << (at & 31);
+          if (depth + 1 < far) anc[(at >> 5) * kRows + t0] |= 1u << (at & 31);
           int up = at - 1;
           if (p.parents) {
             up = __ldg(p.parents + pc.s.q0 + at);
@@ -625,10 +613,9 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
           }
           at = up;
         }
-        lo_s[r] = p.window > 0 ? max(0, P + depth - p.window + 1) : 0;
+        if (p.window > 0) lo = max(0, P + depth - p.window + 1);
       }
-      if (some && !(ok = exchange())) break;
-      const int lo = some && live && p.window > 0 ? lo_s[r] : 0;
+      __syncwarp();
       const int lo_most = p.window > 0 ? P + pc.s.n - p.window : 0;  // no row's first token lies past it
       // Keys of the 32 from key k on that the row sees, on good pages (bit y: page k / 16 + y is bad).
       auto seen32 = [&](int k, uint32_t bm) {
@@ -636,7 +623,7 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
         const int i = k - P;  // the first key's node
         if (i > -32 && i < KVQ_TREE_MAX_NODES) {
           const int w = i >> 5;
-          const uint32_t a = w >= 0 ? anc[w * kRows + r] : 0u, z = w + 1 < kMaskWords ? anc[(w + 1) * kRows + r] : 0u;
+          const uint32_t a = w >= 0 ? anc[w * kRows + t0] : 0u, z = w + 1 < kMaskWords ? anc[(w + 1) * kRows + t0] : 0u;
           s |= __funnelshift_r(a, z, i & 31);
         }
         return s & ~((bm & 1u ? 0xFFFFu : 0u) | (bm & 2u ? 0xFFFF0000u : 0u));
@@ -644,11 +631,11 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
       float m = -INFINITY, l = 0.f, sig = 0.f;
       const float rise = kRescaleThreshold / lscale;
       for (int i = pc.i0; i < pc.i1; ++i, ++g) {
-        const int k0 = pc.s.first + i * KEYS;
+        const int k0 = pc.s.first + i * kKeys, buf = g & 1;
         const int vslot = (2 * g + 1) % S;
-        if (!(ok = wait_w(sfull, g))) break;
+        if (!(ok = wait_w(&sfull[buf], g >> 1))) break;
         const uint32_t bm = bad[g % S];
-        const bool edge = bm != 0u || k0 + KEYS > P || k0 < lo_most;
+        const bool edge = bm != 0u || k0 + kKeys > P || k0 < lo_most;
         if (edge || TS)
           if (!(ok = wait_w(&full[vslot], (2 * g + 1) / S))) break;
         if (edge) {
@@ -656,7 +643,7 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
 #pragma unroll
           for (int y = 0; y < C::kTile / (kSoftWarps * 32 * 16); ++y) {
             const int c = tid + y * kSoftWarps * 32;  // 16 bytes
-            const int key = c / (C::kSpan / 16) % KEYS, t = k0 + key;
+            const int key = c / (C::kSpan / 16) % kKeys, t = k0 + key;
             uint4* at = reinterpret_cast<uint4*>(smem + SM::ring + vslot * C::kTile) + c;
             if (t >= pc.s.L || (bm >> (key / kBS) & 1u)) {
               *at = make_uint4(0u, 0u, 0u, 0u);
@@ -673,56 +660,45 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
         }
         tc::tc_fence_after();
         if (some) {
-          const int kh = half * (KEYS / 2);
-          const float* sk = reinterpret_cast<const float*>(smem + SM::tsc) + g % (S / 2) * 2 * KEYS + kh;
-          const float* sv = sk + KEYS;
-          // 32 logits (as raw products) of the half's chunk c, masked
-          auto load = [&](int c, float (&x)[32]) {
-            tc::tmem_ld32(tm + kh + 32 * c, x);
-            if (TS) {
+          const uint32_t ts = tm + buf * kKeys;
+          const float* sk = reinterpret_cast<const float*>(smem + SM::tsc) + g % (S / 2) * 2 * kKeys;
+          const float* sv = sk + kKeys;
+          // 64 logits (as raw products), masked
+          float x[kKeys];
+          tc::tmem_ld64(ts, x);
+          if (TS) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 s4 = *reinterpret_cast<const float4*>(sk + 32 * c + e);
-                x[e] *= s4.x;
-                x[e + 1] *= s4.y;
-                x[e + 2] *= s4.z;
-                x[e + 3] *= s4.w;
-              }
+            for (int e = 0; e < kKeys; e += 4) {
+              const float4 s4 = *reinterpret_cast<const float4*>(sk + e);
+              x[e] *= s4.x;
+              x[e + 1] *= s4.y;
+              x[e + 2] *= s4.z;
+              x[e + 3] *= s4.w;
             }
-            if (edge) {
-              const uint32_t s = seen32(k0 + kh + 32 * c, bm >> ((kh + 32 * c) / kBS));
-#pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = s >> e & 1u ? x[e] : -INFINITY;
-              return s;
-            }
-            return 0xFFFFFFFFu;
-          };
-          float mx = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < C::kChunks; ++c) {
-            float x[32];
-            load(c, x);
-            float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              a = tc::fmax3(a, x[e], x[e + 1]);
-              b = tc::fmax3(b, x[e + 2], x[e + 3]);
-            }
-            mx = tc::fmax3(mx, a, b);
           }
-          float* slot = mx_s + (g & 1) * 2 * kRows;
-          slot[half * kRows + r] = mx;
-          if (!(ok = exchange())) break;
-          mx = fmaxf(mx, slot[(half ^ 1) * kRows + r]);
+          uint32_t seen[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+          if (edge) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              seen[c] = seen32(k0 + 32 * c, bm >> (2 * c));
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[32 * c + e] = seen[c] >> e & 1u ? x[32 * c + e] : -INFINITY;
+            }
+          }
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < kKeys; e += 8)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) mx4[y] = tc::fmax3(mx4[y], x[e + 2 * y], x[e + 2 * y + 1]);
+          const float mx = tc::fmax3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]);
           const bool grow = mx > m + rise;
           float fs = 1.f;
           if (TS) {  // the largest value scale of the block's tokens, to a power of two
             float s = 0.f;
 #pragma unroll
-            for (int y = 0; y < KEYS / 32; ++y) {
+            for (int y = 0; y < kKeys / 32; ++y) {
               const int key = lane + 32 * y;
-              const float v = sv[key - kh];
-              if (k0 + key < pc.s.L && !(bm >> (key / kBS) & 1u)) s = fmaxf(s, v);
+              if (k0 + key < pc.s.L && !(bm >> (key / kBS) & 1u)) s = fmaxf(s, sv[key]);
             }
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) s = fmaxf(s, __shfl_xor_sync(kFull, s, off));
@@ -734,10 +710,12 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
           }
           if (__any_sync(kFull, grow) || (TS && fs != 1.f)) {
             const float a = m == -INFINITY ? 0.f : fast_exp2((m - mx) * lscale);
-            if (i > pc.i0) {  // (O's last writer is done: S came after it)
+            if (i > pc.i0) {  // O's last writer: the PV of the block before
+              if (!(ok = wait_w(&pdone[buf ^ 1], (g - 1) >> 1))) break;
+              tc::tc_fence_after();
               const float f = (grow ? a : 1.f) * fs;
 #pragma unroll 1
-              for (int c = half * (DH / 2); c < (half + 1) * (DH / 2); c += 16) {
+              for (int c = 0; c < DH; c += 16) {
                 uint32_t o[16];
                 tc::tmem_ld16(tm + kOutCol + c, o);
 #pragma unroll
@@ -753,81 +731,78 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
           const float fm = m == -INFINITY ? 0.f : -m;
           const float inv_sig = TS && sig > 0.f ? 1.f / sig : 0.f;
           const tc::f32x2 fm2 = tc::f32x2_pack(fm, fm), ls2 = tc::f32x2_pack(lscale, lscale), b2 = tc::f32x2_pack(kBias, kBias);
-          tc::f32x2 l2 = tc::f32x2_pack(0.f, 0.f);
-#pragma unroll 1
-          for (int c = 0; c < C::kChunks; ++c) {
-            float x[32];
-            const uint32_t s = load(c, x);
+          tc::f32x2 l2[2] = {tc::f32x2_pack(0.f, 0.f), tc::f32x2_pack(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
             // the maximum is subtracted before the scale: its own weight is 2^7 exactly, however large
-            uint32_t w[3][8];
+            uint32_t w[4][8];
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
+              const int k = 32 * c + e;
               float y[4];
 #pragma unroll
               for (int z = 0; z < 4; z += 2) {
-                tc::f32x2_unpack(tc::f32x2_fma(tc::f32x2_add(tc::f32x2_pack(x[e + z], x[e + z + 1]), fm2), ls2, b2), y[z], y[z + 1]);
+                tc::f32x2_unpack(tc::f32x2_fma(tc::f32x2_add(tc::f32x2_pack(x[k + z], x[k + z + 1]), fm2), ls2, b2), y[z], y[z + 1]);
                 y[z] = fast_exp2(y[z]);
                 y[z + 1] = fast_exp2(y[z + 1]);
-                l2 = tc::f32x2_add(l2, tc::f32x2_pack(y[z], y[z + 1]));
+                l2[z >> 1] = tc::f32x2_add(l2[z >> 1], tc::f32x2_pack(y[z], y[z + 1]));
               }
               if (TS) {
-                const float4 s4 = *reinterpret_cast<const float4*>(sv + 32 * c + e);
-                y[0] = s >> e & 1u ? y[0] * (s4.x * inv_sig) : 0.f;
-                y[1] = s >> (e + 1) & 1u ? y[1] * (s4.y * inv_sig) : 0.f;
-                y[2] = s >> (e + 2) & 1u ? y[2] * (s4.z * inv_sig) : 0.f;
-                y[3] = s >> (e + 3) & 1u ? y[3] * (s4.w * inv_sig) : 0.f;
+                const float4 s4 = *reinterpret_cast<const float4*>(sv + k);
+                y[0] = seen[c] >> e & 1u ? y[0] * (s4.x * inv_sig) : 0.f;
+                y[1] = seen[c] >> (e + 1) & 1u ? y[1] * (s4.y * inv_sig) : 0.f;
+                y[2] = seen[c] >> (e + 2) & 1u ? y[2] * (s4.z * inv_sig) : 0.f;
+                y[3] = seen[c] >> (e + 3) & 1u ? y[3] * (s4.w * inv_sig) : 0.f;
               }
-              if (BF) {  // two keys a column; hi of 16 keys a step, lo of them 16 columns on
+              if (BF) {  // two keys a column: w[0], w[1] the hi parts of 16 keys each, w[2], w[3] the lo parts
                 const uint32_t h0 = f32x2_to_bf16x2(y[0], y[1]), h1 = f32x2_to_bf16x2(y[2], y[3]);
-                const uint32_t l0 = f32x2_to_bf16x2(y[0] - bf16lo_to_f32(h0), y[1] - bf16hi_to_f32(h0));
-                const uint32_t l1 = f32x2_to_bf16x2(y[2] - bf16lo_to_f32(h1), y[3] - bf16hi_to_f32(h1));
-                const uint32_t at = tm + kh + 32 * c + e / 2;
-                asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(at), "r"(h0), "r"(h1) : "memory");
-                asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(at + 16), "r"(l0), "r"(l1) : "memory");
-              } else {
+                w[e >> 4][(e & 15) / 2] = h0;
+                w[e >> 4][(e & 15) / 2 + 1] = h1;
+                w[2 + (e >> 4)][(e & 15) / 2] = f32x2_to_bf16x2(y[0] - bf16lo_to_f32(h0), y[1] - bf16hi_to_f32(h0));
+                w[2 + (e >> 4)][(e & 15) / 2 + 1] = f32x2_to_bf16x2(y[2] - bf16lo_to_f32(h1), y[3] - bf16hi_to_f32(h1));
+              } else {  // four keys a column, a part of all 32 in w[0], w[1], w[2] each
                 uint32_t c0[3], c1[3];
                 weight_parts(f32x2_to_f16x2(y[0], y[1]), c0);
                 weight_parts(f32x2_to_f16x2(y[2], y[3]), c1);
 #pragma unroll
-                for (int k = 0; k < 3; ++k) w[k][e / 4] = prmt(c0[k], c1[k], 0x5410u);
+                for (int z = 0; z < 3; ++z) w[z][e / 4] = prmt(c0[z], c1[z], 0x7531u);
               }
             }
-            if (!BF)
 #pragma unroll
-              for (int k = 0; k < 3; ++k) tc::tmem_st8(tm + kh + 32 * c + 8 * k, w[k]);
+            for (int z = 0; z < (BF ? 4 : 3); ++z) tc::tmem_st8(ts + 32 * c + 8 * z, w[z]);
           }
           float l0, l1;
-          tc::f32x2_unpack(l2, l0, l1);
+          tc::f32x2_unpack(tc::f32x2_add(l2[0], l2[1]), l0, l1);
           l += l0 + l1;
           tc::tmem_st_wait();
         }
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(pfull);
+        if (lane == 0) mbar_arrive(&pfull[buf]);
       }
       if (!ok) break;
-      // ---- the piece's end: rows of O, normalised
-      if (!(ok = wait_w(pdone, g - 1))) break;
+      // ---- the piece's end: the next one's Q (all of this one's S are done), and the rows of O, normalised
+      more = it.next(p, nx);
+      if (more) lscale_nx = write_q(nx);
+      if (!(ok = wait_w(&pdone[(g - 1) & 1], (g - 1) >> 1))) break;
       tc::tc_fence_after();
       if (tid == 0 && !pc.whole() && pc.i0 == 0)
         p.ws_rec[cta] = make_int4(rows, split.cta_of(pc.base + kSegCost + pc.s.blocks - 1), pc.s.q0 + j0, pc.head);
       const bool put_back = *vnan == 1u + piece;
       ++piece;
       if (!some) continue;
-      l_s[half * kRows + r] = l;
-      if (!(ok = exchange())) break;
-      l = l_s[r] + l_s[kRows + r];
       const float svs = TS ? sig : BF ? 1.f : __ldg(p.vs + (p.per_head ? pc.head : 0));
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
       const int64_t part = static_cast<int64_t>(2 * cta + (pc.i0 == 0)) * kRows + r;
-      if (!pc.whole() && live && half == 0) p.ws_ml[part] = make_float2(fp4::merge_max(m, lscale), l);
+      const int64_t qrow = (static_cast<int64_t>(pc.s.q0) + node) * p.Hq + pc.head * p.G + r % p.G;
+      if (!pc.whole() && live) p.ws_ml[part] = make_float2(fp4::merge_max(m, lscale), l);
 #pragma unroll 1
-      for (int c = half * (DH / 2); c < (half + 1) * (DH / 2); c += 32) {
+      for (int c = 0; c < DH; c += 32) {
         float o[32];
         tc::tmem_ld32(tm + kOutCol + c, o);
         if (put_back && live) {
           const int32_t* table = p.block_tables + static_cast<int64_t>(pc.b) * p.max_blocks;
-          for (int k = pc.s.first + pc.i0 * KEYS; k < min(pc.s.L, pc.s.first + pc.i1 * KEYS); ++k) {
+          for (int k = pc.s.first + pc.i0 * kKeys; k < min(pc.s.L, pc.s.first + pc.i1 * kKeys); ++k) {
             if (k >= lo_most && k < P) {
               k = P - 1;
               continue;
@@ -859,7 +834,6 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
             dst[y] = make_float4(o[4 * y] * inv * svs, o[4 * y + 1] * inv * svs, o[4 * y + 2] * inv * svs, o[4 * y + 3] * inv * svs);
         }
       }
-      if (put_back && !(ok = exchange())) break;  // (the next piece's ancestors are written over these)
       tc::tc_fence_before();
     }
     if (!ok) {

@@ -149,7 +149,7 @@ KVQ_API size_t kvq_tree_workspace_size(int num_q_heads, int num_kv_heads, int he
  * Limits: num_seqs <= 4096; num_kv_heads <= 256; num_q_heads / num_kv_heads
  * <= 8; num_blocks * num_kv_heads * block_size < 2^31; max_blocks_per_seq *
  * block_size < 2^30; num_seqs * num_kv_heads * T * (max_blocks_per_seq / 4 +
- * 4) < 2^31 with T = 1 where num_q_tokens * num_q_heads / num_kv_heads <=
+ * 8) < 2^31 with T = 1 where num_q_tokens * num_q_heads / num_kv_heads <=
  * 128, else 16; beyond them KVQ_ERR_UNSUPPORTED.  num_q_tokens == 0 is a no-op.
  */
 KVQ_API int kvq_tree_attn(const void* q, const int32_t* cu_q_lens, int64_t num_q_tokens,
