@@ -9,8 +9,10 @@ static int launch_tree(const TreeParams& p, const CUtensorMap& tk, const CUtenso
   using SM = TreeSmem<FMT, DH, TS>;
   static DeviceOnce once;
   if (!once.run(current_device(), [] {
-        return cudaFuncSetAttribute(tree_kernel<FMT, DH, TS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::total) ==
-               cudaSuccess;
+        cudaFuncAttributes a;  // (the warps' shares of the registers are counted on those of the launch)
+        return cudaFuncGetAttributes(&a, tree_kernel<FMT, DH, TS>) == cudaSuccess && a.numRegs == kTreeRegs &&
+               cudaFuncSetAttribute(tree_kernel<FMT, DH, TS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::total) ==
+                   cudaSuccess;
       }))
     return KVQ_ERR_CUDA;
   if (launch_pdl(tree_kernel<FMT, DH, TS>, dim3(ctas), dim3(kTreeThreads), SM::total, s, p, tk, tv) != cudaSuccess)

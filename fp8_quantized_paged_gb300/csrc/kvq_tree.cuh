@@ -11,10 +11,10 @@
 // leaves its rows' states in the workspace, which a second, dependent launch merges.  (A last
 // arriver would read a piece of 64 KB for each of, say, 38 CTAs alone.)
 //
-//   warp 4 (producer)  copies a block's K pages, then its V pages, by TMA into a ring of 64 KB
-//   warp 5 (issuer)    one lane: S = Q K^T (M 128, N 64) a block ahead, into two buffers in turn;
-//     when the softmax has made P of one, O += P V with P from tensor memory, V as it lies
-//     (token-major: an MN-major operand)
+//   warps 4, 5 (producers of K, of V)  copy a block's pages by TMA into rings of 32 KB
+//   warp 6 (issuer)    one lane: S = Q K^T (M 128, N 64) a block ahead, into two buffers in turn
+//   warp 7 (issuer)    one lane: O += P V once the softmax has made P of an S, P from tensor memory,
+//     V as it lies (token-major: an MN-major operand)
 //   warps 0-3 (softmax)  thread = row (TMEM lane): mask, running maximum (raised lazily), P over the
 //     S columns that it came from
 // The products run on the codes as they are: no conversion, no registers between memory and the
@@ -48,12 +48,15 @@ namespace kvq {
 namespace tree {
 
 constexpr int kRows = 128;  // rows of a tile (MMA M)
-constexpr int kSoftWarps = 4, kProdWarp = 4, kMmaWarp = 5;
-constexpr int kTreeThreads = 192;
+constexpr int kSoftWarps = 4, kProdWarp = 4, kMmaWarp = 6;
+constexpr int kTreeThreads = 256;
+// Registers of a thread at launch, and of the softmax's and the other 128 while they have their parts.
+constexpr int kTreeRegs = 128, kTreeSoftRegs = 168, kTreeRestRegs = 88;
+static_assert(128 * (kTreeSoftRegs + kTreeRestRegs) <= kTreeThreads * kTreeRegs, "registers");
 constexpr int kTreeCtas = 2;                          // CTAs of an SM
 constexpr int kKeys = 64;                             // keys of a block
 constexpr uint32_t kTmemCols = 256, kOutCol = 128;    // S and P at 0 and 64, O at 128
-constexpr int kRing = 64 * 1024;
+constexpr int kRing = 32 * 1024;  // of K, and of V
 constexpr int kEntries = 1024;  // prefix sums of the plan: of every ceil(B / 1024)th sequence
 constexpr int kSegCost = 4;     // a segment's start and end, in blocks
 constexpr int kMinShare = 4;    // least cost of a CTA's stretch
@@ -103,7 +106,7 @@ struct TreeCfg {
   static constexpr int kSpan = kRow > 128 ? 128 : kRow;   // of a tile's row; wider rows take two tiles side by side
   static constexpr int kPages = kKeys / kBS;
   static constexpr int kTile = kKeys * kRow;              // a block's K or V
-  static constexpr int kSlots = kRing / kTile;            // 4, 8 or 16
+  static constexpr int kSlots = kRing / kTile;            // 2, 4 or 8
   static constexpr int kQTile = kRows * kRow;             // one part of Q
   static constexpr int kQParts = kBf ? 1 : 2;
   static constexpr int kPageBytes = kBS * kRow;
@@ -115,11 +118,11 @@ struct TreeSmem {
   static constexpr int S = C::kSlots;
   static constexpr int q = 0;
   static constexpr int ring = q + C::kQParts * C::kQTile;
-  static constexpr int tsc = ring + kRing;  // per-(token, head) scales, K's and V's, that land with a V
-  static constexpr int bars = tsc + (TS ? S * kKeys * 4 : 0);
-  static constexpr int kBars = 2 * S + 8;
-  static constexpr int misc = bars + kBars * 8;  // tmem address, abort, NaN mark, -, bad[S], issued[S], warp sums
-  static constexpr int anc = misc + (4 + 2 * S + kTreeThreads / 32) * 4;  // [kMaskWords][kRows] ancestors
+  static constexpr int tsc = ring + 2 * kRing;  // per-(token, head) scales, K's and V's, that land with a V
+  static constexpr int bars = tsc + (TS ? 2 * S * kKeys * 4 : 0);
+  static constexpr int kBars = 4 * S + 9;
+  static constexpr int misc = bars + kBars * 8;  // tmem address, abort, NaN mark, bad sequences, bad[2 S], issued[2], warp sums
+  static constexpr int anc = misc + (6 + 2 * S + kTreeThreads / 32) * 4;  // [kMaskWords][kRows] ancestors
   static constexpr int plan = anc + kMaskWords * kRows * 4;
   static constexpr int total = plan + (kEntries + 1) * 4 + 1024;
   static_assert(total <= 113 * 1024, "two CTAs an SM");
@@ -249,27 +252,29 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_u32(smem);
-  // Position 2 g of the stream is the K of the CTA's block g, 2 g + 1 its V; slot: position % S.
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::bars);  // [S] a slot landed
-  uint64_t* empty = full + S;     // [S] read by the matrix steps (commit)
-  uint64_t* sfull = empty + S;    // [2] S of a block written (commit, and the issuer's arrival)
+  // The K (V) of the CTA's block g takes slot g % S of its ring; full and empty: [0, S) K's, [S, 2 S) V's.
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::bars);  // [2 S] a slot landed
+  uint64_t* empty = full + 2 * S;  // [2 S] read by the matrix steps (commit)
+  uint64_t* sfull = empty + 2 * S;  // [2] S of a block written (commit, and the issuer's arrival)
   uint64_t* pfull = sfull + 2;    // [2] P of a block written, O rescaled (4 warps)
   uint64_t* pdone = pfull + 2;    // [2] O += P V of a block done (commit, and the issuer's arrival)
   uint64_t* qready = pdone + 2;   // Q of a piece written (4 warps)
-  uint64_t* fin = qready + 1;     // every matrix step done (commit)
+  uint64_t* fin = qready + 1;     // [2] every S, every PV done (commit)
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + SM::misc);
   volatile uint32_t* tmem_slot = misc;
   volatile uint32_t* abort_flag = misc + 1;
   volatile uint32_t* vnan = misc + 2;   // 1 + the last piece that met a NaN or infinity to put back
-  volatile uint32_t* bad = misc + 4;    // [S] masked pages of block g at [g % S]: rewritten for block
-                                        // g + S, whose K waits for the softmax of block g
-  volatile int32_t* issued = reinterpret_cast<volatile int32_t*>(misc + 4 + S);  // [S] last position
-  volatile int32_t* warp_sum = reinterpret_cast<volatile int32_t*>(misc + 4 + 2 * S);
+  volatile uint32_t* any_bad = misc + 3;  // a sequence has an error
+  volatile uint32_t* bad = misc + 4;    // [2 S] masked pages of block g at [g % 2 S]: rewritten for block
+                                        // g + 2 S, whose K waits for the S of block g + S, which waits
+                                        // for the softmax of block g + S - 2
+  volatile int32_t* issued = reinterpret_cast<volatile int32_t*>(misc + 4 + 2 * S);  // [2] blocks copied
+  volatile int32_t* warp_sum = reinterpret_cast<volatile int32_t*>(misc + 6 + 2 * S);
   uint32_t* anc = reinterpret_cast<uint32_t*>(smem + SM::anc);
   int32_t* plan = reinterpret_cast<int32_t*>(smem + SM::plan);
 
   // A parity wait for phase k of a barrier is sound while it has completed k or k + 1 phases.  The
-  // issuer, the producer and the softmax take their barriers' phases in order, one every other block
+  // issuers, the producers and the softmax take their barriers' phases in order, one every other block
   // (a block; a piece: qready).  The softmax also looks at a V slot's full barrier and at pdone, for
   // some blocks only: all earlier phases of them are complete then, as the S of block g comes after
   // the PV of block g - 2, and the next ones wait for this softmax.  (Not at a K slot's: the next K may
@@ -277,18 +282,20 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
-    for (int i = 0; i < S; ++i) {
+    for (int i = 0; i < 2 * S; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
-      issued[i] = -1;
     }
+    issued[0] = issued[1] = 0;
+    *any_bad = 0u;
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 2);
       mbar_init(&pfull[i], kSoftWarps);
       mbar_init(&pdone[i], 2);
     }
     mbar_init(qready, kSoftWarps);
-    mbar_init(fin, 1);
+    mbar_init(&fin[0], 1);
+    mbar_init(&fin[1], 1);
     *abort_flag = 0u;
     *vnan = 0u;
     fence_mbar_init();
@@ -297,6 +304,7 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
     tma_prefetch_desc(&tmk);
     tma_prefetch_desc(&tmv);
   }
+  __syncthreads();  // (any_bad)
   if (warp == kMmaWarp) tc::tmem_alloc(const_cast<uint32_t*>(tmem_slot), kTmemCols);
   pdl_wait();
   pdl_allow_next();
@@ -314,7 +322,11 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
       sum[y] = 0;
       const int e = tid * each + y;
       if (y < each && e < entries)
-        for (int b = e * per; b < min(p.B, (e + 1) * per); ++b) sum[y] += seq_of(p, b).cost;
+        for (int b = e * per; b < min(p.B, (e + 1) * per); ++b) {
+          const Seq s = seq_of(p, b);
+          sum[y] += s.cost;
+          if (s.bad_q || s.bad_len) *any_bad = 1u;
+        }
       mine += sum[y];
     }
     int incl = mine;
@@ -341,8 +353,9 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
     }
     if (tid == 0) p.ws_rec[cta] = make_int4(0, 0, 0, 0);
   }
-  // sequences without work: errors, and zero rows
-  for (int b = cta; b < p.B; b += gridDim.x) {
+  __syncthreads();
+  // sequences with errors: reported, and zero rows
+  for (int b = cta; *any_bad && b < p.B; b += gridDim.x) {
     const Seq s = seq_of(p, b);
     if (tid == 0 && s.bad_q) flag_status(p.status, KVQ_DEV_BAD_QLEN);
     if (!s.bad_len) continue;
@@ -350,7 +363,6 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
     uint4* row = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(s.q0) * p.Hq * DH);
     for (int64_t i = tid; i < static_cast<int64_t>(s.n) * p.Hq * DH / 8; i += kTreeThreads) row[i] = make_uint4(0u, 0u, 0u, 0u);
   }
-  __syncthreads();
   const uint32_t tmem = *tmem_slot;
   // few blocks go to fewer CTAs
   const int Pe = max(1, min(static_cast<int>(gridDim.x), V / kMinShare));
@@ -367,9 +379,13 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
     return __all_sync(kFull, wait_or_abort(bar, static_cast<uint32_t>(phase & 1), abort_flag));
   };
 
-  if (warp == kProdWarp) {
-    // ------------------------------------------------------------ producer
+  if (warp >= kSoftWarps) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTreeRestRegs));
+  if (warp < kMmaWarp) {
+    // ------------------------------------------------------------ producers: K, V
+    const int t = __shfl_sync(kFull, warp, 0) - kProdWarp;
     constexpr int kAhead = 32 / C::kPages;  // blocks of which the lanes hold the block ids
+    const CUtensorMap* map = t ? &tmv : &tmk;
     Pieces it(plan, p.B, v0, v1);
     Piece pc;
     int g = 0;
@@ -382,102 +398,111 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
         const int page = page0 + C::kPages * i + lane;
         if (page >= pages || i >= pc.i1 + kAhead) return -2;
         const int blk = __ldg(table + page);
-        if (blk < 0 || blk >= p.num_blocks) return -1;
+        if (blk < 0 || blk >= p.num_blocks) {
+          if (page < page0 + C::kPages * pc.i1) flag_status(p.status, KVQ_DEV_BAD_BLOCK);
+          return -1;
+        }
         return (blk * p.Hkv + pc.head) * kBS;
       };
       int rows = row_of(pc.i0), rows_next = row_of(pc.i0 + kAhead);
-      for (int i = pc.i0; i < pc.i1 && ok; ++i, ++g) {
-        const int j = (i - pc.i0) % kAhead;
+      for (int i = pc.i0; i < pc.i1; ++i, ++g) {
+        const int j = (i - pc.i0) % kAhead, s = g % S;
         if (j == 0 && i > pc.i0) {
           rows = rows_next;
           rows_next = row_of(i + kAhead);
         }
-        const int row = __shfl_sync(kFull, rows, C::kPages * j + lane % C::kPages);
-        const bool good = lane < C::kPages && row >= 0;
-        const uint32_t goods = __ballot_sync(kFull, good);
-        if (lane < C::kPages && row == -1) flag_status(p.status, KVQ_DEV_BAD_BLOCK);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int pos = 2 * g + t, s = pos % S;
-          ok = pos < S || wait_w(&empty[s], pos / S - 1);
-          if (__any_sync(kFull, !ok || *abort_flag != 0u)) {
-            if (lane == 0) fail();
-            ok = false;
-            break;
-          }
+        const uint32_t goods = (__ballot_sync(kFull, rows >= 0) >> (C::kPages * j)) & ((1u << C::kPages) - 1u);
+        if (g >= S && !(ok = wait_w(&empty[t * S + s], g / S - 1))) break;
 #ifdef KVQ_TEST_HOOKS
-          if (cta == 0 && pos == p.withhold) continue;  // its full barrier never completes
+        if (cta == 0 && 2 * g + t == p.withhold) continue;  // its full barrier never completes
 #endif
-          if (lane == 0) {
-            if (t == 0) bad[g % S] = ~goods & ((1u << C::kPages) - 1u);
-            issued[s] = pos;
-            if (goods == 0)
-              mbar_arrive(&full[s]);  // nothing to copy
-            else
-              mbar_arrive_expect_tx(&full[s], __popc(goods) * (C::kPageBytes + (TS && t == 1 ? 2 * kBS * 4 : 0)));
-          }
-          __syncwarp();
-          if (good) {
-            uint8_t* dst = smem + SM::ring + s * C::kTile + lane * (kBS * C::kSpan);
-            const CUtensorMap* map = t ? &tmv : &tmk;
-            tma_load_2d(dst, map, 0, row, &full[s]);
-            if (C::kRow > 128) tma_load_2d(dst + kKeys * 128, map, 64, row, &full[s]);
+        uint8_t* dst = smem + SM::ring + t * kRing + s * C::kTile;
+        int row[C::kPages];
+#pragma unroll
+        for (int y = 0; y < C::kPages; ++y) row[y] = __shfl_sync(kFull, rows, C::kPages * j + y);
+        if (tc::elect_one()) {
+          if (t == 0) bad[g % (2 * S)] = ~goods & ((1u << C::kPages) - 1u);
+          issued[t] = g + 1;
+          if (goods == 0)
+            mbar_arrive(&full[t * S + s]);  // nothing to copy
+          else
+            mbar_arrive_expect_tx(&full[t * S + s], __popc(goods) * (C::kPageBytes + (TS && t == 1 ? 2 * kBS * 4 : 0)));
+#pragma unroll
+          for (int y = 0; y < C::kPages; ++y) {
+            if (row[y] < 0) continue;
+            tma_load_2d(dst + y * (kBS * C::kSpan), map, 0, row[y], &full[t * S + s]);
+            if (C::kRow > 128) tma_load_2d(dst + y * (kBS * C::kSpan) + kKeys * 128, map, 64, row[y], &full[t * S + s]);
             if (TS && t == 1) {  // (K's own slot goes on to the next K before the softmax is done)
-              uint8_t* sc = smem + SM::tsc + (g % (S / 2) * 2 * kKeys + lane * kBS) * 4;
-              bulk_load(sc, p.ks + row, kBS * 4, &full[s]);
-              bulk_load(sc + kKeys * 4, p.vs + row, kBS * 4, &full[s]);
+              uint8_t* sc = smem + SM::tsc + (s * 2 * kKeys + y * kBS) * 4;
+              bulk_load(sc, p.ks + row[y], kBS * 4, &full[t * S + s]);
+              bulk_load(sc + kKeys * 4, p.vs + row[y], kBS * 4, &full[t * S + s]);
             }
           }
         }
+        __syncwarp();
       }
     }
+    if (!ok && lane == 0) fail();
   } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ matrix steps
+    // ------------------------------------------------------------ S = Q K^T
     const uint32_t tm = __shfl_sync(kFull, tmem, 0);
     if (tc::elect_one()) {
       const bool qf8 = !BF && p.qs != nullptr;
       const uint32_t id_qk = BF ? tc::idesc_bf16(kRows, kKeys)
                                 : tc::idesc_f8(kRows, kKeys, qf8 ? tc::tc_type(FMT) : tc::kTcE4M3, tc::tc_type(FMT), false, false);
-      const uint32_t id_pv = BF ? tc::idesc_bf16(kRows, DH) | (1u << 16)
-                                : tc::idesc_f8(kRows, DH, tc::kTcE5M2, tc::tc_type(FMT), false, true);
       const int parts = BF || qf8 ? 1 : 2;
       auto wait = [&](uint64_t* bar, int phase) { return wait_or_abort(bar, static_cast<uint32_t>(phase & 1), abort_flag); };
       auto desc = [&](uint32_t a) { return C::kSpan == 64 ? tc::sw64_desc(a) : tc::sw128_desc(a); };
-      // S of block g, over the P that the PV of block g - 2 has read
-      auto qk = [&](int g) {
-        const int ks = 2 * g % S, buf = g & 1;
-        if (!wait(&full[ks], 2 * g / S) || (g > 1 && !wait(&pdone[buf], (g - 2) >> 1))) return false;
-        tc::tc_fence_after();
-        const uint32_t a = sbase + SM::q, bk = sbase + SM::ring + ks * C::kTile;
-#pragma unroll
-        for (int k = 0; k < C::kRow / 32; ++k) {  // 32 bytes of a row a step
-          const uint32_t oa = (k >> 2) * (kRows * 128) + (k & 3) * 32, ob = (k >> 2) * (kKeys * 128) + (k & 3) * 32;
-          if (BF) {
-            tc::mma_f16_ss(tm + buf * kKeys, desc(a + oa), desc(bk + ob), id_qk, k > 0 ? 1u : 0u);
-          } else {
-            tc::mma_f8_ss(tm + buf * kKeys, desc(a + oa), desc(bk + ob), id_qk, k > 0 ? 1u : 0u);
-            if (parts > 1) tc::mma_f8_ss(tm + buf * kKeys, desc(a + C::kQTile + oa), desc(bk + ob), id_qk, 1u);
-          }
-        }
-        mbar_arrive(&sfull[buf]);  // hands on what the K slot's arrival showed (bad)
-        tc::mma_commit(&sfull[buf]);
-        tc::mma_commit(&empty[ks]);
-        return true;
-      };
       Pieces it(plan, p.B, v0, v1);
       Piece pc;
-      int g = 0, piece = 0, next = 0;  // next: the block whose S comes next
+      int g = 0, piece = 0;
       bool ok = true;
       while (ok && it.next(p, pc)) {
-        const int first = g, end = g + pc.i1 - pc.i0;
         if (!(ok = wait(qready, piece++))) break;
-        for (; g < end; ++g) {
-          while (ok && next < end && next <= g + 1) ok = qk(next++);
-          const int vs = (2 * g + 1) % S, buf = g & 1;
-          if (!(ok = ok && wait(&full[vs], (2 * g + 1) / S) && wait(&pfull[buf], g >> 1))) break;
+        for (int i = pc.i0; i < pc.i1; ++i, ++g) {
+          const int s = g % S, buf = g & 1;
+          // (over the P that the PV of block g - 2 has read)
+          if (!(ok = wait(&full[s], g / S) && (g < 2 || wait(&pdone[buf], (g - 2) >> 1)))) break;
           tc::tc_fence_after();
-          const uint32_t bv = sbase + SM::ring + vs * C::kTile, tp = tm + buf * kKeys;
-          const uint32_t more = g > first ? 1u : 0u;
+          const uint32_t a = sbase + SM::q, bk = sbase + SM::ring + s * C::kTile;
+#pragma unroll
+          for (int k = 0; k < C::kRow / 32; ++k) {  // 32 bytes of a row a step
+            const uint32_t oa = (k >> 2) * (kRows * 128) + (k & 3) * 32, ob = (k >> 2) * (kKeys * 128) + (k & 3) * 32;
+            if (BF) {
+              tc::mma_f16_ss(tm + buf * kKeys, desc(a + oa), desc(bk + ob), id_qk, k > 0 ? 1u : 0u);
+            } else {
+              tc::mma_f8_ss(tm + buf * kKeys, desc(a + oa), desc(bk + ob), id_qk, k > 0 ? 1u : 0u);
+              if (parts > 1) tc::mma_f8_ss(tm + buf * kKeys, desc(a + C::kQTile + oa), desc(bk + ob), id_qk, 1u);
+            }
+          }
+          mbar_arrive(&sfull[buf]);  // hands on what the K slot's arrival showed (bad)
+          tc::mma_commit(&sfull[buf]);
+          tc::mma_commit(&empty[s]);
+        }
+      }
+      if (!ok) fail();
+      tc::mma_commit(&fin[0]);
+      if (!mbar_wait(&fin[0], 0u)) fail();
+    }
+  } else {
+    // ------------------------------------------------------------ O += P V
+    const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+    if (tc::elect_one()) {
+      const uint32_t id_pv = BF ? tc::idesc_bf16(kRows, DH) | (1u << 16)
+                                : tc::idesc_f8(kRows, DH, tc::kTcE5M2, tc::tc_type(FMT), false, true);
+      auto wait = [&](uint64_t* bar, int phase) { return wait_or_abort(bar, static_cast<uint32_t>(phase & 1), abort_flag); };
+      auto desc = [&](uint32_t a) { return C::kSpan == 64 ? tc::sw64_desc(a) : tc::sw128_desc(a); };
+      Pieces it(plan, p.B, v0, v1);
+      Piece pc;
+      int g = 0;
+      bool ok = true;
+      while (ok && it.next(p, pc)) {
+        for (int i = pc.i0; i < pc.i1; ++i, ++g) {
+          const int s = g % S, buf = g & 1;
+          if (!(ok = wait(&full[S + s], g / S) && wait(&pfull[buf], g >> 1))) break;
+          tc::tc_fence_after();
+          const uint32_t bv = sbase + SM::ring + kRing + s * C::kTile, tp = tm + buf * kKeys;
+          const uint32_t more = i > pc.i0 ? 1u : 0u;
           if (BF) {
 #pragma unroll
             for (int k = 0; k < kKeys / 16; ++k) {
@@ -497,15 +522,17 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
           }
           mbar_arrive(&pdone[buf]);  // hands on what the softmax warps' arrivals showed (vnan)
           tc::mma_commit(&pdone[buf]);
-          tc::mma_commit(&empty[vs]);
+          tc::mma_commit(&empty[S + s]);
         }
       }
       if (!ok) fail();
-      tc::mma_commit(fin);
-      if (!mbar_wait(fin, 0u)) fail();
+      tc::mma_commit(&fin[1]);
+      if (!mbar_wait(&fin[1], 0u)) fail();
     }
+  }
   } else {
     // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTreeSoftRegs));
     // Lane t of tensor memory is row (t - turn) mod 128: the SM's two CTAs begin at different
     // quarters, each of which is one scheduler's, so that tiles of few rows do not share one.
     const int turn = (tmem & 0xFFFFu) ? 64 : 0;
@@ -632,19 +659,19 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
       const float rise = kRescaleThreshold / lscale;
       for (int i = pc.i0; i < pc.i1; ++i, ++g) {
         const int k0 = pc.s.first + i * kKeys, buf = g & 1;
-        const int vslot = (2 * g + 1) % S;
+        const int vslot = g % S;
         if (!(ok = wait_w(&sfull[buf], g >> 1))) break;
-        const uint32_t bm = bad[g % S];
+        const uint32_t bm = bad[g % (2 * S)];
         const bool edge = bm != 0u || k0 + kKeys > P || k0 < lo_most;
         if (edge || TS)
-          if (!(ok = wait_w(&full[vslot], (2 * g + 1) / S))) break;
+          if (!(ok = wait_w(&full[S + vslot], g / S))) break;
         if (edge) {
           // V's rows that no row sees become zeros; the others lose what is not finite
 #pragma unroll
           for (int y = 0; y < C::kTile / (kSoftWarps * 32 * 16); ++y) {
             const int c = tid + y * kSoftWarps * 32;  // 16 bytes
             const int key = c / (C::kSpan / 16) % kKeys, t = k0 + key;
-            uint4* at = reinterpret_cast<uint4*>(smem + SM::ring + vslot * C::kTile) + c;
+            uint4* at = reinterpret_cast<uint4*>(smem + SM::ring + kRing + vslot * C::kTile) + c;
             if (t >= pc.s.L || (bm >> (key / kBS) & 1u)) {
               *at = make_uint4(0u, 0u, 0u, 0u);
             } else if (t >= P || t < lo_most) {
@@ -661,7 +688,7 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
         tc::tc_fence_after();
         if (some) {
           const uint32_t ts = tm + buf * kKeys;
-          const float* sk = reinterpret_cast<const float*>(smem + SM::tsc) + g % (S / 2) * 2 * kKeys;
+          const float* sk = reinterpret_cast<const float*>(smem + SM::tsc) + vslot * 2 * kKeys;
           const float* sv = sk + kKeys;
           // 64 logits (as raw products), masked
           float x[kKeys];
@@ -840,15 +867,20 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
       tc::tmem_st_wait();
       fail();
     }
+    __syncwarp();
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTreeRegs));
   }
 
   __syncwarp();
   tc::tc_fence_before();
   __syncthreads();
-  // After an abort: wait (bounded) for the copies in flight; the issuer waited for its steps.
-  if (*abort_flag && tid == 0)
-    for (int s = 0; s < S; ++s)
-      if (issued[s] >= 0) mbar_wait(&full[s], static_cast<uint32_t>((issued[s] / S) & 1));
+  // Every softmax warp has let go of its registers.  (A warp that took its own back any earlier
+  // could take them from a softmax warp that waits for them at its start.)
+  if (warp >= kSoftWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTreeRegs));
+  // After an abort: wait (bounded) for the copies in flight; the issuers waited for their steps.
+  if (*abort_flag && tid < 2)
+    for (int g = max(0, issued[tid] - S); g < issued[tid]; ++g)
+      mbar_wait(&full[tid * S + g % S], static_cast<uint32_t>((g / S) & 1));
   __syncthreads();
   if (warp == kMmaWarp) {
     tc::tc_fence_after();
