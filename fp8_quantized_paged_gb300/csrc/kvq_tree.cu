@@ -5,28 +5,27 @@ namespace kvq {
 namespace tree {
 
 template <int FMT, int DH, bool TS>
-static int launch_tree(const TreeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, cudaStream_t s) {
+static int launch_tree(const TreeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, int sms, cudaStream_t s) {
   using SM = TreeSmem<FMT, DH, TS>;
   static DeviceOnce once;
   if (!once.run(current_device(), [] {
-        cudaFuncAttributes a;  // (the warps' shares of the registers are counted on those of the launch)
-        return cudaFuncGetAttributes(&a, tree_kernel<FMT, DH, TS>) == cudaSuccess && a.numRegs == kTreeRegs &&
-               cudaFuncSetAttribute(tree_kernel<FMT, DH, TS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::total) ==
-                   cudaSuccess;
+        return cudaFuncSetAttribute(tree_kernel<FMT, DH, TS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::total) ==
+               cudaSuccess;
       }))
     return KVQ_ERR_CUDA;
   if (launch_pdl(tree_kernel<FMT, DH, TS>, dim3(ctas), dim3(kTreeThreads), SM::total, s, p, tk, tv) != cudaSuccess)
     return KVQ_ERR_CUDA;
-  if (launch_pdl(merge_kernel<DH>, dim3(ctas), dim3(kMergeThreads), 0, s, p, ctas) != cudaSuccess) return KVQ_ERR_CUDA;
+  if (launch_pdl(merge_kernel<DH>, dim3(sms * kMergeCtas), dim3(kMergeThreads), 0, s, p, ctas) != cudaSuccess) return KVQ_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 template <int FMT, bool TS>
-static int launch_tree_dh(const TreeParams& p, int dh, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, cudaStream_t s) {
-  return dh == 128 ? launch_tree<FMT, 128, TS>(p, tk, tv, ctas, s) : launch_tree<FMT, 64, TS>(p, tk, tv, ctas, s);
+static int launch_tree_dh(const TreeParams& p, int dh, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, int sms,
+                          cudaStream_t s) {
+  return dh == 128 ? launch_tree<FMT, 128, TS>(p, tk, tv, ctas, sms, s) : launch_tree<FMT, 64, TS>(p, tk, tv, ctas, sms, s);
 }
 
-static int ctas_of(int sms) { return std::min(kTreeCtas * sms, kMaxCtas); }
+static int ctas_of(int sms) { return std::min(sms, kMaxCtas); }
 
 }  // namespace tree
 }  // namespace kvq
@@ -135,10 +134,10 @@ extern "C" int kvq_tree_attn(const void* q, const int32_t* cu_q_lens, int64_t nu
   if (!make_cache_map(&tk, k_cache, fmt, head_dim, rows) || !make_cache_map(&tv, v_cache, fmt, head_dim, rows))
     return KVQ_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (fmt == KVQ_FMT_BF16) return tree::launch_tree_dh<KVQ_FMT_BF16, false>(p, head_dim, tk, tv, ctas, s);
+  if (fmt == KVQ_FMT_BF16) return tree::launch_tree_dh<KVQ_FMT_BF16, false>(p, head_dim, tk, tv, ctas, sms, s);
   if (fmt == KVQ_FMT_E4M3)
-    return ts ? tree::launch_tree_dh<KVQ_FMT_E4M3, true>(p, head_dim, tk, tv, ctas, s)
-              : tree::launch_tree_dh<KVQ_FMT_E4M3, false>(p, head_dim, tk, tv, ctas, s);
-  return ts ? tree::launch_tree_dh<KVQ_FMT_E5M2, true>(p, head_dim, tk, tv, ctas, s)
-            : tree::launch_tree_dh<KVQ_FMT_E5M2, false>(p, head_dim, tk, tv, ctas, s);
+    return ts ? tree::launch_tree_dh<KVQ_FMT_E4M3, true>(p, head_dim, tk, tv, ctas, sms, s)
+              : tree::launch_tree_dh<KVQ_FMT_E4M3, false>(p, head_dim, tk, tv, ctas, sms, s);
+  return ts ? tree::launch_tree_dh<KVQ_FMT_E5M2, true>(p, head_dim, tk, tv, ctas, sms, s)
+            : tree::launch_tree_dh<KVQ_FMT_E5M2, false>(p, head_dim, tk, tv, ctas, sms, s);
 }

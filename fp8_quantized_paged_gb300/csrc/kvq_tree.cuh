@@ -5,18 +5,22 @@
 //   and node j's ancestors and itself,  K^ = float(code) sK
 //
 // A row is a (node, query head of the group) pair, a tile 128 of them (128 / G nodes) of a
-// sequence and KV head: the M of both products.  A segment is a tile's keys, in blocks of
-// kKeys.  The segments are laid end to end and cut into equal stretches, one a CTA, two CTAs
-// an SM, so that a batch of any lengths keeps all SMs busy to the end; a segment that is cut
-// leaves its rows' states in the workspace, which a second, dependent launch merges.  (A last
-// arriver would read a piece of 64 KB for each of, say, 38 CTAs alone.)
+// sequence and KV head: the M of both products.  A segment is a tile's keys, in blocks of 64.
+// The segments are laid end to end and cut into equal stretches, one a CTA, a CTA an SM, so that a
+// batch of any lengths keeps all SMs busy to the end; a segment that is cut leaves its rows'
+// states in the workspace, which a second, dependent launch merges.  (A last arriver would read a
+// piece of 64 KB of each of, say, 19 CTAs alone.)
 //
-//   warps 4, 5 (producers of K, of V)  copy a block's pages by TMA into rings of 32 KB
-//   warp 6 (issuer)    one lane: S = Q K^T (M 128, N 64) a block ahead, into two buffers in turn
-//   warp 7 (issuer)    one lane: O += P V once the softmax has made P of an S, P from tensor memory,
-//     V as it lies (token-major: an MN-major operand)
-//   warps 0-3 (softmax)  thread = row (TMEM lane): mask, running maximum (raised lazily), P over the
-//     S columns that it came from
+//   warps 8, 9 (producers of K, of V)  copy a block's pages by TMA into rings of 64 KB
+//   warp 10 (issuer)  one lane: S = Q K^T (M 128, N 64), up to four blocks ahead
+//   warp 11 (issuer)  one lane: O += P V (M 128, N dh), V as it lies (token-major: an MN-major operand)
+//   warps 0-3, 4-7 (softmax of the even, of the odd blocks)  thread = row (TMEM lane): mask, running
+//     maximum, P over the S columns that it came from.  The maximum is handed from block to block, a
+//     warp of one group to its other's (m_s): it is wanted before the weights, and changes rarely
+// Tensor memory: four buffers of S and P (64 columns each), O (128), Q twice (64 each: the next
+// piece's is written while this one's is in use).  A chain of S, softmax and PV takes about 4000
+// cycles, of which the matrix steps' and barriers' latencies are most; four blocks in flight hide it.
+// (Two CTAs an SM, with two buffers each, took 2450 cycles for 64 keys of each of both.)
 // The products run on the codes as they are: no conversion, no registers between memory and the
 // tensor cores.  For that Q and P are split into parts that 8 bits hold:
 //   q  2^a q = q1 + q2, E4M3 both, 2^a taking the row's largest to [2^7, 2^8): bf16's 8 bits are
@@ -48,16 +52,14 @@ namespace kvq {
 namespace tree {
 
 constexpr int kRows = 128;  // rows of a tile (MMA M)
-constexpr int kSoftWarps = 4, kProdWarp = 4, kMmaWarp = 6;
-constexpr int kTreeThreads = 256;
-// Registers of a thread at launch, and of the softmax's and the other 128 while they have their parts.
-constexpr int kTreeRegs = 128, kTreeSoftRegs = 168, kTreeRestRegs = 88;
-static_assert(128 * (kTreeSoftRegs + kTreeRestRegs) <= kTreeThreads * kTreeRegs, "registers");
-constexpr int kTreeCtas = 2;                          // CTAs of an SM
+constexpr int kGroupWarps = 4, kSoftWarps = 8, kProdWarp = 8, kMmaWarp = 10;
+constexpr int kTreeThreads = 384;
 constexpr int kKeys = 64;                             // keys of a block
-constexpr uint32_t kTmemCols = 256, kOutCol = 128;    // S and P at 0 and 64, O at 128
-constexpr int kRing = 32 * 1024;  // of K, and of V
+constexpr int kBufs = 4;                              // of S and P
+constexpr uint32_t kTmemCols = 512, kOutCol = 256, kQCol = 384;  // buffers at 0, O at 256, Q at 384 and 448
+constexpr int kRing = 64 * 1024;  // of K, and of V
 constexpr int kEntries = 1024;  // prefix sums of the plan: of every ceil(B / 1024)th sequence
+constexpr int kKept = 256;      // sequences up to which their lengths are kept beside the prefix sums
 constexpr int kSegCost = 4;     // a segment's start and end, in blocks
 constexpr int kMinShare = 4;    // least cost of a CTA's stretch
 constexpr float kBias = 7.f;    // log2 of the factor that the weights carry
@@ -106,8 +108,7 @@ struct TreeCfg {
   static constexpr int kSpan = kRow > 128 ? 128 : kRow;   // of a tile's row; wider rows take two tiles side by side
   static constexpr int kPages = kKeys / kBS;
   static constexpr int kTile = kKeys * kRow;              // a block's K or V
-  static constexpr int kSlots = kRing / kTile;            // 2, 4 or 8
-  static constexpr int kQTile = kRows * kRow;             // one part of Q
+  static constexpr int kSlots = kRing / kTile;            // 4, 8 or 16
   static constexpr int kQParts = kBf ? 1 : 2;
   static constexpr int kPageBytes = kBS * kRow;
 };
@@ -116,16 +117,19 @@ template <int FMT, int DH, bool TS>
 struct TreeSmem {
   using C = TreeCfg<FMT, DH>;
   static constexpr int S = C::kSlots;
-  static constexpr int q = 0;
-  static constexpr int ring = q + C::kQParts * C::kQTile;
+  static constexpr int ring = 0;
   static constexpr int tsc = ring + 2 * kRing;  // per-(token, head) scales, K's and V's, that land with a V
   static constexpr int bars = tsc + (TS ? 2 * S * kKeys * 4 : 0);
-  static constexpr int kBars = 4 * S + 9;
+  static constexpr int kBars = 4 * S + 3 * kBufs + 17;
   static constexpr int misc = bars + kBars * 8;  // tmem address, abort, NaN mark, bad sequences, bad[2 S], issued[2], warp sums
-  static constexpr int anc = misc + (6 + 2 * S + kTreeThreads / 32) * 4;  // [kMaskWords][kRows] ancestors
-  static constexpr int plan = anc + kMaskWords * kRows * 4;
+  // [kRows] running maximum, [4] largest value scale, by quarter of the rows
+  static constexpr int m = misc + (6 + 2 * S + kTreeThreads / 32) * 4;
+  static constexpr int l = (m + (kRows + 4) * 4 + 7) / 8 * 8;  // [2][2][kRows] sums and their maxima, by piece and group
+  static constexpr int ls = l + 4 * kRows * 8;                 // [2][kRows] logits' scales, by piece
+  static constexpr int anc = ls + 2 * kRows * 4;                        // [2][kMaskWords][kRows] ancestors, by group
+  static constexpr int plan = anc + 2 * kMaskWords * kRows * 4;
   static constexpr int total = plan + (kEntries + 1) * 4 + 1024;
-  static_assert(total <= 113 * 1024, "two CTAs an SM");
+  static_assert(total <= 227 * 1024, "shared memory");
 };
 
 // What the plan needs to know of a sequence.
@@ -138,11 +142,10 @@ struct Seq {
   bool bad_q, bad_len;
 };
 
-KVQ_DEVI Seq seq_of(const TreeParams& p, int b) {
+KVQ_DEVI Seq seq_from(const TreeParams& p, int q0, int q1, int L) {
   Seq s;
-  s.q0 = __ldg(p.cu_q + b);
-  const int q1 = __ldg(p.cu_q + b + 1);
-  s.L = __ldg(p.seq_lens + b);
+  s.q0 = q0;
+  s.L = L;
   s.bad_q = s.q0 < 0 || q1 < s.q0 || q1 > p.total_q || q1 - s.q0 > KVQ_TREE_MAX_NODES;
   s.n = s.bad_q ? 0 : q1 - s.q0;
   s.bad_len = s.n > 0 && (s.L < s.n || s.L > p.max_blocks * kBS);
@@ -156,6 +159,15 @@ KVQ_DEVI Seq seq_of(const TreeParams& p, int b) {
     s.cost = s.tiles * p.Hkv * (s.blocks + kSegCost);
   }
   return s;
+}
+
+KVQ_DEVI Seq seq_of(const TreeParams& p, int b) {
+  return seq_from(p, __ldg(p.cu_q + b), __ldg(p.cu_q + b + 1), __ldg(p.seq_lens + b));
+}
+// From the plan, whose words kKept + 3 b .. are q0, q1 and L of sequence b where there are few.
+KVQ_DEVI Seq seq_of(const TreeParams& p, const int32_t* plan, int b) {
+  const int32_t* w = plan + kKept + 3 * b;
+  return p.B <= kKept ? seq_from(p, w[0], w[1], w[2]) : seq_of(p, b);
 }
 
 // A CTA's part of a segment: blocks [i0, i1).
@@ -184,10 +196,10 @@ struct Pieces {
         const int e = find_seq(plan, entries, v);
         b = e * per;
         at = plan[e];
-        s = seq_of(p, b);
+        s = seq_of(p, plan, b);
         while (v >= at + s.cost) {
           at += s.cost;
-          s = seq_of(p, ++b);
+          s = seq_of(p, plan, ++b);
         }
       }
       const int len = s.blocks + kSegCost, seg = (v - at) / len;
@@ -234,15 +246,8 @@ KVQ_DEVI void weight_parts(uint32_t h, uint32_t (&c)[3]) {
   c[2] = hsub2(c[1], c[1] & 0xFF00FF00u) + 0x00800080u;  // (rounds; no carry leaves a half)
 }
 
-// Byte `b` of row r in a tile of swizzled rows; rows past 128 bytes go on in a second tile.
-template <int SPAN>
-KVQ_DEVI uint32_t tile_at(int r, int b) {
-  if (SPAN == 64) return static_cast<uint32_t>(r * 64 + (((b >> 4) ^ ((r >> 1) & 3)) << 4) + (b & 15));
-  return static_cast<uint32_t>((b >> 7) * (kRows * 128) + r * 128 + ((((b & 127) >> 4) ^ (r & 7)) << 4) + (b & 15));
-}
-
 template <int FMT, int DH, bool TS>
-__global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
+__global__ void __launch_bounds__(kTreeThreads, 1)
     tree_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUtensorMap tmk,
                 const __grid_constant__ CUtensorMap tmv) {
   using C = TreeCfg<FMT, DH>;
@@ -255,11 +260,14 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
   // The K (V) of the CTA's block g takes slot g % S of its ring; full and empty: [0, S) K's, [S, 2 S) V's.
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::bars);  // [2 S] a slot landed
   uint64_t* empty = full + 2 * S;  // [2 S] read by the matrix steps (commit)
-  uint64_t* sfull = empty + 2 * S;  // [2] S of a block written (commit, and the issuer's arrival)
-  uint64_t* pfull = sfull + 2;    // [2] P of a block written, O rescaled (4 warps)
-  uint64_t* pdone = pfull + 2;    // [2] O += P V of a block done (commit, and the issuer's arrival)
-  uint64_t* qready = pdone + 2;   // Q of a piece written (4 warps)
-  uint64_t* fin = qready + 1;     // [2] every S, every PV done (commit)
+  uint64_t* sfull = empty + 2 * S;      // [kBufs] S of a block written (commit, and the issuer's arrival)
+  uint64_t* pfull = sfull + kBufs;      // [kBufs] P of a block written, O rescaled (4 warps)
+  uint64_t* pdone = pfull + kBufs;      // [kBufs] O += P V of a block done (commit, and the issuer's arrival)
+  uint64_t* qready = pdone + kBufs;     // [2] Q of a piece written (4 warps)
+  uint64_t* ofree = qready + 2;         // O of a piece read (8 warps)
+  uint64_t* token = ofree + 1;          // [2][4] a block's maximum is in m_s: by group, and quarter of the rows
+  uint64_t* lfull = token + 8;          // [4] a piece's sums of a quarter are in l_s (2 warps)
+  uint64_t* fin = lfull + 4;            // [2] every S, every PV done (commit)
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + SM::misc);
   volatile uint32_t* tmem_slot = misc;
   volatile uint32_t* abort_flag = misc + 1;
@@ -267,18 +275,21 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
   volatile uint32_t* any_bad = misc + 3;  // a sequence has an error
   volatile uint32_t* bad = misc + 4;    // [2 S] masked pages of block g at [g % 2 S]: rewritten for block
                                         // g + 2 S, whose K waits for the S of block g + S, which waits
-                                        // for the softmax of block g + S - 2
+                                        // for the PV of block g + S - 4
   volatile int32_t* issued = reinterpret_cast<volatile int32_t*>(misc + 4 + 2 * S);  // [2] blocks copied
   volatile int32_t* warp_sum = reinterpret_cast<volatile int32_t*>(misc + 6 + 2 * S);
-  uint32_t* anc = reinterpret_cast<uint32_t*>(smem + SM::anc);
+  float* m_s = reinterpret_cast<float*>(smem + SM::m);
+  float* sig_s = m_s + kRows;
+  float2* l_s = reinterpret_cast<float2*>(smem + SM::l);
+  float* ls_s = reinterpret_cast<float*>(smem + SM::ls);
   int32_t* plan = reinterpret_cast<int32_t*>(smem + SM::plan);
 
   // A parity wait for phase k of a barrier is sound while it has completed k or k + 1 phases.  The
-  // issuers, the producers and the softmax take their barriers' phases in order, one every other block
-  // (a block; a piece: qready).  The softmax also looks at a V slot's full barrier and at pdone, for
-  // some blocks only: all earlier phases of them are complete then, as the S of block g comes after
-  // the PV of block g - 2, and the next ones wait for this softmax.  (Not at a K slot's: the next K may
-  // land while a warp is late.)
+  // issuers, the producers and the softmax take their barriers' phases in order.  The softmax also looks
+  // at V's full barriers (edge blocks) and at pdone (where O is rescaled, and at a piece's end), now and
+  // then: all earlier phases are complete then, as the S of block g comes after the PV of block g - 4;
+  // and the next ones come after a block of this group that it has not begun with, as PVs go in order.
+  // (Not at a K slot's: the next K may land while a warp is late.)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
@@ -288,12 +299,16 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
     }
     issued[0] = issued[1] = 0;
     *any_bad = 0u;
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kBufs; ++i) {
       mbar_init(&sfull[i], 2);
-      mbar_init(&pfull[i], kSoftWarps);
+      mbar_init(&pfull[i], kGroupWarps);
       mbar_init(&pdone[i], 2);
     }
-    mbar_init(qready, kSoftWarps);
+    mbar_init(&qready[0], kGroupWarps);
+    mbar_init(&qready[1], kGroupWarps);
+    mbar_init(ofree, kSoftWarps);
+    for (int i = 0; i < 8; ++i) mbar_init(&token[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&lfull[i], 2);
     mbar_init(&fin[0], 1);
     mbar_init(&fin[1], 1);
     *abort_flag = 0u;
@@ -323,7 +338,13 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
       const int e = tid * each + y;
       if (y < each && e < entries)
         for (int b = e * per; b < min(p.B, (e + 1) * per); ++b) {
-          const Seq s = seq_of(p, b);
+          const int q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1), L = __ldg(p.seq_lens + b);
+          const Seq s = seq_from(p, q0, q1, L);
+          if (p.B <= kKept) {
+            plan[kKept + 3 * b] = q0;
+            plan[kKept + 3 * b + 1] = q1;
+            plan[kKept + 3 * b + 2] = L;
+          }
           sum[y] += s.cost;
           if (s.bad_q || s.bad_len) *any_bad = 1u;
         }
@@ -375,13 +396,10 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
       flag_status(p.status, KVQ_DEV_WAIT_TIMEOUT);
     }
   };
-  auto wait_w = [&](uint64_t* bar, int phase) {  // warp-uniform
-    return __all_sync(kFull, wait_or_abort(bar, static_cast<uint32_t>(phase & 1), abort_flag));
-  };
+  auto wait = [&](uint64_t* bar, int phase) { return wait_or_abort(bar, static_cast<uint32_t>(phase & 1), abort_flag); };
+  auto wait_w = [&](uint64_t* bar, int phase) { return __all_sync(kFull, wait(bar, phase)); };  // warp-uniform
 
-  if (warp >= kSoftWarps) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTreeRestRegs));
-  if (warp < kMmaWarp) {
+  if (warp >= kProdWarp && warp < kMmaWarp) {
     // ------------------------------------------------------------ producers: K, V
     const int t = __shfl_sync(kFull, warp, 0) - kProdWarp;
     constexpr int kAhead = 32 / C::kPages;  // blocks of which the lanes hold the block ids
@@ -451,28 +469,29 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
       const uint32_t id_qk = BF ? tc::idesc_bf16(kRows, kKeys)
                                 : tc::idesc_f8(kRows, kKeys, qf8 ? tc::tc_type(FMT) : tc::kTcE4M3, tc::tc_type(FMT), false, false);
       const int parts = BF || qf8 ? 1 : 2;
-      auto wait = [&](uint64_t* bar, int phase) { return wait_or_abort(bar, static_cast<uint32_t>(phase & 1), abort_flag); };
       auto desc = [&](uint32_t a) { return C::kSpan == 64 ? tc::sw64_desc(a) : tc::sw128_desc(a); };
       Pieces it(plan, p.B, v0, v1);
       Piece pc;
       int g = 0, piece = 0;
       bool ok = true;
       while (ok && it.next(p, pc)) {
-        if (!(ok = wait(qready, piece++))) break;
+        if (!(ok = wait(&qready[piece & 1], piece >> 1))) break;
+        const uint32_t a = tm + kQCol + (piece & 1) * 64;
+        ++piece;
         for (int i = pc.i0; i < pc.i1; ++i, ++g) {
-          const int s = g % S, buf = g & 1;
-          // (over the P that the PV of block g - 2 has read)
-          if (!(ok = wait(&full[s], g / S) && (g < 2 || wait(&pdone[buf], (g - 2) >> 1)))) break;
+          const int s = g % S, buf = g % kBufs;
+          // (over the P that the PV of block g - 4 has read)
+          if (!(ok = wait(&full[s], g / S) && (g < kBufs || wait(&pdone[buf], g / kBufs - 1)))) break;
           tc::tc_fence_after();
-          const uint32_t a = sbase + SM::q, bk = sbase + SM::ring + s * C::kTile;
+          const uint32_t bk = sbase + SM::ring + s * C::kTile, d = tm + buf * kKeys;
 #pragma unroll
           for (int k = 0; k < C::kRow / 32; ++k) {  // 32 bytes of a row a step
-            const uint32_t oa = (k >> 2) * (kRows * 128) + (k & 3) * 32, ob = (k >> 2) * (kKeys * 128) + (k & 3) * 32;
+            const uint32_t ob = (k >> 2) * (kKeys * 128) + (k & 3) * 32;
             if (BF) {
-              tc::mma_f16_ss(tm + buf * kKeys, desc(a + oa), desc(bk + ob), id_qk, k > 0 ? 1u : 0u);
+              tc::mma_f16_ts(d, a + 8 * k, desc(bk + ob), id_qk, k > 0 ? 1u : 0u);
             } else {
-              tc::mma_f8_ss(tm + buf * kKeys, desc(a + oa), desc(bk + ob), id_qk, k > 0 ? 1u : 0u);
-              if (parts > 1) tc::mma_f8_ss(tm + buf * kKeys, desc(a + C::kQTile + oa), desc(bk + ob), id_qk, 1u);
+              tc::mma_f8_ts(d, a + 8 * k, desc(bk + ob), id_qk, k > 0 ? 1u : 0u);
+              if (parts > 1) tc::mma_f8_ts(d, a + DH / 4 + 8 * k, desc(bk + ob), id_qk, 1u);
             }
           }
           mbar_arrive(&sfull[buf]);  // hands on what the K slot's arrival showed (bad)
@@ -484,22 +503,23 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
       tc::mma_commit(&fin[0]);
       if (!mbar_wait(&fin[0], 0u)) fail();
     }
-  } else {
+  } else if (warp == kMmaWarp + 1) {
     // ------------------------------------------------------------ O += P V
     const uint32_t tm = __shfl_sync(kFull, tmem, 0);
     if (tc::elect_one()) {
       const uint32_t id_pv = BF ? tc::idesc_bf16(kRows, DH) | (1u << 16)
                                 : tc::idesc_f8(kRows, DH, tc::kTcE5M2, tc::tc_type(FMT), false, true);
-      auto wait = [&](uint64_t* bar, int phase) { return wait_or_abort(bar, static_cast<uint32_t>(phase & 1), abort_flag); };
       auto desc = [&](uint32_t a) { return C::kSpan == 64 ? tc::sw64_desc(a) : tc::sw128_desc(a); };
       Pieces it(plan, p.B, v0, v1);
       Piece pc;
-      int g = 0;
+      int g = 0, piece = 0;
       bool ok = true;
       while (ok && it.next(p, pc)) {
+        if (piece > 0 && !(ok = wait(ofree, piece - 1))) break;
+        ++piece;
         for (int i = pc.i0; i < pc.i1; ++i, ++g) {
-          const int s = g % S, buf = g & 1;
-          if (!(ok = wait(&full[S + s], g / S) && wait(&pfull[buf], g >> 1))) break;
+          const int s = g % S, buf = g % kBufs;
+          if (!(ok = wait(&full[S + s], g / S) && wait(&pfull[buf], g / kBufs))) break;
           tc::tc_fence_after();
           const uint32_t bv = sbase + SM::ring + kRing + s * C::kTile, tp = tm + buf * kKeys;
           const uint32_t more = i > pc.i0 ? 1u : 0u;
@@ -529,96 +549,95 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
       tc::mma_commit(&fin[1]);
       if (!mbar_wait(&fin[1], 0u)) fail();
     }
-  }
   } else {
     // ------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTreeSoftRegs));
-    // Lane t of tensor memory is row (t - turn) mod 128: the SM's two CTAs begin at different
-    // quarters, each of which is one scheduler's, so that tiles of few rows do not share one.
-    const int turn = (tmem & 0xFFFFu) ? 64 : 0;
-    const int t0 = warp * 32 + lane, r = (t0 - turn) & (kRows - 1);
-    const uint32_t tm = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    // The query row of a piece into the Q tile, scaled; its logits' scale.
-    auto write_q = [&](const Piece& pc) {
+    const int group = warp / kGroupWarps, quad = warp % kGroupWarps, r = quad * 32 + lane;
+    const uint32_t tm = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    uint32_t* anc = reinterpret_cast<uint32_t*>(smem + SM::anc) + group * kMaskWords * kRows;
+    // The query rows of piece number n into tensor memory, scaled, and their logits' scales: by the group
+    // n % 2, while the piece before is worked on.
+    auto write_q = [&](const Piece& pc, int n) {
       const int TQ = kRows / p.G, j0 = pc.tile * TQ, rows = min(pc.s.n - j0, TQ) * p.G;
       float lscale = (BF || TS ? 1.f : __ldg(p.ks + (p.per_head ? pc.head : 0))) * p.logit_scale;
-      if (r < rows) {
-        const int hq = pc.head * p.G + r % p.G;
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + ((static_cast<int64_t>(pc.s.q0) + j0 + r / p.G) * p.Hq + hq) * DH);
-        uint4 w[DH / 8];
-#pragma unroll
-        for (int c = 0; c < DH / 8; ++c) w[c] = __ldg(src + c);
+      if (quad * 32 < rows) {
+        const bool live = r < rows;
+        const int at = live ? r : 0, hq = pc.head * p.G + at % p.G;
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + ((static_cast<int64_t>(pc.s.q0) + j0 + at / p.G) * p.Hq + hq) * DH);
+        const uint32_t to = tm + kQCol + (n & 1) * 64;
+        // (Loops of few instructions: code that runs once a piece is fetched as slowly as data.  With all
+        // 128 dims unrolled a piece's start took 9000 to 19000 cycles.)
         if (BF) {
-#pragma unroll
-          for (int c = 0; c < DH / 8; ++c) tc::sts128(sbase + SM::q + tile_at<C::kSpan>(t0, 16 * c), w[c].x, w[c].y, w[c].z, w[c].w);
-        } else if (p.qs) {
-          constexpr int F = FMT == KVQ_FMT_E5M2 ? KVQ_FMT_E5M2 : KVQ_FMT_E4M3;
-          const float sq = __ldg(p.qs + (p.q_per_head ? hq : 0));
-          lscale *= sq;
-#pragma unroll
-          for (int c = 0; c < DH / 16; ++c) {
-            uint32_t code[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint4& v = w[2 * c + (e >> 1)];
-              const uint32_t u0 = e & 1 ? v.z : v.x, u1 = e & 1 ? v.w : v.y;
-              code[e] = f32x2_to_fp8x2<F>(__fdiv_rn(bf16lo_to_f32(u0), sq), __fdiv_rn(bf16hi_to_f32(u0), sq)) |
-                        (static_cast<uint32_t>(f32x2_to_fp8x2<F>(__fdiv_rn(bf16lo_to_f32(u1), sq), __fdiv_rn(bf16hi_to_f32(u1), sq))) << 16);
-            }
-            tc::sts128(sbase + SM::q + tile_at<C::kSpan>(t0, 16 * c), code[0], code[1], code[2], code[3]);
+#pragma unroll 4
+          for (int c = 0; c < DH / 8; ++c) {
+            const uint4 w = __ldg(src + c);
+            tc::tmem_st4(to + 4 * c, w.x, w.y, w.z, w.w);
           }
         } else {
-          float amax = 0.f;
-#pragma unroll
-          for (int c = 0; c < DH / 8; ++c) {
-            const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16lo_to_f32(u[e])), fabsf(bf16hi_to_f32(u[e]))));
+          float by = 1.f;  // what the row's values are multiplied (KVQ_Q_FP8: divided) by
+          if (p.qs) {
+            by = __ldg(p.qs + (p.q_per_head ? hq : 0));
+            lscale *= by;
+          } else {
+            uint32_t top = 0u;  // of the magnitudes' bits
+#pragma unroll 8
+            for (int c = 0; c < DH / 8; ++c) {
+              const uint4 w = __ldg(src + c);
+              top = __vmaxu2(__vmaxu2(__vmaxu2(top, w.x & 0x7FFF7FFFu), __vmaxu2(w.y & 0x7FFF7FFFu, w.z & 0x7FFF7FFFu)), w.w & 0x7FFF7FFFu);
+            }
+            const int e = static_cast<int>(max(top & 0xFFFFu, top >> 16) >> 7);  // its exponent, 0 for subnormals
+            const int a = top == 0u ? 0 : min(126, 134 - max(e, 8));  // (-121 .. 126)
+            by = __int_as_float((a + 127) << 23);  // exact: a power of two, no overflow
+            lscale *= __int_as_float((127 - a) << 23);
           }
-          int a = 0;
-          if (amax > 0.f) {
-            a = 7 - (static_cast<int>((__float_as_uint(amax) >> 23) & 0xFFu) - 127);
-            a = a > 126 ? 126 : (a < -126 ? -126 : a);
-          }
-          const float up = __int_as_float((a + 127) << 23);  // exact: a power of two, no overflow
-          lscale *= __int_as_float((127 - a) << 23);
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < DH / 16; ++c) {
             uint32_t hi[4], lo[4];
+            const uint4 w[2] = {__ldg(src + 2 * c), __ldg(src + 2 * c + 1)};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const uint4& v = w[2 * c + (e >> 1)];
+              const uint4& v = w[e >> 1];
               const uint32_t u0 = e & 1 ? v.z : v.x, u1 = e & 1 ? v.w : v.y;
-              const float x[4] = {bf16lo_to_f32(u0) * up, bf16hi_to_f32(u0) * up, bf16lo_to_f32(u1) * up, bf16hi_to_f32(u1) * up};
-              const uint32_t c0 = f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[0], x[1]), c1 = f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[2], x[3]);
-              const uint32_t h0 = fp8x2_to_f16x2<KVQ_FMT_E4M3>(static_cast<uint16_t>(c0));
-              const uint32_t h1 = fp8x2_to_f16x2<KVQ_FMT_E4M3>(static_cast<uint16_t>(c1));
-              hi[e] = c0 | (c1 << 16);
-              lo[e] = f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[0] - f16lo_to_f32(h0), x[1] - f16hi_to_f32(h0)) |
-                      (static_cast<uint32_t>(f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[2] - f16lo_to_f32(h1), x[3] - f16hi_to_f32(h1))) << 16);
+              float x[4] = {bf16lo_to_f32(u0), bf16hi_to_f32(u0), bf16lo_to_f32(u1), bf16hi_to_f32(u1)};
+              if (p.qs) {
+                constexpr int F = FMT == KVQ_FMT_E5M2 ? KVQ_FMT_E5M2 : KVQ_FMT_E4M3;
+#pragma unroll 1
+                for (int z = 0; z < 4; ++z) x[z] = __fdiv_rn(x[z], by);
+                hi[e] = f32x2_to_fp8x2<F>(x[0], x[1]) | (static_cast<uint32_t>(f32x2_to_fp8x2<F>(x[2], x[3])) << 16);
+                lo[e] = 0u;
+              } else {
+#pragma unroll
+                for (int z = 0; z < 4; ++z) x[z] *= by;
+                const uint32_t c0 = f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[0], x[1]), c1 = f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[2], x[3]);
+                const uint32_t h0 = fp8x2_to_f16x2<KVQ_FMT_E4M3>(static_cast<uint16_t>(c0));
+                const uint32_t h1 = fp8x2_to_f16x2<KVQ_FMT_E4M3>(static_cast<uint16_t>(c1));
+                hi[e] = c0 | (c1 << 16);
+                lo[e] = f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[0] - f16lo_to_f32(h0), x[1] - f16hi_to_f32(h0)) |
+                        (static_cast<uint32_t>(f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[2] - f16lo_to_f32(h1), x[3] - f16hi_to_f32(h1))) << 16);
+              }
             }
-            const uint32_t at = sbase + SM::q + tile_at<C::kSpan>(t0, 16 * c);
-            tc::sts128(at, hi[0], hi[1], hi[2], hi[3]);
-            tc::sts128(at + C::kQTile, lo[0], lo[1], lo[2], lo[3]);
+            tc::tmem_st4(to + 4 * c, hi[0], hi[1], hi[2], hi[3]);
+            if (!p.qs) tc::tmem_st4(to + DH / 4 + 4 * c, lo[0], lo[1], lo[2], lo[3]);
           }
         }
-        fence_proxy_async_smem();
+        ls_s[(n & 1) * kRows + r] = fp4::bounded_scale(lscale);
+        tc::tmem_st_wait();
       }
+      tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(qready);
-      return fp4::bounded_scale(lscale);
+      if (lane == 0) mbar_arrive(&qready[n & 1]);
     };
     Pieces it(plan, p.B, v0, v1);
     Piece nx;
     int g = 0, piece = 0;
     bool ok = true, more = it.next(p, nx);
-    float lscale_nx = more ? write_q(nx) : 1.f;
+    if (more && group == 0) write_q(nx, 0);
     while (more) {
       const Piece pc = nx;
-      const float lscale = lscale_nx;
+      more = it.next(p, nx);
+      if (more && group == ((piece + 1) & 1)) write_q(nx, piece + 1);  // (the S of the piece before are done)
       const int TQ = kRows / p.G, j0 = pc.tile * TQ;
       const int rows = min(pc.s.n - j0, TQ) * p.G;
-      const bool live = r < rows, some = ((warp * 32 - turn) & (kRows - 1)) < rows;
+      const bool live = r < rows, some = quad * 32 < rows;
       const int node = j0 + (live ? r / p.G : 0);
       const int P = pc.s.L - pc.s.n;  // tokens before the tree
       // ---- the row's ancestors, and the first token that it sees
@@ -626,10 +645,10 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
       if (live && (p.window > 0 || pc.s.first + pc.i1 * kKeys > P)) {
         const int far = p.window > 0 ? p.window : INT_MAX;
 #pragma unroll
-        for (int w = 0; w < kMaskWords; ++w) anc[w * kRows + t0] = 0u;
+        for (int w = 0; w < kMaskWords; ++w) anc[w * kRows + r] = 0u;
         int depth = -1;
         for (int at = node; at >= 0; ++depth) {
-          if (depth + 1 < far) anc[(at >> 5) * kRows + t0] |= 1u << (at & 31);
+          if (depth + 1 < far) anc[(at >> 5) * kRows + r] |= 1u << (at & 31);
           int up = at - 1;
           if (p.parents) {
             up = __ldg(p.parents + pc.s.q0 + at);
@@ -650,17 +669,19 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
         const int i = k - P;  // the first key's node
         if (i > -32 && i < KVQ_TREE_MAX_NODES) {
           const int w = i >> 5;
-          const uint32_t a = w >= 0 ? anc[w * kRows + t0] : 0u, z = w + 1 < kMaskWords ? anc[(w + 1) * kRows + t0] : 0u;
+          const uint32_t a = w >= 0 ? anc[w * kRows + r] : 0u, z = w + 1 < kMaskWords ? anc[(w + 1) * kRows + r] : 0u;
           s |= __funnelshift_r(a, z, i & 31);
         }
         return s & ~((bm & 1u ? 0xFFFFu : 0u) | (bm & 2u ? 0xFFFF0000u : 0u));
       };
-      float m = -INFINITY, l = 0.f, sig = 0.f;
-      const float rise = kRescaleThreshold / lscale;
+      float m = -INFINITY, l = 0.f, sig = 0.f, lscale = 1.f;
+      const int last = g + pc.i1 - pc.i0 - 1;  // the piece's last block
       for (int i = pc.i0; i < pc.i1; ++i, ++g) {
-        const int k0 = pc.s.first + i * kKeys, buf = g & 1;
+        if ((g & 1) != group) continue;
+        const int k0 = pc.s.first + i * kKeys, buf = g % kBufs;
         const int vslot = g % S;
-        if (!(ok = wait_w(&sfull[buf], g >> 1))) break;
+        if (!(ok = wait_w(&sfull[buf], g / kBufs))) break;
+        lscale = ls_s[(piece & 1) * kRows + r];
         const uint32_t bm = bad[g % (2 * S)];
         const bool edge = bm != 0u || k0 + kKeys > P || k0 < lo_most;
         if (edge || TS)
@@ -668,8 +689,8 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
         if (edge) {
           // V's rows that no row sees become zeros; the others lose what is not finite
 #pragma unroll
-          for (int y = 0; y < C::kTile / (kSoftWarps * 32 * 16); ++y) {
-            const int c = tid + y * kSoftWarps * 32;  // 16 bytes
+          for (int y = 0; y < C::kTile / (kGroupWarps * 32 * 16); ++y) {
+            const int c = r + y * kGroupWarps * 32;  // 16 bytes
             const int key = c / (C::kSpan / 16) % kKeys, t = k0 + key;
             uint4* at = reinterpret_cast<uint4*>(smem + SM::ring + kRing + vslot * C::kTile) + c;
             if (t >= pc.s.L || (bm >> (key / kBS) & 1u)) {
@@ -718,7 +739,14 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
 #pragma unroll
             for (int y = 0; y < 4; ++y) mx4[y] = tc::fmax3(mx4[y], x[e + 2 * y], x[e + 2 * y + 1]);
           const float mx = tc::fmax3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]);
-          const bool grow = mx > m + rise;
+          // what the block before left (with a first block: nothing)
+          if (g > 0 && !(ok = wait_w(&token[(group ^ 1) * 4 + quad], (g - 1) >> 1))) break;
+          const float before = i > pc.i0 ? m_s[r] : -INFINITY;
+          const bool grow = mx > before + kRescaleThreshold / lscale;
+          if (m != before) {  // (the other group raised it)
+            l *= m == -INFINITY ? 0.f : fast_exp2((m - before) * lscale);
+            m = before;
+          }
           float fs = 1.f;
           if (TS) {  // the largest value scale of the block's tokens, to a power of two
             float s = 0.f;
@@ -730,6 +758,7 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) s = fmaxf(s, __shfl_xor_sync(kFull, s, off));
             s = __uint_as_float(min((__float_as_uint(s) + 0x7FFFFFu) & 0x7F800000u, 0x7E800000u));
+            sig = i > pc.i0 ? sig_s[quad] : 0.f;
             if (s > sig) {
               fs = sig / s;
               sig = s;
@@ -738,7 +767,7 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
           if (__any_sync(kFull, grow) || (TS && fs != 1.f)) {
             const float a = m == -INFINITY ? 0.f : fast_exp2((m - mx) * lscale);
             if (i > pc.i0) {  // O's last writer: the PV of the block before
-              if (!(ok = wait_w(&pdone[buf ^ 1], (g - 1) >> 1))) break;
+              if (!(ok = wait_w(&pdone[(g - 1) % kBufs], (g - 1) / kBufs))) break;
               tc::tc_fence_after();
               const float f = (grow ? a : 1.f) * fs;
 #pragma unroll 1
@@ -755,6 +784,10 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
               m = mx;
             }
           }
+          m_s[r] = m;
+          if (TS && lane == 0) sig_s[quad] = sig;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&token[group * 4 + quad]);
           const float fm = m == -INFINITY ? 0.f : -m;
           const float inv_sig = TS && sig > 0.f ? 1.f / sig : 0.f;
           const tc::f32x2 fm2 = tc::f32x2_pack(fm, fm), ls2 = tc::f32x2_pack(lscale, lscale), b2 = tc::f32x2_pack(kBias, kBias);
@@ -802,29 +835,39 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
           tc::f32x2_unpack(tc::f32x2_add(l2[0], l2[1]), l0, l1);
           l += l0 + l1;
           tc::tmem_st_wait();
+        } else {  // (tokens count blocks)
+          if (g > 0 && !(ok = wait_w(&token[(group ^ 1) * 4 + quad], (g - 1) >> 1))) break;
+          if (lane == 0) mbar_arrive(&token[group * 4 + quad]);
         }
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[buf]);
       }
       if (!ok) break;
-      // ---- the piece's end: the next one's Q (all of this one's S are done), and the rows of O, normalised
-      more = it.next(p, nx);
-      if (more) lscale_nx = write_q(nx);
-      if (!(ok = wait_w(&pdone[(g - 1) & 1], (g - 1) >> 1))) break;
+      // ---- the piece's end: rows of O, normalised, half of the dims by each group
+      if (!(ok = wait_w(&pdone[last % kBufs], last / kBufs))) break;
       tc::tc_fence_after();
       if (tid == 0 && !pc.whole() && pc.i0 == 0)
         p.ws_rec[cta] = make_int4(rows, split.cta_of(pc.base + kSegCost + pc.s.blocks - 1), pc.s.q0 + j0, pc.head);
       const bool put_back = *vnan == 1u + piece;
+      // a group's sum is relative to the maximum of its last block, O to that of the last one
+      float2* sums = l_s + (piece & 1) * 2 * kRows;
+      sums[group * kRows + r] = make_float2(l, m);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&lfull[quad]);
+      if (!(ok = wait_w(&lfull[quad], piece))) break;
       ++piece;
-      if (!some) continue;
-      const float svs = TS ? sig : BF ? 1.f : __ldg(p.vs + (p.per_head ? pc.head : 0));
+      const int owner = last & 1;
+      const float2 own = sums[owner * kRows + r], other = sums[(owner ^ 1) * kRows + r];
+      l = own.x + other.x * (other.y == -INFINITY || other.y == own.y ? 1.f : fast_exp2((other.y - own.y) * lscale));
+      const float svs = TS ? sig_s[quad] : BF ? 1.f : __ldg(p.vs + (p.per_head ? pc.head : 0));
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
       const int64_t part = static_cast<int64_t>(2 * cta + (pc.i0 == 0)) * kRows + r;
       const int64_t qrow = (static_cast<int64_t>(pc.s.q0) + node) * p.Hq + pc.head * p.G + r % p.G;
-      if (!pc.whole() && live) p.ws_ml[part] = make_float2(fp4::merge_max(m, lscale), l);
+      if (!pc.whole() && live && group == owner) p.ws_ml[part] = make_float2(fp4::merge_max(m, lscale), l);
+      if (some) {
 #pragma unroll 1
-      for (int c = 0; c < DH; c += 32) {
+      for (int c = group * (DH / 2); c < (group + 1) * (DH / 2); c += 32) {
         float o[32];
         tc::tmem_ld32(tm + kOutCol + c, o);
         if (put_back && live) {
@@ -861,22 +904,20 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
             dst[y] = make_float4(o[4 * y] * inv * svs, o[4 * y + 1] * inv * svs, o[4 * y + 2] * inv * svs, o[4 * y + 3] * inv * svs);
         }
       }
+      }
       tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ofree);
     }
     if (!ok) {
       tc::tmem_st_wait();
       fail();
     }
-    __syncwarp();
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTreeRegs));
   }
 
   __syncwarp();
   tc::tc_fence_before();
   __syncthreads();
-  // Every softmax warp has let go of its registers.  (A warp that took its own back any earlier
-  // could take them from a softmax warp that waits for them at its start.)
-  if (warp >= kSoftWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTreeRegs));
   // After an abort: wait (bounded) for the copies in flight; the issuers waited for their steps.
   if (*abort_flag && tid < 2)
     for (int g = max(0, issued[tid] - S); g < issued[tid]; ++g)
@@ -888,14 +929,16 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeCtas)
   }
 }
 
-// ---- the rows of segments that were cut: a warp a row.  A piece's state is (maximum, sum,
-// normalised row); the rows add with weights sum 2^maximum.
-constexpr int kMergeThreads = 256;
+// ---- the rows of segments that were cut: half a warp a row.  A piece's state is (maximum, sum,
+// normalised row); the rows add with weights sum 2^maximum.  Chains of loads (record, states, rows) that
+// nothing but many rows at once hides.
+constexpr int kMergeThreads = 256, kMergeCtas = 5;  // CTAs of an SM
 constexpr int kMaxCtas = 512;
 
 template <int DH>
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ TreeParams p, int ctas) {
+__global__ void __launch_bounds__(kMergeThreads, kMergeCtas) merge_kernel(const __grid_constant__ TreeParams p, int ctas) {
   __shared__ int off[kMaxCtas + 1];
+  __shared__ int4 recs[kMaxCtas];
   __shared__ int warp_sum[kMergeThreads / 32];
   pdl_wait();
   pdl_allow_next();
@@ -905,7 +948,9 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
 #pragma unroll
   for (int y = 0; y < kPer; ++y) {
     const int c = kPer * tid + y;
-    rows[y] = c < ctas ? __ldcg(p.ws_rec + c).x : 0;
+    const int4 rec = c < ctas ? __ldcg(p.ws_rec + c) : make_int4(0, 0, 0, 0);
+    recs[c] = rec;
+    rows[y] = rec.x;
     mine += rows[y];
   }
   int incl = mine;
@@ -926,60 +971,56 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
     off[kPer * tid + y] = at;
     at += rows[y];
   }
-  if (tid == 0) off[kMaxCtas] = total;
   __syncthreads();
-  constexpr int E = DH / 32;  // values of a lane
-  for (int x = blockIdx.x * (kMergeThreads / 32) + warp; x < total; x += gridDim.x * (kMergeThreads / 32)) {
+  constexpr int E = DH / 16;  // values of a lane, in runs of 4
+  const int l16 = lane & 15;
+  const uint32_t half = 0xFFFFu << (lane & 16);
+  for (int x = blockIdx.x * (kMergeThreads / 16) + (tid >> 4); x < total; x += gridDim.x * (kMergeThreads / 16)) {
     const int c0 = find_seq(off, kMaxCtas, x), r = x - off[c0];
-    const int4 rec = __ldcg(p.ws_rec + c0);
+    const int4 rec = recs[c0];
     const int n = rec.y - c0 + 1;  // pieces
     auto part = [&](int y) { return static_cast<int64_t>(2 * (c0 + y) + (y == 0)) * kRows + r; };
     float M = -INFINITY, L = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int y0 = 0; y0 < n; y0 += 32) {
+    for (int y0 = 0; y0 < n; y0 += 16) {
       float2 ml = make_float2(-INFINITY, 0.f);
-      if (y0 + lane < n) ml = __ldcg(p.ws_ml + part(y0 + lane));
+      if (y0 + l16 < n) ml = __ldcg(p.ws_ml + part(y0 + l16));
       float nm = ml.x;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(kFull, nm, o));
+      for (int o = 8; o > 0; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(half, nm, o));
       nm = fmaxf(nm, M);
       const float a = M == -INFINITY ? 0.f : fast_exp2((M - nm) * fp4::kMergeUnit);
       // (a piece without a maximum has a sum of 0, or a NaN, which stays)
       const float w = ml.y * (ml.x == -INFINITY ? 1.f : fast_exp2((ml.x - nm) * fp4::kMergeUnit));
       float sum = w;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(half, sum, o);
       L = L * a + sum;
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] *= a;
       M = nm;
-      const int k = min(32, n - y0);
-#pragma unroll 8
+      const int k = min(16, n - y0);
+#pragma unroll 4
       for (int y = 0; y < k; ++y) {
-        const float wy = __shfl_sync(kFull, w, y);
-        const float* o = p.ws_o + part(y0 + y) * DH + E * lane;
-        float v[E];
-        if (E == 4) {
-          const float4 f = __ldcg(reinterpret_cast<const float4*>(o));
-          v[0] = f.x;
-          v[1] = f.y;
-          v[E - 2] = f.z;
-          v[E - 1] = f.w;
-        } else {
-          const float2 f = __ldcg(reinterpret_cast<const float2*>(o));
-          v[0] = f.x;
-          v[1] = f.y;
-        }
+        const float wy = __shfl_sync(half, w, (lane & 16) + y);
+        const float4* o = reinterpret_cast<const float4*>(p.ws_o + part(y0 + y) * DH) + l16;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(wy, v[e], acc[e]);
+        for (int e = 0; e < E / 4; ++e) {
+          const float4 f = __ldcg(o + 16 * e);
+          acc[4 * e] = fmaf(wy, f.x, acc[4 * e]);
+          acc[4 * e + 1] = fmaf(wy, f.y, acc[4 * e + 1]);
+          acc[4 * e + 2] = fmaf(wy, f.z, acc[4 * e + 2]);
+          acc[4 * e + 3] = fmaf(wy, f.w, acc[4 * e + 3]);
+        }
       }
     }
     const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-    uint16_t* dst = p.out + ((static_cast<int64_t>(rec.z) + r / p.G) * p.Hq + rec.w * p.G + r % p.G) * DH + E * lane;
-    uint32_t* d32 = reinterpret_cast<uint32_t*>(dst);
+    uint2* dst = reinterpret_cast<uint2*>(p.out + ((static_cast<int64_t>(rec.z) + r / p.G) * p.Hq + rec.w * p.G + r % p.G) * DH) + l16;
 #pragma unroll
-    for (int e = 0; e < E; e += 2) d32[e / 2] = f32x2_to_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    for (int e = 0; e < E / 4; ++e)
+      dst[16 * e] = make_uint2(f32x2_to_bf16x2(acc[4 * e] * inv, acc[4 * e + 1] * inv),
+                               f32x2_to_bf16x2(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv));
   }
 }
 
