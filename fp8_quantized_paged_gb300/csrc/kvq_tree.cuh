@@ -404,6 +404,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const int t = __shfl_sync(kFull, warp, 0) - kProdWarp;
     constexpr int kAhead = 32 / C::kPages;  // blocks of which the lanes hold the block ids
     const CUtensorMap* map = t ? &tmv : &tmk;
+    const uint64_t policy = l2_evict_first_policy();  // (what is read once does not push out the queries, states and code)
     Pieces it(plan, p.B, v0, v1);
     Piece pc;
     int g = 0;
@@ -448,8 +449,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
           for (int y = 0; y < C::kPages; ++y) {
             if (row[y] < 0) continue;
-            tma_load_2d(dst + y * (kBS * C::kSpan), map, 0, row[y], &full[t * S + s]);
-            if (C::kRow > 128) tma_load_2d(dst + y * (kBS * C::kSpan) + kKeys * 128, map, 64, row[y], &full[t * S + s]);
+            tma_load_2d_hint(dst + y * (kBS * C::kSpan), map, 0, row[y], &full[t * S + s], policy);
+            if (C::kRow > 128) tma_load_2d_hint(dst + y * (kBS * C::kSpan) + kKeys * 128, map, 64, row[y], &full[t * S + s], policy);
             if (TS && t == 1) {  // (K's own slot goes on to the next K before the softmax is done)
               uint8_t* sc = smem + SM::tsc + (s * 2 * kKeys + y * kBS) * 4;
               bulk_load(sc, p.ks + row[y], kBS * 4, &full[t * S + s]);
