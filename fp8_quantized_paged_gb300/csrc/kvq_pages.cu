@@ -29,6 +29,7 @@ struct Caches {
 
 struct CommitParams {
   int caches, B, hkv, max_blocks, max_path, first;  // first: this launch writes new_lens
+  int shares;                                       // of a cache's heads, each a warp's
   int64_t num_blocks;
   const int32_t* cu_q;
   const int32_t* tables;
@@ -41,11 +42,11 @@ struct CommitParams {
 
 constexpr int kUnits = 8;  // 16-byte (4-byte) units that a lane has in flight
 
-// Rows [i0, i0 + c) of the path in every head, a T a unit: all of a head's rows are read before
+// Rows [i0, i0 + c) of the path in heads [head0, head1), a T a unit: all of a head's rows are read before
 // the first is written.  A path rises, so rows of later chunks come from at or behind their own places.
 template <typename T>
 KVQ_DEVI void move_rows(const CommitParams& p, uint8_t* data, int64_t page_bytes, int part_off, int row_bytes,
-                        const int32_t* path, const int32_t* table, int before, int taken) {
+                        const int32_t* path, const int32_t* table, int before, int taken, int head0, int head1) {
   const int lane = threadIdx.x & 31;
   const int u = row_bytes / static_cast<int>(sizeof(T));  // units of a row
   if (u == 0) return;
@@ -53,8 +54,8 @@ KVQ_DEVI void move_rows(const CommitParams& p, uint8_t* data, int64_t page_bytes
   for (int i0 = 0; i0 < taken; i0 += most) {
     const int c = min(most, taken - i0), per_head = c * u;
     const int hb = max(1, 32 * kUnits / per_head);  // heads of a batch
-    for (int h0 = 0; h0 < p.hkv; h0 += hb) {
-      const int n = min(hb, p.hkv - h0) * per_head;
+    for (int h0 = head0; h0 < head1; h0 += hb) {
+      const int n = min(hb, head1 - h0) * per_head;
       T val[kUnits];
       T* dst[kUnits];
 #pragma unroll
@@ -63,7 +64,7 @@ KVQ_DEVI void move_rows(const CommitParams& p, uint8_t* data, int64_t page_bytes
         dst[y] = nullptr;
         if (x >= n) continue;
         const int h = x / per_head, r = (x - h * per_head) / u, e = x % u, i = i0 + r;
-        const int from = path[i];
+        const int from = __ldg(path + i);
         if (from == i) continue;  // in its place already
         const int s = before + from, d = before + i;
         const int ps = __ldg(table + s / kTok), pd = __ldg(table + d / kTok);
@@ -86,17 +87,20 @@ KVQ_DEVI void move_rows(const CommitParams& p, uint8_t* data, int64_t page_bytes
   }
 }
 
-// A warp takes a sequence and a cache, all heads: 4 KB of rows in flight behind one chain of
-// lengths, path and table.
+// A warp takes a sequence and a share of a cache's heads: up to 4 KB of rows in flight behind one
+// chain of lengths, path and table (some 4 us with the launch).  Heads are shared out until the GPU's
+// warps are taken: with all of a cache's heads to a warp, 32 sequences' paths in 32 caches of 8 heads
+// took 8.9 us, several chains' time at 7 warps an SM; shared out COMMIT_US.
 __global__ void __launch_bounds__(128) commit_kernel(const __grid_constant__ CommitParams p,
                                                      const __grid_constant__ Caches cs) {
   pdl_wait();
   pdl_allow_next();
   const int lane = threadIdx.x & 31;
-  const int per = max(1, p.caches);
+  const int per = max(1, p.caches * p.shares);
   const int64_t items = static_cast<int64_t>(p.B) * per, warps = static_cast<int64_t>(gridDim.x) * 4;
   for (int64_t it = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5); it < items; it += warps) {
-    const int b = static_cast<int>(it / per), c = static_cast<int>(it - static_cast<int64_t>(b) * per);
+    const int b = static_cast<int>(it / per), at = static_cast<int>(it - static_cast<int64_t>(b) * per);
+    const int c = at / p.shares, share = at - c * p.shares;
     const int L = __ldg(p.seq_lens + b), q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1);
     const int taken = __ldg(p.taken + b);
     const int32_t* path = p.path + static_cast<int64_t>(b) * p.max_path;
@@ -107,13 +111,13 @@ __global__ void __launch_bounds__(128) commit_kernel(const __grid_constant__ Com
     if (good && !bad_q && !bad_len) {
       bool rises = true;
       for (int i = lane; i < taken; i += 32) {
-        const int at = __ldg(path + i);
-        rises = rises && at >= 0 && at < n && (i == 0 || __ldg(path + i - 1) < at);
+        const int node = __ldg(path + i);
+        rises = rises && node >= 0 && node < n && (i == 0 || __ldg(path + i - 1) < node);
       }
       good = __all_sync(kAll, rises);
     }
     const bool moves = good && !bad_q && !bad_len;
-    if (c == 0 && p.first && lane == 0) {
+    if (at == 0 && p.first && lane == 0) {
       p.new_lens[b] = moves ? L - n + taken : L;
       if (!moves) flag_status(p.status, bad_q ? KVQ_DEV_BAD_QLEN : bad_len ? KVQ_DEV_BAD_SEQLEN : KVQ_DEV_BAD_TREE);
     }
@@ -122,11 +126,12 @@ __global__ void __launch_bounds__(128) commit_kernel(const __grid_constant__ Com
     const int32_t* table = p.tables + static_cast<int64_t>(b) * p.max_blocks;
     const int64_t page = static_cast<int64_t>(kTok) * (r.row_bytes + r.sub_bytes);
     uint8_t* data = static_cast<uint8_t*>(r.data);
+    const int h0 = p.hkv * share / p.shares, h1 = p.hkv * (share + 1) / p.shares;
     if (r.row_bytes % 16 == 0 && r.sub_bytes % 4 == 0)
-      move_rows<uint4>(p, data, page, 0, r.row_bytes, path, table, L - n, taken);
+      move_rows<uint4>(p, data, page, 0, r.row_bytes, path, table, L - n, taken, h0, h1);
     else
-      move_rows<uint32_t>(p, data, page, 0, r.row_bytes, path, table, L - n, taken);
-    move_rows<uint32_t>(p, data, page, kTok * r.row_bytes, r.sub_bytes, path, table, L - n, taken);
+      move_rows<uint32_t>(p, data, page, 0, r.row_bytes, path, table, L - n, taken, h0, h1);
+    move_rows<uint32_t>(p, data, page, kTok * r.row_bytes, r.sub_bytes, path, table, L - n, taken, h0, h1);
   }
 }
 
@@ -214,45 +219,47 @@ KVQ_DEVI int64_t block_scan(int64_t v, int64_t& total, int64_t* warp_sum) {
 }
 
 // Page after page of the pool's free ones, lowest first, to take(rank, page) for the ranks below
-// `wanted`: each thread counts four words' bits, a scan gives their ranks.  One CTA.
+// `wanted`.  One CTA: a thread counts a word's bits and a scan gives the words' ranks, then a warp takes
+// a word at a time, a page a lane.  (A thread took its words' pages one after the other before: a pool
+// whose free pages lie together then has a few threads at work, and 64 pages with a look-up each took 25 us.)
+struct Words {
+  uint32_t bits[kPoolThreads];
+  int rank[kPoolThreads];
+  int64_t sum[kPoolThreads / 32];
+};
+
 template <typename F>
-KVQ_DEVI void take_lowest(int32_t* pool, int num_blocks, int64_t wanted, int64_t* warp_sum, F&& take) {
+KVQ_DEVI void take_lowest(int32_t* pool, int num_blocks, int wanted, Words& s, F&& take) {
   uint32_t* bits = reinterpret_cast<uint32_t*>(pool + KVQ_POOL_HEADER + num_blocks);
-  const int words = (num_blocks + 31) / 32;
-  int64_t base = 0;
-  for (int w0 = 0; w0 < words && base < wanted; w0 += 4 * kPoolThreads) {
-    uint32_t w[4];
-    int n = 0;
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      const int at = w0 + 4 * static_cast<int>(threadIdx.x) + y;
-      w[y] = at < words ? bits[at] : 0u;
-      n += __popc(w[y]);
-    }
+  const int words = (num_blocks + 31) / 32, lane = threadIdx.x & 31;
+  int base = 0;
+  for (int w0 = 0; w0 < words && base < wanted; w0 += kPoolThreads) {
+    const int at = w0 + static_cast<int>(threadIdx.x);
+    const uint32_t w = at < words ? bits[at] : 0u;
     int64_t total;
-    int64_t rank = base + block_scan<kPoolThreads>(n, total, warp_sum);
-    base += total;
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      const int at = w0 + 4 * static_cast<int>(threadIdx.x) + y;
-      uint32_t left = w[y];
-      while (left && rank < wanted) {
-        const int bit = __ffs(left) - 1;
-        left &= left - 1;
-        const int page = 32 * at + bit;
-        if (page < num_blocks) take(rank, page);
-        ++rank;
-      }
-      if (left != w[y]) bits[at] = left;
+    const int rank = base + static_cast<int>(block_scan<kPoolThreads>(__popc(w), total, s.sum));
+    s.bits[threadIdx.x] = w;
+    s.rank[threadIdx.x] = rank;
+    __syncthreads();
+    for (int y = threadIdx.x >> 5; y < min(kPoolThreads, words - w0) && s.rank[y] < wanted; y += kPoolThreads / 32) {
+      const uint32_t of = s.bits[y];
+      const int mine = s.rank[y] + __popc(of & ((1u << lane) - 1u)), page = 32 * (w0 + y) + lane;
+      const bool taken = (of >> lane & 1u) && mine < wanted;
+      const uint32_t gone = __ballot_sync(kAll, taken);
+      if (lane == 0 && gone) bits[w0 + y] = of & ~gone;
+      if (taken && page < num_blocks) take(mine, page);
     }
+    base += static_cast<int>(total);
+    __syncthreads();
   }
 }
 
 __global__ void __launch_bounds__(kPoolThreads) alloc_kernel(const __grid_constant__ PoolParams p) {
   __shared__ int32_t off[kMaxTables + 1];
-  __shared__ int64_t warp_sum[kPoolThreads / 32];
+  __shared__ Words words;
   pdl_wait();
   pdl_allow_next();
+  const int free_pages = p.pool[1];
   // what each sequence wants, and where its pages' ranks begin
   constexpr int kPer = kMaxTables / kPoolThreads;
   int need[kPer];
@@ -271,8 +278,8 @@ __global__ void __launch_bounds__(kPoolThreads) alloc_kernel(const __grid_consta
     mine += need[y];
   }
   int64_t total;
-  int64_t at = block_scan<kPoolThreads>(mine, total, warp_sum);
-  if (total > p.pool[1]) {
+  int64_t at = block_scan<kPoolThreads>(mine, total, words.sum);
+  if (total > free_pages) {
     if (threadIdx.x == 0) flag_status(p.status, KVQ_DEV_NO_PAGES);
     return;
   }
@@ -284,24 +291,19 @@ __global__ void __launch_bounds__(kPoolThreads) alloc_kernel(const __grid_consta
   }
   if (threadIdx.x == 0) off[p.B] = static_cast<int32_t>(total);
   __syncthreads();
-  int b = -1;
-  take_lowest(p.pool, p.num_blocks, total, warp_sum, [&](int64_t rank, int page) {
-    if (b < 0 || rank >= off[b + 1] || rank < off[b]) {  // the last b with off[b] <= rank
-      int lo = 0, hi = p.B - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (off[mid] <= rank)
-          lo = mid;
-        else
-          hi = mid - 1;
-      }
-      b = lo;
+  take_lowest(p.pool, p.num_blocks, static_cast<int>(total), words, [&](int rank, int page) {
+    int lo = 0, hi = p.B - 1;  // the last b with off[b] <= rank
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (off[mid] <= rank)
+        lo = mid;
+      else
+        hi = mid - 1;
     }
     p.pool[KVQ_POOL_HEADER + page] = 1;
-    p.tables[static_cast<int64_t>(b) * p.max_blocks + pages_of(p.old_lens[b]) + (rank - off[b])] = page;
+    p.tables[static_cast<int64_t>(lo) * p.max_blocks + pages_of(__ldg(p.old_lens + lo)) + (rank - off[lo])] = page;
   });
-  __syncthreads();
-  if (threadIdx.x == 0) p.pool[1] -= static_cast<int32_t>(total);
+  if (threadIdx.x == 0) p.pool[1] = free_pages - static_cast<int32_t>(total);
 }
 
 // One holder less; the last one's page is free.  False where nothing held it.
@@ -360,7 +362,7 @@ struct ForkRow {
   bool bad_len, bad_page;
 };
 
-// What row b goes on from.  A page that nothing holds stays so until the last CTA is done, one that is
+// What row b goes on from.  A page that nothing holds stays so until every row is written, one that is
 // held is held throughout, so every CTA sees the same.
 KVQ_DEVI ForkRow fork_row(const ForkParams& p, int b) {
   ForkRow r = {-1, 0, -1, false, false};
@@ -383,44 +385,68 @@ KVQ_DEVI ForkRow fork_row(const ForkParams& p, int b) {
   return r;
 }
 
-// CTA 0 takes the pages, the others write the rows; all of them first count the pages wanted, and
-// the last one that is done changes what the others compare with: the count of free pages, and the
-// counts of those taken.
-__global__ void __launch_bounds__(kPoolThreads) fork_kernel(const __grid_constant__ ForkParams p) {
-  __shared__ int32_t off[kMaxTables + 1];  // the row that takes the k-th page
-  __shared__ int64_t warp_sum[kPoolThreads / 32];
-  __shared__ bool is_last;
+// One cluster.  Every CTA counts the pages wanted; the first takes them while the others write the
+// rows; behind the cluster's barrier it changes what the others compare with: the count of free pages,
+// and the counts of those taken.  (With a CTA a row and a counter in memory that the last one of them
+// finds, the fence, the atomic and the last one's reads cost 2 us more than the barrier does.)
+constexpr int kForkCtas = 8;
+
+__global__ void __cluster_dims__(kForkCtas, 1, 1) __launch_bounds__(kPoolThreads)
+    fork_kernel(const __grid_constant__ ForkParams p) {
+  // for each page wanted its row (12 bits), the row's count of full pages (27) and the page to be copied (24)
+  constexpr uint64_t kTaken = 1ull << 63;
+  __shared__ uint64_t wants_s[kMaxTables];
+  __shared__ Words words;
+  static_assert(sizeof(wants_s) + sizeof(Words) <= 48 * 1024 && kMaxTables <= 4096, "packing, shared memory");
   pdl_wait();
   pdl_allow_next();
   constexpr int kPer = kMaxTables / kPoolThreads;
+  const int cta = blockIdx.x;
+  const int free_pages = __ldcg(p.pool + 1);
   uint32_t wants = 0;
+  uint64_t want[kPer];
 #pragma unroll
   for (int y = 0; y < kPer; ++y) {
-    const int b = kPer * static_cast<int>(threadIdx.x) + y;
-    if (b < p.num_out && fork_row(p, b).last >= 0) wants |= 1u << y;
-  }
-  int64_t total;
-  int64_t at = block_scan<kPoolThreads>(__popc(wants), total, warp_sum);
-  const bool enough = total <= __ldcg(p.pool + 1);
-  if (!enough && blockIdx.x == 0 && threadIdx.x == 0) flag_status(p.status, KVQ_DEV_NO_PAGES);
-  if (enough && blockIdx.x == 0) {
-#pragma unroll
-    for (int y = 0; y < kPer; ++y)
-      if (wants >> y & 1u) off[at++] = kPer * static_cast<int>(threadIdx.x) + y;
-    __syncthreads();
-    take_lowest(p.pool, p.num_blocks, total, warp_sum, [&](int64_t rank, int page) {
-      const int b = off[rank];
+    const int b = y * kPoolThreads + static_cast<int>(threadIdx.x);
+    want[y] = 0;
+    if (b < p.num_out) {
       const ForkRow r = fork_row(p, b);
-      p.out_tables[static_cast<int64_t>(b) * p.max_blocks + r.len / kTok] = page;
-      p.copies[2 * b] = r.last;
+      if (r.last >= 0) {
+        wants |= 1u << y;
+        want[y] = static_cast<uint64_t>(r.last) | static_cast<uint64_t>(r.len / kTok) << 24 | static_cast<uint64_t>(b) << 51;
+      }
+    }
+  }
+  // the pages' order is the rows'
+  int64_t all = 0;
+#pragma unroll
+  for (int y = 0; y < kPer; ++y) {
+    if (y * kPoolThreads >= p.num_out) break;
+    int64_t total;
+    const int64_t at = all + block_scan<kPoolThreads>(wants >> y & 1u, total, words.sum);
+    all += total;
+    if (cta == 0 && (wants >> y & 1u)) wants_s[at] = want[y];
+  }
+  const int total = static_cast<int>(all);
+  const bool enough = total <= free_pages;
+  if (enough && cta == 0) {
+    __syncthreads();
+    take_lowest(p.pool, p.num_blocks, total, words, [&](int rank, int page) {
+      const uint64_t w = wants_s[rank];
+      const int64_t b = static_cast<int64_t>(w >> 51), full = static_cast<int64_t>(w >> 24 & 0x7FFFFFFu);
+      p.out_tables[b * p.max_blocks + full] = page;
+      p.copies[2 * b] = static_cast<int32_t>(w & 0xFFFFFFu);
       p.copies[2 * b + 1] = page;
+      wants_s[rank] = kTaken | static_cast<uint64_t>(page);  // (a rank is one thread's)
     });
   }
-  if (enough && (blockIdx.x > 0 || gridDim.x == 1)) {
-    const int first = gridDim.x == 1 ? 0 : blockIdx.x - 1, step = gridDim.x == 1 ? 1 : gridDim.x - 1;
-    for (int b = first; b < p.num_out; b += step) {
+  if (enough && cta > 0) {
+    // a warp a row
+    const int lane = threadIdx.x & 31;
+    for (int b = (cta - 1) + (kForkCtas - 1) * static_cast<int>(threadIdx.x >> 5); b < p.num_out;
+         b += (kForkCtas - 1) * (kPoolThreads / 32)) {
       const ForkRow r = fork_row(p, b);
-      if (threadIdx.x == 0) {
+      if (lane == 0) {
         if (r.bad_len) flag_status(p.status, KVQ_DEV_BAD_SEQLEN);
         if (r.bad_page) flag_status(p.status, KVQ_DEV_BAD_BLOCK);
         p.out_lens[b] = r.len;
@@ -428,36 +454,38 @@ __global__ void __launch_bounds__(kPoolThreads) fork_kernel(const __grid_constan
       }
       int32_t* out = p.out_tables + static_cast<int64_t>(b) * p.max_blocks;
       const int full = r.len / kTok;
-      for (int i = threadIdx.x; i < p.max_blocks; i += kPoolThreads) {
-        if (i == full && r.last >= 0) continue;  // the new page
-        int page = -1;
-        if (i < full) {
-          page = __ldg(p.tables + static_cast<int64_t>(r.src) * p.max_blocks + i);
-          if (page >= 0 && page < p.num_blocks && __ldcg(p.pool + KVQ_POOL_HEADER + page) > 0) {
-            atomicAdd(p.pool + KVQ_POOL_HEADER + page, 1);
-          } else {
-            page = -1;
+      const int32_t* from = p.tables + static_cast<int64_t>(r.src) * p.max_blocks;
+      for (int i0 = lane; i0 < p.max_blocks; i0 += 32 * kPer) {  // four entries of a lane in flight
+        int page[kPer];
+        bool held[kPer];
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) page[y] = i0 + 32 * y < full ? __ldg(from + i0 + 32 * y) : -1;
+#pragma unroll
+        for (int y = 0; y < kPer; ++y)
+          held[y] = page[y] >= 0 && page[y] < p.num_blocks && __ldcg(p.pool + KVQ_POOL_HEADER + page[y]) > 0;
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) {
+          const int i = i0 + 32 * y;
+          if (i >= p.max_blocks || (i == full && r.last >= 0)) continue;  // (the new page's)
+          if (held[y])
+            atomicAdd(p.pool + KVQ_POOL_HEADER + page[y], 1);
+          else if (i < full)
             flag_status(p.status, KVQ_DEV_BAD_BLOCK);
-          }
+          out[i] = held[y] ? page[y] : -1;
         }
-        out[i] = page;
       }
     }
   }
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) is_last = atomicAdd(p.pool, 1) + 1 == static_cast<int>(gridDim.x);
-  __syncthreads();
-  if (!is_last) return;
-  __threadfence();
-  if (threadIdx.x == 0) {
-    p.pool[0] = 0;
-    if (enough) p.pool[1] -= static_cast<int32_t>(total);
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (cta > 0) return;
+  if (!enough) {
+    if (threadIdx.x == 0) flag_status(p.status, KVQ_DEV_NO_PAGES);
+    return;
   }
-  for (int b = threadIdx.x; enough && b < p.num_out; b += kPoolThreads) {
-    const int page = __ldcg(p.copies + 2 * b + 1);
-    if (page >= 0) p.pool[KVQ_POOL_HEADER + page] = 1;
-  }
+  if (threadIdx.x == 0) p.pool[1] = free_pages - total;
+  for (int k = threadIdx.x; k < total; k += kPoolThreads)
+    if (wants_s[k] & kTaken) p.pool[KVQ_POOL_HEADER + static_cast<int>(wants_s[k] & 0xFFFFFFu)] = 1;
 }
 
 __global__ void __launch_bounds__(256) init_kernel(int32_t* pool, const int num_blocks) {
@@ -542,14 +570,16 @@ extern "C" int kvq_tree_commit(const kvq_rows* caches, int num_caches, int64_t n
   if (num_seqs == 0) return KVQ_OK;
   const int sms = device_sm_count();
   if (sms <= 0) return KVQ_ERR_CUDA;
-  CommitParams p = {0, num_seqs, num_kv_heads, max_blocks_per_seq, max_path, 1, num_blocks, cu_q_lens, block_tables,
+  CommitParams p = {0, num_seqs, num_kv_heads, max_blocks_per_seq, max_path, 1, 1, num_blocks, cu_q_lens, block_tables,
                     seq_lens, accepted, num_accepted, new_lens, dev_status};
   int at = 0;
   do {
     Caches cs = {};
     p.caches = num_caches - at < kMaxRowsCaches ? num_caches - at : kMaxRowsCaches;
     for (int i = 0; i < p.caches; ++i) cs.c[i] = caches[at + i];
-    const int64_t warps = static_cast<int64_t>(num_seqs) * (p.caches > 0 ? p.caches : 1);
+    const int64_t each = static_cast<int64_t>(num_seqs) * (p.caches > 0 ? p.caches : 1), most = static_cast<int64_t>(sms) * 64 / each;
+    p.shares = most < 1 ? 1 : most < num_kv_heads ? static_cast<int>(most) : num_kv_heads;
+    const int64_t warps = each * p.shares;
     const int64_t ctas = (warps + 3) / 4, cap = static_cast<int64_t>(sms) * 64;
     const int r = done(launch_pdl(commit_kernel, dim3(static_cast<unsigned>(ctas < cap ? ctas : cap)), dim3(128), 0,
                                   reinterpret_cast<cudaStream_t>(stream), p, cs));
@@ -623,11 +653,8 @@ extern "C" int kvq_pages_fork(int32_t* pool, int64_t num_blocks, const int32_t* 
     return KVQ_ERR_ALIGN;
   if (num_out > 0 && (out_tables == tables || out_lens == lens || out_lens == parents)) return KVQ_ERR_ARG;
   if (num_out == 0) return KVQ_OK;
-  const int sms = device_sm_count();
-  if (sms <= 0) return KVQ_ERR_CUDA;
   ForkParams p = {pool, static_cast<int>(num_blocks), tables, lens, num_src, max_blocks_per_seq, parents, num_out,
                   out_tables, out_lens, copies, dev_status};
-  const int rows = num_out < sms - 1 ? num_out : sms - 1;  // CTAs that write rows
-  return done(launch_pdl(fork_kernel, dim3(1 + (rows > 0 ? rows : 0)), dim3(kPoolThreads), 0,
+  return done(launch_pdl(fork_kernel, dim3(kForkCtas), dim3(kPoolThreads), 0,
                          reinterpret_cast<cudaStream_t>(stream), p));
 }
