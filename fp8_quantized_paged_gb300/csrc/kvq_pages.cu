@@ -40,7 +40,7 @@ struct CommitParams {
   uint32_t* status;
 };
 
-constexpr int kUnits = 8;  // 16-byte (4-byte) units that a lane has in flight
+constexpr int kUnits = 4;  // 16-byte (4-byte) units that a lane has in flight
 
 // Rows [i0, i0 + c) of the path in heads [head0, head1), a T a unit: all of a head's rows are read before
 // the first is written.  A path rises, so rows of later chunks come from at or behind their own places.
@@ -87,11 +87,11 @@ KVQ_DEVI void move_rows(const CommitParams& p, uint8_t* data, int64_t page_bytes
   }
 }
 
-// A warp takes a sequence and a share of a cache's heads: up to 4 KB of rows in flight behind one
+// A warp takes a sequence and a share of a cache's heads: up to 2 KB of rows in flight behind one
 // chain of lengths, path and table (some 4 us with the launch).  Heads are shared out until the GPU's
 // warps are taken: with all of a cache's heads to a warp, 32 sequences' paths in 32 caches of 8 heads
 // took 8.9 us, several chains' time at 7 warps an SM; shared out COMMIT_US.
-__global__ void __launch_bounds__(128) commit_kernel(const __grid_constant__ CommitParams p,
+__global__ void __launch_bounds__(128, 8) commit_kernel(const __grid_constant__ CommitParams p,
                                                      const __grid_constant__ Caches cs) {
   pdl_wait();
   pdl_allow_next();
@@ -577,7 +577,7 @@ extern "C" int kvq_tree_commit(const kvq_rows* caches, int num_caches, int64_t n
     Caches cs = {};
     p.caches = num_caches - at < kMaxRowsCaches ? num_caches - at : kMaxRowsCaches;
     for (int i = 0; i < p.caches; ++i) cs.c[i] = caches[at + i];
-    const int64_t each = static_cast<int64_t>(num_seqs) * (p.caches > 0 ? p.caches : 1), most = static_cast<int64_t>(sms) * 64 / each;
+    const int64_t each = static_cast<int64_t>(num_seqs) * (p.caches > 0 ? p.caches : 1), most = static_cast<int64_t>(sms) * 32 / each;
     p.shares = most < 1 ? 1 : most < num_kv_heads ? static_cast<int>(most) : num_kv_heads;
     const int64_t warps = each * p.shares;
     const int64_t ctas = (warps + 3) / 4, cap = static_cast<int64_t>(sms) * 64;

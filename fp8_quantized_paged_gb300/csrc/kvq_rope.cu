@@ -9,11 +9,15 @@
 // A stream: (2 Hq + 2 Hkv) dh bf16 values in or out and 2 Hkv dh codes out a
 // token.  DH / 16 lanes share a row, 16 dims a lane in two runs of 8: the two
 // halves of its pairs, so that a pair's dims meet in one lane.  A warp takes a
-// token (or a share of its rows, where the tokens are few), so the lane's 8
-// angles are formed once for all of the token's rows: their turns are a 64-bit
-// integer product modulo 2^64, exact at any position, of which the upper 32
-// bits go to sincospif.  The next rows are loaded before the present ones are
-// worked on.
+// token (or a share of its rows, where the tokens are few), so its angles are
+// formed once for all of the token's rows, each by one lane, and handed
+// round: their turns are a 64-bit integer product modulo 2^64, exact at any
+// position, of which the upper 32 bits go to sincospif.
+//
+// At full rate the stream leaves an SM some 9000 issue slots for 1000 rows,
+// so instructions count as much as bytes: a step's rows are all of q, of k or
+// of v (what each needs is all it runs), and two steps' rows are on their way
+// while one is worked on.
 #include "../../include/kvq_step.h"
 #include "kvq_host.h"
 #include "kvq_quant.cuh"
@@ -23,7 +27,8 @@ namespace rope {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kThreads = 256;
-constexpr int kCtasPerSM = 3;
+constexpr int kCtasPerSM = 4;
+constexpr int kAhead = 2;  // steps whose rows are on their way
 
 struct RopeParams {
   const uint16_t* q;
@@ -97,6 +102,7 @@ template <int FMT, int DH, bool TS>
 __global__ void __launch_bounds__(kThreads, kCtasPerSM) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int CH = DH / 16;      // lanes of a row
   constexpr int RW = 32 / CH;      // rows of a warp
+  constexpr int NA = 8 / RW;       // angles that a lane forms, of the eight that it uses
   constexpr bool BF = FMT == KVQ_FMT_BF16;
   pdl_wait();
   pdl_allow_next();
@@ -107,133 +113,194 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) rope_kernel(const __grid
   // the lane's runs of 8 dims: both halves of its pairs, or (interleaved, or past the pairs) neighbours
   const bool apart = !p.interleaved && turned;
   const int d0 = 8 * (apart ? l : 2 * l), d1 = 8 * (apart ? l + pc : 2 * l + 1);
-  const int rows = p.hq + 2 * p.hkv, steps = (rows + RW - 1) / RW;
-  unsigned long long turns[8];
-  uint32_t axes = 0;  // four bits each
+  const int sq = (p.hq + RW - 1) / RW, sk = (p.hkv + RW - 1) / RW, steps = sq + 2 * sk;
+  unsigned long long turns[NA];
+  uint32_t axes[NA];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    turns[i] = turned ? __ldg(p.turns + 8 * l + i) : 0ull;
-    const uint32_t a = turned && p.axis ? __ldg(p.axis + 8 * l + i) : 0u;
-    axes |= (a < static_cast<uint32_t>(p.axes) ? a : 0u) << (4 * i);
+  for (int i = 0; i < NA; ++i) {
+    const int at = 8 * l + NA * g + i;
+    turns[i] = turned ? __ldg(p.turns + at) : 0ull;
+    const uint32_t a = turned && p.axis ? __ldg(p.axis + at) : 0u;
+    axes[i] = a < static_cast<uint32_t>(p.axes) ? a : 0u;
   }
   const int64_t items = p.tokens * p.split;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
   for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); it < items; it += warps) {
     const int64_t t = it / p.split;
     const int first = static_cast<int>(it - t * p.split);
-    auto load = [&](int row, uint4& a, uint4& b) {
-      if (row >= rows) return;
-      const uint16_t* src = row < p.hq            ? p.q + t * p.q_stride + row * DH
-                            : row < p.hq + p.hkv ? p.k + t * p.k_stride + (row - p.hq) * DH
-                                                  : p.v + t * p.v_stride + (row - p.hq - p.hkv) * DH;
+    auto load = [&](int s, uint4& a, uint4& b) {
+      const uint16_t* src;
+      if (s < sq) {
+        if (s * RW + g >= p.hq) return;
+        src = p.q + t * p.q_stride + (s * RW + g) * DH;
+      } else if (s < sq + sk) {
+        if ((s - sq) * RW + g >= p.hkv) return;
+        src = p.k + t * p.k_stride + ((s - sq) * RW + g) * DH;
+      } else {
+        if (s >= steps || (s - sq - sk) * RW + g >= p.hkv) return;
+        src = p.v + t * p.v_stride + ((s - sq - sk) * RW + g) * DH;
+      }
       a = __ldcs(reinterpret_cast<const uint4*>(src + d0));
       b = __ldcs(reinterpret_cast<const uint4*>(src + d1));
     };
-    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-    load(first * RW + g, a, b);
+    uint4 a[kAhead] = {}, b[kAhead] = {};
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y) load(first + y * p.split, a[y], b[y]);
     const int64_t slot = __ldg(p.slots + t);
     float cs[8], sn[8];
+    {
+      float c[NA], n[NA];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t at = __ldg(p.pos + static_cast<int64_t>((axes >> (4 * i)) & 15u) * p.tokens + t);
-      const unsigned long long turn = static_cast<unsigned long long>(at) * turns[i];
-      // the upper 32 bits as [-2^31, 2^31) of 2^32 to a turn; sincospif takes half turns
-      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sn[i], &cs[i]);
+      for (int i = 0; i < NA; ++i) {
+        const int64_t at = __ldg(p.pos + static_cast<int64_t>(axes[i]) * p.tokens + t);
+        const unsigned long long turn = static_cast<unsigned long long>(at) * turns[i];
+        // the upper 32 bits as [-2^31, 2^31) of 2^32 to a turn; sincospif takes half turns
+        sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &n[i], &c[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        cs[i] = __shfl_sync(kAll, c[i % NA], i / NA * CH + l);
+        sn[i] = __shfl_sync(kAll, n[i % NA], i / NA * CH + l);
+      }
     }
     if (slot >= p.capacity && first == 0 && lane == 0) flag_status(p.status, KVQ_DEV_BAD_SLOT);
     const bool kept = slot >= 0 && slot < p.capacity;
-    for (int s = first; s < steps; s += p.split) {
-      uint4 an = make_uint4(0u, 0u, 0u, 0u), bn = an;
-      if (s + p.split < steps) load((s + p.split) * RW + g, an, bn);
-      const int row = s * RW + g;
-      const bool is_q = row < p.hq, is_v = row >= p.hq + p.hkv;
-      float x[8], y[8];
-      unpack8(a, x);
-      unpack8(b, y);
-      const uint16_t* w = is_q ? p.wq : p.wk;
-      if (p.wq || p.wk) {
+    // The rows' norm and turn: x, y are the lane's two runs.
+    auto norm_and_turn = [&](float (&x)[8], float (&y)[8], const uint16_t* w) {
+      if (w) {
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           sum = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), make_float2(x[2 * i], x[2 * i + 1]), sum);
           sum = __ffma2_rn(make_float2(y[2 * i], y[2 * i + 1]), make_float2(y[2 * i], y[2 * i + 1]), sum);
         }
-        float sq = sum.x + sum.y;
+        float sq2 = sum.x + sum.y;
 #pragma unroll
-        for (int off = 1; off < CH; off <<= 1) sq += __shfl_xor_sync(kAll, sq, off);
-        if (!is_v && w) {
-          const float f = rsqrtf(sq * (1.f / DH) + p.eps);
-          float u[8], v[8];
-          unpack8(__ldg(reinterpret_cast<const uint4*>(w + d0)), u);
-          unpack8(__ldg(reinterpret_cast<const uint4*>(w + d1)), v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[i] *= f * u[i];
-            y[i] *= f * v[i];
-          }
-        }
-      }
-      if (!is_v && turned) {
-        if (p.interleaved) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x0 = x[2 * i], x1 = x[2 * i + 1], y0 = y[2 * i], y1 = y[2 * i + 1];
-            x[2 * i] = x0 * cs[i] - x1 * sn[i];
-            x[2 * i + 1] = x0 * sn[i] + x1 * cs[i];
-            y[2 * i] = y0 * cs[4 + i] - y1 * sn[4 + i];
-            y[2 * i + 1] = y0 * sn[4 + i] + y1 * cs[4 + i];
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float x0 = x[i], y0 = y[i];
-            x[i] = x0 * cs[i] - y0 * sn[i];
-            y[i] = x0 * sn[i] + y0 * cs[i];
-          }
-        }
-      }
-      float amax = 0.f;
-      if (TS) {  // every lane of the row takes part, whatever its slot
-        uint32_t m = 0u;
+        for (int off = 1; off < CH; off <<= 1) sq2 += __shfl_xor_sync(kAll, sq2, off);
+        const float f = rsqrtf(sq2 * (1.f / DH) + p.eps);
+        float u[8], v[8];
+        unpack8(__ldg(reinterpret_cast<const uint4*>(w + d0)), u);
+        unpack8(__ldg(reinterpret_cast<const uint4*>(w + d1)), v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint32_t u = __float_as_uint(x[i]) & 0x7FFFFFFFu, v = __float_as_uint(y[i]) & 0x7FFFFFFFu;
-          m = max(m, max(u < 0x7F800000u ? u : 0u, v < 0x7F800000u ? v : 0u));
+          x[i] *= f * u[i];
+          y[i] *= f * v[i];
         }
-#pragma unroll
-        for (int off = 1; off < CH; off <<= 1) m = max(m, __shfl_xor_sync(row_mask, m, off));
-        amax = __uint_as_float(m);
       }
-      if (is_q) {
-        uint16_t* dst = p.out + t * p.out_stride + static_cast<int64_t>(row) * DH;
+      if (!turned) return;
+      if (p.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x0 = x[2 * i], x1 = x[2 * i + 1], y0 = y[2 * i], y1 = y[2 * i + 1];
+          x[2 * i] = x0 * cs[i] - x1 * sn[i];
+          x[2 * i + 1] = x0 * sn[i] + x1 * cs[i];
+          y[2 * i] = y0 * cs[4 + i] - y1 * sn[4 + i];
+          y[2 * i + 1] = y0 * sn[4 + i] + y1 * cs[4 + i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 x2 = make_float2(x[2 * i], x[2 * i + 1]), y2 = make_float2(y[2 * i], y[2 * i + 1]);
+          const float2 c2 = make_float2(cs[2 * i], cs[2 * i + 1]), s2 = make_float2(sn[2 * i], sn[2 * i + 1]);
+          const float2 n2 = make_float2(-s2.x, -s2.y);
+          const float2 u = __ffma2_rn(x2, c2, __fmul2_rn(y2, n2)), v = __ffma2_rn(y2, c2, __fmul2_rn(x2, s2));
+          x[2 * i] = u.x;
+          x[2 * i + 1] = u.y;
+          y[2 * i] = v.x;
+          y[2 * i + 1] = v.y;
+        }
+      }
+    };
+    auto step = [&](int s, const uint4& a, const uint4& b) {
+      if (s < sq) {
+        float x[8], y[8];
+        unpack8(a, x);
+        unpack8(b, y);
+        norm_and_turn(x, y, p.wq);
+        const int row = s * RW + g;
+        if (row >= p.hq) return;
+        uint16_t* dst = p.out + t * p.out_stride + row * DH;
         *reinterpret_cast<uint4*>(dst + d0) = pack8(x);
         *reinterpret_cast<uint4*>(dst + d1) = pack8(y);
-      } else if (row < rows && kept) {
-        const int h = row - p.hq - (is_v ? p.hkv : 0);
-        const int64_t at = ((slot >> 4) * p.hkv + h) * 16 + (slot & 15);
-        void* cache = is_v ? p.vc : p.kc;
+        return;
+      }
+      const bool is_v = s >= sq + sk;
+      const int h = (s - sq - (is_v ? sk : 0)) * RW + g;
+      const bool live = h < p.hkv && kept;
+      const int64_t at = ((slot >> 4) * p.hkv + h) * 16 + (slot & 15);
+      uint2 lo = {}, hi = {};  // codes
+      float* scale = is_v ? p.vs : p.ks;
+      if (is_v) {
         if constexpr (BF) {
-          uint16_t* dst = static_cast<uint16_t*>(cache) + at * DH;
-          *reinterpret_cast<uint4*>(dst + d0) = is_v ? a : pack8(x);
-          *reinterpret_cast<uint4*>(dst + d1) = is_v ? b : pack8(y);
+          if (!live) return;
+          uint16_t* dst = static_cast<uint16_t*>(p.vc) + at * DH;
+          *reinterpret_cast<uint4*>(dst + d0) = a;
+          *reinterpret_cast<uint4*>(dst + d1) = b;
+          return;
         } else {
-          float* scale = is_v ? p.vs : p.ks;
-          const HeadScale hs = head_scale(TS ? scale_of_amax<FMT>(amax) : __ldg(scale + (p.per_head ? h : 0)));
-          uint8_t* dst = static_cast<uint8_t*>(cache) + at * DH;
-          *reinterpret_cast<uint2*>(dst + d0) = quantize8<FMT>(x, hs);
-          *reinterpret_cast<uint2*>(dst + d1) = quantize8<FMT>(y, hs);
-          if (TS && l == 0) scale[at] = hs.s;
+          float f = 0.f;
+          if (TS)  // every lane of the row takes part, whatever its slot
+            f = scale_of_amax<FMT>(row_amax<CH>(a, b, row_mask));
+          if (!live) return;
+          if (!TS) f = __ldg(scale + (p.per_head ? h : 0));
+          const uint4 o = quantize16<FMT>(a, b, head_scale(f));
+          lo = make_uint2(o.x, o.y);
+          hi = make_uint2(o.z, o.w);
+          if (TS && l == 0) scale[at] = f;
+        }
+      } else {
+        float x[8], y[8];
+        unpack8(a, x);
+        unpack8(b, y);
+        norm_and_turn(x, y, p.wk);
+        if constexpr (BF) {
+          if (!live) return;
+          uint16_t* dst = static_cast<uint16_t*>(p.kc) + at * DH;
+          *reinterpret_cast<uint4*>(dst + d0) = pack8(x);
+          *reinterpret_cast<uint4*>(dst + d1) = pack8(y);
+          return;
+        } else {
+          float f = 0.f;
+          if (TS) {
+            uint32_t m = 0u;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t u = __float_as_uint(x[i]) & 0x7FFFFFFFu, v = __float_as_uint(y[i]) & 0x7FFFFFFFu;
+              m = max(m, max(u < 0x7F800000u ? u : 0u, v < 0x7F800000u ? v : 0u));
+            }
+#pragma unroll
+            for (int off = 1; off < CH; off <<= 1) m = max(m, __shfl_xor_sync(row_mask, m, off));
+            f = scale_of_amax<FMT>(__uint_as_float(m));
+          }
+          if (!live) return;
+          if (!TS) f = __ldg(scale + (p.per_head ? h : 0));
+          const HeadScale hs = head_scale(f);
+          lo = quantize8<FMT>(x, hs);
+          hi = quantize8<FMT>(y, hs);
+          if (TS && l == 0) scale[at] = f;
         }
       }
-      a = an;
-      b = bn;
+      uint8_t* dst = static_cast<uint8_t*>(is_v ? p.vc : p.kc) + at * DH;
+      *reinterpret_cast<uint2*>(dst + d0) = lo;
+      *reinterpret_cast<uint2*>(dst + d1) = hi;
+    };
+    for (int s = first; s < steps; s += kAhead * p.split) {
+#pragma unroll
+      for (int y = 0; y < kAhead; ++y) {
+        const int at = s + y * p.split;
+        if (at >= steps) break;
+        const uint4 ha = a[y], hb = b[y];
+        load(at + kAhead * p.split, a[y], b[y]);
+        step(at, ha, hb);
+        __syncwarp();
+      }
     }
   }
 }
 
 template <int FMT, int DH, bool TS>
 static cudaError_t launch_rope(RopeParams& p, cudaStream_t s) {
-  const int rw = 32 / (DH / 16), steps = (p.hq + 2 * p.hkv + rw - 1) / rw;
+  const int rw = 32 / (DH / 16), steps = (p.hq + rw - 1) / rw + 2 * ((p.hkv + rw - 1) / rw);
   const int64_t warps = static_cast<int64_t>(device_sm_count()) * kCtasPerSM * (kThreads / 32);
   // Few tokens are spread over several warps each, as far as those are idle.
   int64_t split = warps / p.tokens;
