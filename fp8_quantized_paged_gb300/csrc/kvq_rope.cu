@@ -16,8 +16,7 @@
 //
 // At full rate the stream leaves an SM some 9000 issue slots for 1000 rows,
 // so instructions count as much as bytes: a step's rows are all of q, of k or
-// of v (what each needs is all it runs), and two steps' rows are on their way
-// while one is worked on.
+// of v, and what each needs is all it runs.
 #include "../../include/kvq_step.h"
 #include "kvq_host.h"
 #include "kvq_quant.cuh"
@@ -26,9 +25,12 @@ namespace kvq {
 namespace rope {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
-constexpr int kThreads = 256;
-constexpr int kCtasPerSM = 4;
-constexpr int kAhead = 2;  // steps whose rows are on their way
+// 28 warps an SM of 72 registers each, and a step's rows on their way while one is worked on.  32768
+// tokens of 32 + 2 * 8 rows of 128 (738 MB): 136 us; with 32 warps (which spill) 141, with two steps'
+// rows on their way 156 to 168.
+constexpr int kThreads = 128;
+constexpr int kCtasPerSM = 7;
+constexpr int kAngles = 1;  // what forming a token's angles takes, in steps
 
 struct RopeParams {
   const uint16_t* q;
@@ -140,12 +142,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) rope_kernel(const __grid
         if (s >= steps || (s - sq - sk) * RW + g >= p.hkv) return;
         src = p.v + t * p.v_stride + ((s - sq - sk) * RW + g) * DH;
       }
-      a = __ldcs(reinterpret_cast<const uint4*>(src + d0));
-      b = __ldcs(reinterpret_cast<const uint4*>(src + d1));
+      a = __ldg(reinterpret_cast<const uint4*>(src + d0));
+      b = __ldg(reinterpret_cast<const uint4*>(src + d1));
     };
-    uint4 a[kAhead] = {}, b[kAhead] = {};
-#pragma unroll
-    for (int y = 0; y < kAhead; ++y) load(first + y * p.split, a[y], b[y]);
+    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+    load(first, a, b);
     const int64_t slot = __ldg(p.slots + t);
     float cs[8], sn[8];
     {
@@ -220,8 +221,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) rope_kernel(const __grid
         const int row = s * RW + g;
         if (row >= p.hq) return;
         uint16_t* dst = p.out + t * p.out_stride + row * DH;
-        *reinterpret_cast<uint4*>(dst + d0) = pack8(x);
-        *reinterpret_cast<uint4*>(dst + d1) = pack8(y);
+        __stcs(reinterpret_cast<uint4*>(dst + d0), pack8(x));
+        __stcs(reinterpret_cast<uint4*>(dst + d1), pack8(y));
         return;
       }
       const bool is_v = s >= sq + sk;
@@ -284,16 +285,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) rope_kernel(const __grid
       *reinterpret_cast<uint2*>(dst + d0) = lo;
       *reinterpret_cast<uint2*>(dst + d1) = hi;
     };
-    for (int s = first; s < steps; s += kAhead * p.split) {
-#pragma unroll
-      for (int y = 0; y < kAhead; ++y) {
-        const int at = s + y * p.split;
-        if (at >= steps) break;
-        const uint4 ha = a[y], hb = b[y];
-        load(at + kAhead * p.split, a[y], b[y]);
-        step(at, ha, hb);
-        __syncwarp();
-      }
+    for (int s = first; s < steps; s += p.split) {
+      const uint4 ha = a, hb = b;
+      load(s + p.split, a, b);
+      step(s, ha, hb);
+      __syncwarp();
     }
   }
 }
@@ -302,9 +298,16 @@ template <int FMT, int DH, bool TS>
 static cudaError_t launch_rope(RopeParams& p, cudaStream_t s) {
   const int rw = 32 / (DH / 16), steps = (p.hq + rw - 1) / rw + 2 * ((p.hkv + rw - 1) / rw);
   const int64_t warps = static_cast<int64_t>(device_sm_count()) * kCtasPerSM * (kThreads / 32);
-  // Few tokens are spread over several warps each, as far as those are idle.
-  int64_t split = warps / p.tokens;
-  split = split < 1 ? 1 : (split > steps ? steps : split);
+  // A token's steps are shared by as many warps as make the longest warp's work least, a share's
+  // angles counted as kAngles steps.
+  int64_t split = 1, least = INT64_MAX;
+  for (int n = 1; n <= steps && n <= 64; ++n) {
+    const int64_t work = (p.tokens * n + warps - 1) / warps * ((steps + n - 1) / n + kAngles);
+    if (work < least) {
+      least = work;
+      split = n;
+    }
+  }
   p.split = static_cast<int>(split);
   const int64_t need = (p.tokens * split + kThreads / 32 - 1) / (kThreads / 32);
   const int64_t cap = static_cast<int64_t>(device_sm_count()) * kCtasPerSM;
