@@ -12,15 +12,16 @@
 // piece of 64 KB of each of, say, 19 CTAs alone.)
 //
 //   warps 8, 9 (producers of K, of V)  copy a block's pages by TMA into rings of 64 KB
-//   warp 10 (issuer)  one lane: S = Q K^T (M 128, N 64), up to four blocks ahead
+//   warp 10 (issuer)  one lane: S = Q K^T (M 128, N 64), up to six blocks ahead
 //   warp 11 (issuer)  one lane: O += P V (M 128, N dh), V as it lies (token-major: an MN-major operand)
 //   warps 0-3, 4-7 (softmax of the even, of the odd blocks)  thread = row (TMEM lane): mask, running
 //     maximum, P over the S columns that it came from.  The maximum is handed from block to block, a
 //     warp of one group to its other's (m_s): it is wanted before the weights, and changes rarely
-// Tensor memory: four buffers of S and P (64 columns each), O (128), Q twice (64 each: the next
-// piece's is written while this one's is in use).  A chain of S, softmax and PV takes about 4000
-// cycles, of which the matrix steps' and barriers' latencies are most; four blocks in flight hide it.
-// (Two CTAs an SM, with two buffers each, took 2450 cycles for 64 keys of each of both.)
+// Tensor memory: six buffers of S and P (64 columns each) and O (128).  A block's way through S,
+// softmax and PV takes about 4300 cycles, of which the matrix steps' and barriers' latencies are most;
+// six blocks in flight hide it.  Q lies in shared memory, twice: the next piece's is written while this
+// one's is in use.  (Two CTAs an SM with two buffers each: 2450 cycles for 64 keys of each of both.
+// Four buffers, and Q in tensor memory, whose steps take 32 cycles where these take 48: 1080 for 64 keys.)
 // The products run on the codes as they are: no conversion, no registers between memory and the
 // tensor cores.  For that Q and P are split into parts that 8 bits hold:
 //   q  2^a q = q1 + q2, E4M3 both, 2^a taking the row's largest to [2^7, 2^8): bf16's 8 bits are
@@ -52,17 +53,19 @@ namespace kvq {
 namespace tree {
 
 constexpr int kRows = 128;  // rows of a tile (MMA M)
-constexpr int kGroupWarps = 4, kSoftWarps = 8, kProdWarp = 8, kMmaWarp = 10;
-constexpr int kTreeThreads = 384;
+constexpr int kGroups = 3, kGroupWarps = 4, kSoftWarps = kGroups * kGroupWarps, kProdWarp = kSoftWarps, kMmaWarp = kProdWarp + 2;
+constexpr int kTreeThreads = 32 * (kMmaWarp + 2);
 constexpr int kKeys = 64;                             // keys of a block
-constexpr int kBufs = 4;                              // of S and P
-constexpr uint32_t kTmemCols = 512, kOutCol = 256, kQCol = 384;  // buffers at 0, O at 256, Q at 384 and 448
+constexpr int kBufs = 6;                              // of S and P
+constexpr uint32_t kTmemCols = 512, kOutCol = 384;    // the buffers at 0, O at 384
 constexpr int kRing = 64 * 1024;  // of K, and of V
 constexpr int kEntries = 1024;  // prefix sums of the plan: of every ceil(B / 1024)th sequence
 constexpr int kKept = 256;      // sequences up to which their lengths are kept beside the prefix sums
 constexpr int kSegCost = 4;     // a segment's start and end, in blocks
 constexpr int kMinShare = 4;    // least cost of a CTA's stretch
 constexpr float kBias = 7.f;    // log2 of the factor that the weights carry
+constexpr int kPieces = 32;     // descriptions of pieces
+constexpr int kBadRing = 32;
 constexpr int kMaskWords = KVQ_TREE_MAX_NODES / 32;
 
 struct TreeParams {
@@ -111,23 +114,26 @@ struct TreeCfg {
   static constexpr int kSlots = kRing / kTile;            // 4, 8 or 16
   static constexpr int kQParts = kBf ? 1 : 2;
   static constexpr int kPageBytes = kBS * kRow;
+  static constexpr int kQTile = kRows * kRow;             // one part of Q
 };
 
 template <int FMT, int DH, bool TS>
 struct TreeSmem {
   using C = TreeCfg<FMT, DH>;
   static constexpr int S = C::kSlots;
-  static constexpr int ring = 0;
+  static constexpr int q = 0;  // [2] Q, by piece
+  static constexpr int ring = q + 2 * C::kQParts * C::kQTile;
   static constexpr int tsc = ring + 2 * kRing;  // per-(token, head) scales, K's and V's, that land with a V
   static constexpr int bars = tsc + (TS ? 2 * S * kKeys * 4 : 0);
-  static constexpr int kBars = 4 * S + 3 * kBufs + 17;
-  static constexpr int misc = bars + kBars * 8;  // tmem address, abort, NaN mark, bad sequences, bad[2 S], issued[2], warp sums
-  // [kRows] running maximum, [4] largest value scale, by quarter of the rows
-  static constexpr int m = misc + (6 + 2 * S + kTreeThreads / 32) * 4;
-  static constexpr int l = (m + (kRows + 4) * 4 + 7) / 8 * 8;  // [2][2][kRows] sums and their maxima, by piece and group
-  static constexpr int ls = l + 4 * kRows * 8;                 // [2][kRows] logits' scales, by piece
-  static constexpr int anc = ls + 2 * kRows * 4;                        // [2][kMaskWords][kRows] ancestors, by group
-  static constexpr int plan = anc + 2 * kMaskWords * kRows * 4;
+  static constexpr int kBars = 4 * S + 3 * kBufs + 2 + 1 + kGroups * 4 + 4 + 2 + 1 + kPieces;
+  static constexpr int misc = bars + kBars * 8;  // tmem address, abort, NaN mark, bad sequences, bad[kBadRing], issued[2], warp sums
+  // [kRows] running maximum, [4] largest value scale by quarter of the rows, [2][4] that at a piece's end
+  static constexpr int m = misc + (6 + kBadRing + kTreeThreads / 32) * 4;
+  static constexpr int l = (m + (kRows + 12) * 4 + 7) / 8 * 8;  // [2][kGroups][kRows] sums and their maxima, by piece
+  static constexpr int ls = l + 2 * kGroups * kRows * 8;                 // [2][kRows] logits' scales, by piece
+  static constexpr int anc = ls + 2 * kRows * 4;                        // [kGroups][kMaskWords][kRows] ancestors
+  static constexpr int pieces = (anc + kGroups * kMaskWords * kRows * 4 + 15) / 16 * 16;  // [kPieces] of 12 words
+  static constexpr int plan = pieces + kPieces * 48;
   static constexpr int total = plan + (kEntries + 1) * 4 + 1024;
   static_assert(total <= 227 * 1024, "shared memory");
 };
@@ -246,6 +252,13 @@ KVQ_DEVI void weight_parts(uint32_t h, uint32_t (&c)[3]) {
   c[2] = hsub2(c[1], c[1] & 0xFF00FF00u) + 0x00800080u;  // (rounds; no carry leaves a half)
 }
 
+// Byte `b` of row r in a tile of swizzled rows; rows past 128 bytes go on in a second tile.
+template <int SPAN>
+KVQ_DEVI uint32_t tile_at(int r, int b) {
+  if (SPAN == 64) return static_cast<uint32_t>(r * 64 + (((b >> 4) ^ ((r >> 1) & 3)) << 4) + (b & 15));
+  return static_cast<uint32_t>((b >> 7) * (kRows * 128) + r * 128 + ((((b & 127) >> 4) ^ (r & 7)) << 4) + (b & 15));
+}
+
 template <int FMT, int DH, bool TS>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     tree_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUtensorMap tmk,
@@ -262,34 +275,41 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   uint64_t* empty = full + 2 * S;  // [2 S] read by the matrix steps (commit)
   uint64_t* sfull = empty + 2 * S;      // [kBufs] S of a block written (commit, and the issuer's arrival)
   uint64_t* pfull = sfull + kBufs;      // [kBufs] P of a block written, O rescaled (4 warps)
-  uint64_t* pdone = pfull + kBufs;      // [kBufs] O += P V of a block done (commit, and the issuer's arrival)
-  uint64_t* qready = pdone + kBufs;     // [2] Q of a piece written (4 warps)
-  uint64_t* ofree = qready + 2;         // O of a piece read (8 warps)
-  uint64_t* token = ofree + 1;          // [2][4] a block's maximum is in m_s: by group, and quarter of the rows
-  uint64_t* lfull = token + 8;          // [4] a piece's sums of a quarter are in l_s (2 warps)
+  uint64_t* pdone = pfull + kBufs;      // [kBufs] O += P V of a block done (commit)
+  uint64_t* qready = pdone + kBufs;     // [2] Q of a piece written (12 warps)
+  uint64_t* ofree = qready + 2;         // O of a piece read (12 warps)
+  uint64_t* token = ofree + 1;          // [kGroups][4] a block's maximum is in m_s: by quarter of the rows
+  uint64_t* lfull = token + kGroups * 4;  // [4] a piece's sums of a quarter are in l_s (3 warps)
   uint64_t* fin = lfull + 4;            // [2] every S, every PV done (commit)
+  uint64_t* odone = fin + 2;            // a piece's last O += P V done (commit, and the issuer's arrival)
+  uint64_t* known = odone + 1;          // [kPieces] a piece's description is there
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + SM::misc);
   volatile uint32_t* tmem_slot = misc;
   volatile uint32_t* abort_flag = misc + 1;
   volatile uint32_t* vnan = misc + 2;   // 1 + the last piece that met a NaN or infinity to put back
   volatile uint32_t* any_bad = misc + 3;  // a sequence has an error
-  volatile uint32_t* bad = misc + 4;    // [2 S] masked pages of block g at [g % 2 S]: rewritten for block
-                                        // g + 2 S, whose K waits for the S of block g + S, which waits
-                                        // for the PV of block g + S - 4
-  volatile int32_t* issued = reinterpret_cast<volatile int32_t*>(misc + 4 + 2 * S);  // [2] blocks copied
-  volatile int32_t* warp_sum = reinterpret_cast<volatile int32_t*>(misc + 6 + 2 * S);
+  volatile uint32_t* bad = misc + 4;    // [kBadRing] masked pages of block g: rewritten for block g + 32,
+                                        // whose K waits for the S of block g + 32 - S, and that for the PV of
+                                        // block g + 26 - S
+  volatile int32_t* issued = reinterpret_cast<volatile int32_t*>(misc + 4 + kBadRing);  // [2] blocks copied
+  volatile int32_t* warp_sum = reinterpret_cast<volatile int32_t*>(misc + 6 + kBadRing);
+  // Piece n's description in [n % kPieces].  It is rewritten for piece n + 32, when all blocks of piece
+  // n + 30 but its last have their K's slots: the PV of block g - S - 7 of the last block g is done then, and
+  // every role past the piece that has it, which at a block a piece is n + 30 - S - 7 > n.
+  int4* pieces_s = reinterpret_cast<int4*>(smem + SM::pieces);
   float* m_s = reinterpret_cast<float*>(smem + SM::m);
   float* sig_s = m_s + kRows;
+  float* sige_s = sig_s + 4;
   float2* l_s = reinterpret_cast<float2*>(smem + SM::l);
   float* ls_s = reinterpret_cast<float*>(smem + SM::ls);
   int32_t* plan = reinterpret_cast<int32_t*>(smem + SM::plan);
 
-  // A parity wait for phase k of a barrier is sound while it has completed k or k + 1 phases.  The
-  // issuers, the producers and the softmax take their barriers' phases in order.  The softmax also looks
-  // at V's full barriers (edge blocks) and at pdone (where O is rescaled, and at a piece's end), now and
-  // then: all earlier phases are complete then, as the S of block g comes after the PV of block g - 4;
-  // and the next ones come after a block of this group that it has not begun with, as PVs go in order.
-  // (Not at a K slot's: the next K may land while a warp is late.)
+  // A parity wait for phase k of a barrier is sound while it has completed k or k + 1 phases.  All roles
+  // take their barriers' phases in order, except that the softmax looks at V's full barriers (edge blocks)
+  // and at pdone (where O is rescaled) now and then: all earlier phases are complete then, as the S of
+  // block g comes after the PV of block g - 6, and PVs go in order; and the next ones come after a block
+  // that this warp has not begun with.  (Not at a K slot's: the next K may land while a warp is late.
+  // Nor at pdone for a piece's end: a group that had no block of it may be several phases behind.)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
@@ -302,13 +322,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(&sfull[i], 2);
       mbar_init(&pfull[i], kGroupWarps);
-      mbar_init(&pdone[i], 2);
+      mbar_init(&pdone[i], 1);
     }
-    mbar_init(&qready[0], kGroupWarps);
-    mbar_init(&qready[1], kGroupWarps);
+    mbar_init(&qready[0], kSoftWarps);
+    mbar_init(&qready[1], kSoftWarps);
     mbar_init(ofree, kSoftWarps);
-    for (int i = 0; i < 8; ++i) mbar_init(&token[i], 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&lfull[i], 2);
+    for (int i = 0; i < kGroups * 4; ++i) mbar_init(&token[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&lfull[i], kGroups);
+    for (int i = 0; i < kPieces; ++i) mbar_init(&known[i], 1);
+    mbar_init(odone, 2);
     mbar_init(&fin[0], 1);
     mbar_init(&fin[1], 1);
     *abort_flag = 0u;
@@ -399,7 +421,26 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   auto wait = [&](uint64_t* bar, int phase) { return wait_or_abort(bar, static_cast<uint32_t>(phase & 1), abort_flag); };
   auto wait_w = [&](uint64_t* bar, int phase) { return __all_sync(kFull, wait(bar, phase)); };  // warp-uniform
 
-  if (warp >= kProdWarp && warp < kMmaWarp) {
+  // Piece n, as the producer of K describes it; without blocks: the end.
+  auto piece_at = [&](int n, Piece& pc) {
+    if (!wait(&known[n % kPieces], n / kPieces)) return false;
+    const int4 a = pieces_s[3 * (n % kPieces)], b = pieces_s[3 * (n % kPieces) + 1], c = pieces_s[3 * (n % kPieces) + 2];
+    pc.i0 = a.x;
+    pc.i1 = a.y;
+    pc.head = a.z;
+    pc.tile = a.w;
+    pc.s.q0 = b.x;
+    pc.s.n = b.y;
+    pc.s.L = b.z;
+    pc.s.first = b.w;
+    pc.s.blocks = c.x;
+    pc.b = c.y;
+    pc.base = c.z;
+    return true;
+  };
+
+  if (warp >= kProdWarp) {
+  if (warp < kMmaWarp) {
     // ------------------------------------------------------------ producers: K, V
     const int t = __shfl_sync(kFull, warp, 0) - kProdWarp;
     constexpr int kAhead = 32 / C::kPages;  // blocks of which the lanes hold the block ids
@@ -407,9 +448,29 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const uint64_t policy = l2_evict_first_policy();  // (what is read once does not push out the queries, states and code)
     Pieces it(plan, p.B, v0, v1);
     Piece pc;
-    int g = 0;
-    bool ok = true;
-    while (ok && it.next(p, pc)) {
+    pc.i0 = pc.i1 = 0;
+    int described = 0, begun = 0, i = 0, rows = 0, rows_next = 0;
+    bool ok = true, fetch = t == 0;
+    for (int g = 0;; ++g) {
+      if (fetch) {  // (K's) a piece is described once the one before has begun: the softmax wants its queries
+        Piece nx = {};
+        const bool more = it.next(p, nx);
+        if (lane == 0) {
+          int4* d = pieces_s + 3 * (described % kPieces);
+          d[0] = more ? make_int4(nx.i0, nx.i1, nx.head, nx.tile) : make_int4(0, 0, 0, 0);
+          d[1] = make_int4(nx.s.q0, nx.s.n, nx.s.L, nx.s.first);
+          d[2] = make_int4(nx.s.blocks, nx.b, nx.base, 0);
+          mbar_arrive(&known[described % kPieces]);
+        }
+        __syncwarp();
+        ++described;
+        fetch = false;
+      }
+      const bool begins = i == pc.i1;
+      if (begins) {
+        if (!(ok = __all_sync(kFull, piece_at(begun++, pc))) || pc.i1 == 0) break;
+        i = pc.i0;
+      }
       const int pages = (pc.s.L + kBS - 1) / kBS, page0 = pc.s.first / kBS;
       const int32_t* table = p.block_tables + static_cast<int64_t>(pc.b) * p.max_blocks;
       // the cache row of page `page0 + kPages i + lane`, -1: masked out, -2: past the sequence
@@ -423,24 +484,25 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         return (blk * p.Hkv + pc.head) * kBS;
       };
-      int rows = row_of(pc.i0), rows_next = row_of(pc.i0 + kAhead);
-      for (int i = pc.i0; i < pc.i1; ++i, ++g) {
-        const int j = (i - pc.i0) % kAhead, s = g % S;
-        if (j == 0 && i > pc.i0) {
-          rows = rows_next;
-          rows_next = row_of(i + kAhead);
-        }
+      const int j = (i - pc.i0) % kAhead, s = g % S;
+      if (begins) rows_next = row_of(i);
+      if (j == 0) {
+        rows = rows_next;
+        rows_next = row_of(i + kAhead);
+      }
+      {
         const uint32_t goods = (__ballot_sync(kFull, rows >= 0) >> (C::kPages * j)) & ((1u << C::kPages) - 1u);
         if (g >= S && !(ok = wait_w(&empty[t * S + s], g / S - 1))) break;
+        bool copies = true;
 #ifdef KVQ_TEST_HOOKS
-        if (cta == 0 && 2 * g + t == p.withhold) continue;  // its full barrier never completes
+        copies = cta != 0 || 2 * g + t != p.withhold;  // (its full barrier never completes)
 #endif
         uint8_t* dst = smem + SM::ring + t * kRing + s * C::kTile;
         int row[C::kPages];
 #pragma unroll
         for (int y = 0; y < C::kPages; ++y) row[y] = __shfl_sync(kFull, rows, C::kPages * j + y);
-        if (tc::elect_one()) {
-          if (t == 0) bad[g % (2 * S)] = ~goods & ((1u << C::kPages) - 1u);
+        if (copies && tc::elect_one()) {
+          if (t == 0) bad[g % kBadRing] = ~goods & ((1u << C::kPages) - 1u);
           issued[t] = g + 1;
           if (goods == 0)
             mbar_arrive(&full[t * S + s]);  // nothing to copy
@@ -460,6 +522,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         __syncwarp();
       }
+      ++i;
+      fetch = t == 0 && begins;
     }
     if (!ok && lane == 0) fail();
   } else if (warp == kMmaWarp) {
@@ -471,28 +535,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                 : tc::idesc_f8(kRows, kKeys, qf8 ? tc::tc_type(FMT) : tc::kTcE4M3, tc::tc_type(FMT), false, false);
       const int parts = BF || qf8 ? 1 : 2;
       auto desc = [&](uint32_t a) { return C::kSpan == 64 ? tc::sw64_desc(a) : tc::sw128_desc(a); };
-      Pieces it(plan, p.B, v0, v1);
       Piece pc;
       int g = 0, piece = 0;
       bool ok = true;
-      while (ok && it.next(p, pc)) {
+      while (ok && (ok = piece_at(piece, pc)) && pc.i1 > 0) {
         if (!(ok = wait(&qready[piece & 1], piece >> 1))) break;
-        const uint32_t a = tm + kQCol + (piece & 1) * 64;
+        const uint32_t a = sbase + SM::q + (piece & 1) * C::kQParts * C::kQTile;
         ++piece;
         for (int i = pc.i0; i < pc.i1; ++i, ++g) {
           const int s = g % S, buf = g % kBufs;
-          // (over the P that the PV of block g - 4 has read)
+          // (over the P that the PV of block g - 6 has read)
           if (!(ok = wait(&full[s], g / S) && (g < kBufs || wait(&pdone[buf], g / kBufs - 1)))) break;
           tc::tc_fence_after();
           const uint32_t bk = sbase + SM::ring + s * C::kTile, d = tm + buf * kKeys;
 #pragma unroll
           for (int k = 0; k < C::kRow / 32; ++k) {  // 32 bytes of a row a step
-            const uint32_t ob = (k >> 2) * (kKeys * 128) + (k & 3) * 32;
+            const uint32_t oa = (k >> 2) * (kRows * 128) + (k & 3) * 32, ob = (k >> 2) * (kKeys * 128) + (k & 3) * 32;
             if (BF) {
-              tc::mma_f16_ts(d, a + 8 * k, desc(bk + ob), id_qk, k > 0 ? 1u : 0u);
+              tc::mma_f16_ss(d, desc(a + oa), desc(bk + ob), id_qk, k > 0 ? 1u : 0u);
             } else {
-              tc::mma_f8_ts(d, a + 8 * k, desc(bk + ob), id_qk, k > 0 ? 1u : 0u);
-              if (parts > 1) tc::mma_f8_ts(d, a + DH / 4 + 8 * k, desc(bk + ob), id_qk, 1u);
+              tc::mma_f8_ss(d, desc(a + oa), desc(bk + ob), id_qk, k > 0 ? 1u : 0u);
+              if (parts > 1) tc::mma_f8_ss(d, desc(a + C::kQTile + oa), desc(bk + ob), id_qk, 1u);
             }
           }
           mbar_arrive(&sfull[buf]);  // hands on what the K slot's arrival showed (bad)
@@ -511,11 +574,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const uint32_t id_pv = BF ? tc::idesc_bf16(kRows, DH) | (1u << 16)
                                 : tc::idesc_f8(kRows, DH, tc::kTcE5M2, tc::tc_type(FMT), false, true);
       auto desc = [&](uint32_t a) { return C::kSpan == 64 ? tc::sw64_desc(a) : tc::sw128_desc(a); };
-      Pieces it(plan, p.B, v0, v1);
       Piece pc;
       int g = 0, piece = 0;
       bool ok = true;
-      while (ok && it.next(p, pc)) {
+      while (ok && (ok = piece_at(piece, pc)) && pc.i1 > 0) {
         if (piece > 0 && !(ok = wait(ofree, piece - 1))) break;
         ++piece;
         for (int i = pc.i0; i < pc.i1; ++i, ++g) {
@@ -541,101 +603,109 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 tc::mma_f8_ts(tm + kOutCol, tp + k * 32 + y * 8, d, id_pv, k > 0 || y > 0 ? 1u : more);
             }
           }
-          mbar_arrive(&pdone[buf]);  // hands on what the softmax warps' arrivals showed (vnan)
           tc::mma_commit(&pdone[buf]);
           tc::mma_commit(&empty[S + s]);
         }
+        mbar_arrive(odone);  // hands on what the softmax warps' arrivals showed (vnan)
+        tc::mma_commit(odone);
       }
       if (!ok) fail();
       tc::mma_commit(&fin[1]);
       if (!mbar_wait(&fin[1], 0u)) fail();
     }
+  }
   } else {
     // ------------------------------------------------------------ softmax
     const int group = warp / kGroupWarps, quad = warp % kGroupWarps, r = quad * 32 + lane;
     const uint32_t tm = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     uint32_t* anc = reinterpret_cast<uint32_t*>(smem + SM::anc) + group * kMaskWords * kRows;
-    // The query rows of piece number n into tensor memory, scaled, and their logits' scales: by the group
-    // n % 2, while the piece before is worked on.
+    // The query rows of piece number n into shared memory, scaled, and their logits' scales, while the
+    // piece before is worked on: a warp two rows (dh 64: four) at a time, three such steps in flight.
+    // (Code that runs once a piece is fetched as slowly as data, so it is kept short: a thread a row and
+    // its 128 dims unrolled took 9000 to 19000 cycles, in loops 7000 with the small L1 missed twice.)
     auto write_q = [&](const Piece& pc, int n) {
-      const int TQ = kRows / p.G, j0 = pc.tile * TQ, rows = min(pc.s.n - j0, TQ) * p.G;
-      float lscale = (BF || TS ? 1.f : __ldg(p.ks + (p.per_head ? pc.head : 0))) * p.logit_scale;
-      if (quad * 32 < rows) {
-        const bool live = r < rows;
-        const int at = live ? r : 0, hq = pc.head * p.G + at % p.G;
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + ((static_cast<int64_t>(pc.s.q0) + j0 + at / p.G) * p.Hq + hq) * DH);
-        const uint32_t to = tm + kQCol + (n & 1) * 64;
-        // (Loops of few instructions: code that runs once a piece is fetched as slowly as data.  With all
-        // 128 dims unrolled a piece's start took 9000 to 19000 cycles.)
-        if (BF) {
-#pragma unroll 4
-          for (int c = 0; c < DH / 8; ++c) {
-            const uint4 w = __ldg(src + c);
-            tc::tmem_st4(to + 4 * c, w.x, w.y, w.z, w.w);
-          }
-        } else {
-          float by = 1.f;  // what the row's values are multiplied (KVQ_Q_FP8: divided) by
-          if (p.qs) {
-            by = __ldg(p.qs + (p.q_per_head ? hq : 0));
-            lscale *= by;
-          } else {
-            uint32_t top = 0u;  // of the magnitudes' bits
-#pragma unroll 8
-            for (int c = 0; c < DH / 8; ++c) {
-              const uint4 w = __ldg(src + c);
-              top = __vmaxu2(__vmaxu2(__vmaxu2(top, w.x & 0x7FFF7FFFu), __vmaxu2(w.y & 0x7FFF7FFFu, w.z & 0x7FFF7FFFu)), w.w & 0x7FFF7FFFu);
-            }
-            const int e = static_cast<int>(max(top & 0xFFFFu, top >> 16) >> 7);  // its exponent, 0 for subnormals
-            const int a = top == 0u ? 0 : min(126, 134 - max(e, 8));  // (-121 .. 126)
-            by = __int_as_float((a + 127) << 23);  // exact: a power of two, no overflow
-            lscale *= __int_as_float((127 - a) << 23);
-          }
+      constexpr int kLanes = DH / 8, kStep = kSoftWarps * (32 / kLanes);
+      const int TQ = kRows / p.G, j0 = pc.tile * TQ, rows = min(pc.s.n - j0, TQ) * p.G, ql = lane % kLanes;
+      const float lscale0 = (BF || TS ? 1.f : __ldg(p.ks + (p.per_head ? pc.head : 0))) * p.logit_scale;
+      const uint32_t to = sbase + SM::q + (n & 1) * C::kQParts * C::kQTile;
 #pragma unroll 1
-          for (int c = 0; c < DH / 16; ++c) {
-            uint32_t hi[4], lo[4];
-            const uint4 w[2] = {__ldg(src + 2 * c), __ldg(src + 2 * c + 1)};
+      for (int r0 = warp * (32 / kLanes) + lane / kLanes; __any_sync(kFull, r0 < rows); r0 += 3 * kStep) {
+        uint4 w[3];
+        float qs[3];
+#pragma unroll
+        for (int y = 0; y < 3; ++y) {
+          const int at = r0 + y * kStep < rows ? r0 + y * kStep : 0, hq = pc.head * p.G + at % p.G;
+          w[y] = __ldg(reinterpret_cast<const uint4*>(p.q + ((static_cast<int64_t>(pc.s.q0) + j0 + at / p.G) * p.Hq + hq) * DH) + ql);
+          qs[y] = p.qs ? __ldg(p.qs + (p.q_per_head ? hq : 0)) : 1.f;
+        }
+#pragma unroll
+        for (int y = 0; y < 3; ++y) {
+          const int at = r0 + y * kStep;
+          float lscale = lscale0;
+          if (BF) {
+            if (at < rows) tc::sts128(to + tile_at<C::kSpan>(at, 16 * ql), w[y].x, w[y].y, w[y].z, w[y].w);
+          } else {
+            const uint32_t u[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
+            float x[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const uint4& v = w[e >> 1];
-              const uint32_t u0 = e & 1 ? v.z : v.x, u1 = e & 1 ? v.w : v.y;
-              float x[4] = {bf16lo_to_f32(u0), bf16hi_to_f32(u0), bf16lo_to_f32(u1), bf16hi_to_f32(u1)};
-              if (p.qs) {
-                constexpr int F = FMT == KVQ_FMT_E5M2 ? KVQ_FMT_E5M2 : KVQ_FMT_E4M3;
-#pragma unroll 1
-                for (int z = 0; z < 4; ++z) x[z] = __fdiv_rn(x[z], by);
-                hi[e] = f32x2_to_fp8x2<F>(x[0], x[1]) | (static_cast<uint32_t>(f32x2_to_fp8x2<F>(x[2], x[3])) << 16);
-                lo[e] = 0u;
-              } else {
+              x[2 * e] = bf16lo_to_f32(u[e]);
+              x[2 * e + 1] = bf16hi_to_f32(u[e]);
+            }
+            uint32_t hi[2], lo[2] = {0u, 0u};
+            if (p.qs) {
+              constexpr int F = FMT == KVQ_FMT_E5M2 ? KVQ_FMT_E5M2 : KVQ_FMT_E4M3;
+              lscale *= qs[y];
 #pragma unroll
-                for (int z = 0; z < 4; ++z) x[z] *= by;
-                const uint32_t c0 = f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[0], x[1]), c1 = f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[2], x[3]);
+              for (int e = 0; e < 8; ++e) x[e] = __fdiv_rn(x[e], qs[y]);
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                hi[e] = f32x2_to_fp8x2<F>(x[4 * e], x[4 * e + 1]) | (static_cast<uint32_t>(f32x2_to_fp8x2<F>(x[4 * e + 2], x[4 * e + 3])) << 16);
+            } else {
+              uint32_t top = __vmaxu2(__vmaxu2(u[0] & 0x7FFF7FFFu, u[1] & 0x7FFF7FFFu), __vmaxu2(u[2] & 0x7FFF7FFFu, u[3] & 0x7FFF7FFFu));
+#pragma unroll
+              for (int off = 1; off < kLanes; off <<= 1) top = __vmaxu2(top, __shfl_xor_sync(kFull, top, off));
+              const int e = static_cast<int>(max(top & 0xFFFFu, top >> 16) >> 7);  // its exponent, 0 for subnormals
+              const int a = top == 0u ? 0 : min(126, 134 - max(e, 8));  // (-121 .. 126)
+              const float by = __int_as_float((a + 127) << 23);  // exact: a power of two, no overflow
+              lscale *= __int_as_float((127 - a) << 23);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] *= by;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t c0 = f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[4 * e], x[4 * e + 1]);
+                const uint32_t c1 = f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[4 * e + 2], x[4 * e + 3]);
                 const uint32_t h0 = fp8x2_to_f16x2<KVQ_FMT_E4M3>(static_cast<uint16_t>(c0));
                 const uint32_t h1 = fp8x2_to_f16x2<KVQ_FMT_E4M3>(static_cast<uint16_t>(c1));
                 hi[e] = c0 | (c1 << 16);
-                lo[e] = f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[0] - f16lo_to_f32(h0), x[1] - f16hi_to_f32(h0)) |
-                        (static_cast<uint32_t>(f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[2] - f16lo_to_f32(h1), x[3] - f16hi_to_f32(h1))) << 16);
+                lo[e] = f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[4 * e] - f16lo_to_f32(h0), x[4 * e + 1] - f16hi_to_f32(h0)) |
+                        (static_cast<uint32_t>(f32x2_to_fp8x2<KVQ_FMT_E4M3>(x[4 * e + 2] - f16lo_to_f32(h1), x[4 * e + 3] - f16hi_to_f32(h1))) << 16);
               }
             }
-            tc::tmem_st4(to + 4 * c, hi[0], hi[1], hi[2], hi[3]);
-            if (!p.qs) tc::tmem_st4(to + DH / 4 + 4 * c, lo[0], lo[1], lo[2], lo[3]);
+            if (at < rows) {
+              uint8_t* dst = smem + SM::q + (n & 1) * C::kQParts * C::kQTile + tile_at<C::kSpan>(at, 8 * ql);
+              *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+              if (!p.qs) *reinterpret_cast<uint2*>(dst + C::kQTile) = make_uint2(lo[0], lo[1]);
+            }
           }
+          if (at < rows && ql == 0) ls_s[(n & 1) * kRows + at] = fp4::bounded_scale(lscale);
         }
-        ls_s[(n & 1) * kRows + r] = fp4::bounded_scale(lscale);
-        tc::tmem_st_wait();
       }
-      tc::tc_fence_before();
+      fence_proxy_async_smem();  // generic writes -> the tensor core's reads
       __syncwarp();
       if (lane == 0) mbar_arrive(&qready[n & 1]);
     };
-    Pieces it(plan, p.B, v0, v1);
-    Piece nx;
-    int g = 0, piece = 0;
-    bool ok = true, more = it.next(p, nx);
-    if (more && group == 0) write_q(nx, 0);
-    while (more) {
-      const Piece pc = nx;
-      more = it.next(p, nx);
-      if (more && group == ((piece + 1) & 1)) write_q(nx, piece + 1);  // (the S of the piece before are done)
+    int g = 0, piece = 0, written = 0;
+    bool ok = true;
+    for (;;) {
+      Piece pc;
+      while (written <= piece + 1) {  // (the S of the piece that this Q's place was of are done)
+        if (!(ok = __all_sync(kFull, piece_at(written, pc))) || pc.i1 == 0) break;
+        write_q(pc, written++);
+      }
+      if (!ok || !(ok = __all_sync(kFull, piece_at(piece, pc))) || pc.i1 == 0) break;
+      // the logits' scales are other warps'
+      if (!(ok = wait_w(&qready[piece & 1], piece >> 1))) break;
       const int TQ = kRows / p.G, j0 = pc.tile * TQ;
       const int rows = min(pc.s.n - j0, TQ) * p.G;
       const bool live = r < rows, some = quad * 32 < rows;
@@ -675,15 +745,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         return s & ~((bm & 1u ? 0xFFFFu : 0u) | (bm & 2u ? 0xFFFF0000u : 0u));
       };
-      float m = -INFINITY, l = 0.f, sig = 0.f, lscale = 1.f;
+      float m = -INFINITY, l = 0.f, sig = 0.f;
+      const float lscale = live ? ls_s[(piece & 1) * kRows + r] : 1.f;
       const int last = g + pc.i1 - pc.i0 - 1;  // the piece's last block
       for (int i = pc.i0; i < pc.i1; ++i, ++g) {
-        if ((g & 1) != group) continue;
+        if (g % kGroups != group) continue;
         const int k0 = pc.s.first + i * kKeys, buf = g % kBufs;
         const int vslot = g % S;
+        // what the block before left
+        if (g > 0 && !(ok = wait_w(&token[(group + kGroups - 1) % kGroups * 4 + quad], (g - 1) / kGroups))) break;
+        const float before = i > pc.i0 ? m_s[r] : -INFINITY;
         if (!(ok = wait_w(&sfull[buf], g / kBufs))) break;
-        lscale = ls_s[(piece & 1) * kRows + r];
-        const uint32_t bm = bad[g % (2 * S)];
+        const uint32_t bm = bad[g % kBadRing];
         const bool edge = bm != 0u || k0 + kKeys > P || k0 < lo_most;
         if (edge || TS)
           if (!(ok = wait_w(&full[S + vslot], g / S))) break;
@@ -740,11 +813,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
             for (int y = 0; y < 4; ++y) mx4[y] = tc::fmax3(mx4[y], x[e + 2 * y], x[e + 2 * y + 1]);
           const float mx = tc::fmax3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]);
-          // what the block before left (with a first block: nothing)
-          if (g > 0 && !(ok = wait_w(&token[(group ^ 1) * 4 + quad], (g - 1) >> 1))) break;
-          const float before = i > pc.i0 ? m_s[r] : -INFINITY;
-          const bool grow = mx > before + kRescaleThreshold / lscale;
-          if (m != before) {  // (the other group raised it)
+          const bool grow = live && mx > before + kRescaleThreshold / lscale;
+          if (m != before) {  // (another group raised it)
             l *= m == -INFINITY ? 0.f : fast_exp2((m - before) * lscale);
             m = before;
           }
@@ -837,7 +907,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           l += l0 + l1;
           tc::tmem_st_wait();
         } else {  // (tokens count blocks)
-          if (g > 0 && !(ok = wait_w(&token[(group ^ 1) * 4 + quad], (g - 1) >> 1))) break;
           if (lane == 0) mbar_arrive(&token[group * 4 + quad]);
         }
         tc::tc_fence_before();
@@ -845,32 +914,41 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (lane == 0) mbar_arrive(&pfull[buf]);
       }
       if (!ok) break;
-      // ---- the piece's end: rows of O, normalised, half of the dims by each group
-      if (!(ok = wait_w(&pdone[last % kBufs], last / kBufs))) break;
+      // ---- the piece's end: rows of O, normalised, every third run of 16 dims by a group
+      if (!(ok = wait_w(odone, piece))) break;
       tc::tc_fence_after();
       if (tid == 0 && !pc.whole() && pc.i0 == 0)
         p.ws_rec[cta] = make_int4(rows, split.cta_of(pc.base + kSegCost + pc.s.blocks - 1), pc.s.q0 + j0, pc.head);
       const bool put_back = *vnan == 1u + piece;
       // a group's sum is relative to the maximum of its last block, O to that of the last one
-      float2* sums = l_s + (piece & 1) * 2 * kRows;
+      float2* sums = l_s + (piece & 1) * kGroups * kRows;
       sums[group * kRows + r] = make_float2(l, m);
+      const int owner = last % kGroups;
+      if (TS && group == owner && lane == 0) sige_s[(piece & 1) * 4 + quad] = sig;
       __syncwarp();
       if (lane == 0) mbar_arrive(&lfull[quad]);
       if (!(ok = wait_w(&lfull[quad], piece))) break;
       ++piece;
-      const int owner = last & 1;
-      const float2 own = sums[owner * kRows + r], other = sums[(owner ^ 1) * kRows + r];
-      l = own.x + other.x * (other.y == -INFINITY || other.y == own.y ? 1.f : fast_exp2((other.y - own.y) * lscale));
-      const float svs = TS ? sig_s[quad] : BF ? 1.f : __ldg(p.vs + (p.per_head ? pc.head : 0));
+      m = sums[owner * kRows + r].y;
+      l = 0.f;
+#pragma unroll
+      for (int y = 0; y < kGroups; ++y) {
+        const float2 s = sums[y * kRows + r];
+        l += s.x * (s.y == -INFINITY || s.y == m ? 1.f : fast_exp2((s.y - m) * lscale));
+      }
+      const float svs = TS ? sige_s[((piece - 1) & 1) * 4 + quad] : BF ? 1.f : __ldg(p.vs + (p.per_head ? pc.head : 0));
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
       const int64_t part = static_cast<int64_t>(2 * cta + (pc.i0 == 0)) * kRows + r;
       const int64_t qrow = (static_cast<int64_t>(pc.s.q0) + node) * p.Hq + pc.head * p.G + r % p.G;
       if (!pc.whole() && live && group == owner) p.ws_ml[part] = make_float2(fp4::merge_max(m, lscale), l);
       if (some) {
 #pragma unroll 1
-      for (int c = group * (DH / 2); c < (group + 1) * (DH / 2); c += 32) {
-        float o[32];
-        tc::tmem_ld32(tm + kOutCol + c, o);
+      for (int c = 16 * group; c < DH; c += 16 * kGroups) {
+        float o[16];
+        uint32_t bits[16];
+        tc::tmem_ld16(tm + kOutCol + c, bits);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(bits[e]);
         if (put_back && live) {
           const int32_t* table = p.block_tables + static_cast<int64_t>(pc.b) * p.max_blocks;
           for (int k = pc.s.first + pc.i0 * kKeys; k < min(pc.s.L, pc.s.first + pc.i1 * kKeys); ++k) {
@@ -883,11 +961,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             if (blk < 0 || blk >= p.num_blocks) continue;
             const uint8_t* row = p.vc + ((static_cast<int64_t>(blk) * p.Hkv + pc.head) * kBS + k % kBS) * C::kRow;
 #pragma unroll 1
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < 16; ++e) {
               const float v = code_value<FMT>(row, c + e);
               if (!(fabsf(v) <= 3.4028235e38f)) {
 #pragma unroll
-                for (int z = 0; z < 32; ++z) o[z] = z == e ? o[z] + v : o[z];
+                for (int z = 0; z < 16; ++z) o[z] = z == e ? o[z] + v : o[z];
               }
             }
           }
@@ -895,13 +973,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (live && pc.whole()) {
           uint4* dst = reinterpret_cast<uint4*>(p.out + qrow * DH + c);
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
+          for (int y = 0; y < 2; ++y)
             dst[y] = make_uint4(fp4::output2(o[8 * y], o[8 * y + 1], inv, svs), fp4::output2(o[8 * y + 2], o[8 * y + 3], inv, svs),
                                 fp4::output2(o[8 * y + 4], o[8 * y + 5], inv, svs), fp4::output2(o[8 * y + 6], o[8 * y + 7], inv, svs));
         } else if (live) {
           float4* dst = reinterpret_cast<float4*>(p.ws_o + part * DH + c);
 #pragma unroll
-          for (int y = 0; y < 8; ++y)
+          for (int y = 0; y < 4; ++y)
             dst[y] = make_float4(o[4 * y] * inv * svs, o[4 * y + 1] * inv * svs, o[4 * y + 2] * inv * svs, o[4 * y + 3] * inv * svs);
         }
       }
