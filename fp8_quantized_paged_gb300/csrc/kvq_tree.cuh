@@ -61,7 +61,7 @@ constexpr uint32_t kTmemCols = 512, kOutCol = 384;    // the buffers at 0, O at 
 constexpr int kRing = 64 * 1024;  // of K, and of V
 constexpr int kEntries = 1024;  // prefix sums of the plan: of every ceil(B / 1024)th sequence
 constexpr int kKept = 256;      // sequences up to which their lengths are kept beside the prefix sums
-constexpr int kSegCost = 4;     // a segment's start and end, in blocks
+constexpr int kSegCost = 10;     // a segment's start and end, in blocks (128 mixed sequences: 161 us; with 4, 195; with 16, 168)
 constexpr int kMinShare = 4;    // least cost of a CTA's stretch
 constexpr float kBias = 7.f;    // log2 of the factor that the weights carry
 constexpr int kPieces = 32;     // descriptions of pieces
@@ -760,7 +760,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const bool edge = bm != 0u || k0 + kKeys > P || k0 < lo_most;
         if (edge || TS)
           if (!(ok = wait_w(&full[S + vslot], g / S))) break;
-        if (edge) {
+        if (__builtin_expect(edge, 0)) {
           // V's rows that no row sees become zeros; the others lose what is not finite
 #pragma unroll
           for (int y = 0; y < C::kTile / (kGroupWarps * 32 * 16); ++y) {
@@ -799,10 +799,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
           }
           uint32_t seen[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-          if (edge) {
+          if (__builtin_expect(edge, 0)) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) seen[c] = seen32(k0 + 32 * c, bm >> (2 * c));
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              seen[c] = seen32(k0 + 32 * c, bm >> (2 * c));
 #pragma unroll
               for (int e = 0; e < 32; ++e) x[32 * c + e] = seen[c] >> e & 1u ? x[32 * c + e] : -INFINITY;
             }
@@ -835,7 +836,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               sig = s;
             }
           }
-          if (__any_sync(kFull, grow) || (TS && fs != 1.f)) {
+          if (__builtin_expect(__any_sync(kFull, grow) || (TS && fs != 1.f), 0)) {
             const float a = m == -INFINITY ? 0.f : fast_exp2((m - mx) * lscale);
             if (i > pc.i0) {  // O's last writer: the PV of the block before
               if (!(ok = wait_w(&pdone[(g - 1) % kBufs], (g - 1) / kBufs))) break;
@@ -1008,7 +1009,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   }
 }
 
-// ---- the rows of segments that were cut: half a warp a row.  A piece's state is (maximum, sum,
+// ---- the rows of segments that were cut: half a warp a row, or a warp.  A piece's state is (maximum, sum,
 // normalised row); the rows add with weights sum 2^maximum.  Chains of loads (record, states, rows) that
 // nothing but many rows at once hides.
 constexpr int kMergeThreads = 256, kMergeCtas = 5;  // CTAs of an SM
@@ -1054,7 +1055,11 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeCtas) merge_kernel(const 
   constexpr int E = DH / 16;  // values of a lane, in runs of 4
   const int l16 = lane & 15;
   const uint32_t half = 0xFFFFu << (lane & 16);
-  for (int x = blockIdx.x * (kMergeThreads / 16) + (tid >> 4); x < total; x += gridDim.x * (kMergeThreads / 16)) {
+  // Few rows take a warp each, a half of it every second piece.
+  const bool wide = 2 * total <= static_cast<int>(gridDim.x) * (kMergeThreads / 16);
+  const int step = wide ? 2 : 1, sub = wide ? lane >> 4 : 0;
+  const int each = kMergeThreads / 16 / step;  // rows of a CTA
+  for (int x = blockIdx.x * each + (tid >> 4) / step; x < total; x += gridDim.x * each) {
     const int c0 = find_seq(off, kMaxCtas, x), r = x - off[c0];
     const int4 rec = recs[c0];
     const int n = rec.y - c0 + 1;  // pieces
@@ -1081,7 +1086,7 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeCtas) merge_kernel(const 
       M = nm;
       const int k = min(16, n - y0);
 #pragma unroll 4
-      for (int y = 0; y < k; ++y) {
+      for (int y = sub; y < k; y += step) {
         const float wy = __shfl_sync(half, w, (lane & 16) + y);
         const float4* o = reinterpret_cast<const float4*>(p.ws_o + part(y0 + y) * DH) + l16;
 #pragma unroll
@@ -1093,6 +1098,11 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeCtas) merge_kernel(const 
           acc[4 * e + 3] = fmaf(wy, f.w, acc[4 * e + 3]);
         }
       }
+    }
+    if (wide) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += __shfl_xor_sync(kFull, acc[e], 16);
+      if (sub) continue;
     }
     const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
     uint2* dst = reinterpret_cast<uint2*>(p.out + ((static_cast<int64_t>(rec.z) + r / p.G) * p.Hq + rec.w * p.G + r % p.G) * DH) + l16;
