@@ -69,7 +69,9 @@ extern "C" int kvq_tree_attn(const void* q, const int32_t* cu_q_lens, int64_t nu
   if (num_q_tokens > (int64_t(1) << 30) || static_cast<int64_t>(max_blocks_per_seq) * kBS >= (int64_t(1) << 30))
     return KVQ_ERR_UNSUPPORTED;
   const int64_t tiles = num_q_tokens * G <= tree::kRows ? 1 : 16;
-  if (num_seqs * tiles * num_kv_heads * (max_blocks_per_seq / 4 + 8) >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
+  // (the sum of all costs: a tile has at most max_blocks_per_seq / 4 + 1 blocks)
+  if (num_seqs * tiles * num_kv_heads * (max_blocks_per_seq / 4 + 2 + tree::kSegCost) >= (int64_t(1) << 31))
+    return KVQ_ERR_UNSUPPORTED;
   if (num_blocks > ((int64_t(1) << 31) - 1) / (static_cast<int64_t>(num_kv_heads) * kBS)) return KVQ_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u) ||

@@ -129,7 +129,7 @@ KVQ_API size_t kvq_tree_workspace_size(int num_q_heads, int num_kv_heads, int he
  *   workspace       device scratch of kvq_tree_workspace_size bytes, 256-byte
  *                   aligned; calls that may run at the same time (two graphs
  *                   among them) need one each
- *   out             bf16 [num_q_tokens][num_q_heads][head_dim]
+ *   out             bf16 [num_q_tokens][num_q_heads][head_dim]; no input
  *   dev_status      optional; KVQ_DEV_BAD_BLOCK (the page is masked out),
  *                   KVQ_DEV_BAD_SEQLEN (L_b < n_b or L_b > max_blocks_per_seq
  *                   * block_size: zero rows), KVQ_DEV_BAD_QLEN (n_b past
@@ -149,7 +149,7 @@ KVQ_API size_t kvq_tree_workspace_size(int num_q_heads, int num_kv_heads, int he
  * Limits: num_seqs <= 4096; num_kv_heads <= 256; num_q_heads / num_kv_heads
  * <= 8; num_blocks * num_kv_heads * block_size < 2^31; max_blocks_per_seq *
  * block_size < 2^30; num_seqs * num_kv_heads * T * (max_blocks_per_seq / 4 +
- * 8) < 2^31 with T = 1 where num_q_tokens * num_q_heads / num_kv_heads <=
+ * 12) < 2^31 with T = 1 where num_q_tokens * num_q_heads / num_kv_heads <=
  * 128, else 16; beyond them KVQ_ERR_UNSUPPORTED.  num_q_tokens == 0 is a no-op.
  */
 KVQ_API int kvq_tree_attn(const void* q, const int32_t* cu_q_lens, int64_t num_q_tokens,
@@ -189,7 +189,7 @@ typedef struct {
  * rise; rows are read before any of them is written over.
  *
  *   caches          host array of num_caches tensors (any number, kinds mixed),
- *                   all of num_blocks blocks and num_kv_heads heads
+ *                   all of num_blocks blocks and num_kv_heads heads; each once
  *   accepted        int32 [num_seqs][max_path]
  *   num_accepted    int32 [num_seqs], 0 .. min(n_b, max_path)
  *   new_lens        int32 [num_seqs], out; not seq_lens
@@ -212,7 +212,7 @@ KVQ_API int kvq_tree_commit(const kvq_rows* caches, int num_caches, int64_t num_
 
 /*
  * A pool of pages: KVQ_POOL_WORDS(num_blocks) int32 words on the device.
- *   [0]   0 between calls    [1] how many pages are free    [2], [3] 0
+ *   [0], [2], [3]   0    [1]   how many pages are free
  *   [4 + i]                  how many table entries hold page i
  *   [4 + num_blocks + i / 32], bit i % 32    page i is free
  * The calls below take the lowest free pages first, so tables and pool

@@ -45,7 +45,7 @@ def call(lib_, g):
 @pytest.mark.parametrize("seqs,hq,hkv,dh,fmt,gran", [
     ([(32768, 16)], 32, 8, 128, E4M3, PER_HEAD),              # a segment over many CTAs
     ([(300, 9)] * 200, 8, 2, 64, E4M3, PER_TOKEN_HEAD),       # several pieces a CTA
-    ([(8000, 70)], 16, 8, 128, BF16, PER_HEAD)])              # rings of four blocks
+    ([(20000, 70)], 16, 8, 128, BF16, PER_HEAD)])             # rings of four blocks
 @pytest.mark.parametrize("at", [0, 1, 2, 5, 12, 13])          # twice CTA 0's block, K or V
 def test_copy_withheld(kvq, hooked, seqs, hq, hkv, dh, fmt, gran, at):  # noqa: F811
     g = lib.OnGpu(kvq, lib.TreeBatch(seqs, hq, hkv, dh, fmt, gran, seed=at))
