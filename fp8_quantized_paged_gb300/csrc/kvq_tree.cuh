@@ -306,10 +306,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
   // A parity wait for phase k of a barrier is sound while it has completed k or k + 1 phases.  All roles
   // take their barriers' phases in order, except that the softmax looks at V's full barriers (edge blocks)
-  // and at pdone (where O is rescaled) now and then: all earlier phases are complete then, as the S of
-  // block g comes after the PV of block g - 6, and PVs go in order; and the next ones come after a block
-  // that this warp has not begun with.  (Not at a K slot's: the next K may land while a warp is late.
-  // Nor at pdone for a piece's end: a group that had no block of it may be several phases behind.)
+  // and at pdone now and then.  All earlier phases are complete then: the S of block g comes after the PV
+  // of block g - 6, PVs go in order, and a V's slot has had its last V once the PV of block g - S is done.
+  // And the next phases come after a block that this warp has not begun with.  (Not at a K slot's full
+  // barrier: the next K may land while a warp is late.  Nor at pdone for a piece's end: a group that had
+  // no block of it may be several phases behind.)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
@@ -758,8 +759,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (!(ok = wait_w(&sfull[buf], g / kBufs))) break;
         const uint32_t bm = bad[g % kBadRing];
         const bool edge = bm != 0u || k0 + kKeys > P || k0 < lo_most;
-        if (edge || TS)
+        if (edge || TS) {
+          // (with rings of fewer blocks than buffers, the slot's last V may still be to come: it is there
+          // once the PV of block g - S is done)
+          if (S < kBufs && g >= S && !(ok = wait_w(&pdone[(g - S) % kBufs], (g - S) / kBufs))) break;
           if (!(ok = wait_w(&full[S + vslot], g / S))) break;
+        }
         if (__builtin_expect(edge, 0)) {
           // V's rows that no row sees become zeros; the others lose what is not finite
 #pragma unroll

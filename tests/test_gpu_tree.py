@@ -305,3 +305,19 @@ def test_one_node_is_the_decode(kvq):
     ref, bound = b.reference()
     torch.cuda.synchronize()
     assert bool(((out.double() - ref).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("fmt,gran", [(BF16, PER_HEAD), (E4M3, PER_TOKEN_HEAD), (E4M3, PER_HEAD)])
+@pytest.mark.parametrize("dh", [128, 64])
+def test_edges_behind_long_runs(kvq, fmt, gran, dh):
+    """Edge blocks, whose V is looked at and cleared, behind many others of the same CTA: a V that is still to
+    come into the slot before is not touched.  (Rings hold 4 to 16 blocks, and 6 are in flight.)"""
+    seqs = [(700 + 226 * i, 30) for i in range(16)]
+    g = OnGpu(kvq, TreeBatch(seqs, 28, 4, dh, fmt, gran, seed=dh))
+    g.call()
+    g.check()
+    first = g.out.clone()
+    for _ in range(30):
+        g.out.fill_(7.0)
+        g.call()
+        assert torch.equal(g.out.view(torch.uint8), first.view(torch.uint8))
