@@ -155,8 +155,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) rope_kernel(const __grid
       for (int i = 0; i < NA; ++i) {
         const int64_t at = __ldg(p.pos + static_cast<int64_t>(axes[i]) * p.tokens + t);
         const unsigned long long turn = static_cast<unsigned long long>(at) * turns[i];
-        // the upper 32 bits as [-2^31, 2^31) of 2^32 to a turn; sincospif takes half turns
-        sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &n[i], &c[i]);
+        // the upper 32 bits, 2^32 to a turn: the nearest quarter turn, and what is left of it, at most an
+        // eighth of a turn, which binary32 holds within 2^-27 half turns (sincospif takes half turns)
+        const uint32_t a = static_cast<uint32_t>(turn >> 32), quarter = (a + 0x20000000u) >> 30;
+        float sine, cosine;
+        sincospif(static_cast<float>(static_cast<int32_t>(a - (quarter << 30))) * 0x1p-31f, &sine, &cosine);
+        c[i] = __uint_as_float(__float_as_uint(quarter & 1u ? sine : cosine) ^ ((quarter + 1u & 2u) << 30));
+        n[i] = __uint_as_float(__float_as_uint(quarter & 1u ? cosine : sine) ^ ((quarter & 2u) << 30));
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
