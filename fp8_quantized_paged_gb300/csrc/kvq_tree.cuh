@@ -11,17 +11,29 @@
 // states in the workspace, which a second, dependent launch merges.  (A last arriver would read a
 // piece of 64 KB of each of, say, 19 CTAs alone.)
 //
-//   warps 8, 9 (producers of K, of V)  copy a block's pages by TMA into rings of 64 KB
-//   warp 10 (issuer)  one lane: S = Q K^T (M 128, N 64), up to six blocks ahead
-//   warp 11 (issuer)  one lane: O += P V (M 128, N dh), V as it lies (token-major: an MN-major operand)
-//   warps 0-3, 4-7 (softmax of the even, of the odd blocks)  thread = row (TMEM lane): mask, running
+//   warps 12, 13 (producers of K, of V)  copy a block's pages by TMA into rings of 64 KB; the first
+//     also works out the CTA's pieces, one ahead, and describes them to the others in shared memory
+//   warp 14 (issuer)  one lane: S = Q K^T (M 128, N 64), up to six blocks ahead
+//   warp 15 (issuer)  one lane: O += P V (M 128, N dh), V as it lies (token-major: an MN-major operand)
+//   warps 0-3, 4-7, 8-11 (softmax of every third block)  thread = row (TMEM lane): mask, running
 //     maximum, P over the S columns that it came from.  The maximum is handed from block to block, a
-//     warp of one group to its other's (m_s): it is wanted before the weights, and changes rarely
+//     warp of one group to the next one's (m_s): it is wanted before the weights, and changes rarely
 // Tensor memory: six buffers of S and P (64 columns each) and O (128).  A block's way through S,
-// softmax and PV takes about 4300 cycles, of which the matrix steps' and barriers' latencies are most;
+// softmax and PV takes about 5000 cycles, of which the matrix steps' and barriers' latencies are most;
 // six blocks in flight hide it.  Q lies in shared memory, twice: the next piece's is written while this
-// one's is in use.  (Two CTAs an SM with two buffers each: 2450 cycles for 64 keys of each of both.
-// Four buffers, and Q in tensor memory, whose steps take 32 cycles where these take 48: 1080 for 64 keys.)
+// one's is in use.
+//
+// What bounds it: instructions.  64 keys of 128 rows take some 1100 cycles, of which the tensor cores
+// are busy 770, and each scheduler issues some 900 instructions: 64 weights of a row and their parts
+// are about 8 each (a softmax thread), the roles beside it the rest.  A segment's start and end cost
+// ten blocks.  32 trees of 16 nodes (64 rows) over 2049 tokens of 8 KV heads, 134 MB: 56 us, of which
+// the merge 6; one of 64 nodes over 32768: 56 us; 128 of 24 over 17 to 16384 with a window of 4096:
+// 163 us.  What was tried and is slower, in us for the first and the second of these: two CTAs an SM
+// with two buffers each 77 and 78; two groups, four buffers and Q in tensor memory (steps of 32 cycles
+// and not 48) 58 and 58; the maximum handed on behind S's loads, so that the groups go in step, 61 and
+// 60; two producers each of K and V and two issuers of S, the logits read twice so that 608 threads
+// find registers, 62 and 63; the next piece's Q written between blocks 66 and 63 (code that is rare
+// but lies in the loop).
 // The products run on the codes as they are: no conversion, no registers between memory and the
 // tensor cores.  For that Q and P are split into parts that 8 bits hold:
 //   q  2^a q = q1 + q2, E4M3 both, 2^a taking the row's largest to [2^7, 2^8): bf16's 8 bits are
