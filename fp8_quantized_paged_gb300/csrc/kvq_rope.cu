@@ -142,8 +142,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) rope_kernel(const __grid
         if (s >= steps || (s - sq - sk) * RW + g >= p.hkv) return;
         src = p.v + t * p.v_stride + ((s - sq - sk) * RW + g) * DH;
       }
-      a = __ldg(reinterpret_cast<const uint4*>(src + d0));
-      b = __ldg(reinterpret_cast<const uint4*>(src + d1));
+      // (not as constant data: q_out may be q)
+      a = __ldcg(reinterpret_cast<const uint4*>(src + d0));
+      b = __ldcg(reinterpret_cast<const uint4*>(src + d1));
     };
     uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
     load(first, a, b);
