@@ -236,3 +236,67 @@ def test_two_streams_at_once(kvq):
     torch.cuda.synchronize()
     for g, w in zip(gs, want):
         assert torch.equal(g.out.view(torch.uint8), w.view(torch.uint8)) and int(g.st) == 0
+
+
+def test_caches_past_32_bits(kvq):
+    """The same step on pages at the end of caches of 4.4 GB: the small caches' bits."""
+    far, small, hkv, dh = 270000 - 40, 40, 8, 128
+    N, g = 30, torch.Generator().manual_seed(5)
+    qkv = torch.randn(N, (16 + 2 * hkv) * dh, generator=g).to(torch.bfloat16).cuda()
+    q, k, v = (x.unflatten(1, (-1, dh)) for x in qkv.split([16 * dh, hkv * dh, hkv * dh], 1))
+    fill = torch.randint(0, 120, (2, small, hkv, BS, dh), generator=g, dtype=torch.uint8).cuda()
+    scale, turns, pos = torch.full((hkv,), 0.02, device="cuda"), kvq.rope_turns([0.3 ** i for i in range(64)]), torch.arange(N, dtype=torch.int32, device="cuda")
+    parents, accepted = i32([-1] + [i // 2 for i in range(N - 1)]), i32([[0, 2, 5, 12]])
+    ws, cu = kvq.new_tree_workspace(16, hkv, dh), i32([0, N])
+    results = []
+    for at in (0, far):
+        caches = [torch.empty(at + small, hkv, BS, dh, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        for c, f in zip(caches, fill):
+            c[at:] = f
+        bt = (torch.arange(30, dtype=torch.int32, device="cuda").flip(0) + at)[None].contiguous()
+        lens, new, st = i32([450 + N]), i32([0]), i32([0])
+        t = torch.arange(450, 450 + N, device="cuda")
+        slots = bt[0][t // BS].long() * BS + t % BS
+        rot, out = torch.empty_like(q).contiguous(), torch.empty(N, 16, dh, dtype=torch.bfloat16, device="cuda")
+        kvq.kvq_rope_write(q, k, v, pos, turns, None, None, None, 0.0, False, slots, *caches, scale, scale, PER_HEAD, E4M3, rot, st)
+        kvq.kvq_tree_attn(rot, cu, parents, *caches, bt, lens, scale, scale, PER_HEAD, E4M3, 0, ws, out, st)
+        kvq.kvq_tree_commit(caches, cu, bt, lens, accepted, i32([4]), new, st)
+        kvq.kvq_copy_pages(caches, i32([[at + 3, at + 39], [at + 29, at + 35]]), st)
+        torch.cuda.synchronize()
+        assert int(st) == 0 and int(new) == 454
+        results.append([rot, out] + [c[at:].clone() for c in caches])
+        del caches
+    for a, b in zip(*results):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_batches_without_a_tree(kvq):
+    """Sequences of no nodes, empty ones among them: nothing is read of them and no row is written."""
+    for lens in ([0, 20, 0], [0], [300] * 500):
+        B = len(lens)
+        kc = torch.full((4, HKV, BS, 64), 0x7F, dtype=torch.uint8, device="cuda")
+        q, st = torch.randn(3, HQ, 64, device="cuda").to(torch.bfloat16), i32([0])
+        out = torch.full_like(q, 7.0)
+        bt = torch.full((B, 20), -1, dtype=torch.int32, device="cuda")
+        kvq.kvq_tree_attn(q, i32([0] * (B + 1)), None, kc, kc.clone(), bt, i32(lens), *[torch.ones(1, device="cuda")] * 2, 0, E4M3, 0,
+                          kvq.new_tree_workspace(HQ, HKV, 64), out, st)
+        torch.cuda.synchronize()
+        assert int(st) == 0 and bool((out == 7.0).all())
+
+
+def test_another_stream_by_argument(kvq):
+    """A call on a stream that is not the current one is ordered with that stream's work."""
+    b = lib.TreeBatch([(2000, 20)], HQ, HKV, 128, E4M3, seed=6)
+    g = lib.OnGpu(kvq, b)
+    want = g.call().clone()
+    s, q = torch.cuda.Stream(), b.q.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        late = torch.zeros_like(q)
+        torch.cuda._sleep(20_000_000)
+        late.copy_(q)
+    g.out.fill_(7.0)
+    torch.cuda.current_stream().synchronize()
+    g.call(q=late, stream=s.cuda_stream)
+    s.synchronize()
+    assert torch.equal(g.out.view(torch.uint8), want.view(torch.uint8)) and int(g.st) == 0
