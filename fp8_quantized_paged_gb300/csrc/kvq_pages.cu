@@ -9,6 +9,9 @@
 // that a prefix sum over num_blocks / 32 words (200 000 pages are 25 KB, where
 // their counts are 800 KB) whose result depends on nothing but the pool:
 // giving pages back in any order, by atomics, leaves the same pool.
+#include <algorithm>
+#include <functional>
+
 #include "../../include/kvq_step.h"
 #include "kvq_common.cuh"
 #include "kvq_host.h"
@@ -526,6 +529,18 @@ static int check_rows(const kvq_rows* caches, int num_caches, int64_t num_blocks
   return KVQ_OK;
 }
 
+// Whether a cache is listed twice: its rows would be moved twice.  Lists mostly rise; others are sorted.
+constexpr int kMaxCommitCaches = 1024;
+static bool listed_twice(const kvq_rows* caches, int n) {
+  bool rises = true;
+  for (int i = 1; i < n; ++i) rises = rises && std::less<const void*>()(caches[i - 1].data, caches[i].data);
+  if (rises) return false;
+  const void* at[kMaxCommitCaches];
+  for (int i = 0; i < n; ++i) at[i] = caches[i].data;
+  std::sort(at, at + n, std::less<const void*>());
+  return std::adjacent_find(at, at + n) != at + n;
+}
+
 static int check_pool(const int32_t* pool, int64_t num_blocks, int max_blocks, int n) {
   if (num_blocks <= 0 || max_blocks <= 0 || n < 0) return KVQ_ERR_ARG;
   if (!pool) return KVQ_ERR_NULL;
@@ -563,7 +578,9 @@ extern "C" int kvq_tree_commit(const kvq_rows* caches, int num_caches, int64_t n
   if (num_seqs < 0 || max_path < 0 || max_blocks_per_seq <= 0) return KVQ_ERR_ARG;
   if (num_seqs > 0 && (!cu_q_lens || !block_tables || !seq_lens || !num_accepted || !new_lens || (max_path > 0 && !accepted)))
     return KVQ_ERR_NULL;
-  if (num_seqs > 65535 || max_path > 4096 || max_blocks_per_seq > INT32_MAX / kTok) return KVQ_ERR_UNSUPPORTED;
+  if (num_seqs > 65535 || max_path > 4096 || max_blocks_per_seq > INT32_MAX / kTok || num_caches > kMaxCommitCaches)
+    return KVQ_ERR_UNSUPPORTED;
+  if (listed_twice(caches, num_caches)) return KVQ_ERR_ARG;
   if (!aligned4(cu_q_lens) || !aligned4(block_tables) || !aligned4(seq_lens) || !aligned4(accepted) ||
       !aligned4(num_accepted) || !aligned4(new_lens))
     return KVQ_ERR_ALIGN;

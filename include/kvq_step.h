@@ -188,8 +188,9 @@ typedef struct {
  * accepted[b] holds node numbers from the tree's first level down, so they
  * rise; rows are read before any of them is written over.
  *
- *   caches          host array of num_caches tensors (any number, kinds mixed),
- *                   all of num_blocks blocks and num_kv_heads heads; each once
+ *   caches          host array of num_caches tensors (kinds mixed), all of
+ *                   num_blocks blocks and num_kv_heads heads; at most 1024,
+ *                   none twice (KVQ_ERR_ARG)
  *   accepted        int32 [num_seqs][max_path]
  *   num_accepted    int32 [num_seqs], 0 .. min(n_b, max_path)
  *   new_lens        int32 [num_seqs], out; not seq_lens
@@ -282,7 +283,7 @@ KVQ_API int kvq_pages_fork(int32_t* pool, int64_t num_blocks, const int32_t* tab
  * kvq_copy_pages -- page copies[i][0] onto page copies[i][1] of every cache,
  * all heads, for every i < num_copies with neither below 0.  Pages outside
  * [0, num_blocks): KVQ_DEV_BAD_BLOCK, not copied.  Targets are distinct and no
- * pair's source.  caches as for kvq_tree_commit.  num_copies <= 2^20.
+ * pair's source.  caches as for kvq_tree_commit, but of any number.  num_copies <= 2^20.
  */
 KVQ_API int kvq_copy_pages(const kvq_rows* caches, int num_caches, int64_t num_blocks,
                            int num_kv_heads, int block_size, const int32_t* copies,

@@ -87,7 +87,7 @@ def call(clib, name, **over):
     assert set(over) <= set(args)
     args.update(over)
     if args.get("caches", 0) is None:
-        args["caches"] = (Rows * max(1, args["nc"]))(*([Rows(A, 128, 0)] * max(0, args["nc"])))
+        args["caches"] = (Rows * max(1, args["nc"]))(*(Rows(A + 4096 * i, 128, 0) for i in range(max(0, args["nc"]))))
     out = []
     for n, t, _ in CALLS[name][1]:
         out.append((_vp(args[n]) if args[n] else None) if t is _vp else args[n])
@@ -131,7 +131,9 @@ REFUSED = {
         (dict(cu=0), NULL), (dict(bt=0), NULL), (dict(sl=0), NULL), (dict(path=0), NULL), (dict(taken=0), NULL), (dict(new=0), NULL),
         (dict(B=-1), ARG), (dict(most=-1), ARG), (dict(mb=0), ARG), (dict(B=65536), UNSUPPORTED), (dict(most=4097), UNSUPPORTED),
         (dict(mb=1 << 28), UNSUPPORTED), (dict(cu=A + 1), ALIGN), (dict(path=A + 2), ALIGN), (dict(new=A + 66), ALIGN),
-        (dict(new=A), ARG)],  # the lengths in place
+        (dict(new=A), ARG),  # the lengths in place
+        (dict(nc=3, caches=(Rows * 3)(Rows(A, 64, 8), Rows(A + 64, 64, 8), Rows(A, 64, 8))), ARG),  # a cache twice
+        (dict(nc=2, caches=(Rows * 2)(Rows(A, 64, 8), Rows(A, 4, 0))), ARG), (dict(nc=1025), UNSUPPORTED)],
     "kvq_copy_pages": ROWS + [(dict(copies=0), NULL), (dict(n=-1), ARG), (dict(n=(1 << 20) + 1), UNSUPPORTED), (dict(copies=A + 2), ALIGN)],
     "kvq_pages_init": POOL,
     "kvq_pages_alloc": TABLES,
