@@ -1,4 +1,6 @@
 // kvq_tree.cu -- entry point and launches of the attention over drafted trees.
+#include <atomic>
+
 #include "kvq_tree.cuh"
 
 namespace kvq {
@@ -31,6 +33,11 @@ static int ctas_of(int sms) { return std::min(sms, kMaxCtas); }
 }  // namespace kvq
 
 using namespace kvq;
+
+#ifdef KVQ_TEST_HOOKS
+static std::atomic<int> g_late{-1};
+extern "C" __attribute__((visibility("default"))) void kvq_test_late_warp(int warp) { g_late.store(warp); }
+#endif
 
 extern "C" size_t kvq_tree_workspace_size(int num_q_heads, int num_kv_heads, int head_dim, int num_sms) {
   if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > 8) return 0;
@@ -128,8 +135,9 @@ extern "C" int kvq_tree_attn(const void* q, const int32_t* cu_q_lens, int64_t nu
   p.status = dev_status;
 #ifdef KVQ_TEST_HOOKS
   p.withhold = test_withheld();
+  p.late = g_late.load();
 #else
-  p.withhold = -1;
+  p.withhold = p.late = -1;
 #endif
   const uint64_t rows = static_cast<uint64_t>(num_blocks) * num_kv_heads * kBS;
   CUtensorMap tk, tv;

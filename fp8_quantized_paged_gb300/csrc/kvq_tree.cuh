@@ -79,6 +79,8 @@ constexpr float kBias = 7.f;    // log2 of the factor that the weights carry
 constexpr int kPieces = 32;     // descriptions of pieces
 constexpr int kBadRing = 32;
 constexpr int kMaskWords = KVQ_TREE_MAX_NODES / 32;
+constexpr int kScaleBufs = 3;   // pieces whose logits' scales are in shared memory
+constexpr int kNanMarks = 2;    // pieces whose mark of a NaN or infinity is
 
 struct TreeParams {
   const uint16_t* q;
@@ -101,6 +103,7 @@ struct TreeParams {
   uint16_t* out;
   uint32_t* status;
   int withhold;  // test builds: position of CTA 0's stream that is never copied; -1
+  int late;      // test builds: softmax warp that sleeps before it reads what other quarters' warps write; -1
 };
 
 struct TreeWs {
@@ -138,12 +141,13 @@ struct TreeSmem {
   static constexpr int tsc = ring + 2 * kRing;  // per-(token, head) scales, K's and V's, that land with a V
   static constexpr int bars = tsc + (TS ? 2 * S * kKeys * 4 : 0);
   static constexpr int kBars = 4 * S + 3 * kBufs + 2 + 1 + kGroups * 4 + 4 + 2 + 1 + kPieces;
-  static constexpr int misc = bars + kBars * 8;  // tmem address, abort, NaN mark, bad sequences, bad[kBadRing], issued[2], warp sums
+  // tmem address, abort, bad sequences, NaN marks, bad[kBadRing], issued[2], warp sums
+  static constexpr int misc = bars + kBars * 8;
   // [kRows] running maximum, [4] largest value scale by quarter of the rows, [2][4] that at a piece's end
-  static constexpr int m = misc + (6 + kBadRing + kTreeThreads / 32) * 4;
+  static constexpr int m = misc + (5 + kNanMarks + kBadRing + kTreeThreads / 32) * 4;
   static constexpr int l = (m + (kRows + 12) * 4 + 7) / 8 * 8;  // [2][kGroups][kRows] sums and their maxima, by piece
-  static constexpr int ls = l + 2 * kGroups * kRows * 8;                 // [2][kRows] logits' scales, by piece
-  static constexpr int anc = ls + 2 * kRows * 4;                        // [kGroups][kMaskWords][kRows] ancestors
+  static constexpr int ls = l + 2 * kGroups * kRows * 8;                 // [kScaleBufs][kRows] logits' scales, by piece
+  static constexpr int anc = ls + kScaleBufs * kRows * 4;               // [kGroups][kMaskWords][kRows] ancestors
   static constexpr int pieces = (anc + kGroups * kMaskWords * kRows * 4 + 15) / 16 * 16;  // [kPieces] of 12 words
   static constexpr int plan = pieces + kPieces * 48;
   static constexpr int total = plan + (kEntries + 1) * 4 + 1024;
@@ -298,13 +302,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + SM::misc);
   volatile uint32_t* tmem_slot = misc;
   volatile uint32_t* abort_flag = misc + 1;
-  volatile uint32_t* vnan = misc + 2;   // 1 + the last piece that met a NaN or infinity to put back
-  volatile uint32_t* any_bad = misc + 3;  // a sequence has an error
-  volatile uint32_t* bad = misc + 4;    // [kBadRing] masked pages of block g: rewritten for block g + 32,
+  volatile uint32_t* any_bad = misc + 2;  // a sequence has an error
+  volatile uint32_t* vnan = misc + 3;   // [kNanMarks] 1 + the last piece that met a NaN or infinity to put back
+  volatile uint32_t* bad = vnan + kNanMarks;  // [kBadRing] masked pages of block g: rewritten for block g + 32,
                                         // whose K waits for the S of block g + 32 - S, and that for the PV of
                                         // block g + 26 - S
-  volatile int32_t* issued = reinterpret_cast<volatile int32_t*>(misc + 4 + kBadRing);  // [2] blocks copied
-  volatile int32_t* warp_sum = reinterpret_cast<volatile int32_t*>(misc + 6 + kBadRing);
+  volatile int32_t* issued = reinterpret_cast<volatile int32_t*>(bad + kBadRing);  // [2] blocks copied
+  volatile int32_t* warp_sum = issued + 2;
   // Piece n's description in [n % kPieces].  It is rewritten for piece n + 32, when all blocks of piece
   // n + 30 but its last have their K's slots: the PV of block g - S - 7 of the last block g is done then, and
   // every role past the piece that has it, which at a block a piece is n + 30 - S - 7 > n.
@@ -323,6 +327,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   // And the next phases come after a block that this warp has not begun with.  (Not at a K slot's full
   // barrier: the next K may land while a warp is late.  Nor at pdone for a piece's end: a group that had
   // no block of it may be several phases behind.)
+  //
+  // What a softmax warp writes for others between pieces: at the start of piece n the logits' scales of piece
+  // n + 1 (rows of any quarter), in its edge blocks the mark of a NaN, at its end its group's sums.  A piece's
+  // end holds up only a quarter's three warps (lfull), so a warp of another quarter may still be at the start
+  // of piece n, its scales not read, when one is in piece n + 1; not in n + 2, whose way leads through the PV
+  // of piece n + 1 (odone) and so through every warp's end of piece n (ofree).  So scales are kept for three
+  // pieces, marks for two (sums too, though a warp that writes them is past that PV).
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
@@ -347,7 +358,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     mbar_init(&fin[0], 1);
     mbar_init(&fin[1], 1);
     *abort_flag = 0u;
-    *vnan = 0u;
+    for (int i = 0; i < kNanMarks; ++i) vnan[i] = 0u;
     fence_mbar_init();
   }
   if (warp == kProdWarp && lane == 0) {
@@ -701,12 +712,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               if (!p.qs) *reinterpret_cast<uint2*>(dst + C::kQTile) = make_uint2(lo[0], lo[1]);
             }
           }
-          if (at < rows && ql == 0) ls_s[(n & 1) * kRows + at] = fp4::bounded_scale(lscale);
+          if (at < rows && ql == 0) ls_s[(n % kScaleBufs) * kRows + at] = fp4::bounded_scale(lscale);
         }
       }
       fence_proxy_async_smem();  // generic writes -> the tensor core's reads
       __syncwarp();
       if (lane == 0) mbar_arrive(&qready[n & 1]);
+    };
+    auto late = [&] {
+#ifdef KVQ_TEST_HOOKS
+      if (warp == p.late) __nanosleep(20000);
+#endif
     };
     int g = 0, piece = 0, written = 0;
     bool ok = true;
@@ -759,7 +775,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         return s & ~((bm & 1u ? 0xFFFFu : 0u) | (bm & 2u ? 0xFFFF0000u : 0u));
       };
       float m = -INFINITY, l = 0.f, sig = 0.f;
-      const float lscale = live ? ls_s[(piece & 1) * kRows + r] : 1.f;
+      late();
+      const float lscale = live ? ls_s[(piece % kScaleBufs) * kRows + r] : 1.f;
       const int last = g + pc.i1 - pc.i0 - 1;  // the piece's last block
       for (int i = pc.i0; i < pc.i1; ++i, ++g) {
         if (g % kGroups != group) continue;
@@ -791,7 +808,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               const uint4 f = make_uint4(not_finite<FMT>(w.x), not_finite<FMT>(w.y), not_finite<FMT>(w.z), not_finite<FMT>(w.w));
               if (f.x | f.y | f.z | f.w) {
                 *at = make_uint4(w.x & ~f.x, w.y & ~f.y, w.z & ~f.z, w.w & ~f.w);
-                *vnan = 1u + piece;
+                vnan[piece % kNanMarks] = 1u + piece;
               }
             }
           }
@@ -937,7 +954,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       tc::tc_fence_after();
       if (tid == 0 && !pc.whole() && pc.i0 == 0)
         p.ws_rec[cta] = make_int4(rows, split.cta_of(pc.base + kSegCost + pc.s.blocks - 1), pc.s.q0 + j0, pc.head);
-      const bool put_back = *vnan == 1u + piece;
+      late();
+      const bool put_back = vnan[piece % kNanMarks] == 1u + piece;
       // a group's sum is relative to the maximum of its last block, O to that of the last one
       float2* sums = l_s + (piece & 1) * kGroups * kRows;
       sums[group * kRows + r] = make_float2(l, m);
