@@ -39,8 +39,11 @@
 //   q  2^a q = q1 + q2, E4M3 both, 2^a taking the row's largest to [2^7, 2^8): bf16's 8 bits are
 //     4 + 4, so exact within 2^8 of the largest; the parts add in one accumulator
 //   P  weights times 2^7 as f16, then p1 + p2 + p3, E5M2 each: f16's upper byte is an E5M2 number,
-//     so a part is a byte of what the parts before left, subtracted exactly in f16, the last one
-//     rounded: 2^-9 of the weight, or 2^-24 of the row's largest.  Three
+//     so a part is the rounded byte of what the parts before left, subtracted exactly in f16.  What the
+//     first two leave of 11 bits is a multiple of 1 and at most 8 in units of the last one, 3 bits: the
+//     parts add up to the f16, but for what lies below E5M2's least step: 2^-11 of the weight and 2^-24 of
+//     the row's largest.  (Parts cut and not rounded, the last one excepted, have 9 bits and take 5
+//     instructions a pair of weights, not 7: 1 to 3 % of the time.)  Three
 //     E5M2 parts and not two E4M3 ones, whose range of 2^17 would drop a long context's small
 //     weights beside one large one
 // Over bf16 caches the operands are bf16: q itself, P as two parts.
@@ -261,11 +264,13 @@ KVQ_DEVI uint32_t hsub2(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// The E5M2 parts of two weights (f16, not negative), each the upper byte of a half of c[k].
+// The E5M2 parts of two weights (f16, not negative, at most 2^15), each the upper byte of a half of c[k].
+// Half a step added rounds a magnitude; no carry leaves a half.  A NaN becomes a zero: it is in the row's sum.
 KVQ_DEVI void weight_parts(uint32_t h, uint32_t (&c)[3]) {
-  c[0] = h;
-  c[1] = hsub2(h, h & 0xFF00FF00u);
-  c[2] = hsub2(c[1], c[1] & 0xFF00FF00u) + 0x00800080u;  // (rounds; no carry leaves a half)
+  c[0] = h + 0x00800080u;
+  const uint32_t r1 = hsub2(h, c[0] & 0xFF00FF00u);
+  c[1] = r1 + 0x00800080u;
+  c[2] = hsub2(r1, c[1] & 0xFF00FF00u) + 0x00800080u;
 }
 
 // Byte `b` of row r in a tile of swizzled rows; rows past 128 bytes go on in a second tile.
