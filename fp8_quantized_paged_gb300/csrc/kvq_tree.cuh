@@ -146,9 +146,9 @@ struct TreeSmem {
   static constexpr int kBars = 4 * S + 3 * kBufs + 2 + 1 + kGroups * 4 + 4 + 2 + 1 + kPieces;
   // tmem address, abort, bad sequences, NaN marks, bad[kBadRing], issued[2], warp sums
   static constexpr int misc = bars + kBars * 8;
-  // [kRows] running maximum, [4] largest value scale by quarter of the rows, [2][4] that at a piece's end
+  // [kRows] running maximum; (TS) [kRows] largest value scale that the row has seen, [2][kRows] that at a piece's end
   static constexpr int m = misc + (5 + kNanMarks + kBadRing + kTreeThreads / 32) * 4;
-  static constexpr int l = (m + (kRows + 12) * 4 + 7) / 8 * 8;  // [2][kGroups][kRows] sums and their maxima, by piece
+  static constexpr int l = (m + (TS ? 4 : 1) * kRows * 4 + 7) / 8 * 8;  // [2][kGroups][kRows] sums and their maxima, by piece
   static constexpr int ls = l + 2 * kGroups * kRows * 8;                 // [kScaleBufs][kRows] logits' scales, by piece
   static constexpr int anc = ls + kScaleBufs * kRows * 4;               // [kGroups][kMaskWords][kRows] ancestors
   static constexpr int pieces = (anc + kGroups * kMaskWords * kRows * 4 + 15) / 16 * 16;  // [kPieces] of 12 words
@@ -264,6 +264,9 @@ KVQ_DEVI uint32_t hsub2(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+// 1 / s of a power of two from 2^-126 to 2^126.
+KVQ_DEVI float inverse_power(float s) { return __uint_as_float(0x7F000000u - __float_as_uint(s)); }
+
 // The E5M2 parts of two weights (f16, not negative, at most 2^15), each the upper byte of a half of c[k].
 // Half a step added rounds a magnitude; no carry leaves a half.  A NaN becomes a zero: it is in the row's sum.
 KVQ_DEVI void weight_parts(uint32_t h, uint32_t (&c)[3]) {
@@ -320,7 +323,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   int4* pieces_s = reinterpret_cast<int4*>(smem + SM::pieces);
   float* m_s = reinterpret_cast<float*>(smem + SM::m);
   float* sig_s = m_s + kRows;
-  float* sige_s = sig_s + 4;
+  float* sige_s = sig_s + kRows;
   float2* l_s = reinterpret_cast<float2*>(smem + SM::l);
   float* ls_s = reinterpret_cast<float*>(smem + SM::ls);
   int32_t* plan = reinterpret_cast<int32_t*>(smem + SM::plan);
@@ -859,23 +862,29 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             m = before;
           }
           float fs = 1.f;
-          if (TS) {  // the largest value scale of the block's tokens, to a power of two
-            float s = 0.f;
+          if (TS) {  // the largest value scale of the block's tokens that the row sees, to a power of two
+            uint32_t top = 0u;  // (its bits)
+            if (__builtin_expect(edge, 0)) {
+#pragma unroll 1
+              for (int e = 0; e < kKeys; e += 4) {
+                const uint4 s4 = *reinterpret_cast<const uint4*>(sv + e);
+                const uint32_t of[4] = {s4.x, s4.y, s4.z, s4.w}, see = (e < 32 ? seen[0] : seen[1]) >> (e & 31);
 #pragma unroll
-            for (int y = 0; y < kKeys / 32; ++y) {
-              const int key = lane + 32 * y;
-              if (k0 + key < pc.s.L && !(bm >> (key / kBS) & 1u)) s = fmaxf(s, sv[key]);
+                for (int z = 0; z < 4; ++z) top = max(top, see >> z & 1u ? of[z] & 0x7FFFFFFFu : 0u);
+              }
+            } else {  // every row sees them all
+              const uint32_t* bits = reinterpret_cast<const uint32_t*>(sv);
+              top = __reduce_max_sync(kFull, max(bits[lane] & 0x7FFFFFFFu, bits[lane + 32] & 0x7FFFFFFFu));
             }
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) s = fmaxf(s, __shfl_xor_sync(kFull, s, off));
-            s = __uint_as_float(min((__float_as_uint(s) + 0x7FFFFFu) & 0x7F800000u, 0x7E800000u));
-            sig = i > pc.i0 ? sig_s[quad] : 0.f;
+            if (top > 0x7F800000u) l = __uint_as_float(top);  // (a NaN: no part of a weight is one, the sum is)
+            const float s = __uint_as_float(min((top + 0x7FFFFFu) & 0x7F800000u, 0x7E800000u));
+            sig = i > pc.i0 ? sig_s[r] : 0.f;
             if (s > sig) {
-              fs = sig / s;
+              fs = sig * inverse_power(s);
               sig = s;
             }
           }
-          if (__builtin_expect(__any_sync(kFull, grow) || (TS && fs != 1.f), 0)) {
+          if (__builtin_expect(__any_sync(kFull, grow || (TS && fs != 1.f)), 0)) {
             const float a = m == -INFINITY ? 0.f : fast_exp2((m - mx) * lscale);
             if (i > pc.i0) {  // O's last writer: the PV of the block before
               if (!(ok = wait_w(&pdone[(g - 1) % kBufs], (g - 1) / kBufs))) break;
@@ -896,11 +905,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
           }
           m_s[r] = m;
-          if (TS && lane == 0) sig_s[quad] = sig;
+          if (TS) sig_s[r] = sig;
           __syncwarp();
           if (lane == 0) mbar_arrive(&token[group * 4 + quad]);
           const float fm = m == -INFINITY ? 0.f : -m;
-          const float inv_sig = TS && sig > 0.f ? 1.f / sig : 0.f;
+          const float inv_sig = TS && sig > 0.f ? inverse_power(sig) : 0.f;
           const tc::f32x2 fm2 = tc::f32x2_pack(fm, fm), ls2 = tc::f32x2_pack(lscale, lscale), b2 = tc::f32x2_pack(kBias, kBias);
           tc::f32x2 l2[2] = {tc::f32x2_pack(0.f, 0.f), tc::f32x2_pack(0.f, 0.f)};
 #pragma unroll
@@ -965,7 +974,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       float2* sums = l_s + (piece & 1) * kGroups * kRows;
       sums[group * kRows + r] = make_float2(l, m);
       const int owner = last % kGroups;
-      if (TS && group == owner && lane == 0) sige_s[(piece & 1) * 4 + quad] = sig;
+      if (TS && group == owner) sige_s[(piece & 1) * kRows + r] = sig;
       __syncwarp();
       if (lane == 0) mbar_arrive(&lfull[quad]);
       if (!(ok = wait_w(&lfull[quad], piece))) break;
@@ -977,7 +986,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const float2 s = sums[y * kRows + r];
         l += s.x * (s.y == -INFINITY || s.y == m ? 1.f : fast_exp2((s.y - m) * lscale));
       }
-      const float svs = TS ? sige_s[((piece - 1) & 1) * 4 + quad] : BF ? 1.f : __ldg(p.vs + (p.per_head ? pc.head : 0));
+      const float svs = TS ? sige_s[((piece - 1) & 1) * kRows + r] : BF ? 1.f : __ldg(p.vs + (p.per_head ? pc.head : 0));
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
       const int64_t part = static_cast<int64_t>(2 * cta + (pc.i0 == 0)) * kRows + r;
       const int64_t qrow = (static_cast<int64_t>(pc.s.q0) + node) * p.Hq + pc.head * p.G + r % p.G;

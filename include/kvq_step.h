@@ -145,7 +145,9 @@ KVQ_API size_t kvq_tree_workspace_size(int num_q_heads, int num_kv_heads, int he
  * product with V^ as its f16, in three E5M2 parts: within 2^-11 of its value
  * and 2^-24 of the row's largest.  Over a bf16 cache the query is taken as it is and a
  * weight as two bf16 parts, within 2^-17.  With KVQ_SCALE_PER_TOKEN_HEAD the
- * weight carries its value's scale relative to the largest so far.
+ * weight carries its value's scale relative to the largest that its row has
+ * seen, and the 2^-24 is of the row's largest weight times that scale; scales
+ * of tokens that a row does not see are nothing to it.
  * Limits: num_seqs <= 4096; num_kv_heads <= 256; num_q_heads / num_kv_heads
  * <= 8; num_blocks * num_kv_heads * block_size < 2^31; max_blocks_per_seq *
  * block_size < 2^30; num_seqs * num_kv_heads * T * (max_blocks_per_seq / 4 +

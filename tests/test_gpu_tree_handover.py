@@ -8,9 +8,10 @@ import pytest
 import torch
 
 import step_testlib as lib
-from step_testlib import BF16, E4M3, E5M2, PER_HEAD
+from step_testlib import BF16, E4M3, E5M2, PER_HEAD, PER_TOKEN_HEAD
 from test_gpu_step_wait_timeout import call, hooked  # noqa: F401
 from test_gpu_tree import kvq  # noqa: F401
+from test_gpu_tree_precision import check_scaled
 from test_gpu_wait_timeout import tlib  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -41,7 +42,7 @@ def with_nan(b):
     return where
 
 
-CASES = [(E4M3, PER_HEAD, 128), (BF16, PER_HEAD, 128), (E5M2, PER_HEAD, 64)]
+CASES = [(E4M3, PER_HEAD, 128), (BF16, PER_HEAD, 128), (E4M3, PER_TOKEN_HEAD, 64), (E5M2, PER_HEAD, 64)]
 
 
 @pytest.mark.parametrize("fmt,gran,dh", CASES)
@@ -49,7 +50,7 @@ def test_short_pieces(kvq, hooked, fmt, gran, dh):  # noqa: F811
     b = batch(fmt, gran, dh)
     g = lib.OnGpu(kvq, b)
     g.call()
-    g.check()
+    check_scaled(g) if gran == PER_TOKEN_HEAD else g.check()
     clean = g.out.clone()
     where = with_nan(b)
     hooked.kvq_test_late_warp.restype, hooked.kvq_test_late_warp.argtypes = None, [ctypes.c_int]

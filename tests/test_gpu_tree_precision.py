@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import step_testlib as lib
-from step_testlib import E4M3, E5M2, PER_TENSOR, OnGpu, TreeBatch
+from step_testlib import E4M3, E5M2, PER_TENSOR, PER_TOKEN_HEAD, OnGpu, TreeBatch
 from test_gpu_tree import kvq  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -52,3 +52,92 @@ def test_weights_have_eleven_bits(kvq, fmt):  # noqa: F811
     assert int(o.st.item()) == 0
     err = (o.out.double() - ref[..., None]).abs()
     assert bool((err <= bound[..., None]).all()), float((err / bound[..., None]).max())
+
+
+@pytest.mark.parametrize("fmt,dh", [(E4M3, 128), (E5M2, 128), (E4M3, 64)])
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("outlier", [2.0 ** 30, 2.0 ** 100, math.inf, math.nan])
+def test_scales_of_tokens_that_a_row_does_not_see(kvq, fmt, dh, window, outlier):  # noqa: F811
+    """Outliers among the scales, K's and V's, of two nodes and of tokens about the window's start: the rows that do not
+    see them keep their bits, those that see a NaN are NaN."""
+    b = TreeBatch([(300, 30), (90, 20), (2000, 16)], 8, 2, dh, fmt, PER_TOKEN_HEAD, window=window, seed=31)
+    clean = OnGpu(kvq, b)
+    clean.call()
+    clean.check()
+    P = 270
+    nodes, before = (4, 11), ((P - 33, P - 60) if window else ())
+    for i, t in enumerate([P + j for j in nodes] + list(before)):
+        for s in (b.ks, b.vs) if i % 2 else (b.vs,):
+            s[int(b.bt[0, t // 16]), 1, t % 16] = outlier
+    g = OnGpu(kvq, b)
+    g.call()
+    torch.cuda.synchronize()
+    assert int(g.st.item()) == 0
+    assert torch.equal(g.out[:, :4], clean.out[:, :4]) and torch.equal(g.out[30:], clean.out[30:])
+    saw = 0
+    for j in range(30):
+        way = lib.way_up(b.parents[0], j)
+        near = way[:window] if window else way
+        first = max(0, P + len(way) - window) if window else 0
+        sees = any(n in near for n in nodes) or any(t >= first for t in before)
+        saw += sees
+        if not sees:
+            assert torch.equal(g.out[j, 4:], clean.out[j, 4:]), j
+        elif math.isnan(outlier):
+            assert bool(g.out[j, 4:].isnan().all()), j
+    assert saw >= 2  # (a window of 40 shows every node the token 33 before the tree)
+
+
+@pytest.mark.parametrize("outlier", [2.0 ** 30, math.inf, math.nan])
+def test_scales_before_the_window(kvq, outlier):  # noqa: F811
+    """A chain of drafts: outliers among the scales of tokens that leave the window one node after the other."""
+    window, P = 40, 270
+    b = TreeBatch([(300, 30), (2000, 16)], 8, 2, 128, E4M3, PER_TOKEN_HEAD, window=window, kind="chain", seed=33)
+    clean = OnGpu(kvq, b)
+    clean.call()
+    clean.check()
+    before = (P - 33, P - 30, P - 60)
+    for i, t in enumerate(before):
+        for s in (b.ks, b.vs) if i == 1 else (b.vs,):
+            s[int(b.bt[0, t // 16]), 1, t % 16] = outlier
+    g = OnGpu(kvq, b)
+    g.call()
+    torch.cuda.synchronize()
+    assert torch.equal(g.out[:, :4], clean.out[:, :4]) and torch.equal(g.out[30:], clean.out[30:])
+    assert torch.equal(g.out[10:, 4:], clean.out[10:, 4:])  # node j sees from P + j - 39 on
+    if math.isnan(outlier):
+        assert bool(g.out[:10, 4:].isnan().all())
+
+
+@pytest.mark.parametrize("fmt", [E4M3, E5M2])
+@pytest.mark.parametrize("far", [2.0 ** 6, 2.0 ** 12])
+def test_one_scale_far_above_the_rest(kvq, fmt, far):  # noqa: F811
+    """A node's value scale above all others: the rows that see it, within the bound."""
+    b = TreeBatch([(300, 30), (2000, 16)], 8, 2, 128, fmt, PER_TOKEN_HEAD, seed=32)
+    for L, n, i in ((300, 30, 0), (2000, 16, 1)):
+        t = L - n + 4
+        at = (int(b.bt[i, t // 16]), slice(None), t % 16)
+        b.vs[at] *= far
+        b.V[at] *= far
+    g = OnGpu(kvq, b)
+    g.call()
+    check_scaled(g)
+
+
+def check_scaled(g):
+    """The batch's bound, and for per-(token, head) scales what 2^-24 of the row's largest weight is there: a weight enters
+    as y s / sigma, sigma the power of two in [s_max, 2 s_max) of the scales seen, so it is off by 2^-24 sigma in y s, for
+    every code of the dim that the row sees; the sum of weights is 1 at least."""
+    b = g.b
+    torch.cuda.synchronize()
+    assert int(g.st.item()) == 0
+    ref, bound = b.reference()
+    for i, (L, n) in enumerate(zip(b.lens, b.nodes)):
+        t = torch.arange(L, device=b.dev)
+        blk = b.bt[i][t // 16].long()
+        s = b.vs[blk, :, t % 16].double()                                        # [L][hkv]
+        codes = lib.decode(b.vc, b.fmt)[blk, :, t % 16].abs().sum(0)              # [hkv][dh]
+        more = 2.0 ** -23 * s.amax(0)[:, None] * codes
+        bound[int(b.cu[i]):int(b.cu[i + 1])] += more.repeat_interleave(b.hq // b.hkv, 0)
+    err = (g.out.double() - ref).abs()
+    assert bool((err <= bound).all()), float((err / bound).max())
