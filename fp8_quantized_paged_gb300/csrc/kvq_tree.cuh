@@ -674,10 +674,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         for (int y = 0; y < 3; ++y) {
           const int at = r0 + y * kStep;
           float lscale = lscale0;
-          if (BF) {
-            if (at < rows) tc::sts128(to + tile_at<C::kSpan>(at, 16 * ql), w[y].x, w[y].y, w[y].z, w[y].w);
+          uint32_t u[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
+          if (BF) {  // (infinities as NaN: logits of -inf alone would be a row that sees nothing)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[e] |= __vcmpeq2(u[e] & 0x7FFF7FFFu, 0x7F807F80u) & 0x00400040u;
+            if (at < rows) tc::sts128(to + tile_at<C::kSpan>(at, 16 * ql), u[0], u[1], u[2], u[3]);
           } else {
-            const uint32_t u[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
             float x[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -699,7 +701,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               for (int off = 1; off < kLanes; off <<= 1) top = __vmaxu2(top, __shfl_xor_sync(kFull, top, off));
               const int e = static_cast<int>(max(top & 0xFFFFu, top >> 16) >> 7);  // its exponent, 0 for subnormals
               const int a = top == 0u ? 0 : min(126, 134 - max(e, 8));  // (-121 .. 126)
-              const float by = __int_as_float((a + 127) << 23);  // exact: a power of two, no overflow
+              // exact: a power of two, no overflow; in a row with a NaN or an infinity 0, which leaves NaN for these
+              const float by = e == 255 ? 0.f : __int_as_float((a + 127) << 23);
               lscale *= __int_as_float((127 - a) << 23);
 #pragma unroll
               for (int e = 0; e < 8; ++e) x[e] *= by;

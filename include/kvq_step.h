@@ -141,7 +141,8 @@ KVQ_API size_t kvq_tree_workspace_size(int num_q_heads, int num_kv_heads, int he
  * caches the query row is scaled by a power of two that takes its largest
  * value to [2^7, 2^8) and enters the products as two E4M3 parts: exact for
  * values within 2^8 of the row's largest, off by 2^-18 of that at most
- * below; finite queries of any magnitude are fine.  A weight enters the
+ * below; finite queries of any magnitude are fine.  A NaN or an infinity in a
+ * query row makes that row NaN (with KVQ_Q_FP8 an infinity is cast_fp8's).  A weight enters the
  * product with V^ as its f16, in three E5M2 parts: within 2^-11 of its value
  * and 2^-24 of the row's largest.  Over a bf16 cache the query is taken as it is and a
  * weight as two bf16 parts, within 2^-17.  With KVQ_SCALE_PER_TOKEN_HEAD the

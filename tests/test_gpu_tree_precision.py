@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import step_testlib as lib
-from step_testlib import E4M3, E5M2, PER_TENSOR, PER_TOKEN_HEAD, OnGpu, TreeBatch
+from step_testlib import BF16, E4M3, E5M2, PER_HEAD, PER_TENSOR, PER_TOKEN_HEAD, OnGpu, TreeBatch
 from test_gpu_tree import kvq  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -141,3 +141,47 @@ def check_scaled(g):
         bound[int(b.cu[i]):int(b.cu[i + 1])] += more.repeat_interleave(b.hq // b.hkv, 0)
     err = (g.out.double() - ref).abs()
     assert bool((err <= bound).all()), float((err / bound).max())
+
+
+@pytest.mark.parametrize("fmt,gran,dh", [(E4M3, PER_HEAD, 128), (E5M2, PER_HEAD, 64), (E4M3, PER_TOKEN_HEAD, 128), (BF16, PER_HEAD, 128),
+                                         (BF16, PER_HEAD, 64)])
+def test_bad_queries_stay_in_their_rows(kvq, fmt, gran, dh):  # noqa: F811
+    """A NaN or an infinity in a query row is that row's output, whatever the keys' signs; the other rows keep their bits.
+    A row that sees nothing stays zero."""
+    b = TreeBatch([(300, 20), (2, 1), (2500, 16), (9, 9)], 8, 2, dh, fmt, gran, seed=41)
+    b.bt[3] = -1
+    clean = OnGpu(kvq, b)
+    clean.call()
+    rows = []
+    for i, (row, head, d, x) in enumerate([(0, 1, 3, math.nan), (5, 0, dh - 1, math.inf), (19, 7, 0, -math.inf), (20, 0, 0, math.inf),
+                                           (20, 1, 0, -math.inf), (20, 2, 1, math.inf), (20, 5, dh - 2, -math.inf), (30, 6, 9, math.inf),
+                                           (36, 3, 17, -math.inf)]):
+        b.q[row, head, d] = x
+        rows.append((row, head))
+    b.q[37:] = math.inf
+    g = OnGpu(kvq, b)
+    g.call()
+    torch.cuda.synchronize()
+    assert int(g.st.item()) == int(clean.st.item()) == kvq.KVQ_DEV_BAD_BLOCK
+    bad = torch.zeros(b.q.shape[:2], dtype=torch.bool, device="cuda")
+    for row, head in rows:
+        bad[row, head] = True
+    assert bool(g.out[bad].isnan().all())
+    assert torch.equal(g.out[~bad], clean.out[~bad]) and bool((g.out[37:] == 0).all())
+
+
+@pytest.mark.parametrize("fmt", [E4M3, BF16])
+@pytest.mark.parametrize("x", [math.inf, -math.inf])
+def test_infinite_queries_against_keys_of_one_sign(kvq, fmt, x):  # noqa: F811
+    """Logits that are all -inf (or all inf) are not a row that sees nothing."""
+    b = TreeBatch([(70, 9), (300, 16)], 4, 2, 128, fmt, seed=42)
+    b.kc[..., 5] = -1.0 if fmt == BF16 else 0xB8
+    clean = OnGpu(kvq, b)
+    clean.call()
+    b.q[::2, 1, 5] = x
+    g = OnGpu(kvq, b)
+    g.call()
+    torch.cuda.synchronize()
+    assert int(g.st.item()) == 0 and bool(g.out[::2, 1].isnan().all())
+    g.out[::2, 1] = clean.out[::2, 1]
+    assert torch.equal(g.out, clean.out)
