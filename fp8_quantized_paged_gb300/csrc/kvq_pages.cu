@@ -514,6 +514,12 @@ static int done(cudaError_t e) {
 
 static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Whether na words at a and nb at b share one (none at a NULL).
+static bool share(const int32_t* a, int64_t na, const int32_t* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x && y && na > 0 && nb > 0 && x < y + 4 * static_cast<uint64_t>(nb) && y < x + 4 * static_cast<uint64_t>(na);
+}
+
 static int check_rows(const kvq_rows* caches, int num_caches, int64_t num_blocks, int num_kv_heads, int block_size) {
   if (num_caches < 0 || num_blocks <= 0 || num_kv_heads <= 0) return KVQ_ERR_ARG;
   if (num_caches > 0 && !caches) return KVQ_ERR_NULL;
@@ -584,7 +590,11 @@ extern "C" int kvq_tree_commit(const kvq_rows* caches, int num_caches, int64_t n
   if (!aligned4(cu_q_lens) || !aligned4(block_tables) || !aligned4(seq_lens) || !aligned4(accepted) ||
       !aligned4(num_accepted) || !aligned4(new_lens))
     return KVQ_ERR_ALIGN;
-  if (num_seqs > 0 && new_lens == seq_lens) return KVQ_ERR_ARG;
+  // (written while other warps, and later launches, still read their sequence's lengths and path)
+  const int64_t B = num_seqs;
+  if (share(new_lens, B, seq_lens, B) || share(new_lens, B, num_accepted, B) || share(new_lens, B, cu_q_lens, B + 1) ||
+      share(new_lens, B, accepted, B * max_path) || share(new_lens, B, block_tables, B * max_blocks_per_seq))
+    return KVQ_ERR_ARG;
   if (num_seqs == 0) return KVQ_OK;
   const int sms = device_sm_count();
   if (sms <= 0) return KVQ_ERR_CUDA;

@@ -196,7 +196,7 @@ typedef struct {
  *                   none twice (KVQ_ERR_ARG)
  *   accepted        int32 [num_seqs][max_path]
  *   num_accepted    int32 [num_seqs], 0 .. min(n_b, max_path)
- *   new_lens        int32 [num_seqs], out; not seq_lens
+ *   new_lens        int32 [num_seqs], out; no part of an input (KVQ_ERR_ARG)
  *   dev_status      optional; KVQ_DEV_BAD_TREE (a path that does not rise,
  *                   leaves [0, n_b), or a count outside its range: nothing of
  *                   the sequence moves, new_lens[b] = seq_lens[b]),
