@@ -679,7 +679,19 @@ extern "C" int kvq_pages_fork(int32_t* pool, int64_t num_blocks, const int32_t* 
   if (!aligned4(tables) || !aligned4(lens) || !aligned4(parents) || !aligned4(out_tables) || !aligned4(out_lens) ||
       !aligned4(copies))
     return KVQ_ERR_ALIGN;
-  if (num_out > 0 && (out_tables == tables || out_lens == lens || out_lens == parents)) return KVQ_ERR_ARG;
+  // (rows are written while others are still read, from the pool too)
+  const int64_t columns = max_blocks_per_seq, words = KVQ_POOL_WORDS(num_blocks);
+  const struct {
+    const int32_t* p;
+    int64_t n;
+  } in[4] = {{tables, num_src * columns}, {lens, num_src}, {parents, num_out}, {pool, words}},
+    out[3] = {{out_tables, num_out * columns}, {out_lens, num_out}, {copies, 2 * static_cast<int64_t>(num_out)}};
+  for (int i = 0; i < 3; ++i) {
+    for (const auto& x : in)
+      if (share(out[i].p, out[i].n, x.p, x.n)) return KVQ_ERR_ARG;
+    for (int j = 0; j < i; ++j)
+      if (share(out[i].p, out[i].n, out[j].p, out[j].n)) return KVQ_ERR_ARG;
+  }
   if (num_out == 0) return KVQ_OK;
   ForkParams p = {pool, static_cast<int>(num_blocks), tables, lens, num_src, max_blocks_per_seq, parents, num_out,
                   out_tables, out_lens, copies, dev_status};

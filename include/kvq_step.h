@@ -272,7 +272,8 @@ KVQ_API int kvq_pages_free(int32_t* pool, int64_t num_blocks, int32_t* block_tab
  *   tables       int32 [num_src][max_blocks_per_seq], lens int32 [num_src]
  *   parents      int32 [num_out]
  *   out_tables   int32 [num_out][max_blocks_per_seq], out_lens int32
- *                [num_out], copies int32 [num_out][2]; none of them an input
+ *                [num_out], copies int32 [num_out][2]; apart from the inputs,
+ *                the pool and each other (KVQ_ERR_ARG)
  * What out_tables held before is not given back: free it first.
  * num_src, num_out <= 4096.
  */

@@ -30,3 +30,20 @@ def test_commit_lengths_in_the_counts_are_refused(kvq):  # noqa: F811
     with pytest.raises(kvq.KvqError) as e:
         kvq.kvq_tree_commit(make_caches(3, 2, 64, ["fp8"]), t([0, 4]), t([[0, 1]]), t([20]), t([[2]]), taken, taken)
     assert e.value.status == -7 and taken.tolist() == [1]
+
+
+def test_fork_arrays_side_by_side(kvq):  # noqa: F811
+    """The halves of one table, lengths and copies behind it: the outputs only touch the inputs."""
+    t = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    pool, st = kvq.new_page_pool(12), t([0])
+    flat = torch.full((2 * 3 + 3 * 3 + 2 + 3 + 3 + 6,), -1, dtype=torch.int32, device="cuda")
+    tables, out, lens, out_lens, parents, copies = flat.split([6, 9, 2, 3, 3, 6])
+    tables, out, copies = tables.view(2, 3), out.view(3, 3), copies.view(3, 2)
+    lens.copy_(t([40, 20]))
+    parents.copy_(t([1, 0, 0]))
+    kvq.kvq_pages_alloc(pool, tables, t([0, 0]), lens, st)
+    kvq.kvq_pages_fork(pool, tables, lens, parents, out, out_lens, copies, st)
+    torch.cuda.synchronize()
+    assert int(st) == 0 and tables.tolist() == [[0, 1, 2], [3, 4, -1]]
+    assert out.tolist() == [[3, 5, -1], [0, 1, 6], [0, 1, 7]] and out_lens.tolist() == [20, 40, 40]
+    assert copies.tolist() == [[4, 5], [2, 6], [2, 7]]
