@@ -26,8 +26,8 @@ namespace rope {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 // 28 warps an SM of 72 registers each, and a step's rows on their way while one is worked on.  32768
-// tokens of 32 + 2 * 8 rows of 128 (738 MB): 136 us; with 32 warps (which spill) 141, with two steps'
-// rows on their way 156 to 168.
+// tokens of 32 + 2 * 8 rows of 128 (738 MB): 133 us.  When the squares were no loop, and spilled: 136; then
+// with 32 warps 141, with two steps' rows on their way 156 to 168.
 constexpr int kThreads = 128;
 constexpr int kCtasPerSM = 7;
 constexpr int kAngles = 1;  // what forming a token's angles takes, in steps
@@ -175,16 +175,34 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSM) rope_kernel(const __grid
     // The rows' norm and turn: x, y are the lane's two runs.
     auto norm_and_turn = [&](float (&x)[8], float (&y)[8], const uint16_t* w) {
       if (w) {
-        float2 sum = make_float2(0.f, 0.f);
+        // Squares leave binary32 where values pass 2^63, or lie below 2^-63 beside an eps that is as small:
+        // such rows are multiplied by a power of two, and summed once more.  (A loop that ordinary rows go
+        // through once: with the second sum written out after the first, 48 bytes spilled, 12.6 us where
+        // 4100 tokens of 16 + 2 * 16 rows of 64 in bf16 take 11.5.)
+        float mean, eps = p.eps;
+#pragma unroll 1
+        for (int again = 0;; ++again) {
+          float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sum = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), make_float2(x[2 * i], x[2 * i + 1]), sum);
-          sum = __ffma2_rn(make_float2(y[2 * i], y[2 * i + 1]), make_float2(y[2 * i], y[2 * i + 1]), sum);
+          for (int i = 0; i < 4; ++i) {
+            sum = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), make_float2(x[2 * i], x[2 * i + 1]), sum);
+            sum = __ffma2_rn(make_float2(y[2 * i], y[2 * i + 1]), make_float2(y[2 * i], y[2 * i + 1]), sum);
+          }
+          float sq2 = sum.x + sum.y;
+#pragma unroll
+          for (int off = 1; off < CH; off <<= 1) sq2 += __shfl_xor_sync(kAll, sq2, off);
+          mean = sq2 * (1.f / DH) + eps;
+          if (__builtin_expect(again || !__any_sync(kAll, !(mean > 0x1p-90f && mean < 0x1p120f)), 1)) break;
+          const float by = mean <= 0x1p-90f ? 0x1p100f : mean < 0x1p120f ? 1.f : 0x1p-70f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x[i] *= by;
+            y[i] *= by;
+          }
+          eps *= by;
+          eps *= by;
         }
-        float sq2 = sum.x + sum.y;
-#pragma unroll
-        for (int off = 1; off < CH; off <<= 1) sq2 += __shfl_xor_sync(kAll, sq2, off);
-        const float f = rsqrtf(sq2 * (1.f / DH) + p.eps);
+        const float f = rsqrtf(mean);
         float u[8], v[8];
         unpack8(__ldg(reinterpret_cast<const uint4*>(w + d0)), u);
         unpack8(__ldg(reinterpret_cast<const uint4*>(w + d1)), v);

@@ -52,8 +52,8 @@ extern "C" {
  *   q_out[t] = bf16(z)
  *   the cache row of slot_mapping[t] gets cast_fp8(z / sK) and cast_fp8(v / sV)
  * as kvq_write forms them (bf16(z) and v's bits with KVQ_FMT_BF16), with z in
- * binary32: K is rounded once.  A NaN or an infinity in a row reaches that row
- * only.  Codes and scales for KVQ_SCALE_PER_TOKEN_HEAD as kvq_write_token_head
+ * binary32: K is rounded once.  Finite rows of any magnitude are normed; a NaN
+ * or an infinity in a row reaches that row only.  Codes and scales for KVQ_SCALE_PER_TOKEN_HEAD as kvq_write_token_head
  * forms them, amax / fmt_max over the finite values of z (and v).
  *
  *   q, k, v         bf16 [num_tokens][heads][head_dim]; a token's heads are
