@@ -1,7 +1,10 @@
 """Ordinary calls of the step's operators at the edges of what they take."""
+import random
+
 import pytest
 import torch
 
+import step_testlib as lib
 from test_gpu_pages import commit_plain, kvq, make_caches  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -47,3 +50,29 @@ def test_fork_arrays_side_by_side(kvq):  # noqa: F811
     assert int(st) == 0 and tables.tolist() == [[0, 1, 2], [3, 4, -1]]
     assert out.tolist() == [[3, 5, -1], [0, 1, 6], [0, 1, 7]] and out_lens.tolist() == [20, 40, 40]
     assert copies.tolist() == [[4, 5], [2, 6], [2, 7]]
+
+
+@pytest.mark.parametrize("blocks,sources,beams,pages", [(300000, 512, 4096, 300), (40000, 16, 256, 2048), (20000, 4096, 4096, 3)])
+def test_forks_at_full_width(kvq, blocks, sources, beams, pages):  # noqa: F811
+    """As many rows as a call takes, and long tables, against the pool's rules in Python."""
+    rng = random.Random(blocks)
+    plain, mb = lib.Pool(blocks), pages + 2
+    lens = [rng.choice((0, 16, rng.randint(1, 16 * pages), 16 * pages)) for _ in range(sources)]
+    rows = [[-1] * mb for _ in range(sources)]
+    t = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    pool, tables, st = kvq.new_page_pool(blocks), t(rows), t([0])
+    assert plain.alloc(rows, [0] * sources, lens)
+    kvq.kvq_pages_alloc(pool, tables, t([0] * sources), t(lens), st)
+    parents = [rng.choice((-1, rng.randrange(sources), rng.randrange(sources), 0)) for _ in range(beams)]
+    out, out_lens, copies = (torch.full(s, 77, dtype=torch.int32, device="cuda") for s in ((beams, mb), (beams,), (beams, 2)))
+    kvq.kvq_pages_fork(pool, tables, t(lens), t(parents), out, out_lens, copies, st)
+    want = plain.fork(rows, lens, parents, mb)
+    torch.cuda.synchronize()
+    assert int(st) == 0 and tables.tolist() == rows
+    assert torch.equal(out.cpu(), torch.tensor(want[0], dtype=torch.int32))
+    assert out_lens.tolist() == want[1] and copies.tolist() == want[2] and pool.tolist() == plain.words()
+    # both sides given back: every page is free
+    kvq.kvq_pages_free(pool, out, out_lens, torch.zeros_like(out_lens), st)
+    kvq.kvq_pages_free(pool, tables, t(lens), t([0] * sources), st)
+    torch.cuda.synchronize()
+    assert int(st) == 0 and pool.tolist() == lib.Pool(blocks).words()

@@ -185,3 +185,59 @@ def test_infinite_queries_against_keys_of_one_sign(kvq, fmt, x):  # noqa: F811
     assert int(g.st.item()) == 0 and bool(g.out[::2, 1].isnan().all())
     g.out[::2, 1] = clean.out[::2, 1]
     assert torch.equal(g.out, clean.out)
+
+
+def check_by_ties(g):
+    """Every row, however large its logits: the output lies, dim by dim, between the least and the largest value of the keys
+    whose logit may be the largest.
+
+    A logit is off by D at most: over FP8 caches the query's parts leave 2^-18 of the row's largest value, times the key's
+    magnitudes; binary32 sums 2^-19 of the sum of magnitudes.  A key more than 2 D + 40 below the largest logit has a weight of
+    e^-40; 20000 of them and values 2^12 apart are below 2^-30 of the largest value that the row sees.  Beside that half a
+    step of bf16, and 2^-11 and 2^-19 for weights and sums."""
+    b = g.b
+    torch.cuda.synchronize()
+    assert int(g.st.item()) == 0 and bool(g.out.isfinite().all())
+    G, q = b.hq // b.hkv, b.query()
+    for i, (L, n) in enumerate(zip(b.lens, b.nodes)):
+        P, a = L - n, int(b.cu[i])
+        t = torch.arange(L, device=b.dev)
+        blk = b.bt[i][t // 16].long()
+        see = torch.zeros(n, L, dtype=torch.bool)
+        see[:, :P] = True
+        for j in range(n):
+            see[j, [P + k for k in lib.way_up(b.parents[i], j)]] = True
+        see = see.cuda()
+        for h in range(b.hkv):
+            K, V = b.K[blk, h, t % 16], b.V[blk, h, t % 16]
+            for j in range(n):
+                qq = q[a + j, h * G:(h + 1) * G]                                     # [G][dh]
+                x = (qq @ K.T / math.sqrt(b.dh)).masked_fill(~see[j], -math.inf)    # [G][L]
+                D = 2.0 ** -19 * (qq.abs() @ K.abs().T).amax(1) / math.sqrt(b.dh)
+                if b.fmt != BF16:
+                    D = D + 2.0 ** -18 * qq.abs().amax(1) * K.abs().sum(1).max() / math.sqrt(b.dh)
+                near = x >= (x.amax(1) - 2 * D - 40)[:, None]
+                v = V[None].expand(G, -1, -1)
+                lo = v.masked_fill(~near[..., None], math.inf).amin(1)
+                hi = v.masked_fill(~near[..., None], -math.inf).amax(1)
+                slack = (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -19) * torch.maximum(lo.abs(), hi.abs()) + 2.0 ** -30 * V[see[j]].abs().amax()
+                out = g.out[a + j, h * G:(h + 1) * G].double()
+                assert bool(((out >= lo - slack) & (out <= hi + slack)).all()), (i, h, j)
+
+
+@pytest.mark.parametrize("amp", [1e4, 1e30])
+@pytest.mark.parametrize("fmt,gran", [(E4M3, PER_HEAD), (E5M2, PER_HEAD), (E4M3, PER_TOKEN_HEAD), (BF16, PER_HEAD)])
+def test_large_queries_row_by_row(kvq, amp, fmt, gran):  # noqa: F811
+    """Small trees, and long contexts that are cut into many pieces and merged."""
+    for seqs in ([(300, 20), (40, 5)], [(20000, 5), (9000, 17)]):
+        g = OnGpu(kvq, TreeBatch(seqs, 4, 2, 128, fmt, gran, amp=amp, seed=51))
+        g.call()
+        check_by_ties(g)
+
+
+@pytest.mark.parametrize("fmt", [E4M3, BF16])
+def test_small_queries_over_long_contexts(kvq, fmt):  # noqa: F811
+    for amp in (1e-30, 1e-4):
+        g = OnGpu(kvq, TreeBatch([(20000, 5), (9000, 17)], 4, 2, 128, fmt, amp=amp, seed=52))
+        g.call()
+        g.check()
