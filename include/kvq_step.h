@@ -140,7 +140,7 @@ KVQ_API size_t kvq_tree_workspace_size(int num_q_heads, int num_kv_heads, int he
  * Statistics and sums are binary32, the output is rounded once.  Over FP8
  * caches the query row is scaled by a power of two that takes its largest
  * value to [2^7, 2^8) and enters the products as two E4M3 parts: exact for
- * values within 2^8 of the row's largest, off by 2^-18 of that at most
+ * values within 2^8 of the row's largest, off by 2^-17 of that at most
  * below; finite queries of any magnitude are fine.  A NaN or an infinity in a
  * query row makes that row NaN (with KVQ_Q_FP8 an infinity is cast_fp8's).  A weight enters the
  * product with V^ as its f16, in three E5M2 parts: within 2^-11 of its value

@@ -191,7 +191,7 @@ def check_by_ties(g):
     """Every row, however large its logits: the output lies, dim by dim, between the least and the largest value of the keys
     whose logit may be the largest.
 
-    A logit is off by D at most: over FP8 caches the query's parts leave 2^-18 of the row's largest value, times the key's
+    A logit is off by D at most: over FP8 caches the query's parts leave 2^-17 of the row's largest value, times the key's
     magnitudes; binary32 sums 2^-19 of the sum of magnitudes.  A key more than 2 D + 40 below the largest logit has a weight of
     e^-40; 20000 of them and values 2^12 apart are below 2^-30 of the largest value that the row sees.  Beside that half a
     step of bf16, and 2^-11 and 2^-19 for weights and sums."""
@@ -215,7 +215,7 @@ def check_by_ties(g):
                 x = (qq @ K.T / math.sqrt(b.dh)).masked_fill(~see[j], -math.inf)    # [G][L]
                 D = 2.0 ** -19 * (qq.abs() @ K.abs().T).amax(1) / math.sqrt(b.dh)
                 if b.fmt != BF16:
-                    D = D + 2.0 ** -18 * qq.abs().amax(1) * K.abs().sum(1).max() / math.sqrt(b.dh)
+                    D = D + 2.0 ** -17 * qq.abs().amax(1) * K.abs().sum(1).max() / math.sqrt(b.dh)
                 near = x >= (x.amax(1) - 2 * D - 40)[:, None]
                 v = V[None].expand(G, -1, -1)
                 lo = v.masked_fill(~near[..., None], math.inf).amin(1)
@@ -241,3 +241,32 @@ def test_small_queries_over_long_contexts(kvq, fmt):  # noqa: F811
         g = OnGpu(kvq, TreeBatch([(20000, 5), (9000, 17)], 4, 2, 128, fmt, amp=amp, seed=52))
         g.call()
         g.check()
+
+
+@pytest.mark.parametrize("fmt", [E4M3, E5M2])
+@pytest.mark.parametrize("small", [2.0 ** -17, 2.0 ** -16 * 0.75, 2.0 ** -15 * 1.3, 2.0 ** -9 * 1.01])
+def test_small_query_values_beside_a_large_one(kvq, fmt, small):  # noqa: F811
+    """127 equal values far below a row's first, which meets keys of 0: what the two E4M3 parts leave of them shows.
+
+    The row's largest value is taken to 2^7 at least, where E4M3's least step is 2^-9: a value is off by half of it, 2^-17
+    of the largest.  The logit is off by that times the key's magnitudes, and 2^-19 of itself; the weights by twice as much."""
+    n, dh = 8, 128
+    t = TreeBatch([(2 + n, n)], 4, 1, dh, fmt, PER_TENSOR, kind="forest", seed=61)
+    K, V = torch.zeros(2 + n, dh), torch.zeros(2 + n, dh)
+    K[1:2, 1:] = lib.TOP[fmt] if fmt == E4M3 else 512.0
+    V[0], V[1] = -1.0, 1.0
+    fill(t, K, V)
+    q = torch.full((n, 4, dh), small)
+    q[..., 0] = torch.linspace(1.0, 1.9, n)[:, None]
+    t.q = q.to(torch.bfloat16).cuda()
+    o = OnGpu(kvq, t)
+    o.call()
+    torch.cuda.synchronize()
+    assert int(o.st.item()) == 0
+    x = t.q.double() @ K[1].double().cuda() / math.sqrt(dh)
+    a = torch.exp(x)  # the first token and the node itself weigh 1
+    ref = (a - 1) / (a + 2)
+    d = (2.0 ** -17 * t.q.double().amax(-1) * K[1].sum().item() + 2.0 ** -19 * x.abs()) / math.sqrt(dh) + 2.0 ** -19 * x.abs()
+    bound = 2.0 ** -8 * ref.abs() + (2.0 ** -11 + 2.0 ** -18 + 2 * d) * (a + 1) / (a + 2)
+    err = (o.out.double() - ref[..., None]).abs()
+    assert bool((err <= bound[..., None]).all()), float((err / bound[..., None]).max())
