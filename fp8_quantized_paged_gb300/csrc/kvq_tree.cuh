@@ -23,12 +23,13 @@
 // six blocks in flight hide it.  Q lies in shared memory, twice: the next piece's is written while this
 // one's is in use.
 //
-// What bounds it: instructions.  64 keys of 128 rows take some 1100 cycles, of which the tensor cores
-// are busy 770, and each scheduler issues some 900 instructions: 64 weights of a row and their parts
-// are about 8 each (a softmax thread), the roles beside it the rest.  A segment's start and end cost
-// ten blocks.  32 trees of 16 nodes (64 rows) over 2049 tokens of 8 KV heads, 134 MB: 56 us, of which
-// the merge 6; one of 64 nodes over 32768: 56 us; 128 of 24 over 17 to 16384 with a window of 4096:
-// 163 us.  What was tried and is slower, in us for the first and the second of these: two CTAs an SM
+// What bounds it: instructions.  64 keys of 128 rows take 0.63 us of a CTA, some 1250 cycles, of which the
+// tensor cores are busy 770, and each scheduler issues some 900 instructions: 64 weights of a row and
+// their parts are about 9 each (a softmax thread), the roles beside it the rest.  A segment's start and end
+// cost ten blocks.  32 trees of 16 nodes (64 rows) over 2049 tokens of 8 KV heads, 134 MB: 58 to 60 us, of
+// which the merge 6; one of 64 nodes over 32768: 56 to 61; 128 of 24 over 17 to 16384 with a window of 4096:
+// 166 to 169; with scales per (token, head) the first takes 82.  What was tried and is slower, in us for the
+// first and the second of these, then at 57 and 56 (weights of 9 bits): two CTAs an SM
 // with two buffers each 77 and 78; two groups, four buffers and Q in tensor memory (steps of 32 cycles
 // and not 48) 58 and 58; the maximum handed on behind S's loads, so that the groups go in step, 61 and
 // 60; two producers each of K and V and two issuers of S, the logits read twice so that 608 threads
@@ -76,7 +77,9 @@ constexpr uint32_t kTmemCols = 512, kOutCol = 384;    // the buffers at 0, O at 
 constexpr int kRing = 64 * 1024;  // of K, and of V
 constexpr int kEntries = 1024;  // prefix sums of the plan: of every ceil(B / 1024)th sequence
 constexpr int kKept = 256;      // sequences up to which their lengths are kept beside the prefix sums
-constexpr int kSegCost = 10;     // a segment's start and end, in blocks (128 mixed sequences: 161 us; with 4, 195; with 16, 168)
+// A segment's start and end, in blocks.  Swept on 128 mixed sequences, in us, with weights of 9 bits: 4 195,
+// 8 168, 10 161, 12 159, 16 168; 16 bf16 ones: 4 41, 8 and 10 37, 12 39.
+constexpr int kSegCost = 10;
 constexpr int kMinShare = 4;    // least cost of a CTA's stretch
 constexpr float kBias = 7.f;    // log2 of the factor that the weights carry
 constexpr int kPieces = 32;     // descriptions of pieces

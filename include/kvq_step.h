@@ -148,7 +148,21 @@ KVQ_API size_t kvq_tree_workspace_size(int num_q_heads, int num_kv_heads, int he
  * weight as two bf16 parts, within 2^-17.  With KVQ_SCALE_PER_TOKEN_HEAD the
  * weight carries its value's scale relative to the largest that its row has
  * seen, and the 2^-24 is of the row's largest weight times that scale; scales
- * of tokens that a row does not see are nothing to it.
+ * of tokens that a row does not see are nothing to it.  A NaN or an infinity in
+ * a cache reaches the rows that see its token, and no others: one in V^ its own
+ * dim, an infinity as an infinity or a NaN.  V of a bf16 cache may be finite
+ * values up to 2^90.
+ *
+ * Without parents the call does what kvq_prefill_attn does, and with one node
+ * a sequence what kvq_decode_attn does, as exactly (the decode's weights have
+ * two f16 parts).  Which is faster (GB300, 32 heads of 128 over 8 KV heads):
+ * one token a sequence, kvq_decode_attn (32 x 2049 tokens of FP8: 34 us, here
+ * 56, kvq_prefill_attn 122); chunks over an FP8 cache, this call up to some 16
+ * tokens, and while sequences are few and long (32 x 16 tokens over 2048: 62
+ * us against 106; 1 x 64 over 32768: 60 against 497), kvq_prefill_attn from
+ * some 64 tokens of many sequences on (32 x 64 over 2048: 133 against 103;
+ * 8 x 256: 196 against 104); chunks over a bf16 cache, this call (32 x 64 over
+ * 2048: 127 against 979).
  * Limits: num_seqs <= 4096; num_kv_heads <= 256; num_q_heads / num_kv_heads
  * <= 8; num_blocks * num_kv_heads * block_size < 2^31; max_blocks_per_seq *
  * block_size < 2^30; num_seqs * num_kv_heads * T * (max_blocks_per_seq / 4 +
@@ -169,8 +183,9 @@ KVQ_API int kvq_tree_attn(const void* q, const int32_t* cu_q_lens, int64_t num_q
 /*
  * One cache tensor of one layer, for the calls that move rows or pages.  A
  * page of one KV head is 16 rows of row_bytes, then 16 rows of sub_bytes:
- *   FP8 / bf16 cache      row_bytes = head_dim / 2 * head_dim, sub_bytes = 0
- *   its scale cache       row_bytes = 4, sub_bytes = 0
+ *   FP8 cache             row_bytes = head_dim, sub_bytes = 0
+ *   bf16 cache            row_bytes = 2 * head_dim, sub_bytes = 0
+ *   scale cache           row_bytes = 4, sub_bytes = 0
  *   4-bit cache           row_bytes = head_dim / 2, sub_bytes = head_dim / 16
  * row_bytes and sub_bytes are multiples of 4 up to 512 (sub_bytes may be 0);
  * data is 16-byte aligned, [num_blocks][num_kv_heads] pages.

@@ -270,3 +270,44 @@ def test_small_query_values_beside_a_large_one(kvq, fmt, small):  # noqa: F811
     bound = 2.0 ** -8 * ref.abs() + (2.0 ** -11 + 2.0 ** -18 + 2 * d) * (a + 1) / (a + 2)
     err = (o.out.double() - ref[..., None]).abs()
     assert bool((err <= bound[..., None]).all()), float((err / bound[..., None]).max())
+
+
+@pytest.mark.parametrize("dh", [64, 128])
+def test_large_values_of_bf16_caches(kvq, dh):  # noqa: F811
+    """V times 2^84 (values to 2^90) gives the outputs times 2^84, bit for bit: no sum leaves binary32."""
+    b = TreeBatch([(9000, 20), (300, 40), (17, 17)], 8, 2, dh, BF16, seed=71)
+    g = OnGpu(kvq, b)
+    g.call()
+    clean = g.out.clone()
+    b.vc.copy_(torch.nan_to_num(b.vc.double()) * 2.0 ** 84)
+    g.call()
+    torch.cuda.synchronize()
+    assert torch.equal(g.out.double(), clean.double() * 2.0 ** 84)
+
+
+@pytest.mark.parametrize("fmt,gran,dh", [(E4M3, PER_HEAD, 128), (E5M2, PER_TOKEN_HEAD, 64), (BF16, PER_HEAD, 128)])
+def test_bad_values_before_the_tree(kvq, fmt, gran, dh):  # noqa: F811
+    """NaN and infinities in tokens that every row of a sequence sees, far from its tree: a value's in its own dim, a key's in
+    its head's rows, nothing elsewhere."""
+    b = TreeBatch([(3000, 20), (500, 30), (9000, 9)], 8, 2, dh, fmt, gran, seed=72)
+    g = OnGpu(kvq, b)
+    g.call()
+    clean = g.out.clone()
+    nan = math.nan if fmt == BF16 else 0x7F
+    at = lambda i, t: (int(b.bt[i, t // 16]), t % 16)  # noqa: E731
+    blk, s = at(0, 700)
+    b.vc[blk, 1, s, 3] = nan
+    blk, s = at(1, 100)
+    b.kc[blk, 0, s, 5] = nan
+    bad = torch.zeros(b.q.shape, dtype=torch.bool, device="cuda")
+    bad[:20, 4:, 3] = True
+    bad[20:50, :4] = True
+    if fmt != E4M3:
+        blk, s = at(2, 4000)
+        b.vc[blk, 1, s, 9] = math.inf if fmt == BF16 else 0x7C
+        bad[50:, 4:, 9] = True
+    g.call()
+    torch.cuda.synchronize()
+    assert int(g.st.item()) == 0
+    assert bool(g.out[:50][bad[:50]].isnan().all()) and not bool(g.out[50:][bad[50:]].isfinite().any())
+    assert torch.equal(g.out[~bad], clean[~bad])
